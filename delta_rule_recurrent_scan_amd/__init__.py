@@ -110,6 +110,7 @@ def load_library():
     L.osdn_kernel_timing.restype = None
     L.osdn_kernel_times.argtypes = [I, P, P, P]
     L.osdn_kernel_times.restype = I
+    mixer.bind(L)
     _lib = L
     return L
 
@@ -658,3 +659,9 @@ def osdn_gated_forward(q, k, v, beta, log_alpha, r=None, eta=0.1, d0=None,
     if rc != 0:
         raise OsdnError(rc, "osdn_gated_forward")
     return o, S_T, d_T
+
+
+from . import mixer  # noqa: E402  (uses the helpers above)
+from .mixer import *  # noqa: E402,F401,F403
+
+__all__ += mixer.__all__

@@ -1,50 +1,16 @@
 // C ABI of libosdn.so: host-side validation, workspace sizing and the launch
 // sequence. Declarations and the full contract are in include/osdn.h.
-#include "../../include/osdn.h"
-
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "api_common.hpp"
 #include "launch.hpp"
+
+using namespace osdn_api;
 
 namespace {
 
-bool dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
 bool chunk_ok(int c) { return c == 16 || c == 32 || c == 64; }
-size_t elem(int dtype) { return dtype == OSDN_BF16 ? 2 : 4; }
-size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
-
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi)
-  bool valid() const { return lo != 0 && hi > lo; }
-};
-Range rng(const void* p, size_t bytes) {
-  return Range{(uintptr_t)p, (uintptr_t)p + bytes};
-}
-bool overlap(Range a, Range b) {
-  return a.valid() && b.valid() && a.lo < b.hi && b.lo < a.hi;
-}
-bool same(Range a, Range b) { return a.lo == b.lo && a.hi == b.hi; }
-
-// Outputs must not overlap inputs or each other, except for the exact
-// in-place pairs listed in `allowed` (output index, input index).
-template <int NO, int NI>
-bool aliasing_ok(const Range (&outs)[NO], const Range (&ins)[NI],
-                 const int (*allowed)[2], int nallowed) {
-  for (int i = 0; i < NO; ++i) {
-    for (int j = 0; j < NI; ++j) {
-      if (!overlap(outs[i], ins[j])) continue;
-      bool ok = false;
-      for (int a = 0; a < nallowed; ++a)
-        if (allowed[a][0] == i && allowed[a][1] == j && same(outs[i], ins[j]))
-          ok = true;
-      if (!ok) return false;
-    }
-    for (int j = i + 1; j < NO; ++j)
-      if (overlap(outs[i], outs[j])) return false;
-  }
-  return true;
-}
 
 // The gated forward forms K~ inside the engine at chunk 64 where that layout
 // fits; otherwise it goes through the preconditioned keys in the workspace.
@@ -90,12 +56,14 @@ const char* osdn_strerror(int status) {
   switch (status) {
     case OSDN_OK: return "ok";
     case OSDN_ERR_NULL_ARG: return "a required pointer argument is NULL";
-    case OSDN_ERR_BAD_DIMS: return "bad dimensions: B, H and T must be >= 0";
+    case OSDN_ERR_BAD_DIMS: 
+      return "bad dimensions: sizes and strides must be >= 0, groups divide the heads";
     case OSDN_ERR_UNSUPPORTED:
-      return "unsupported combination of Dk, Dv, chunk and dtype";
+      return "unsupported combination of sizes and dtype";
     case OSDN_ERR_WORKSPACE: return "workspace missing or too small";
     case OSDN_ERR_ALIASING:
       return "an output overlaps an input or another output";
+    case OSDN_ERR_MISALIGNED: return "a tensor is not 16-byte aligned";
     case OSDN_ERR_HIP: return "the HIP runtime rejected a kernel launch";
   }
   return "unknown status";

@@ -1,0 +1,490 @@
+// Short causal depthwise convolution with SiLU and, per head, an L2 row norm:
+//   u_t = bias + sum_k weight[:, k] * x_{t - W + 1 + k}
+//   v   = u * sigmoid(u)                               (activation)
+//   y   = v * rsqrt(sum_head v^2 + eps)                (l2norm)
+// from token rows x [B,T,C] (any row stride: a slice of a wider projection)
+// to the heads [B,H,T,D] that the recurrences read, with the last W - 1
+// inputs carried as a state.
+//
+// Bound by HBM: x is read once and y written once (2 x 2 bytes an element in
+// bf16), some 15 VALU operations an element beside it. A thread owns 8
+// consecutive channels and walks a segment of tokens with the last W - 1
+// inputs and the weights in registers, so a wave moves 1 KB contiguous pieces
+// of a row; a segment re-reads W - 1 rows of its predecessor (from L2). A
+// head of 32, 64 or 128 channels is 4, 8 or 16 adjacent lanes, and its norm a
+// DPP sum: no LDS.
+//
+// Backward, with dv = r (dy - v r^2 <v, dy>) for the norm (r = rsqrt(..)),
+// du = dv * sigmoid(u) (1 + u (1 - sigmoid(u))) and the inputs with their
+// state as rows 0 .. T + W - 2:
+//   dfull_r = sum_k weight[:, k] du_{r - k},  dweight_k = sum_t du_t full_{t+k}
+// A thread recomputes u while it walks, keeps the W rows still open in
+// registers and emits a row when its last term is in; weight gradients stay
+// in registers over the segment, are added over the workgroup's segments in
+// LDS, and leave as one partial a workgroup (summed in a fixed order by
+// column_sum).
+#include "launch.hpp"
+#include "mixer.hpp"
+#include "row_common.hpp"
+
+namespace osdn {
+namespace {
+
+// Tokens a thread fetches before it works on them: 8 rows of 16 bytes in
+// flight a lane.
+constexpr int kBatch = 8;
+
+template <typename T>
+struct ConvIn {
+  const T* x;
+  long long xts;
+  const T* st;  // state rows of this batch entry, or null
+  int C, W, c, nv;
+  // row t of the inputs, t < 0 reading the state before them
+  template <bool ALN>
+  __device__ __forceinline__ void row(int t, float (&v)[8]) const {
+    if (t >= 0) {
+      load8<ALN>(x + t * xts + c, nv, v);
+    } else if (st) {
+      load8<ALN>(st + (size_t)(W - 1 + t) * C + c, nv, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    }
+  }
+};
+
+template <int W>
+__device__ __forceinline__ void load_weights(const float* weight, const float* bias, int c,
+                                             int nv, float (&w)[W][8], float (&bi)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const bool ok = i < nv;
+    bi[i] = ok && bias ? bias[c + i] : 0.f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) w[k][i] = ok ? weight[(size_t)(c + i) * W + k] : 0.f;
+  }
+}
+
+template <typename T, bool ALN>
+__device__ __forceinline__ void store_heads(T* y, long long bh0, int Tn, int D, int t, int c,
+                                            int nv, const float (&v)[8]) {
+  if constexpr (ALN) {
+    store8<true>(y + ((bh0 + c / D) * Tn + t) * (long long)D + c % D, 8, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < nv)
+        y[((bh0 + (c + i) / D) * Tn + t) * (long long)D + (c + i) % D] = from_f32<T>(v[i]);
+  }
+}
+
+template <typename T, bool ALN>
+__device__ __forceinline__ void load_heads(const T* y, long long bh0, int Tn, int D, int t,
+                                           int c, int nv, float (&v)[8]) {
+  if constexpr (ALN) {
+    load8<true>(y + ((bh0 + c / D) * Tn + t) * (long long)D + c % D, 8, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = i < nv ? to_f32(y[((bh0 + (c + i) / D) * Tn + t) * (long long)D + (c + i) % D])
+                    : 0.f;
+  }
+}
+
+template <typename Tin, int W, bool ALN>
+__global__ __launch_bounds__(kRowThreads) void conv_kernel(ConvArgs a, int cx, int seg,
+                                                           int nseg) {
+  const int C = a.H * a.D, ng = (C + 7) / 8;
+  const int ncb = (ng + cx - 1) / cx, cb = blockIdx.x % ncb, rb = blockIdx.x / ncb;
+  const int cg = cb * cx + (threadIdx.x & (cx - 1));
+  const long long by = rb * (long long)(kRowThreads / cx) + threadIdx.x / cx;
+  const int sg = (int)(by % nseg);
+  const long long b = by / nseg;
+  if (cg >= ng || b >= a.B) return;  // a head's lanes leave together
+  const int c = cg * 8, nv = C - c;
+  int n = a.lengths ? a.lengths[b] : a.T;
+  n = n < 0 ? 0 : n > a.T ? a.T : n;
+  ConvIn<Tin> in{(const Tin*)a.x + b * a.xbs, a.xts,
+                 a.state0 ? (const Tin*)a.state0 + b * (W - 1) * C : nullptr, C, W, c, nv};
+  float w[W][8], bi[8];
+  load_weights<W>(a.weight, a.bias, c, nv, w, bi);
+
+  const int t0 = sg * seg, t1 = min(t0 + seg, a.T), tn = min(t1, n);
+  const int L = a.D / 8;  // lanes of a head (l2 only)
+  Tin* y = (Tin*)a.y;
+  float h[W][8];  // h[k] = input t - W + 1 + k
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k) in.template row<ALN>(t0 - (W - 1) + k, h[k + 1]);
+  auto token = [&](int t) {
+    float u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      u[i] = bi[i];
+#pragma unroll
+      for (int k = 0; k < W; ++k) u[i] += w[k][i] * h[k][i];
+    }
+    if (a.act) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] *= sigmoid_f(u[i]);
+    }
+    if (a.l2) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += u[i] * u[i];
+      const float r = rsqrtf(head_sum(s, L) + a.eps);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] *= r;
+    }
+    store_heads<Tin, ALN>(y, b * a.H, a.T, a.D, t, c, nv, u);
+  };
+  int t = t0;
+  for (; t + kBatch <= tn; t += kBatch) {
+    float f[kBatch][8];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) in.template row<ALN>(t + j, f[j]);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) h[k][i] = h[k + 1][i];
+        h[W - 1][i] = f[j][i];
+      }
+      token(t + j);
+    }
+  }
+  for (; t < tn; ++t) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int k = 0; k < W - 1; ++k) h[k][i] = h[k + 1][i];
+    in.template row<ALN>(t, h[W - 1]);
+    token(t);
+  }
+  const float zero[8] = {};
+  for (; t < t1; ++t) store_heads<Tin, ALN>(y, b * a.H, a.T, a.D, t, c, nv, zero);
+
+  if (sg == 0 && a.stateT) {
+    // all rows read before any is written: state_T may be state0
+    float f[W][8];
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) in.template row<ALN>(n - (W - 1) + k, f[k]);
+    Tin* st = (Tin*)a.stateT + b * (W - 1) * C + c;
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) store8<ALN>(st + (size_t)k * C, nv, f[k]);
+  }
+}
+
+template <typename Tin, typename Tdy, int W, bool ALN>
+__global__ __launch_bounds__(kRowThreads) void conv_bwd_kernel(ConvBackwardArgs p, int cx,
+                                                               int seg, int nseg) {
+  const ConvArgs& a = p.f;
+  const int C = a.H * a.D, ng = (C + 7) / 8;
+  const int lx = threadIdx.x & (cx - 1), ly = threadIdx.x / cx;
+  const int ncb = (ng + cx - 1) / cx, cb = blockIdx.x % ncb, rb = blockIdx.x / ncb;
+  const int cg = cb * cx + lx;
+  const long long by = rb * (long long)(kRowThreads / cx) + ly;
+  const int sg = (int)(by % nseg);
+  const long long b = by / nseg;
+  const bool on = cg < ng && b < a.B;
+  const int c = cg * 8, nv = C - c;
+  float dw[W + 1][8] = {};  // weight gradients, then the bias'
+  if (on) {
+    int n = a.lengths ? a.lengths[b] : a.T;
+    n = n < 0 ? 0 : n > a.T ? a.T : n;
+    ConvIn<Tin> in{(const Tin*)a.x + b * a.xbs, a.xts,
+                   a.state0 ? (const Tin*)a.state0 + b * (W - 1) * C : nullptr, C, W, c, nv};
+    float w[W][8], bi[8];
+    load_weights<W>(a.weight, a.bias, c, nv, w, bi);
+    const int L = a.D / 8;
+    // rows [r0, r1) of the T + W - 1 of the inputs with their state
+    const int rows = a.T + W - 1;
+    const int r0 = sg * seg, r1 = min(r0 + seg, rows);
+    const Tin* dst = p.dstateT ? (const Tin*)p.dstateT + b * (W - 1) * C + c : nullptr;
+    float h[W][8], acc[W][8] = {};
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) {
+      const int t = r0 - 2 * (W - 1) + k;
+      if (t >= -(W - 1) && t < n) {
+        in.template row<ALN>(t, h[k + 1]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[k + 1][i] = 0.f;
+      }
+    }
+    // du_t enters rows t .. t + W - 1 (acc[k] = row t + k); row t is then whole
+    auto token = [&](int t, const float (&xt)[8], const float (&dy)[8]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) h[k][i] = h[k + 1][i];
+        h[W - 1][i] = xt[i];
+      }
+      if (t >= 0 && t < n) {
+        float u[8], d[8], sl[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          u[i] = bi[i];
+#pragma unroll
+          for (int k = 0; k < W; ++k) u[i] += w[k][i] * h[k][i];
+          d[i] = dy[i];
+          sl[i] = 1.f;
+        }
+        if (a.act) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float sgm = sigmoid_f(u[i]);
+            sl[i] = sgm * (1.f + u[i] * (1.f - sgm));
+            u[i] *= sgm;
+          }
+        }
+        if (a.l2) {
+          float s = 0.f, q = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            s += u[i] * u[i];
+            q += u[i] * d[i];
+          }
+          const float r = rsqrtf(head_sum(s, L) + a.eps);
+          q = head_sum(q, L) * r * r;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d[i] = r * (d[i] - u[i] * q);
+        }
+        const bool mine = t >= r0;  // earlier tokens: a predecessor's sums
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          d[i] *= sl[i];
+          const float dm = mine ? d[i] : 0.f;
+#pragma unroll
+          for (int k = 0; k < W; ++k) {
+            acc[k][i] += w[k][i] * d[i];
+            dw[k][i] += dm * h[k][i];
+          }
+          dw[W][i] += dm;
+        }
+      }
+      if (t >= r0) {
+        if (dst && t >= n && t < n + W - 1) {
+          float f[8];
+          load8<ALN>(dst + (size_t)(t - n) * C, nv, f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[0][i] += f[i];
+        }
+        if (t >= W - 1) {
+          store8<ALN>((Tin*)p.dx + (b * a.T + (t - (W - 1))) * (long long)C + c, nv, acc[0]);
+        } else if (p.dstate0) {
+          store8<ALN>((Tin*)p.dstate0 + (b * (W - 1) + t) * (long long)C + c, nv, acc[0]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) acc[k][i] = acc[k + 1][i];
+        acc[W - 1][i] = 0.f;
+      }
+    };
+    auto fetch = [&](int t, float (&xt)[8], float (&dy)[8]) {
+      if (t >= -(W - 1) && t < n) {
+        in.template row<ALN>(t, xt);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) xt[i] = 0.f;
+      }
+      if (t >= 0 && t < n) {
+        load_heads<Tdy, ALN>((const Tdy*)p.dy, b * a.H, a.T, a.D, t, c, nv, dy);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dy[i] = 0.f;
+      }
+    };
+    constexpr int kB = 4;
+    int t = r0 - (W - 1);
+    for (; t + kB <= r1; t += kB) {
+      float xt[kB][8], dy[kB][8];
+#pragma unroll
+      for (int j = 0; j < kB; ++j) fetch(t + j, xt[j], dy[j]);
+#pragma unroll
+      for (int j = 0; j < kB; ++j) token(t + j, xt[j], dy[j]);
+    }
+    for (; t < r1; ++t) {
+      float xt[8], dy[8];
+      fetch(t, xt, dy);
+      token(t, xt, dy);
+    }
+  }
+  // the workgroup's segments added: one partial row [W + 1][C] a workgroup
+  __shared__ float red[kRowThreads * 9];  // 9: adjacent threads on other banks
+  float* part = (float*)p.ws + (size_t)rb * (W + 1) * C;
+#pragma unroll
+  for (int k = 0; k <= W; ++k) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) red[threadIdx.x * 9 + i] = dw[k][i];
+    __syncthreads();
+    for (int e = threadIdx.x; e < cx * 8; e += kRowThreads) {
+      const int col = (cb * cx + e / 8) * 8 + e % 8;
+      if (col >= C) continue;
+      float s = 0.f;
+      for (int r = 0; r < kRowThreads / cx; ++r) s += red[(r * cx + e / 8) * 9 + e % 8];
+      part[(size_t)k * C + col] = s;
+    }
+  }
+}
+
+__global__ __launch_bounds__(256) void column_sum_kernel(const float* __restrict__ in, int rows,
+                                                         int cols, int c, int w, float* out0,
+                                                         float* out1) {
+  // 32 columns x 8 row lanes; each adds every 8th row, then LDS
+  __shared__ float red[8][33];
+  const int x = threadIdx.x & 31, r0 = threadIdx.x >> 5;
+  const int j = blockIdx.x * 32 + x;
+  float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+  if (j < cols) {
+    int r = r0;
+    for (; r + 24 < rows; r += 32) {
+      s0 += in[(size_t)r * cols + j];
+      s1 += in[(size_t)(r + 8) * cols + j];
+      s2 += in[(size_t)(r + 16) * cols + j];
+      s3 += in[(size_t)(r + 24) * cols + j];
+    }
+    for (; r < rows; r += 8) s0 += in[(size_t)r * cols + j];
+  }
+  red[r0][x] = (s0 + s1) + (s2 + s3);
+  __syncthreads();
+  if (r0 == 0 && j < cols) {
+    float s = 0.f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) s += red[r][x];
+    const int k = j / c, ch = j % c;
+    if (k < w) {
+      out0[(size_t)ch * w + k] = s;
+    } else if (out1) {
+      out1[ch] = s;
+    }
+  }
+}
+
+// Tokens a thread walks: long enough that the W - 1 re-read rows are a small
+// part, short enough that some 16 waves a CU are in flight. `per` = threads a
+// segment length of one token would give.
+int pick_seg(double per, int T, int least, int most) {
+  int seg = most;
+  while (seg > least && per / seg < 256.0 * 16 * 64) seg /= 2;
+  return seg < T ? seg : (T > 0 ? T : 1);
+}
+
+template <typename Tin, int W>
+int run_conv(const ConvArgs& a, hipStream_t s) {
+  const int C = a.H * a.D, ng = (C + 7) / 8, cx = row_cx(ng);
+  const int seg = a.whole ? (a.T > 0 ? a.T : 1)
+                          : pick_seg((double)a.B * a.T * ng, a.T, 8, 32);
+  const int nseg = a.T > 0 ? (a.T + seg - 1) / seg : 1;
+  const long long rows = (long long)a.B * nseg;
+  const int per = kRowThreads / cx;
+  const dim3 grid((unsigned)((ng + cx - 1) / cx * ((rows + per - 1) / per)));
+  const size_t m = 16 - 1, es = sizeof(Tin);
+  const bool aln = a.D % 8 == 0 && ((size_t)a.x & m) == 0 && ((size_t)a.y & m) == 0 &&
+                   ((size_t)a.state0 & m) == 0 && ((size_t)a.stateT & m) == 0 &&
+                   (a.xbs * es & m) == 0 && (a.xts * es & m) == 0;
+  const int tk = ktimer_before(s, "short_conv");
+  if (aln) {
+    hipLaunchKernelGGL((conv_kernel<Tin, W, true>), grid, dim3(kRowThreads), 0, s, a, cx, seg,
+                       nseg);
+  } else {
+    hipLaunchKernelGGL((conv_kernel<Tin, W, false>), grid, dim3(kRowThreads), 0, s, a, cx, seg,
+                       nseg);
+  }
+  ktimer_after(s, tk);
+  return (int)hipGetLastError();
+}
+
+constexpr int kConvBwdSeg = 32;
+
+struct BwdGrid {
+  int cx, nseg, per, parts;
+};
+BwdGrid bwd_grid(int B, int T, int C, int W) {
+  BwdGrid g;
+  g.cx = row_cx((C + 7) / 8);
+  g.nseg = (T + W - 1 + kConvBwdSeg - 1) / kConvBwdSeg;
+  g.per = kRowThreads / g.cx;
+  g.parts = (int)(((long long)B * g.nseg + g.per - 1) / g.per);
+  return g;
+}
+
+template <typename Tin, typename Tdy, int W>
+int run_conv_bwd(const ConvBackwardArgs& p, hipStream_t s) {
+  const ConvArgs& a = p.f;
+  const int C = a.H * a.D, ng = (C + 7) / 8;
+  const BwdGrid g = bwd_grid(a.B, a.T, C, W);
+  const dim3 grid((unsigned)((ng + g.cx - 1) / g.cx * g.parts));
+  const size_t m = 16 - 1, es = sizeof(Tin);
+  const bool aln = a.D % 8 == 0 && ((size_t)a.x & m) == 0 && ((size_t)p.dy & m) == 0 &&
+                   ((size_t)a.state0 & m) == 0 && ((size_t)p.dstateT & m) == 0 &&
+                   ((size_t)p.dx & m) == 0 && ((size_t)p.dstate0 & m) == 0 &&
+                   (a.xbs * es & m) == 0 && (a.xts * es & m) == 0;
+  const int tk = ktimer_before(s, "short_conv_bwd");
+  if (g.parts == 0) {
+    // an empty batch: the sums below are zeros
+  } else if (aln) {
+    hipLaunchKernelGGL((conv_bwd_kernel<Tin, Tdy, W, true>), grid, dim3(kRowThreads), 0, s, p,
+                       g.cx, kConvBwdSeg, g.nseg);
+  } else {
+    hipLaunchKernelGGL((conv_bwd_kernel<Tin, Tdy, W, false>), grid, dim3(kRowThreads), 0, s, p,
+                       g.cx, kConvBwdSeg, g.nseg);
+  }
+  ktimer_after(s, tk);
+  const int rc = (int)hipGetLastError();
+  if (rc) return rc;
+  return launch_column_sum((const float*)p.ws, g.parts, (W + 1) * C, C, W, p.dweight, p.dbias,
+                           s);
+}
+
+template <typename Tin>
+int run_conv_w(const ConvArgs& a, hipStream_t s) {
+  switch (a.W) {
+    case 2: return run_conv<Tin, 2>(a, s);
+    case 3: return run_conv<Tin, 3>(a, s);
+    case 4: return run_conv<Tin, 4>(a, s);
+  }
+  return -1;
+}
+
+template <typename Tin, typename Tdy>
+int run_conv_bwd_w(const ConvBackwardArgs& a, hipStream_t s) {
+  switch (a.f.W) {
+    case 2: return run_conv_bwd<Tin, Tdy, 2>(a, s);
+    case 3: return run_conv_bwd<Tin, Tdy, 3>(a, s);
+    case 4: return run_conv_bwd<Tin, Tdy, 4>(a, s);
+  }
+  return -1;
+}
+
+}  // namespace
+
+int launch_column_sum(const float* in, int rows, int cols, int c, int w, float* out0,
+                      float* out1, hipStream_t s) {
+  const int tk = ktimer_before(s, "column_sum");
+  hipLaunchKernelGGL(column_sum_kernel, dim3((cols + 31) / 32), dim3(256), 0, s, in, rows, cols,
+                     c, w, out0, out1);
+  ktimer_after(s, tk);
+  return (int)hipGetLastError();
+}
+
+int launch_short_conv(const ConvArgs& a, hipStream_t s) {
+  return a.bf16 ? run_conv_w<__bf16>(a, s) : run_conv_w<float>(a, s);
+}
+
+size_t short_conv_backward_ws(int B, int T, int H, int D, int W) {
+  if (B == 0 || H == 0 || D == 0) return 0;
+  return (size_t)bwd_grid(B, T, H * D, W).parts * (W + 1) * H * D * sizeof(float);
+}
+
+int launch_short_conv_backward(const ConvBackwardArgs& a, hipStream_t s) {
+  if (a.f.bf16)
+    return a.dy_bf16 ? run_conv_bwd_w<__bf16, __bf16>(a, s) : run_conv_bwd_w<__bf16, float>(a, s);
+  return a.dy_bf16 ? -1 : run_conv_bwd_w<float, float>(a, s);
+}
+
+}  // namespace osdn

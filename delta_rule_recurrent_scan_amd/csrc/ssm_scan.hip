@@ -1,0 +1,302 @@
+// Selective state space scan, prompts. Per (batch, head), with a_t =
+// exp(dt_t A) and the head's group's keys B and queries C:
+//   S_t = a_t S_{t-1} + dt_t x_t B_t^T        (P x N)
+//   y_t = S_t C_t + D x_t
+// in chunks of Q tokens: with L_ij = exp(sum of dt A over (j, i]),
+//   y_i = sum_{j<=i} (C_i . B_j) L_ij dt_j x_j + L_i0 S_in C_i + D x_i
+//   S_out = L_Q0 S_in + sum_j L_Qj dt_j x_j B_j^T
+// as matrix products on MFMA.
+//
+// One workgroup walks a segment of the chunks of one (batch, head) with the
+// state in accumulators: wave w owns P / waves rows of it (all N columns), so
+// that the state never leaves registers between chunks; its tiles, read as
+// (row p, k = n) fragments in accumulator order, are the operand of the
+// readout without a trip through LDS. Scores are formed once a chunk, each
+// wave a share of the token rows, and pass through LDS. The next chunk's rows
+// are in flight while one is worked on.
+//
+// A (batch, head) is cut into segments where B * H alone leaves CUs idle:
+// a first pass forms each segment's own contribution to the state (keys and
+// values only), a small kernel chains them, and the segments then run at once.
+//
+// Rounding (bf16 inputs): scores and the state are rounded to bf16 once where
+// they enter the two products of y, which is rounded to bf16 itself; the
+// state's own update takes dt x L in two bf16 parts (16 bits), and is
+// accumulated in fp32. fp32 inputs use fp32 MFMA throughout (Q = 32).
+#include "launch.hpp"
+#include "mixer.hpp"
+#include "ssm_common.hpp"
+
+namespace osdn {
+namespace {
+
+constexpr int kScanWaves = 4;
+
+template <int P>
+constexpr int scan_waves() { return P / 16 < kScanWaves ? P / 16 : kScanWaves; }
+
+template <typename Tin>
+constexpr int scan_q() { return sizeof(Tin) == 2 ? 64 : 32; }
+
+// Segments of the T tokens: `len` tokens each (a multiple of the chunk).
+struct Segments {
+  int n, len;
+};
+
+template <int P, int N, typename Tin, bool YOUT>
+__global__ __launch_bounds__(64 * scan_waves<P>()) void ssm_scan_kernel(SsmArgs a, int nseg,
+                                                                        int seglen,
+                                                                        float* seg_state,
+                                                                        float* seg_log) {
+  constexpr int Q = scan_q<Tin>(), NW = scan_waves<P>(), NT = 64 * NW;
+  constexpr int QT = Q / 16, PT = P / 16 / NW, NTL = N / 16;
+  constexpr int LN = N + 16 / sizeof(Tin), LP = P + 16 / sizeof(Tin), LQ = Q + 16 / sizeof(Tin);
+  __shared__ __attribute__((aligned(16))) Tin Bs[Q * LN];
+  __shared__ __attribute__((aligned(16))) Tin Cs[YOUT ? Q * LN : 16];
+  __shared__ __attribute__((aligned(16))) Tin Xs[Q * LP];
+  __shared__ __attribute__((aligned(16))) Tin Ms[YOUT ? Q * LQ : 16];
+  __shared__ __attribute__((aligned(16))) ChunkDecay<Q> dec;
+  __shared__ __attribute__((aligned(16))) float wts[Q];
+
+  const int lane = threadIdx.x & 63, w = wave_id();
+  const int nwg = YOUT ? nseg : nseg - 1;  // the last segment hands nothing on
+  const int bh = blockIdx.x / nwg, sg = blockIdx.x % nwg;
+  const int b = bh / a.H, h = bh % a.H;
+  const int n = ssm_length(a.lengths, b, a.T);
+  const float A = a.A[h], D = a.D ? a.D[h] : 0.f, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+  const size_t th = (size_t)bh * a.T;
+  const size_t tg = ((size_t)b * a.G + h / (a.H / a.G)) * a.T;
+  const Tin* x = (const Tin*)a.x + th * P;
+  const Tin* Bm = (const Tin*)a.Bm + tg * N;
+  const Tin* Cm = (const Tin*)a.Cm + tg * N;
+  Tin* y = (Tin*)a.y + th * P;
+  const float* dt = a.dt + th;
+
+  const int t0 = sg * seglen, t1 = min(t0 + seglen, a.T), tn = min(t1, n);
+
+  // S[pt][nt]: rows n = 16 nt + 4 (l / 16) + e of column p = l % 16 of the
+  // wave's p tile
+  f32x4 S[PT][NTL];
+  const int p0 = w * PT * 16 + (lane & 15), n0 = 4 * (lane >> 4);
+  const float* in = !YOUT ? nullptr
+                    : sg > 0 ? seg_state + ((size_t)bh * (nseg - 1) + sg - 1) * P * N
+                    : a.S0  ? a.S0 + (size_t)bh * P * N
+                            : nullptr;
+#pragma unroll
+  for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+    for (int nt = 0; nt < NTL; ++nt)
+      S[pt][nt] = in ? load4(in + (size_t)(p0 + 16 * pt) * N + 16 * nt + n0)
+                     : f32x4{0.f, 0.f, 0.f, 0.f};
+  float logsum = 0.f;
+
+  Stage<Q, N, Tin, NT> fb, fc;
+  Stage<Q, P, Tin, NT> fx;
+  float fdt = 0.f;
+  auto fetch = [&](int t) {
+    const int valid = tn - t;
+    fb.fetch(Bm + (size_t)t * N, valid);
+    if (YOUT) fc.fetch(Cm + (size_t)t * N, valid);
+    fx.fetch(x + (size_t)t * P, valid);
+    if (w == 0) fdt = lane < Q && lane < valid ? dt[t + lane] : 0.f;
+  };
+  if (t0 < tn) fetch(t0);
+  for (int t = t0; t < tn; t += Q) {
+    const int valid = tn - t;
+    __syncthreads();
+    fb.put(Bs, LN);
+    if (YOUT) fc.put(Cs, LN);
+    fx.put(Xs, LP);
+    if (w == 0) {
+      const float st = lane < Q && lane < valid ? ssm_step(fdt, bias, a.softplus) : 0.f;
+      dec.fill(st, st * A);
+      wave_lds_sync();
+      if (lane < Q) wts[lane] = st * dec.ext[lane];
+    }
+    if (t + Q < tn) fetch(t + Q);
+    __syncthreads();
+
+    if constexpr (YOUT) {
+      // scores of this wave's query tiles, key tiles up to the diagonal
+#pragma unroll
+      for (int q = 0; q < QT / NW + (QT % NW != 0); ++q) {
+        const int it = q * NW + w;
+        if (it >= QT) break;
+        Frag<N, Tin> cf;
+        cf.load(Cs + it * 16 * LN, LN);
+#pragma unroll
+        for (int jt = 0; jt < QT; ++jt) {
+          f32x4 s = {0.f, 0.f, 0.f, 0.f};
+          if (jt <= it) {
+            Frag<N, Tin> bf;
+            bf.load(Bs + jt * 16 * LN, LN);
+            mma(s, bf, cf);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[r] *= pair_decay<Q>(dec, it, jt, r);
+          }
+          store4(Ms + (it * 16 + (lane & 15)) * LQ + jt * 16 + n0, s);
+        }
+      }
+      __syncthreads();
+    }
+
+    Frag<Q, Tin> xf[PT];
+#pragma unroll
+    for (int pt = 0; pt < PT; ++pt) xf[pt].load_kmajor(Xs + (w * PT + pt) * 16, LP);
+    if constexpr (YOUT) {
+      Frag<N, Tin> sf[PT];
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) frag_from_acc<N>(sf[pt], S[pt]);
+#pragma unroll
+      for (int it = 0; it < QT; ++it) {
+        Frag<N, Tin> cf;
+        cf.load_perm(Cs + it * 16 * LN, LN);
+        Frag<Q, Tin> mf;
+        mf.load(Ms + it * 16 * LQ, LQ);
+        const int ti = it * 16 + (lane & 15);
+        const float ent = dec.ent[ti];
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) {
+          f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+          mma(acc, sf[pt], cf);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[e] *= ent;
+          mma_upto<Q>(acc, xf[pt], mf, 16 * (it + 1));
+          const int p = (w * PT + pt) * 16 + n0;
+          const f32x4 xv = load4(Xs + ti * LP + p);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[e] = ti < valid ? acc[e] + D * xv[e] : 0.f;
+          if (t + ti < t1) store4(y + (size_t)(t + ti) * P + p, acc);
+        }
+      }
+    }
+
+    const float total = dec.total;
+    logsum += dec.logtot;
+    Frag<Q, Tin> hi[PT], lo[PT];
+#pragma unroll
+    for (int pt = 0; pt < PT; ++pt) scale_split<Q>(xf[pt], wts, hi[pt], lo[pt]);
+#pragma unroll
+    for (int nt = 0; nt < NTL; ++nt) {
+      Frag<Q, Tin> bf;
+      bf.load_kmajor(Bs + nt * 16, LN);
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[pt][nt][e] *= total;
+        mma(S[pt][nt], bf, hi[pt]);
+        if constexpr (sizeof(Tin) == 2) mma(S[pt][nt], bf, lo[pt]);
+      }
+    }
+  }
+
+  if constexpr (YOUT) {
+    // rows behind the sequence's last chunk
+    const int from = tn > t0 ? t0 + (tn - t0 + Q - 1) / Q * Q : t0;
+    constexpr int VE = 16 / sizeof(Tin);
+    for (int e = threadIdx.x; e < max(t1 - from, 0) * (P / VE); e += NT)
+      *reinterpret_cast<uint4*>(y + (size_t)from * P + (size_t)e * VE) = uint4{0u, 0u, 0u, 0u};
+  }
+  float* out = YOUT ? (a.ST && sg == nseg - 1 ? a.ST + (size_t)bh * P * N : nullptr)
+                    : seg_state + ((size_t)bh * (nseg - 1) + sg) * P * N;
+  if (out) {
+#pragma unroll
+    for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+      for (int nt = 0; nt < NTL; ++nt)
+        store4(out + (size_t)(p0 + 16 * pt) * N + 16 * nt + n0, S[pt][nt]);
+    if (!YOUT && threadIdx.x == 0) seg_log[(size_t)bh * (nseg - 1) + sg] = logsum;
+  }
+}
+
+// The segments' entry states from their own contributions, in place: slot i
+// (segment i's contribution) becomes the state entering segment i + 1.
+__global__ __launch_bounds__(256) void ssm_chain_kernel(int PN, int nslots, const float* S0,
+                                                        float* state, const float* logd) {
+  const int bh = blockIdx.y;
+  const int e = (blockIdx.x * 256 + threadIdx.x) * 4;
+  if (e >= PN) return;
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  if (S0) s = load4(S0 + (size_t)bh * PN + e);
+  for (int i = 0; i < nslots; ++i) {
+    float* p = state + ((size_t)bh * nslots + i) * PN + e;
+    const float f = expf(logd[(size_t)bh * nslots + i]);
+    const f32x4 c = load4(p);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s[k] = f * s[k] + c[k];
+    store4(p, s);
+  }
+}
+
+// Segments: enough to give every CU two workgroups' work, none shorter than
+// 4 chunks (a segment costs the first pass over its keys and values and two
+// trips of its state).
+Segments segments(int B, int H, int T, int Q) {
+  const int nch = (T + Q - 1) / Q;
+  const long long bh = (long long)B * H;
+  long long want = bh > 0 ? (1024 + bh - 1) / bh : 1;
+  if (want > nch / 4) want = nch / 4;
+  if (want < 1) want = 1;
+  const int per = nch > 0 ? (int)((nch + want - 1) / want) : 1;
+  Segments s;
+  s.len = per * Q;
+  s.n = nch > 0 ? (nch + per - 1) / per : 1;
+  return s;
+}
+
+template <int P, int N, typename Tin>
+int run_scan(const SsmArgs& a, hipStream_t s) {
+  const int BH = a.B * a.H, PN = P * N;
+  const Segments g = segments(a.B, a.H, a.T, scan_q<Tin>());
+  float* st = (float*)a.ws;
+  float* lg = st + (size_t)BH * (g.n - 1) * PN;
+  constexpr int NT = 64 * scan_waves<P>();
+  if (g.n > 1) {
+    int tk = ktimer_before(s, "ssm_state");
+    hipLaunchKernelGGL((ssm_scan_kernel<P, N, Tin, false>), dim3((unsigned)(BH * (g.n - 1))),
+                       dim3(NT), 0, s, a, g.n, g.len, st, lg);
+    ktimer_after(s, tk);
+    tk = ktimer_before(s, "ssm_chain");
+    hipLaunchKernelGGL(ssm_chain_kernel, dim3((PN / 4 + 255) / 256, BH), dim3(256), 0, s, PN,
+                       g.n - 1, a.S0, st, lg);
+    ktimer_after(s, tk);
+  }
+  const int tk = ktimer_before(s, "ssm_scan");
+  hipLaunchKernelGGL((ssm_scan_kernel<P, N, Tin, true>), dim3((unsigned)(BH * g.n)), dim3(NT), 0,
+                     s, a, g.n, g.len, st, lg);
+  ktimer_after(s, tk);
+  return (int)hipGetLastError();
+}
+
+template <int P, int N>
+int run_scan_t(const SsmArgs& a, hipStream_t s) {
+  return a.bf16 ? run_scan<P, N, __bf16>(a, s) : run_scan<P, N, float>(a, s);
+}
+
+template <int P>
+int run_scan_n(const SsmArgs& a, hipStream_t s) {
+  switch (a.N) {
+    case 32: return run_scan_t<P, 32>(a, s);
+    case 64: return run_scan_t<P, 64>(a, s);
+    case 128: return run_scan_t<P, 128>(a, s);
+  }
+  return -1;
+}
+
+}  // namespace
+
+size_t ssm_forward_ws(int B, int H, int T, int P, int N, int bf16) {
+  const Segments g = segments(B, H, T, bf16 ? scan_q<__bf16>() : scan_q<float>());
+  return (size_t)B * H * (g.n - 1) * ((size_t)P * N + 1) * sizeof(float);
+}
+
+int launch_ssm_forward(const SsmArgs& a, hipStream_t s) {
+  switch (a.P) {
+    case 32: return run_scan_n<32>(a, s);
+    case 64: return run_scan_n<64>(a, s);
+    case 128: return run_scan_n<128>(a, s);
+  }
+  return -1;
+}
+
+}  // namespace osdn

@@ -50,11 +50,12 @@ enum { OSDN_F32 = 0, OSDN_BF16 = 1 };
 enum {
   OSDN_OK = 0,
   OSDN_ERR_NULL_ARG = 1,     /* a required pointer is NULL                */
-  OSDN_ERR_BAD_DIMS = 2,     /* B, H or T negative                        */
-  OSDN_ERR_UNSUPPORTED = 3,  /* Dk, Dv, chunk or dtype has no kernel      */
+  OSDN_ERR_BAD_DIMS = 2,     /* a size or stride negative or out of range */
+  OSDN_ERR_UNSUPPORTED = 3,  /* the sizes or dtypes have no kernel        */
   OSDN_ERR_WORKSPACE = 4,    /* workspace NULL or smaller than required   */
   OSDN_ERR_ALIASING = 5,     /* partial overlap of an input and an output */
-  OSDN_ERR_HIP = 6           /* the HIP runtime rejected a launch         */
+  OSDN_ERR_HIP = 6,          /* the HIP runtime rejected a launch         */
+  OSDN_ERR_MISALIGNED = 7    /* a tensor is not 16-byte aligned           */
 };
 
 /* Human-readable text for a status code (static storage, never NULL). */
@@ -425,6 +426,182 @@ int gdn2_backward(int B, int H, int T, int Dk, int Dv, int dtype,
                   void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Operators around the recurrences: the short convolution that makes q, k, v
+ * (or x, B, C) out of a projection, the selective scan, the gated norm that
+ * takes the heads back to token rows, and the residual norm before a block.
+ * Their own conventions, beside the shared ones above:
+ *  - `lengths` ([B] int32 on the device, NULL: T each): a padded batch. Tokens
+ *    at and behind a sequence's length are never used (they may hold anything,
+ *    NaN included), their outputs and gradients are written as zeros, and
+ *    states are those after the last token inside. Values are clamped to
+ *    [0, T].
+ *  - Backward: adjoints and gradients of activations and of the convolution's
+ *    state are in the activation's dtype (each rounded once, at the end), so
+ *    that one operator's gradient is the next one's adjoint; gradients of
+ *    parameters, steps and fp32 states are fp32. Sums over tokens run in a
+ *    fixed order: the same call gives the same bits.
+ *  - Parameters (weights, biases, A, D) are fp32.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Short causal depthwise convolution over W tokens (W in {2, 3, 4}), with
+ * SiLU and an L2 norm of each head's row, from token rows to heads. Per batch
+ * entry and channel c = h*D + i:
+ *   u_t = bias_c + sum_{k<W} weight[c,k] * x_{t-W+1+k}
+ *   v_t = u_t * sigmoid(u_t)                       (activation != 0, else u_t)
+ *   y_t = v_t * rsqrt(sum over the head of v_t^2 + eps)   (l2norm != 0, else v_t)
+ *
+ *   x        [B,T,C], C = H*D, dtype: element (b,t,c) at x[b*x_batch_stride +
+ *            t*x_token_stride + c] (strides in elements, >= 0), so that a
+ *            channel range of a wider projection is read in place
+ *   weight   [C,W] fp32 (required);  bias [C] fp32 (NULL: zeros)
+ *   state0   [B,W-1,C] dtype: the W-1 inputs before the first (NULL: zeros)
+ *   y        [B,H,T,D] dtype. H = 1, D = C gives token rows; any C is taken.
+ *   state_T  [B,W-1,C] dtype: the last W-1 inputs (NULL: not written)
+ * l2norm needs D in {32, 64, 128}. Rows that start on 16 bytes with D a
+ * multiple of 8 take 16-byte accesses; others go element by element.
+ */
+int short_conv_forward(int B, int T, int H, int D, int W, int dtype,
+                       const void* x, long long x_batch_stride,
+                       long long x_token_stride, const float* weight,
+                       const float* bias, const void* state0,
+                       const int* lengths, int activation, int l2norm,
+                       float eps, void* y, void* state_T, void* stream);
+
+/*
+ * The same for the few tokens (usually T = 1) of a decode step: one thread
+ * walks all T tokens of its channels, and state_out may be exactly `state`
+ * (updated in place). Both are required.
+ */
+int short_conv_decode(int B, int T, int H, int D, int W, int dtype,
+                      const void* x, long long x_batch_stride,
+                      long long x_token_stride, const float* weight,
+                      const float* bias, const void* state, int activation,
+                      int l2norm, float eps, void* y, void* state_out,
+                      void* stream);
+
+/*
+ * Backward of short_conv_forward: the gradient of sum <dy, y> + <dstate_T,
+ * state_T>.
+ *   dy       [B,H,T,D] in dy_dtype: the dtype of x or fp32 (what the
+ *            recurrences' backward returns)
+ *   dstate_T [B,W-1,C] dtype (NULL: zero)
+ *   dx       [B,T,C] dtype OUT, contiguous;  dstate0 [B,W-1,C] dtype OUT
+ *            (NULL: not written);  dweight [C,W], dbias [C] fp32 OUT (dbias
+ *            NULL: not written)
+ *   workspace: short_conv_backward_workspace_bytes(...) bytes, 256-byte
+ *            aligned: partial sums of the weight gradients
+ */
+size_t short_conv_backward_workspace_bytes(int B, int T, int H, int D, int W);
+int short_conv_backward(int B, int T, int H, int D, int W, int dtype,
+                        int dy_dtype, const void* x, long long x_batch_stride,
+                        long long x_token_stride, const float* weight,
+                        const float* bias, const void* state0,
+                        const int* lengths, int activation, int l2norm,
+                        float eps, const void* dy, const void* dstate_T,
+                        void* dx, void* dstate0, float* dweight, float* dbias,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Selective state space scan: a recurrence with one decay per token and head
+ * and no erase, its keys and queries shared by the H / G heads of a group (g =
+ * h / (H / G); G divides H). Per (batch, head), with
+ * dt_t = softplus(dt[t] + dt_bias_h) (softplus == 0: the sum itself):
+ *   S_t = exp(dt_t A_h) S_{t-1} + dt_t x_t B_t^T     (P x N)
+ *   y_t = S_t C_t + D_h x_t                          (after token t's update)
+ *
+ *   x        [B,H,T,P] dtype;  Bm, Cm [B,G,T,N] dtype
+ *   dt       [B,H,T] fp32;  A [H] fp32 (< 0 for a decay);  D, dt_bias [H] fp32
+ *            (NULL: zeros)
+ *   S0       [B,H,P,N] fp32 (NULL: zeros)
+ *   y        [B,H,T,P] dtype;  S_T [B,H,P,N] fp32 (NULL: not written); S_T may
+ *            be exactly S0
+ * P, N in {32, 64, 128}; any T. Tensors start on 16 bytes
+ * (OSDN_ERR_MISALIGNED). workspace: ssm_forward_workspace_bytes(...) bytes,
+ * 256-byte aligned: the states between the segments that long sequences of
+ * few (batch, head) streams are cut into (0 where they are not).
+ */
+size_t ssm_forward_workspace_bytes(int B, int H, int G, int T, int P, int N,
+                                   int dtype);
+int ssm_forward(int B, int H, int G, int T, int P, int N, int dtype,
+                const void* x, const float* dt, const float* A, const void* Bm,
+                const void* Cm, const float* D, const float* dt_bias,
+                int softplus, const float* S0, const int* lengths, void* y,
+                float* S_T, void* workspace, size_t workspace_bytes,
+                void* stream);
+
+/*
+ * T tokens (usually 1) of the same recurrence with the state read from S and
+ * written to S_out, which may be exactly S (in place). No workspace.
+ */
+int ssm_decode(int B, int H, int G, int T, int P, int N, int dtype,
+               const void* x, const float* dt, const float* A, const void* Bm,
+               const void* Cm, const float* D, const float* dt_bias,
+               int softplus, const float* S, void* y, float* S_out,
+               void* stream);
+
+/*
+ * Norm of each head's row with a gate, from heads to token rows:
+ *   gate_first == 0:  y = x * rsqrt(mean_D x^2 + eps) * weight * silu(z)
+ *   gate_first != 0:  v = x * silu(z),  y = v * rsqrt(mean_D v^2 + eps) * weight
+ *
+ *   x        [B,H,T,D] dtype (D in {32, 64, 128})
+ *   z        [B,T,H*D] dtype rows with strides as short_conv_forward's x
+ *            (NULL: no gate)
+ *   weight   [D] fp32, or [H,D] when weight_per_head
+ *   y        [B,T,H*D] dtype
+ * x, y and the backward's dy, dx, dz start on 16 bytes.
+ */
+int gated_norm_forward(int B, int H, int T, int D, int dtype, const void* x,
+                       const void* z, long long z_batch_stride,
+                       long long z_token_stride, const float* weight,
+                       int weight_per_head, float eps, int gate_first, void* y,
+                       void* stream);
+
+/* Its backward: dy [B,T,H*D] dtype; dx [B,H,T,D], dz [B,T,H*D] dtype OUT (dz
+ * required with z), dweight fp32 OUT of weight's shape; workspace: partial
+ * sums of dweight, gated_norm_backward_workspace_bytes(...) bytes. */
+size_t gated_norm_backward_workspace_bytes(int B, int H, int T, int D);
+int gated_norm_backward(int B, int H, int T, int D, int dtype, const void* x,
+                        const void* z, long long z_batch_stride,
+                        long long z_token_stride, const float* weight,
+                        int weight_per_head, float eps, int gate_first,
+                        const void* dy, void* dx, void* dz, float* dweight,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Residual add and norm of R rows of C channels:
+ *   h = residual + scale * x (residual NULL: scale * x)
+ *   y = h * rsqrt(mean h^2 + eps) * weight
+ * y is formed from the 32-bit h; the stored h is rounded to res_dtype (the
+ * dtype of x, or fp32 beside bf16).
+ *   x, y     [R,C] dtype;  residual, h [R,C] res_dtype (h NULL: not written;
+ *            h may be exactly residual);  weight [C] fp32
+ * Any C up to OSDN_RESIDUAL_NORM_MAX_WIDTH (more: OSDN_ERR_UNSUPPORTED).
+ */
+#define OSDN_RESIDUAL_NORM_MAX_WIDTH 16384
+int residual_norm_forward(long long R, int C, int dtype, int res_dtype,
+                          const void* x, const void* residual, float scale,
+                          const float* weight, float eps, void* y, void* h,
+                          void* stream);
+
+/*
+ * Its backward from the stored h: dy [R,C] dtype is the adjoint of y, dh [R,C]
+ * res_dtype the adjoint that reaches h from the blocks behind (NULL: zero).
+ * dresidual [R,C] res_dtype OUT (NULL: not written) is the gradient of h, dx
+ * [R,C] dtype OUT is scale times it, dweight [C] fp32 OUT.
+ */
+size_t residual_norm_backward_workspace_bytes(long long R, int C);
+int residual_norm_backward(long long R, int C, int dtype, int res_dtype,
+                           const void* dy, const void* h, const void* dh,
+                           float scale, const float* weight, float eps,
+                           void* dx, void* dresidual, float* dweight,
+                           void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
  * Per-kernel timing for measurement harnesses. While enabled, every entry
  * point records a HIP event on its stream before and after each kernel it
  * launches (two event records per kernel; events are created on first use
@@ -447,7 +624,9 @@ void osdn_kernel_timing(int enable);
  * backbone), osdn_decode, gdn2_decode (recurrent decode), osdn_bwd_record,
  * osdn_bwd, osdn_bwd_learner (backward), gated_bwd_record, gated_bwd,
  * gated_bwd_learner, gdn2_bwd_record, gdn2_bwd, gdn2_bwd_out (gate-aware
- * backward).
+ * backward), short_conv, short_conv_bwd, ssm_state, ssm_chain, ssm_scan,
+ * ssm_decode, gated_norm, gated_norm_bwd, residual_norm, residual_norm_bwd,
+ * column_sum (the operators around the recurrences).
  */
 int osdn_kernel_times(int max, const char** names, int* counts, float* mean_ms);
 
