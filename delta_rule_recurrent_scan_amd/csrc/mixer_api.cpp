@@ -337,4 +337,41 @@ int ssm_decode(int B, int H, int G, int T, int P, int N, int dtype, const void* 
       (hipStream_t)stream));
 }
 
+size_t ssm_backward_workspace_bytes(int B, int H, int G, int T, int P, int N, int dtype) {
+  if (ssm_dims(B, H, G, T, P, N, dtype) != OSDN_OK) return 0;
+  return round256(osdn::ssm_backward_ws(B, H, G, T, P, N, dtype == OSDN_BF16));
+}
+
+int ssm_backward(int B, int H, int G, int T, int P, int N, int dtype, const void* x,
+                 const float* dt, const float* A, const void* Bm, const void* Cm, const float* D,
+                 const float* dt_bias, int softplus, const float* S0, const int* lengths,
+                 const void* dy, const float* dS_T, void* dx, float* ddt, float* dA, void* dB,
+                 void* dC, float* dD, float* ddt_bias, float* dS0, void* workspace,
+                 size_t workspace_bytes, void* stream) {
+  const int rc = ssm_dims(B, H, G, T, P, N, dtype);
+  if (rc != OSDN_OK) return rc;
+  const size_t BH = (size_t)B * H, es = elem(dtype), st = BH * P * N * 4;
+  if (H == 0) return OSDN_OK;
+  if (!A || !dA ||
+      (BH * T > 0 && (!x || !dt || !Bm || !Cm || !dy || !dx || !ddt || !dB || !dC)))
+    return OSDN_ERR_NULL_ARG;
+  const size_t need = ssm_backward_workspace_bytes(B, H, G, T, P, N, dtype);
+  if (!workspace_ok(workspace, workspace_bytes, need)) return OSDN_ERR_WORKSPACE;
+  if (!aligned16(x) || !aligned16(Bm) || !aligned16(Cm) || !aligned16(dy) || !aligned16(dx) ||
+      !aligned16(dB) || !aligned16(dC))
+    return OSDN_ERR_MISALIGNED;
+  const size_t tx = BH * T * P * es, tg = (size_t)B * G * T * N * es, hb = (size_t)H * 4;
+  const Range ins[] = {rng(x, tx), rng(dt, BH * T * 4), rng(A, hb), rng(Bm, tg), rng(Cm, tg),
+                       rng(D, hb), rng(dt_bias, hb), rng(S0, st), rng(lengths, (size_t)B * 4),
+                       rng(dy, tx), rng(dS_T, st)};
+  const Range outs[] = {rng(dx, tx), rng(ddt, BH * T * 4), rng(dA, hb), rng(dB, tg), rng(dC, tg),
+                        rng(dD, hb), rng(ddt_bias, hb), rng(dS0, st), rng(workspace, need)};
+  if (!aliasing_ok(outs, ins, nullptr, 0)) return OSDN_ERR_ALIASING;
+  osdn::SsmArgs a = ssm_args(B, H, G, T, P, N, dtype, x, dt, A, Bm, Cm, D, dt_bias, softplus, S0,
+                             lengths, nullptr, nullptr, workspace);
+  a.dy = dy; a.dST = dS_T; a.dx = dx; a.dB = dB; a.dC = dC;
+  a.ddt = ddt; a.dA = dA; a.dD = dD; a.dbias = ddt_bias; a.dS0 = dS0;
+  return status(osdn::launch_ssm_backward(a, (hipStream_t)stream));
+}
+
 }  // extern "C"

@@ -195,8 +195,8 @@ int run_gated_bwd(const GatedNormArgs& a, hipStream_t s) {
   // a weight shared by the heads: every head of every partial is a row
   if (a.per_head)
     return launch_column_sum((const float*)a.ws, nrb, a.H * a.D, a.H * a.D, 1, a.dweight,
-                             nullptr, s);
-  return launch_column_sum((const float*)a.ws, nrb * a.H, a.D, a.D, 1, a.dweight, nullptr, s);
+                             nullptr, nullptr, s);
+  return launch_column_sum((const float*)a.ws, nrb * a.H, a.D, a.D, 1, a.dweight, nullptr, nullptr, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -393,7 +393,7 @@ int run_res(const ResidualNormArgs& a, int bwd, hipStream_t s) {
     if (rc) return rc;
   }
   return launch_column_sum((const float*)a.ws, nb * rows_per_wg(WPR), a.C, a.C, 1, a.dweight,
-                           nullptr, s);
+                           nullptr, nullptr, s);
 }
 
 template <typename Tin, typename Tr>

@@ -334,7 +334,7 @@ __global__ __launch_bounds__(kRowThreads) void conv_bwd_kernel(ConvBackwardArgs 
 
 __global__ __launch_bounds__(256) void column_sum_kernel(const float* __restrict__ in, int rows,
                                                          int cols, int c, int w, float* out0,
-                                                         float* out1) {
+                                                         float* out1, float* out2) {
   // 32 columns x 8 row lanes; each adds every 8th row, then LDS
   __shared__ float red[8][33];
   const int x = threadIdx.x & 31, r0 = threadIdx.x >> 5;
@@ -359,8 +359,8 @@ __global__ __launch_bounds__(256) void column_sum_kernel(const float* __restrict
     const int k = j / c, ch = j % c;
     if (k < w) {
       out0[(size_t)ch * w + k] = s;
-    } else if (out1) {
-      out1[ch] = s;
+    } else if (float* o = k == w ? out1 : out2) {
+      o[ch] = s;
     }
   }
 }
@@ -438,7 +438,7 @@ int run_conv_bwd(const ConvBackwardArgs& p, hipStream_t s) {
   const int rc = (int)hipGetLastError();
   if (rc) return rc;
   return launch_column_sum((const float*)p.ws, g.parts, (W + 1) * C, C, W, p.dweight, p.dbias,
-                           s);
+                           nullptr, s);
 }
 
 template <typename Tin>
@@ -464,10 +464,10 @@ int run_conv_bwd_w(const ConvBackwardArgs& a, hipStream_t s) {
 }  // namespace
 
 int launch_column_sum(const float* in, int rows, int cols, int c, int w, float* out0,
-                      float* out1, hipStream_t s) {
+                      float* out1, float* out2, hipStream_t s) {
   const int tk = ktimer_before(s, "column_sum");
   hipLaunchKernelGGL(column_sum_kernel, dim3((cols + 31) / 32), dim3(256), 0, s, in, rows, cols,
-                     c, w, out0, out1);
+                     c, w, out0, out1, out2);
   ktimer_after(s, tk);
   return (int)hipGetLastError();
 }

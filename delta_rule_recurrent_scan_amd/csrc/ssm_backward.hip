@@ -1,0 +1,689 @@
+// Backward of the selective state space scan. With the state adjoint
+//   dS_t = dy_t C_t^T + a_{t+1} dS_{t+1}        (P x N, from dS_T)
+// the gradients of a (batch, head) are
+//   dx_t = dt_t dS_t B_t + D dy_t
+//   dB_t = dt_t dS_t^T x_t,  dC_t = S_t^T dy_t  (summed over the group's heads)
+//   d dt_t = x_t . dS_t B_t + A g_t,  dA = sum dt_t g_t,  dD = sum dy . x
+//   g_t = a_t <dS_t, S_{t-1}>                   (of the log decay dt_t A)
+// and dS_0 = a_1 dS_1. In chunks of Q tokens, with L_ij the decay from token j
+// to i, S the state entering the chunk and dS the adjoint leaving it:
+//   K_ij = (C_i . B_j) L_ij dt_j,  Z_ij = (dy_i . x_j) L_ij dt_j      (j <= i)
+//   dx_j = sum_i K_ij dy_i + L_Qj dt_j dS B_j + D dy_j
+//   dC_i = sum_j Z_ij B_j + L_i0 S^T dy_i
+//   dB_j = sum_i Z_ij C_i + L_Qj dt_j dS^T x_j
+// g_t is the sum over every pair of a source before t (the entering state, a
+// token j < t) and a use at or after it (a token i >= t, the leaving adjoint):
+//   g_t = sum_{i>=t>j} (C_i . B_j) Z_ij + sum_{i>=t} w_i + sum_{j<t} u_j
+//         + L_Q0 <dS, S>,   w_i = C_i . (L_i0 S^T dy_i),
+//                           u_j = B_j . (L_Qj dt_j dS^T x_j)
+// of which the last three are sums of one sign of index, and the first, a
+// suffix sum of (row - column) sums, stays inside one chunk: nothing grows
+// with the sequence and then cancels.
+//
+// Two kernels. The walk forms S at every chunk's entry and dS at every
+// chunk's exit (both directions in one launch, a workgroup a segment of one
+// (batch, head), the state in accumulators as in the forward) and writes them
+// in fp32 in accumulator order, so that the second kernel's fragments are
+// contiguous 16-byte loads. The chunk kernel then takes every chunk at once: a
+// workgroup loops over heads of a group, with the group's scores C B^T held
+// and dB, dC accumulated in registers, so the sum over heads costs no memory
+// and no atomics. The wave's share is a token tile for the scores and dx, and
+// tiles of state columns n for dB and dC.
+//
+// Rounding (bf16 inputs): K, Z and dS are rounded to bf16 once where they
+// enter products that leave in bf16; S, dS and the walks' dt x L enter in
+// three bf16 parts (24 bits) wherever the result reaches an fp32 output.
+#include "launch.hpp"
+#include "mixer.hpp"
+#include "ssm_common.hpp"
+
+namespace osdn {
+namespace {
+
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
+
+template <typename Tin>
+constexpr int bwd_q() { return sizeof(Tin) == 2 ? 64 : 32; }
+
+// Where an element of a state lies in accumulator order: tile (p / 16, n / 16)
+// of 64 lanes x 4 values, lane (n % 16) + 16 * (p % 16 / 4), value p % 4.
+__device__ __forceinline__ void state_elem(int e, int ntl, int& p, int& n) {
+  const int tile = e / 256, lane = e % 256 / 4;
+  p = tile / ntl * 16 + 4 * (lane / 16) + e % 4;
+  n = tile % ntl * 16 + lane % 16;
+}
+
+// ---------------------------------------------------------------------------
+// The walk. Streams 0 .. BH - 1 run forward (x, B, weights dt L_Qj, from S0),
+// BH .. 2 BH - 1 in reverse (dy, C, weights L_i0, from dS_T). Segment k counts
+// along the direction.
+// ---------------------------------------------------------------------------
+template <int P, int N, typename Tin, bool WRITE>
+__global__ __launch_bounds__(64 * (P / 16 < kWaves ? P / 16 : kWaves)) void ssm_walk_kernel(
+    SsmArgs a, int nseg, int segch, float* slots, float* slot_log, float* states) {
+  constexpr int Q = bwd_q<Tin>(), NW = P / 16 < kWaves ? P / 16 : kWaves, NT = 64 * NW;
+  constexpr int PT = P / 16 / NW, NTL = N / 16;
+  constexpr int LN = N + 16 / sizeof(Tin), LP = P + 16 / sizeof(Tin);
+  __shared__ __attribute__((aligned(16))) Tin Ks[Q * LN];
+  __shared__ __attribute__((aligned(16))) Tin Vs[Q * LP];
+  __shared__ __attribute__((aligned(16))) ChunkDecay<Q> dec;
+  __shared__ __attribute__((aligned(16))) float wts[Q];
+
+  const int lane = threadIdx.x & 63, w = wave_id();
+  const int BH = a.B * a.H, nwg = WRITE ? nseg : nseg - 1;
+  const int stream = blockIdx.x / nwg, k = blockIdx.x % nwg;
+  const bool rev = stream >= BH;
+  const int bh = rev ? stream - BH : stream;
+  const int b = bh / a.H, h = bh % a.H, sg = rev ? nseg - 1 - k : k;
+  const int n = ssm_length(a.lengths, b, a.T), nch = (a.T + Q - 1) / Q;
+  const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+  const size_t th = (size_t)bh * a.T;
+  const size_t tg = ((size_t)b * a.G + h / (a.H / a.G)) * a.T;
+  const Tin* val = (const Tin*)(rev ? a.dy : a.x) + th * P;
+  const Tin* key = (const Tin*)(rev ? a.Cm : a.Bm) + tg * N;
+  const float* dt = a.dt + th;
+
+  // S[pt][nt]: rows p = 4 (l / 16) + e of the wave's p tile, column n = l % 16
+  f32x4 S[PT][NTL];
+  const float* from = rev ? a.dST : a.S0;
+#pragma unroll
+  for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+    for (int nt = 0; nt < NTL; ++nt) {
+      const int tile = (w * PT + pt) * NTL + nt;
+      if (!WRITE || (k == 0 && !from)) {
+        S[pt][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+      } else if (k > 0) {
+        S[pt][nt] = load4(slots + ((size_t)stream * (nseg - 1) + k - 1) * P * N +
+                          (tile * 64 + lane) * 4);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          int p, c;
+          state_elem((tile * 64 + lane) * 4 + e, NTL, p, c);
+          S[pt][nt][e] = from[((size_t)bh * P + p) * N + c];
+        }
+      }
+    }
+  float logsum = 0.f;
+
+  const int c0 = sg * segch, c1 = min(c0 + segch, nch);
+  const int cn = min(c1, (n + Q - 1) / Q);  // chunks with tokens
+  Stage<Q, N, Tin, NT> fk;
+  Stage<Q, P, Tin, NT> fv;
+  float fdt = 0.f;
+  auto fetch = [&](int c) {
+    const int t = c * Q, valid = n - t;
+    fk.fetch(key + (size_t)t * N, valid);
+    fv.fetch(val + (size_t)t * P, valid);
+    if (w == 0) fdt = lane < Q && lane < valid ? dt[t + lane] : 0.f;
+  };
+  const int count = max(cn - c0, 0);
+  if (count) fetch(rev ? cn - 1 : c0);
+  for (int i = 0; i < count; ++i) {
+    const int c = rev ? cn - 1 - i : c0 + i, valid = n - c * Q;
+    __syncthreads();
+    fk.put(Ks, LN);
+    fv.put(Vs, LP);
+    if (w == 0) {
+      const float st = lane < Q && lane < valid ? ssm_step(fdt, bias, a.softplus) : 0.f;
+      dec.fill(st, st * A);
+      wave_lds_sync();
+      if (lane < Q) wts[lane] = rev ? dec.ent[lane] : st * dec.ext[lane];
+    }
+    if (i + 1 < count) fetch(rev ? c - 1 : c + 1);
+    if constexpr (WRITE) {
+      float* out = states + ((size_t)stream * nch + c) * P * N;
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+        for (int nt = 0; nt < NTL; ++nt)
+          store4(out + (((w * PT + pt) * NTL + nt) * 64 + lane) * 4, S[pt][nt]);
+    }
+    __syncthreads();
+    const float total = dec.total;
+    logsum += dec.logtot;
+    Parts<Q, Tin> vw[PT];
+#pragma unroll
+    for (int pt = 0; pt < PT; ++pt) {
+      Frag<Q, Tin> vf;
+      vf.load_kmajor(Vs + (w * PT + pt) * 16, LP);
+      scale_parts<Q>(vf, wts, vw[pt]);
+    }
+#pragma unroll
+    for (int nt = 0; nt < NTL; ++nt) {
+      Frag<Q, Tin> kf;
+      kf.load_kmajor(Ks + nt * 16, LN);
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[pt][nt][e] *= total;
+        mma_parts(S[pt][nt], vw[pt], kf);
+      }
+    }
+  }
+
+  if constexpr (!WRITE) {
+    float* out = slots + ((size_t)stream * (nseg - 1) + k) * P * N;
+#pragma unroll
+    for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+      for (int nt = 0; nt < NTL; ++nt)
+        store4(out + (((w * PT + pt) * NTL + nt) * 64 + lane) * 4, S[pt][nt]);
+    if (threadIdx.x == 0) slot_log[(size_t)stream * (nseg - 1) + k] = logsum;
+  } else if (rev && k == nseg - 1 && a.dS0) {
+#pragma unroll
+    for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+      for (int nt = 0; nt < NTL; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          int p, c;
+          state_elem((((w * PT + pt) * NTL + nt) * 64 + lane) * 4 + e, NTL, p, c);
+          a.dS0[((size_t)bh * P + p) * N + c] = S[pt][nt][e];
+        }
+  }
+}
+
+// Segments' contributions (slot k: segment k's own) into the states entering
+// segment k + 1, in place, along each stream.
+__global__ __launch_bounds__(256) void ssm_walk_chain_kernel(int BH, int PN, int N, int nslots,
+                                                             const float* S0, const float* dST,
+                                                             float* slots, const float* logd) {
+  const int stream = blockIdx.y, e = (blockIdx.x * 256 + threadIdx.x) * 4;
+  if (e >= PN) return;
+  const bool rev = stream >= BH;
+  const float* from = rev ? dST : S0;
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  if (from) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      int p, n;
+      state_elem(e + i, N / 16, p, n);
+      s[i] = from[(size_t)(rev ? stream - BH : stream) * PN + (size_t)p * N + n];
+    }
+  }
+  for (int i = 0; i < nslots; ++i) {
+    float* q = slots + ((size_t)stream * nslots + i) * PN + e;
+    const float f = expf(logd[(size_t)stream * nslots + i]);
+    const f32x4 c = load4(q);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = f * s[j] + c[j];
+    store4(q, s);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The chunk kernel: workgroup (batch, group, chunk, part of the group's heads).
+// ---------------------------------------------------------------------------
+struct ChunkOut {
+  const float* states;  // [2][BH][nch][P N], accumulator order
+  float* sums;          // [B nch][3][H]: dA, dD, dbias of a chunk
+  float *dBp, *dCp;     // [parts][B G T N] fp32 where the heads are split
+  int parts, hper;      // head parts of a group, heads of a part
+};
+
+template <int P, int N, typename Tin>
+__global__ __launch_bounds__(kThreads) void ssm_bwd_chunk_kernel(SsmArgs a, ChunkOut o) {
+  constexpr int Q = bwd_q<Tin>(), QT = Q / 16, NTL = N / 16, PTL = P / 16;
+  constexpr int NQ = (NTL + kWaves - 1) / kWaves;  // n tiles of a wave
+  constexpr int PAD = 16 / sizeof(Tin), LN = N + PAD, LP = P + PAD, LQ = Q + PAD;
+  constexpr int PH = kWaves / QT;  // waves that share a token tile of dx
+  __shared__ __attribute__((aligned(16))) Tin Bs[Q * LN];
+  __shared__ __attribute__((aligned(16))) Tin Cs[Q * LN];
+  __shared__ __attribute__((aligned(16))) Tin Xs[Q * LP];
+  __shared__ __attribute__((aligned(16))) Tin Ys[Q * LP];
+  __shared__ __attribute__((aligned(16))) Tin Ks[Q * LQ];
+  __shared__ __attribute__((aligned(16))) Tin Zs[Q * LQ];
+  __shared__ __attribute__((aligned(16))) Tin dSs[N * LP];
+  __shared__ __attribute__((aligned(16))) ChunkDecay<Q> dec;
+  __shared__ float rowv[Q], diag[Q], colv[kWaves][Q], wv[kWaves][Q], uv[kWaves][Q];
+  __shared__ float dots[kWaves], dds[kWaves];
+
+  const int lane = threadIdx.x & 63, w = wave_id(), lc = lane & 15, g4 = 4 * (lane >> 4);
+  const int nch = (a.T + Q - 1) / Q, Hg = a.H / a.G;
+  int id = blockIdx.x;
+  const int part = id % o.parts;
+  id /= o.parts;
+  const int c = id % nch;
+  id /= nch;
+  const int g = id % a.G, b = id / a.G;
+  const int BH = a.B * a.H, t0 = c * Q;
+  const int n = ssm_length(a.lengths, b, a.T), valid = n - t0, rows = min(Q, a.T - t0);
+  const int h0 = g * Hg + part * o.hper, h1 = min(h0 + o.hper, (g + 1) * Hg);
+  const size_t tg = ((size_t)b * a.G + g) * a.T + t0;
+  const size_t GTN = (size_t)a.B * a.G * a.T * N;
+  float* sums = o.sums + ((size_t)b * nch + c) * 3 * a.H;
+
+  f32x4 dB[NQ][QT], dC[NQ][QT];
+#pragma unroll
+  for (int q = 0; q < NQ; ++q)
+#pragma unroll
+    for (int it = 0; it < QT; ++it)
+      dB[q][it] = dC[q][it] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  if (valid > 0) {
+    Stage<Q, P, Tin, kThreads> fx, fy;
+    float fdt = 0.f;
+    auto fetch = [&](int h) {
+      const size_t th = ((size_t)b * a.H + h) * a.T + t0;
+      fx.fetch((const Tin*)a.x + th * P, valid);
+      fy.fetch((const Tin*)a.dy + th * P, valid);
+      if (w == 0) fdt = lane < Q && lane < valid ? a.dt[th + lane] : 0.f;
+    };
+    {
+      Stage<Q, N, Tin, kThreads> fb, fc;
+      fb.fetch((const Tin*)a.Bm + tg * N, valid);
+      fc.fetch((const Tin*)a.Cm + tg * N, valid);
+      fetch(h0);
+      fb.put(Bs, LN);
+      fc.put(Cs, LN);
+    }
+    __syncthreads();
+    // scores of the wave's query tile: rows j = 4 (l / 16) + r, column i = l % 16
+    f32x4 CB[QT];
+    if (w < QT) {
+      Frag<N, Tin> cf;
+      cf.load(Cs + w * 16 * LN, LN);
+#pragma unroll
+      for (int jt = 0; jt < QT; ++jt) {
+        CB[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (jt <= w) {
+          Frag<N, Tin> bf;
+          bf.load(Bs + jt * 16 * LN, LN);
+          mma(CB[jt], bf, cf);
+        }
+      }
+    }
+
+    for (int h = h0; h < h1; ++h) {
+      const size_t bh = (size_t)b * a.H + h, th = bh * a.T + t0;
+      const float A = a.A[h], D = a.D ? a.D[h] : 0.f, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+      // the previous head's readers of these buffers are behind a barrier
+      fx.put(Xs, LP);
+      fy.put(Ys, LP);
+      const float raw = fdt;
+      float step = 0.f;
+      if (w == 0) {
+        step = lane < Q && lane < valid ? ssm_step(raw, bias, a.softplus) : 0.f;
+        dec.fill(step, step * A);
+      }
+      f32x4 sv[NQ][PTL], dv[NQ][PTL];
+      {
+        const float* sf = o.states + (bh * nch + c) * P * N;
+        const float* sr = sf + (size_t)BH * nch * P * N;
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          const int nt = q * kWaves + w;
+          if (nt >= NTL) break;
+#pragma unroll
+          for (int pb = 0; pb < PTL; ++pb) {
+            sv[q][pb] = load4(sf + ((pb * NTL + nt) * 64 + lane) * 4);
+            dv[q][pb] = load4(sr + ((pb * NTL + nt) * 64 + lane) * 4);
+          }
+        }
+      }
+      if (h + 1 < h1) fetch(h + 1);
+      __syncthreads();
+
+      // scores of dy and x, K and Z, and the pairs' sums
+      if (w < QT) {
+        Frag<P, Tin> yf;
+        yf.load(Ys + w * 16 * LP, LP);
+        float rsum = 0.f;
+        const int i = w * 16 + lc;
+#pragma unroll
+        for (int jt = 0; jt < QT; ++jt) {
+          f32x4 kk = {0.f, 0.f, 0.f, 0.f}, zz = {0.f, 0.f, 0.f, 0.f};
+          if (jt <= w) {
+            f32x4 m = {0.f, 0.f, 0.f, 0.f};
+            Frag<P, Tin> xf;
+            xf.load(Xs + jt * 16 * LP, LP);
+            mma(m, xf, yf);
+            const f32x4 l = pair_decay<Q>(dec, w, jt), dj = tile_steps<Q>(dec, jt);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int j = jt * 16 + g4 + r;
+              const float z = m[r] * l[r];
+              kk[r] = CB[jt][r] * l[r] * dj[r];
+              zz[r] = z * dj[r];
+              float v = CB[jt][r] * z;  // the pair without its step
+              if (j == i) {
+                diag[j] = v;  // no decay between: not part of g
+                v = 0.f;
+              }
+              rsum += v * dj[r];
+              const float cs = row16_sum(v);
+              if (lc == 0) colv[w][j] = cs;
+            }
+          } else if (lc == 0) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) colv[w][jt * 16 + g4 + r] = 0.f;
+          }
+          store4(Ks + i * LQ + jt * 16 + g4, kk);
+          store4(Zs + i * LQ + jt * 16 + g4, zz);
+        }
+        rsum = add_swap32(add_swap16(rsum));
+        if (lane < 16) rowv[i] = rsum;
+      }
+      float dot = 0.f;
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        const int nt = q * kWaves + w;
+        if (nt >= NTL) break;
+#pragma unroll
+        for (int pb = 0; pb < PTL; ++pb) {
+          store4(dSs + (nt * 16 + lc) * LP + pb * 16 + g4, dv[q][pb]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dot += sv[q][pb][e] * dv[q][pb][e];
+        }
+      }
+      dot = wave_sum(dot);
+      if (lane == 0) dots[w] = dot;
+      __syncthreads();
+
+      // dB, dC over the wave's columns n
+      float ws[QT], us[QT];
+#pragma unroll
+      for (int it = 0; it < QT; ++it) ws[it] = us[it] = 0.f;
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        const int nt = q * kWaves + w;
+        if (nt >= NTL) break;
+        Frag<Q, Tin> bT, cT;  // rows n, k = token
+        bT.load_kmajor(Bs + nt * 16, LN);
+        cT.load_kmajor(Cs + nt * 16, LN);
+        {
+          Parts<P, Tin> sp;
+          parts_from_acc<P>(sp, sv[q]);
+#pragma unroll
+          for (int it = 0; it < QT; ++it) {
+            Frag<P, Tin> yf;
+            yf.load_perm(Ys + it * 16 * LP, LP);
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+            mma_parts(acc, sp, yf);
+            const int i = it * 16 + lc;
+            const f32x4 cv = load4(Cs + i * LN + nt * 16 + g4);
+            const float ent = dec.ent[i];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              acc[e] *= ent;
+              ws[it] += acc[e] * cv[e];
+              dC[q][it][e] += acc[e];
+            }
+            Frag<Q, Tin> zf;
+            zf.load(Zs + it * 16 * LQ, LQ);
+            mma_upto<Q>(dC[q][it], bT, zf, 16 * (it + 1));
+          }
+        }
+        {
+          Parts<P, Tin> dp;
+          parts_from_acc<P>(dp, dv[q]);
+#pragma unroll
+          for (int jt = 0; jt < QT; ++jt) {
+            Frag<P, Tin> xf;
+            xf.load_perm(Xs + jt * 16 * LP, LP);
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+            mma_parts(acc, dp, xf);
+            const int j = jt * 16 + lc;
+            const f32x4 bv = load4(Bs + j * LN + nt * 16 + g4);
+            const float ex = dec.ext[j], dtj = dec.dt[j];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              acc[e] *= ex;
+              us[jt] += acc[e] * bv[e];
+              dB[q][jt][e] += acc[e] * dtj;
+            }
+            Frag<Q, Tin> zf;
+            zf.load_kmajor(Zs + jt * 16, LQ);  // rows j, k = i
+            mma(dB[q][jt], cT, zf);
+          }
+        }
+      }
+#pragma unroll
+      for (int it = 0; it < QT; ++it) {
+        const float x = add_swap32(add_swap16(ws[it])), y = add_swap32(add_swap16(us[it]));
+        if (lane < 16) {
+          wv[w][it * 16 + lane] = x;
+          uv[w][it * 16 + lane] = y;
+        }
+      }
+
+      // dx of token tile jt, and its share of dD
+      float dd = 0.f;
+      {
+        const int jt = w % QT, j = jt * 16 + lc;
+        Frag<N, Tin> bf;
+        bf.load(Bs + jt * 16 * LN, LN);
+        Frag<Q, Tin> kf;
+        kf.load_kmajor(Ks + jt * 16, LQ);  // rows j, k = i
+        const float f = dec.ext[j] * dec.dt[j];
+#pragma unroll
+        for (int q = 0; q < PTL / PH + (PTL % PH != 0); ++q) {
+          const int pt = q * PH + w / QT;
+          if (pt >= PTL) break;
+          Frag<N, Tin> df;
+          df.load_kmajor(dSs + pt * 16, LP);  // rows p, k = n
+          f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+          mma(acc, df, bf);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[e] *= f;
+          Frag<Q, Tin> yT;
+          yT.load_kmajor(Ys + pt * 16, LP);  // rows p, k = i
+          mma(acc, yT, kf);
+          const f32x4 yv = load4(Ys + j * LP + pt * 16 + g4);
+          const f32x4 xv = load4(Xs + j * LP + pt * 16 + g4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            dd += yv[e] * xv[e];
+            acc[e] = j < valid ? acc[e] + D * yv[e] : 0.f;
+          }
+          if (j < rows) store4((Tin*)a.dx + (th + j) * P + pt * 16 + g4, acc);
+        }
+      }
+      dd = wave_sum(dd);
+      if (lane == 0) dds[w] = dd;
+      __syncthreads();
+
+      // per token: the step's gradient
+      if (w == 0) {
+        float R = 0.f, col = 0.f, wi = 0.f, uj = 0.f, own = 0.f;
+        if (lane < Q) {
+          R = rowv[lane];
+#pragma unroll
+          for (int q = 0; q < kWaves; ++q) {
+            if (q < QT) col += colv[q][lane];
+            if (q < NTL) {
+              wi += wv[q][lane];
+              uj += uv[q][lane];
+            }
+          }
+          own = diag[lane] + col + uj;
+        }
+        float dot4 = 0.f, dd4 = 0.f;
+#pragma unroll
+        for (int q = 0; q < kWaves; ++q) {
+          if (q < NTL) dot4 += dots[q];
+          dd4 += dds[q];
+        }
+        const float gt = wave_suffix_sum(R - col * step + wi) + wave_prefix_before(uj * step) +
+                         dec.total * dot4;
+        const bool in = lane < Q && lane < valid;
+        const float draw =
+            in ? (own + A * gt) * ssm_step_slope(raw, bias, a.softplus) : 0.f;
+        if (lane < rows) a.ddt[th + lane] = draw;
+        const float sa = wave_sum(in ? step * gt : 0.f), sb = wave_sum(draw);
+        if (lane == 0) {
+          sums[h] = sa;
+          sums[a.H + h] = dd4;
+          sums[2 * a.H + h] = sb;
+        }
+      }
+    }
+  } else {
+    // a chunk behind its sequence: zeros
+    for (int h = h0; h < h1; ++h) {
+      const size_t th = ((size_t)b * a.H + h) * a.T + t0;
+      constexpr int VE = 16 / sizeof(Tin);
+      for (int e = threadIdx.x; e < rows * (P / VE); e += kThreads)
+        *reinterpret_cast<uint4*>((Tin*)a.dx + th * P + (size_t)e * VE) = uint4{0u, 0u, 0u, 0u};
+      if (threadIdx.x < rows) a.ddt[th + threadIdx.x] = 0.f;
+      if (threadIdx.x < 3) sums[threadIdx.x * a.H + h] = 0.f;
+    }
+  }
+
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) {
+    const int nt = q * kWaves + w;
+    if (nt >= NTL) break;
+#pragma unroll
+    for (int it = 0; it < QT; ++it) {
+      const int t = it * 16 + lc;
+      if (t >= rows) continue;
+      const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+      const f32x4 vb = t < valid ? dB[q][it] : zero, vc = t < valid ? dC[q][it] : zero;
+      const size_t at = (tg + t) * N + nt * 16 + g4;
+      if (o.parts == 1) {
+        store4((Tin*)a.dB + at, vb);
+        store4((Tin*)a.dC + at, vc);
+      } else {
+        store4(o.dBp + part * GTN + at, vb);
+        store4(o.dCp + part * GTN + at, vc);
+      }
+    }
+  }
+}
+
+// dB, dC from the head parts' sums, in order.
+template <typename Tin>
+__global__ __launch_bounds__(256) void ssm_part_sum_kernel(size_t n4, int parts, const float* dBp,
+                                                           const float* dCp, Tin* dB, Tin* dC) {
+  const size_t e = blockIdx.x * (size_t)256 + threadIdx.x;
+  if (e >= n4) return;
+  f32x4 sb = {0.f, 0.f, 0.f, 0.f}, sc = sb;
+  for (int p = 0; p < parts; ++p) {
+    const f32x4 x = load4(dBp + (p * n4 + e) * 4), y = load4(dCp + (p * n4 + e) * 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sb[i] += x[i];
+      sc[i] += y[i];
+    }
+  }
+  store4(dB + e * 4, sb);
+  store4(dC + e * 4, sc);
+}
+
+struct Plan {
+  int nch, nseg, segch, parts, hper;
+  size_t states, slots, logs, sums, parts_at, total;  // offsets in floats
+};
+
+Plan make_plan(int B, int H, int G, int T, int P, int N, int Q) {
+  Plan p{};
+  const long long BH = (long long)B * H;
+  p.nch = (T + Q - 1) / Q;
+  // walks: about 1024 workgroups over both directions, segments of 4 chunks
+  // at least (a second segment costs a pass that writes no states)
+  long long want = BH > 0 ? (1024 + 2 * BH - 1) / (2 * BH) : 1;
+  if (want > p.nch / 4) want = p.nch / 4;
+  if (want < 1) want = 1;
+  p.segch = p.nch > 0 ? (int)((p.nch + want - 1) / want) : 1;
+  p.nseg = p.nch > 0 ? (p.nch + p.segch - 1) / p.segch : 1;
+  // chunks: heads of a group are split where the chunks alone leave CUs idle
+  const int Hg = G > 0 ? H / G : 1;
+  const long long wgs = (long long)B * G * p.nch;
+  long long parts = wgs > 0 ? (256 + wgs - 1) / wgs : 1;
+  if (parts > Hg) parts = Hg;
+  p.hper = Hg > 0 ? (int)((Hg + parts - 1) / parts) : 1;
+  p.parts = Hg > 0 ? (Hg + p.hper - 1) / p.hper : 1;
+  const size_t PN = (size_t)P * N;
+  p.states = 0;
+  p.slots = p.states + 2 * BH * p.nch * PN;
+  p.logs = p.slots + 2 * BH * (p.nseg - 1) * PN;
+  p.sums = p.logs + (2 * BH * (p.nseg - 1) + 3) / 4 * 4;
+  p.parts_at = p.sums + ((size_t)3 * B * p.nch * H + 3) / 4 * 4;
+  p.total = p.parts_at + (p.parts > 1 ? (size_t)2 * p.parts * B * G * T * N : 0);
+  return p;
+}
+
+template <int P, int N, typename Tin>
+int run_bwd(const SsmArgs& a, hipStream_t s) {
+  const int BH = a.B * a.H, PN = P * N;
+  const Plan p = make_plan(a.B, a.H, a.G, a.T, P, N, bwd_q<Tin>());
+  float* ws = (float*)a.ws;
+  constexpr int NT = 64 * (P / 16 < kWaves ? P / 16 : kWaves);
+  float *slots = ws + p.slots, *logs = ws + p.logs, *states = ws + p.states;
+  if (BH == 0)  // an empty batch: zeros for the parameters
+    return launch_column_sum(ws, 0, 3 * a.H, a.H, 1, a.dA, a.dD, a.dbias, s);
+  int tk;
+  if (p.nseg > 1) {
+    tk = ktimer_before(s, "ssm_bwd_state");
+    hipLaunchKernelGGL((ssm_walk_kernel<P, N, Tin, false>),
+                       dim3((unsigned)(2 * BH * (p.nseg - 1))), dim3(NT), 0, s, a, p.nseg,
+                       p.segch, slots, logs, states);
+    ktimer_after(s, tk);
+    tk = ktimer_before(s, "ssm_bwd_chain");
+    hipLaunchKernelGGL(ssm_walk_chain_kernel, dim3((PN / 4 + 255) / 256, 2 * BH), dim3(256), 0, s,
+                       BH, PN, N, p.nseg - 1, a.S0, a.dST, slots, logs);
+    ktimer_after(s, tk);
+  }
+  tk = ktimer_before(s, "ssm_bwd_walk");
+  hipLaunchKernelGGL((ssm_walk_kernel<P, N, Tin, true>), dim3((unsigned)(2 * BH * p.nseg)),
+                     dim3(NT), 0, s, a, p.nseg, p.segch, slots, logs, states);
+  ktimer_after(s, tk);
+  int rc = (int)hipGetLastError();
+  if (rc) return rc;
+  if (p.nch > 0) {
+    const size_t GTN = (size_t)a.B * a.G * a.T * N;
+    const ChunkOut o{states, ws + p.sums, ws + p.parts_at,
+                     ws + p.parts_at + (size_t)p.parts * GTN, p.parts, p.hper};
+    tk = ktimer_before(s, "ssm_bwd");
+    hipLaunchKernelGGL((ssm_bwd_chunk_kernel<P, N, Tin>),
+                       dim3((unsigned)((long long)a.B * a.G * p.nch * p.parts)), dim3(kThreads),
+                       0, s, a, o);
+    ktimer_after(s, tk);
+    if (p.parts > 1) {
+      tk = ktimer_before(s, "ssm_bwd_parts");
+      hipLaunchKernelGGL((ssm_part_sum_kernel<Tin>), dim3((unsigned)((GTN / 4 + 255) / 256)),
+                         dim3(256), 0, s, GTN / 4, p.parts, o.dBp, o.dCp, (Tin*)a.dB,
+                         (Tin*)a.dC);
+      ktimer_after(s, tk);
+    }
+    rc = (int)hipGetLastError();
+    if (rc) return rc;
+  }
+  return launch_column_sum(ws + p.sums, a.B * p.nch, 3 * a.H, a.H, 1, a.dA, a.dD, a.dbias, s);
+}
+
+template <int P, int N>
+int run_bwd_t(const SsmArgs& a, hipStream_t s) {
+  return a.bf16 ? run_bwd<P, N, __bf16>(a, s) : run_bwd<P, N, float>(a, s);
+}
+
+template <int P>
+int run_bwd_n(const SsmArgs& a, hipStream_t s) {
+  switch (a.N) {
+    case 32: return run_bwd_t<P, 32>(a, s);
+    case 64: return run_bwd_t<P, 64>(a, s);
+    case 128: return run_bwd_t<P, 128>(a, s);
+  }
+  return -1;
+}
+
+}  // namespace
+
+size_t ssm_backward_ws(int B, int H, int G, int T, int P, int N, int bf16) {
+  return make_plan(B, H, G, T, P, N, bf16 ? bwd_q<__bf16>() : bwd_q<float>()).total *
+         sizeof(float);
+}
+
+int launch_ssm_backward(const SsmArgs& a, hipStream_t s) {
+  switch (a.P) {
+    case 32: return run_bwd_n<32>(a, s);
+    case 64: return run_bwd_n<64>(a, s);
+    case 128: return run_bwd_n<128>(a, s);
+  }
+  return -1;
+}
+
+}  // namespace osdn

@@ -54,7 +54,7 @@ struct ChunkDecay {
   float dt[Q];    // step
   float up[Q];    // log: block start .. token, inclusive
   float eup[Q];   // exp(up)
-  float edn[Q];   // exp(log: after token .. block end) * dt
+  float edn[Q];   // exp(log: after token .. block end)
   float ent[Q];   // chunk entry .. token
   float ext[Q];   // after token .. chunk exit
   float gap[16];  // [a][b], a > b: exp over the blocks strictly between
@@ -83,7 +83,7 @@ struct ChunkDecay {
       dt[t] = step;
       up[t] = u;
       eup[t] = __expf(u);
-      edn[t] = __expf(d) * step;
+      edn[t] = __expf(d);
       ent[t] = __expf(before + u);
       ext[t] = __expf(d + after);
     }
@@ -102,18 +102,46 @@ struct ChunkDecay {
   }
 };
 
-// Scores of one tile: acc = (key tile jt) x (query tile it)^T, lane holding
-// keys j = 4 (l / 16) + r of query i = l % 16; returns the factor exp(decay
-// j -> i) times dt_j, 0 above the diagonal.
+// Decays of one tile of pairs in accumulator layout: lane l holds the factors
+// from the tokens j = 16 jt + 4 (l / 16) + r to i = 16 it + l % 16, zero where
+// j > i.
 template <int Q>
-__device__ __forceinline__ float pair_decay(const ChunkDecay<Q>& d, int it, int jt, int r) {
-  const int i = it * 16 + acc_col(), j = jt * 16 + acc_row(r);
+__device__ __forceinline__ f32x4 pair_decay(const ChunkDecay<Q>& d, int it, int jt) {
+  f32x4 f = {0.f, 0.f, 0.f, 0.f};
+  const int i = it * 16 + acc_col(), j = jt * 16 + acc_row(0);
   if (jt < it) {
     const float g = d.eup[i] * d.gap[it * 4 + jt];
-    return g * d.edn[j];
+    const f32x4 e = *reinterpret_cast<const f32x4*>(d.edn + j);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) f[r] = g * e[r];
+  } else if (jt == it) {
+    const f32x4 u = *reinterpret_cast<const f32x4*>(d.up + j);
+    const float v = d.up[i];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) f[r] = j + r <= i ? __expf(v - u[r]) : 0.f;
   }
-  if (jt > it || j > i) return 0.f;
-  return __expf(d.up[i] - d.up[j]) * d.dt[j];
+  return f;
+}
+
+// The steps of the tile's tokens j.
+template <int Q>
+__device__ __forceinline__ f32x4 tile_steps(const ChunkDecay<Q>& d, int jt) {
+  return *reinterpret_cast<const f32x4*>(d.dt + jt * 16 + acc_row(0));
+}
+
+// Inclusive sum of lanes l .. 63, and exclusive sum of lanes 0 .. l - 1.
+__device__ __forceinline__ float wave_suffix_sum(float x) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const float y = __shfl_down(x, d, 64);
+    if (lane + d < 64) x += y;
+  }
+  return x;
+}
+__device__ __forceinline__ float wave_prefix_before(float x) {
+  const float y = __shfl_up(wave_prefix_sum(x), 1, 64);
+  return (threadIdx.x & 63) ? y : 0.f;
 }
 
 // acc += A * B^T over the first kmax (a multiple of 16) of the K indices.
@@ -152,14 +180,28 @@ __device__ __forceinline__ void frag_from_acc(Frag<KEXT, float>& f, const f32x4 
     for (int e = 0; e < 4; ++e) f.v[4 * b + e] = t[b][e];
 }
 
-// x scaled by w[k] (natural k order, w in LDS) as a bf16 fragment and the
-// fragment of what its rounding lost: the pair carries 16 bits of the
-// product, so that sums which leave in fp32 (states, step gradients) keep an
-// error of some 3e-6 where one rounding would leave 2e-3. fp32 needs no
-// second part.
+// An fp32 operand as bf16 fragments that add up to it: the rounded value, what
+// its rounding lost, and what that one's lost (24 bits in all, an error of
+// some 6e-8). Used where a product's sum leaves in fp32 (states, step and
+// parameter gradients); one rounding would leave 2e-3 there. fp32 operands
+// are one fragment.
+template <int KEXT, typename Tin>
+struct Parts {
+  static constexpr int M = sizeof(Tin) == 2 ? 3 : 1;
+  Frag<KEXT, Tin> f[M];
+};
+
+__device__ __forceinline__ void split3(float p, __bf16& a, __bf16& b, __bf16& c) {
+  a = (__bf16)p;
+  p -= (float)a;
+  b = (__bf16)p;
+  c = (__bf16)(p - (float)b);
+}
+
+// x scaled by w[k] (natural k order, w in LDS).
 template <int KEXT>
-__device__ __forceinline__ void scale_split(const Frag<KEXT, __bf16>& x, const float* w,
-                                            Frag<KEXT, __bf16>& hi, Frag<KEXT, __bf16>& lo) {
+__device__ __forceinline__ void scale_parts(const Frag<KEXT, __bf16>& x, const float* w,
+                                            Parts<KEXT, __bf16>& o) {
   const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
   for (int i = 0; i < KEXT / 32; ++i) {
@@ -167,18 +209,55 @@ __device__ __forceinline__ void scale_split(const Frag<KEXT, __bf16>& x, const f
     const f32x4 b = *reinterpret_cast<const f32x4*>(w + 32 * i + 8 * g + 4);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float p = (float)x.v[i][e] * (e < 4 ? a[e & 3] : b[e & 3]);
-      hi.v[i][e] = (__bf16)p;
-      lo.v[i][e] = (__bf16)(p - (float)hi.v[i][e]);
+      __bf16 p0, p1, p2;
+      split3((float)x.v[i][e] * (e < 4 ? a[e & 3] : b[e & 3]), p0, p1, p2);
+      o.f[0].v[i][e] = p0;
+      o.f[1].v[i][e] = p1;
+      o.f[2].v[i][e] = p2;
     }
   }
 }
 template <int KEXT>
-__device__ __forceinline__ void scale_split(const Frag<KEXT, float>& x, const float* w,
-                                            Frag<KEXT, float>& hi, Frag<KEXT, float>&) {
+__device__ __forceinline__ void scale_parts(const Frag<KEXT, float>& x, const float* w,
+                                            Parts<KEXT, float>& o) {
   const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
-  for (int i = 0; i < KEXT / 4; ++i) hi.v[i] = x.v[i] * w[4 * i + g];
+  for (int i = 0; i < KEXT / 4; ++i) o.f[0].v[i] = x.v[i] * w[4 * i + g];
+}
+
+// Accumulator tiles of a k range as a split operand (permuted k order).
+template <int KEXT>
+__device__ __forceinline__ void parts_from_acc(Parts<KEXT, __bf16>& o,
+                                               const f32x4 (&t)[KEXT / 16]) {
+#pragma unroll
+  for (int i = 0; i < KEXT / 32; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      __bf16 p0, p1, p2;
+      split3(t[2 * i + e / 4][e & 3], p0, p1, p2);
+      o.f[0].v[i][e] = p0;
+      o.f[1].v[i][e] = p1;
+      o.f[2].v[i][e] = p2;
+    }
+}
+template <int KEXT>
+__device__ __forceinline__ void parts_from_acc(Parts<KEXT, float>& o,
+                                               const f32x4 (&t)[KEXT / 16]) {
+  frag_from_acc<KEXT>(o.f[0], t);
+}
+
+// acc += A B^T with one operand in parts, smallest part first.
+template <int KEXT, typename Tin>
+__device__ __forceinline__ void mma_parts(f32x4& acc, const Parts<KEXT, Tin>& a,
+                                          const Frag<KEXT, Tin>& b) {
+#pragma unroll
+  for (int m = Parts<KEXT, Tin>::M - 1; m >= 0; --m) mma(acc, a.f[m], b);
+}
+template <int KEXT, typename Tin>
+__device__ __forceinline__ void mma_parts(f32x4& acc, const Frag<KEXT, Tin>& a,
+                                          const Parts<KEXT, Tin>& b) {
+#pragma unroll
+  for (int m = Parts<KEXT, Tin>::M - 1; m >= 0; --m) mma(acc, a, b.f[m]);
 }
 
 // Four consecutive values of a row in LDS or global memory, widened / rounded.

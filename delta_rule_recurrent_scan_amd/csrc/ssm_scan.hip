@@ -21,7 +21,7 @@
 //
 // Rounding (bf16 inputs): scores and the state are rounded to bf16 once where
 // they enter the two products of y, which is rounded to bf16 itself; the
-// state's own update takes dt x L in two bf16 parts (16 bits), and is
+// state's own update takes dt x L in three bf16 parts (24 bits), and is
 // accumulated in fp32. fp32 inputs use fp32 MFMA throughout (Q = 32).
 #include "launch.hpp"
 #include "mixer.hpp"
@@ -131,8 +131,9 @@ __global__ __launch_bounds__(64 * scan_waves<P>()) void ssm_scan_kernel(SsmArgs 
             Frag<N, Tin> bf;
             bf.load(Bs + jt * 16 * LN, LN);
             mma(s, bf, cf);
+            const f32x4 l = pair_decay<Q>(dec, it, jt), dj = tile_steps<Q>(dec, jt);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) s[r] *= pair_decay<Q>(dec, it, jt, r);
+            for (int r = 0; r < 4; ++r) s[r] *= l[r] * dj[r];
           }
           store4(Ms + (it * 16 + (lane & 15)) * LQ + jt * 16 + n0, s);
         }
@@ -173,9 +174,9 @@ __global__ __launch_bounds__(64 * scan_waves<P>()) void ssm_scan_kernel(SsmArgs 
 
     const float total = dec.total;
     logsum += dec.logtot;
-    Frag<Q, Tin> hi[PT], lo[PT];
+    Parts<Q, Tin> xw[PT];
 #pragma unroll
-    for (int pt = 0; pt < PT; ++pt) scale_split<Q>(xf[pt], wts, hi[pt], lo[pt]);
+    for (int pt = 0; pt < PT; ++pt) scale_parts<Q>(xf[pt], wts, xw[pt]);
 #pragma unroll
     for (int nt = 0; nt < NTL; ++nt) {
       Frag<Q, Tin> bf;
@@ -184,8 +185,7 @@ __global__ __launch_bounds__(64 * scan_waves<P>()) void ssm_scan_kernel(SsmArgs 
       for (int pt = 0; pt < PT; ++pt) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) S[pt][nt][e] *= total;
-        mma(S[pt][nt], bf, hi[pt]);
-        if constexpr (sizeof(Tin) == 2) mma(S[pt][nt], bf, lo[pt]);
+        mma_parts(S[pt][nt], bf, xw[pt]);
       }
     }
   }

@@ -15,7 +15,8 @@ from . import (_DTYPE_CODE, OsdnError, _check, _ptr, _stream, load_library)
 
 __all__ = ["short_conv_forward", "short_conv_decode", "short_conv_backward",
            "short_conv_backward_workspace_bytes", "ssm_forward", "ssm_decode",
-           "ssm_forward_workspace_bytes", "gated_norm_forward",
+           "ssm_backward", "ssm_forward_workspace_bytes",
+           "ssm_backward_workspace_bytes", "gated_norm_forward",
            "gated_norm_backward", "gated_norm_backward_workspace_bytes",
            "residual_norm_forward", "residual_norm_backward",
            "residual_norm_backward_workspace_bytes"]
@@ -35,6 +36,8 @@ SIGNATURES = {
     "ssm_forward_workspace_bytes": ([_I] * 7, _Z),
     "ssm_forward": ([_I] * 7 + [_P] * 7 + [_I, _P, _P, _P, _P, _P, _Z, _P], _I),
     "ssm_decode": ([_I] * 7 + [_P] * 7 + [_I, _P, _P, _P, _P], _I),
+    "ssm_backward_workspace_bytes": ([_I] * 7, _Z),
+    "ssm_backward": ([_I] * 7 + [_P] * 7 + [_I] + [_P] * 13 + [_Z, _P], _I),
     "gated_norm_forward": ([_I] * 5 + [_P, _P, _L, _L, _P, _I, _F, _I, _P, _P],
                            _I),
     "gated_norm_backward_workspace_bytes": ([_I] * 4, _Z),
@@ -304,6 +307,46 @@ def ssm_decode(x, dt, A, B, C, S, D=None, dt_bias=None, softplus=True, out=None,
           _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(dt_bias),
           int(softplus), _ptr(S), _ptr(y), _ptr(so))
     return y
+
+
+def ssm_backward_workspace_bytes(B, H, G, T, P, N, dtype):
+    return int(load_library().ssm_backward_workspace_bytes(
+        B, H, G, T, P, N, _DTYPE_CODE[dtype]))
+
+
+def ssm_backward(x, dt, A, B, C, dy, D=None, dt_bias=None, S0=None, dS_T=None,
+                 lengths=None, softplus=True, out=None, workspace=None):
+    """Backward of ssm_forward: the gradient of sum <dy, y> + <dS_T, S_T>, dy
+    [B,H,T,P] in the dtype of x and dS_T [B,H,P,N] fp32 (None: zero). Returns
+    a dict x, B, C (in the dtype of x; B and C summed over their group's
+    heads), dt [B,H,T] (of the raw dt), A, D, dt_bias [H] and S0 [B,H,P,N]
+    (fp32). ``out`` may pass such a dict preallocated (D, dt_bias and S0 may be
+    None to skip them) and ``workspace`` a uint8 device buffer of
+    ssm_backward_workspace_bytes()."""
+    L, code, dev, (nb, H, G, T, P, N) = _ssm_checks(x, dt, A, B, C, D, dt_bias)
+    f32 = torch.float32
+    _check(S0, "S0", (nb, H, P, N), f32, dev)
+    _check(lengths, "lengths", (nb,), torch.int32, dev)
+    _check(dy, "dy", (nb, H, T, P), x.dtype, dev)
+    _check(dS_T, "dS_T", (nb, H, P, N), f32, dev)
+    shapes = dict(x=((nb, H, T, P), x.dtype), dt=((nb, H, T), f32),
+                  A=((H,), f32), B=((nb, G, T, N), x.dtype),
+                  C=((nb, G, T, N), x.dtype), D=((H,), f32),
+                  dt_bias=((H,), f32), S0=((nb, H, P, N), f32))
+    g = out if out is not None else {
+        n: torch.empty(s, dtype=d, device=dev) for n, (s, d) in shapes.items()}
+    _required(g, ("x", "dt", "A", "B", "C"))
+    for n, (s, d) in shapes.items():
+        _check(g.get(n), "out[%s]" % n, s, d, dev)
+    ws = _workspace(workspace, L.ssm_backward_workspace_bytes(
+        nb, H, G, T, P, N, code), dev)
+    _call(L.ssm_backward, "ssm_backward", dev, nb, H, G, T, P, N, code, _ptr(x),
+          _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(dt_bias),
+          int(softplus), _ptr(S0), _ptr(lengths), _ptr(dy), _ptr(dS_T),
+          _ptr(g["x"]), _ptr(g["dt"]), _ptr(g["A"]), _ptr(g["B"]), _ptr(g["C"]),
+          _ptr(g.get("D")), _ptr(g.get("dt_bias")), _ptr(g.get("S0")),
+          _ptr(ws), ws.numel())
+    return g
 
 
 # ---------------------------------------------------------------------------

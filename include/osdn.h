@@ -543,6 +543,30 @@ int ssm_decode(int B, int H, int G, int T, int P, int N, int dtype,
                void* stream);
 
 /*
+ * Backward of ssm_forward: the gradient of sum <dy, y> + <dS_T, S_T>.
+ *   dy       [B,H,T,P] dtype (required);  dS_T [B,H,P,N] fp32 (NULL: zero)
+ *   dx       [B,H,T,P], dB, dC [B,G,T,N] dtype OUT (required; dB and dC are
+ *            sums over the group's heads)
+ *   ddt      [B,H,T] fp32 OUT (required): of the raw dt, through the softplus
+ *   dA       [H] fp32 OUT (required);  dD, ddt_bias [H], dS0 [B,H,P,N] fp32 OUT
+ *            (NULL: not written)
+ *   workspace: ssm_backward_workspace_bytes(...) bytes, 256-byte aligned: the
+ *            state and its adjoint at every chunk's ends (2 P N floats for each
+ *            64 tokens (bf16) or 32 (fp32) of a (batch, head)), the states
+ *            between segments, and partial sums
+ */
+size_t ssm_backward_workspace_bytes(int B, int H, int G, int T, int P, int N,
+                                    int dtype);
+int ssm_backward(int B, int H, int G, int T, int P, int N, int dtype,
+                 const void* x, const float* dt, const float* A,
+                 const void* Bm, const void* Cm, const float* D,
+                 const float* dt_bias, int softplus, const float* S0,
+                 const int* lengths, const void* dy, const float* dS_T,
+                 void* dx, float* ddt, float* dA, void* dB, void* dC,
+                 float* dD, float* ddt_bias, float* dS0, void* workspace,
+                 size_t workspace_bytes, void* stream);
+
+/*
  * Norm of each head's row with a gate, from heads to token rows:
  *   gate_first == 0:  y = x * rsqrt(mean_D x^2 + eps) * weight * silu(z)
  *   gate_first != 0:  v = x * silu(z),  y = v * rsqrt(mean_D v^2 + eps) * weight
@@ -625,7 +649,8 @@ void osdn_kernel_timing(int enable);
  * osdn_bwd, osdn_bwd_learner (backward), gated_bwd_record, gated_bwd,
  * gated_bwd_learner, gdn2_bwd_record, gdn2_bwd, gdn2_bwd_out (gate-aware
  * backward), short_conv, short_conv_bwd, ssm_state, ssm_chain, ssm_scan,
- * ssm_decode, gated_norm, gated_norm_bwd, residual_norm, residual_norm_bwd,
+ * ssm_decode, ssm_bwd_state, ssm_bwd_chain, ssm_bwd_walk, ssm_bwd,
+ * ssm_bwd_parts, gated_norm, gated_norm_bwd, residual_norm, residual_norm_bwd,
  * column_sum (the operators around the recurrences).
  */
 int osdn_kernel_times(int max, const char** names, int* counts, float* mean_ms);

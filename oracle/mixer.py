@@ -133,7 +133,8 @@ def ssm_backward_ref(x, dt, A, B, C, dy, D=None, dt_bias=None, S0=None,
                      dS_T=None, lengths=None, use_softplus=True, bound=False):
     """Gradients of sum <dy, y> + <dS_T, S_T>: dict(x, dt, A, B, C, D,
     dt_bias, S0). ``bound``: with absolute inputs, the sums of the absolute
-    terms (the decay's own factor A enters by its absolute value)."""
+    terms (the decay's own factor A enters by its absolute value), and beside
+    them ``own`` [B,H,T], the step's part of d dt_t times the step."""
     nb, H, T, P = x.shape
     G, N = B.shape[1], B.shape[3]
     n = _lengths(lengths, nb, T)
@@ -157,6 +158,8 @@ def ssm_backward_ref(x, dt, A, B, C, dy, D=None, dt_bias=None, S0=None,
                 g["x"][b, h, t] = st * (dS @ bt) + (0 if D is None else D[h] * yt)
                 g["B"][b, k, t] += st * (dS.T @ xt)
                 da = a * (dS * S[b][h][t]).sum()       # d / d(st A)
+                if bound:
+                    g.setdefault("own", np.zeros_like(dt))[b, h, t] = st * (xt @ dS @ bt)
                 ds = xt @ dS @ bt + (abs(A[h]) if bound else A[h]) * da
                 g["A"][h] += st * da
                 g["dt"][b, h, t] = ds * slope[b, h, t]

@@ -1,5 +1,5 @@
-"""GPU parity of the selective scan (forward, decode) against the fp64 token
-recurrence."""
+"""GPU parity of the selective scan (forward, decode, backward) against the
+fp64 token recurrence."""
 import numpy as np
 import pytest
 import torch
@@ -9,10 +9,10 @@ from mixer_checks import DEV, U, f64, held
 from oracle import mixer as M
 
 BF, F32 = torch.bfloat16, torch.float32
-# bf16 matrix operands: scores and states rounded once for the outputs; two
-# parts (2^-16) where a sum leaves in fp32
+# bf16 matrix operands: scores and states rounded once for the outputs; three
+# parts (2^-24) where a sum leaves in fp32
 OP1 = {BF: U[BF], F32: 0.0}
-OP2 = {BF: U[BF] ** 2, F32: 0.0}
+OP2 = {BF: U[BF] ** 3, F32: 0.0}
 K = 320  # fp32 roundings: T terms in chunks, N or P products, decays, exps
 
 
@@ -174,3 +174,150 @@ def test_decode_continues_forward():
         out.append(osdn.ssm_decode(**sl(t, t + 1), S=S, **k))
     k.update(S0=S0, lengths=None)
     check_forward(a, k, (torch.cat(out, 2), S), what="prompt then tokens ")
+
+
+# ---------------------------------------------------------------------------
+# Backward
+# ---------------------------------------------------------------------------
+
+def adjoints(a, k, seed=9):
+    g = torch.Generator().manual_seed(seed)
+    dy = torch.randn(a["x"].shape, generator=g).to(a["x"].dtype).to(DEV)
+    nb, H, T, P = a["x"].shape
+    N = a["B"].shape[-1]
+    dS = (torch.randn((nb, H, P, N), generator=g) * N ** -0.5).to(DEV)
+    return dy, dS
+
+
+def check_backward(a, k, dy, dS, got, softplus=True):
+    dt = a["x"].dtype
+    r, q, ab, qb = ref_args(a, k)
+    ref = M.ssm_backward_ref(**r, dy=f64(dy), dS_T=f64(dS), **q, use_softplus=softplus)
+    ady, adS = np.abs(f64(dy)), None if dS is None else np.abs(f64(dS))
+    mag = M.ssm_backward_ref(**ab, dy=ady, dS_T=adS, **qb, use_softplus=softplus,
+                             bound=True)
+    # inside a chunk the decay's gradient is a suffix sum of row minus column
+    # sums: its rounding goes by the chunk's pairs, not by those crossing t
+    own = mag.pop("own", np.zeros_like(r["dt"]))
+    T = own.shape[2]
+    pairs = np.zeros_like(own)
+    for c in range(0, T, 64):
+        pairs[:, :, c:c + 64] = 2 * own[:, :, c:c + 64].sum(2, keepdims=True)
+    absA = np.abs(r["A"])
+    mag["dt"] = mag["dt"] + absA[None, :, None] * pairs
+    mag["dt_bias"] = mag["dt_bias"] + absA * pairs.sum((0, 2))
+    step = M._steps(r["dt"], q["dt_bias"], softplus)
+    mag["A"] = mag["A"] + (np.abs(step) * pairs).sum((0, 2))
+    for n in ("x", "B", "C"):
+        held(got[n], ref[n], mag[n], 2 * K, 2 * OP1[dt], "d" + n)
+    for n in ("dt", "A", "D", "dt_bias", "S0"):
+        held(got[n], ref[n], mag[n], 2 * K, OP2[dt], "d" + n)
+    return ref
+
+
+def check_l2(got, ref, names, tol):
+    for n in names:
+        e = np.linalg.norm(f64(got[n]) - ref[n]) / max(np.linalg.norm(ref[n]), 1e-30)
+        print("d%s: rel L2 %.2e" % (n, e), flush=True)
+        assert e <= tol, (n, e)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_backward(case):
+    print("case:", case, flush=True)
+    B, H, G, T, P, N, dt, lens = case
+    a, k = inputs(B, H, G, T, P, N, dt, lens=lens, seed=1)
+    dy, dS = adjoints(a, k)
+    got = osdn.ssm_backward(**a, dy=dy, dS_T=dS, **k)
+    torch.cuda.synchronize()
+    ref = check_backward(a, k, dy, dS, got)
+    # and as a whole: 2 K independent fp32 roundings of terms some 6 times the
+    # sums they cancel to (sqrt(640) 2^-24 6 = 9e-6)
+    check_l2(got, ref, ("dt", "A", "D", "dt_bias", "S0"), 1e-5)
+    # one rounding of the output and two of operands, half a step at most each
+    check_l2(got, ref, ("x", "B", "C"), 3 * U[BF] if dt is BF else 1e-5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("T", [100, 600])
+def test_backward_plain_options(dt, T):
+    """No D, bias, states, adjoint of the state or softplus; zero steps."""
+    a, k = inputs(2, 4, 1, T, 64, 64, dt, seed=2)
+    a["dt"] = a["dt"].abs() * 0.1
+    a["dt"][:, :, ::7] = 0
+    k.update(D=None, dt_bias=None, S0=None)
+    dy, _ = adjoints(a, k)
+    got = osdn.ssm_backward(**a, dy=dy, softplus=False, **k)
+    check_backward(a, k, dy, None, got, softplus=False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("A", [(0.0, 0.0), (200.0, 2000.0)], ids=["none", "strong"])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_backward_decay_range(A, dt):
+    a, k = inputs(1, 2, 1, 200, 64, 64, dt, A=A, seed=3)
+    dy, dS = adjoints(a, k)
+    check_backward(a, k, dy, dS, osdn.ssm_backward(**a, dy=dy, dS_T=dS, **k))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [200, 900])
+def test_backward_padding_is_never_used(T):
+    lens = [T, 70, 0]
+    a, k = inputs(3, 2, 1, T, 64, 64, BF, lens=lens, seed=4)
+    dy, dS = adjoints(a, k)
+    g1 = osdn.ssm_backward(**a, dy=dy, dS_T=dS, **k)
+    for b, n in enumerate(lens):
+        for m in ("x", "B", "C"):
+            a[m][b, :, n:] = float("nan")
+        a["dt"][b, :, n:] = float("nan")
+        dy[b, :, n:] = float("nan")
+    g2 = osdn.ssm_backward(**a, dy=dy, dS_T=dS, **k)
+    for m in g1:
+        assert torch.equal(g1[m], g2[m]), m
+    for b, n in enumerate(lens):
+        for m in ("x", "dt", "B", "C"):
+            assert not g2[m][b, :, n:].any()
+    assert torch.equal(g2["S0"][2], dS[2])
+
+
+@pytest.mark.gpu
+def test_backward_no_tokens_and_no_batch():
+    a, k = inputs(2, 2, 1, 0, 64, 64, BF)
+    dy, dS = adjoints(a, k)
+    g = osdn.ssm_backward(**a, dy=dy, dS_T=dS, **k)
+    assert torch.equal(g["S0"], dS)
+    assert not any(bool(g[m].any()) for m in ("A", "D", "dt_bias"))
+    a, k = inputs(0, 2, 1, 5, 64, 64, BF)
+    dy, dS = adjoints(a, k)
+    g = osdn.ssm_backward(**a, dy=dy, dS_T=dS, **k)
+    assert not any(bool(g[m].any()) for m in ("A", "D", "dt_bias"))
+
+
+@pytest.mark.gpu
+def test_backward_against_differences():
+    """The gradients against central differences of the forward, fp32."""
+    a, k = inputs(1, 2, 1, 70, 32, 32, F32, seed=6)
+    dy, dS = adjoints(a, k)
+    got = osdn.ssm_backward(**a, dy=dy, dS_T=dS, **k)
+    gen = torch.Generator().manual_seed(7)
+
+    def loss(p, q):
+        y, S = osdn.ssm_forward(**p, **q)
+        return float((y.double() * dy.double()).sum() + (S.double() * dS.double()).sum())
+    for n in ("x", "dt", "A", "B", "C", "D", "dt_bias", "S0"):
+        src = a if n in a else k
+        d = torch.randn(src[n].shape, generator=gen).to(DEV)
+        h = 2.0 ** -9
+
+        def at(s):
+            moved = {n: src[n] + s * d}
+            return loss(dict(a, **moved) if n in a else a, dict(k, **moved) if n in k else k)
+        num = (at(h) - at(-h)) / (2 * h)
+        ana = float((got[n].double() * d.double()).sum())
+        # fp32 outputs of size up to 10, some 6600 of them: 2^-24 * 10 * 80 of
+        # noise over 2h, and h^2 times a third derivative of the gradient's size
+        scale = float(got[n].double().norm() * d.double().norm())
+        assert abs(num - ana) <= 2e-3 * scale + 5e-2, (n, num, ana)
