@@ -40,7 +40,7 @@
 namespace osdn {
 namespace {
 
-constexpr int kWaves = 4, kThreads = 64 * kWaves;
+constexpr int kWaves = 8, kThreads = 64 * kWaves;  // of the chunk kernel
 
 template <typename Tin>
 constexpr int bwd_q() { return sizeof(Tin) == 2 ? 64 : 32; }
@@ -58,20 +58,24 @@ __device__ __forceinline__ void state_elem(int e, int ntl, int& p, int& n) {
 // BH .. 2 BH - 1 in reverse (dy, C, weights L_i0, from dS_T). Segment k counts
 // along the direction.
 // ---------------------------------------------------------------------------
+// Rows p of the state a workgroup walks: 16 a wave.
+template <int P>
+constexpr int walk_rows() { return P < 64 ? P : 64; }
+
 template <int P, int N, typename Tin, bool WRITE>
-__global__ __launch_bounds__(64 * (P / 16 < kWaves ? P / 16 : kWaves)) void ssm_walk_kernel(
+__global__ __launch_bounds__(4 * walk_rows<P>(), 3) void ssm_walk_kernel(
     SsmArgs a, int nseg, int segch, float* slots, float* slot_log, float* states) {
-  constexpr int Q = bwd_q<Tin>(), NW = P / 16 < kWaves ? P / 16 : kWaves, NT = 64 * NW;
-  constexpr int PT = P / 16 / NW, NTL = N / 16;
-  constexpr int LN = N + 16 / sizeof(Tin), LP = P + 16 / sizeof(Tin);
+  constexpr int Q = bwd_q<Tin>(), SP = walk_rows<P>(), NW = SP / 16, NT = 64 * NW;
+  constexpr int NTL = N / 16;
+  constexpr int LN = N + 16 / sizeof(Tin), LP = SP + 16 / sizeof(Tin);
   __shared__ __attribute__((aligned(16))) Tin Ks[Q * LN];
   __shared__ __attribute__((aligned(16))) Tin Vs[Q * LP];
-  __shared__ __attribute__((aligned(16))) ChunkDecay<Q> dec;
-  __shared__ __attribute__((aligned(16))) float wts[Q];
+  __shared__ __attribute__((aligned(16))) ChunkDecay<Q> decs[2];
 
   const int lane = threadIdx.x & 63, w = wave_id();
   const int BH = a.B * a.H, nwg = WRITE ? nseg : nseg - 1;
-  const int stream = blockIdx.x / nwg, k = blockIdx.x % nwg;
+  const int ps = blockIdx.x % (P / SP), id = blockIdx.x / (P / SP);
+  const int stream = id / nwg, k = id % nwg;
   const bool rev = stream >= BH;
   const int bh = rev ? stream - BH : stream;
   const int b = bh / a.H, h = bh % a.H, sg = rev ? nseg - 1 - k : k;
@@ -79,109 +83,108 @@ __global__ __launch_bounds__(64 * (P / 16 < kWaves ? P / 16 : kWaves)) void ssm_
   const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f;
   const size_t th = (size_t)bh * a.T;
   const size_t tg = ((size_t)b * a.G + h / (a.H / a.G)) * a.T;
-  const Tin* val = (const Tin*)(rev ? a.dy : a.x) + th * P;
+  const Tin* val = (const Tin*)(rev ? a.dy : a.x) + th * P + ps * SP;
   const Tin* key = (const Tin*)(rev ? a.Cm : a.Bm) + tg * N;
   const float* dt = a.dt + th;
 
-  // S[pt][nt]: rows p = 4 (l / 16) + e of the wave's p tile, column n = l % 16
-  f32x4 S[PT][NTL];
+  // S[nt]: rows p = 4 (l / 16) + e of the wave's p tile, column n = l % 16
+  f32x4 S[NTL];
   const float* from = rev ? a.dST : a.S0;
+  const int tile0 = (ps * NW + w) * NTL;
 #pragma unroll
-  for (int pt = 0; pt < PT; ++pt)
+  for (int nt = 0; nt < NTL; ++nt) {
+    const int at = ((tile0 + nt) * 64 + lane) * 4;
+    if (!WRITE || (k == 0 && !from)) {
+      S[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    } else if (k > 0) {
+      S[nt] = load4(slots + ((size_t)stream * (nseg - 1) + k - 1) * P * N + at);
+    } else {
 #pragma unroll
-    for (int nt = 0; nt < NTL; ++nt) {
-      const int tile = (w * PT + pt) * NTL + nt;
-      if (!WRITE || (k == 0 && !from)) {
-        S[pt][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
-      } else if (k > 0) {
-        S[pt][nt] = load4(slots + ((size_t)stream * (nseg - 1) + k - 1) * P * N +
-                          (tile * 64 + lane) * 4);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          int p, c;
-          state_elem((tile * 64 + lane) * 4 + e, NTL, p, c);
-          S[pt][nt][e] = from[((size_t)bh * P + p) * N + c];
-        }
+      for (int e = 0; e < 4; ++e) {
+        int p, c;
+        state_elem(at + e, NTL, p, c);
+        S[nt][e] = from[((size_t)bh * P + p) * N + c];
       }
     }
+  }
   float logsum = 0.f;
 
   const int c0 = sg * segch, c1 = min(c0 + segch, nch);
   const int cn = min(c1, (n + Q - 1) / Q);  // chunks with tokens
-  Stage<Q, N, Tin, NT> fk;
-  Stage<Q, P, Tin, NT> fv;
-  float fdt = 0.f;
-  auto fetch = [&](int c) {
-    const int t = c * Q, valid = n - t;
+  const int count = max(cn - c0, 0);
+  auto chunk = [&](int i) { return rev ? cn - 1 - i : c0 + i; };
+  Stage<Q, N, Tin, NT, LN> fk;
+  Stage<Q, SP, Tin, NT, LP, P> fv;
+  auto fetch = [&](int i) {
+    const int t = chunk(i) * Q, valid = n - t;
     fk.fetch(key + (size_t)t * N, valid);
     fv.fetch(val + (size_t)t * P, valid);
-    if (w == 0) fdt = lane < Q && lane < valid ? dt[t + lane] : 0.f;
   };
-  const int count = max(cn - c0, 0);
-  if (count) fetch(rev ? cn - 1 : c0);
+  // decays a chunk ahead, by wave 0, from steps fetched another chunk earlier
+  auto steps = [&](int i) {
+    const int t = i < count ? chunk(i) * Q : n;
+    return w == 0 ? buffer_load_f32(make_buffer(dt + t, (n - t) * 4ll), lane * 4) : 0.f;
+  };
+  auto fill = [&](ChunkDecay<Q>& d, int i, float raw) {
+    float sl = 0.f, st = 0.f;
+    if (lane < Q && chunk(i) * Q + lane < n) st = ssm_step(raw, bias, a.softplus, sl);
+    d.fill(st, st * A, sl);
+  };
+  float raw = 0.f;
+  if (count) {
+    fetch(0);
+    raw = steps(0);
+    if (w == 0) fill(decs[0], 0, raw);
+    raw = steps(1);
+  }
   for (int i = 0; i < count; ++i) {
-    const int c = rev ? cn - 1 - i : c0 + i, valid = n - c * Q;
+    const ChunkDecay<Q>& dec = decs[i & 1];
     __syncthreads();
-    fk.put(Ks, LN);
-    fv.put(Vs, LP);
-    if (w == 0) {
-      const float st = lane < Q && lane < valid ? ssm_step(fdt, bias, a.softplus) : 0.f;
-      dec.fill(st, st * A);
-      wave_lds_sync();
-      if (lane < Q) wts[lane] = rev ? dec.ent[lane] : st * dec.ext[lane];
-    }
-    if (i + 1 < count) fetch(rev ? c - 1 : c + 1);
+    fk.put(Ks);
+    fv.put(Vs);
+    if (i + 1 < count) fetch(i + 1);
     if constexpr (WRITE) {
-      float* out = states + ((size_t)stream * nch + c) * P * N;
+      float* out = states + ((size_t)stream * nch + chunk(i)) * P * N;
 #pragma unroll
-      for (int pt = 0; pt < PT; ++pt)
-#pragma unroll
-        for (int nt = 0; nt < NTL; ++nt)
-          store4(out + (((w * PT + pt) * NTL + nt) * 64 + lane) * 4, S[pt][nt]);
+      for (int nt = 0; nt < NTL; ++nt) store4(out + (tile0 + nt) * 256 + (unsigned)(lane * 4), S[nt]);
     }
     __syncthreads();
     const float total = dec.total;
     logsum += dec.logtot;
-    Parts<Q, Tin> vw[PT];
-#pragma unroll
-    for (int pt = 0; pt < PT; ++pt) {
+    Parts<Q, Tin> vw;
+    {
       Frag<Q, Tin> vf;
-      vf.load_kmajor(Vs + (w * PT + pt) * 16, LP);
-      scale_parts<Q>(vf, wts, vw[pt]);
+      vf.load_kmajor(Vs + w * 16, LP);
+      scale_parts<Q>(vf, rev ? dec.ent : dec.wx, vw);
     }
 #pragma unroll
     for (int nt = 0; nt < NTL; ++nt) {
       Frag<Q, Tin> kf;
       kf.load_kmajor(Ks + nt * 16, LN);
 #pragma unroll
-      for (int pt = 0; pt < PT; ++pt) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) S[pt][nt][e] *= total;
-        mma_parts(S[pt][nt], vw[pt], kf);
-      }
+      for (int e = 0; e < 4; ++e) S[nt][e] *= total;
+      mma_parts(S[nt], vw, kf);
+    }
+    if (w == 0 && i + 1 < count) {
+      fill(decs[(i + 1) & 1], i + 1, raw);
+      raw = steps(i + 2);
     }
   }
 
   if constexpr (!WRITE) {
     float* out = slots + ((size_t)stream * (nseg - 1) + k) * P * N;
 #pragma unroll
-    for (int pt = 0; pt < PT; ++pt)
-#pragma unroll
-      for (int nt = 0; nt < NTL; ++nt)
-        store4(out + (((w * PT + pt) * NTL + nt) * 64 + lane) * 4, S[pt][nt]);
-    if (threadIdx.x == 0) slot_log[(size_t)stream * (nseg - 1) + k] = logsum;
+    for (int nt = 0; nt < NTL; ++nt) store4(out + (tile0 + nt) * 256 + (unsigned)(lane * 4), S[nt]);
+    if (threadIdx.x == 0 && ps == 0) slot_log[(size_t)stream * (nseg - 1) + k] = logsum;
   } else if (rev && k == nseg - 1 && a.dS0) {
 #pragma unroll
-    for (int pt = 0; pt < PT; ++pt)
+    for (int nt = 0; nt < NTL; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < NTL; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          int p, c;
-          state_elem((((w * PT + pt) * NTL + nt) * 64 + lane) * 4 + e, NTL, p, c);
-          a.dS0[((size_t)bh * P + p) * N + c] = S[pt][nt][e];
-        }
+      for (int e = 0; e < 4; ++e) {
+        int p, c;
+        state_elem(((tile0 + nt) * 64 + lane) * 4 + e, NTL, p, c);
+        a.dS0[((size_t)bh * P + p) * N + c] = S[nt][e];
+      }
   }
 }
 
@@ -224,11 +227,13 @@ struct ChunkOut {
 };
 
 template <int P, int N, typename Tin>
-__global__ __launch_bounds__(kThreads) void ssm_bwd_chunk_kernel(SsmArgs a, ChunkOut o) {
+__global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(SsmArgs a, ChunkOut o) {
   constexpr int Q = bwd_q<Tin>(), QT = Q / 16, NTL = N / 16, PTL = P / 16;
-  constexpr int NQ = (NTL + kWaves - 1) / kWaves;  // n tiles of a wave
   constexpr int PAD = 16 / sizeof(Tin), LN = N + PAD, LP = P + PAD, LQ = Q + PAD;
-  constexpr int PH = kWaves / QT;  // waves that share a token tile of dx
+  // shares of the waves: state columns (n tile, token tiles tn, tn + TN, ..);
+  // scores (query tile, key tiles jh, jh + JH, ..); dx (token tile, p tiles)
+  constexpr int TN = kWaves / NTL, JH = kWaves / QT, TM = (QT + TN - 1) / TN,
+                JM = (QT + JH - 1) / JH;
   __shared__ __attribute__((aligned(16))) Tin Bs[Q * LN];
   __shared__ __attribute__((aligned(16))) Tin Cs[Q * LN];
   __shared__ __attribute__((aligned(16))) Tin Xs[Q * LP];
@@ -236,9 +241,12 @@ __global__ __launch_bounds__(kThreads) void ssm_bwd_chunk_kernel(SsmArgs a, Chun
   __shared__ __attribute__((aligned(16))) Tin Ks[Q * LQ];
   __shared__ __attribute__((aligned(16))) Tin Zs[Q * LQ];
   __shared__ __attribute__((aligned(16))) Tin dSs[N * LP];
-  __shared__ __attribute__((aligned(16))) ChunkDecay<Q> dec;
-  __shared__ float rowv[Q], diag[Q], colv[kWaves][Q], wv[kWaves][Q], uv[kWaves][Q];
-  __shared__ float dots[kWaves], dds[kWaves];
+  __shared__ __attribute__((aligned(16))) ChunkDecay<Q, true> decs[2];
+  // sums of a head, read while the next one is worked on
+  struct Sums {
+    float row[JH][Q], diag[Q], col[QT][Q], w[NTL][Q], u[NTL][Q], dot[kWaves], dd[kWaves];
+  };
+  __shared__ Sums acc2[2];
 
   const int lane = threadIdx.x & 63, w = wave_id(), lc = lane & 15, g4 = 4 * (lane >> 4);
   const int nch = (a.T + Q - 1) / Q, Hg = a.H / a.G;
@@ -255,212 +263,270 @@ __global__ __launch_bounds__(kThreads) void ssm_bwd_chunk_kernel(SsmArgs a, Chun
   const size_t GTN = (size_t)a.B * a.G * a.T * N;
   float* sums = o.sums + ((size_t)b * nch + c) * 3 * a.H;
 
-  f32x4 dB[NQ][QT], dC[NQ][QT];
+  const int nt = w % NTL, tn = w / NTL, qi = w % QT, jh = w / QT;
+  f32x4 dB[TM], dC[TM];  // token tiles tn + TN m
 #pragma unroll
-  for (int q = 0; q < NQ; ++q)
-#pragma unroll
-    for (int it = 0; it < QT; ++it)
-      dB[q][it] = dC[q][it] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int m = 0; m < TM; ++m) dB[m] = dC[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   if (valid > 0) {
-    Stage<Q, P, Tin, kThreads> fx, fy;
-    float fdt = 0.f;
+    Stage<Q, P, Tin, kThreads, LP> fx, fy;
     auto fetch = [&](int h) {
       const size_t th = ((size_t)b * a.H + h) * a.T + t0;
       fx.fetch((const Tin*)a.x + th * P, valid);
       fy.fetch((const Tin*)a.dy + th * P, valid);
-      if (w == 0) fdt = lane < Q && lane < valid ? a.dt[th + lane] : 0.f;
     };
+    // decays a head ahead, by the last wave, from steps fetched another head
+    // earlier
+    auto steps = [&](int h) {
+      const size_t th = ((size_t)b * a.H + h) * a.T + t0;
+      return w == kWaves - 1 && h < h1
+                 ? buffer_load_f32(make_buffer(a.dt + th, min(valid, Q) * 4ll), lane * 4)
+                 : 0.f;
+    };
+    auto fill = [&](int h, float raw) {
+      float sl = 0.f, st = 0.f;
+      if (lane < Q && lane < valid)
+        st = ssm_step(raw, a.dt_bias ? a.dt_bias[h] : 0.f, a.softplus, sl);
+      decs[(h - h0) & 1].fill(st, st * a.A[h], sl);
+    };
+    // the step's gradient of every token, from the sums of head h
+    auto finish = [&](int h) {
+      const Sums& z = acc2[(h - h0) & 1];
+      const ChunkDecay<Q, true>& dec = decs[(h - h0) & 1];
+      float R = 0.f, col = 0.f, wi = 0.f, uj = 0.f, own = 0.f, step = 0.f, slope = 0.f;
+      if (lane < Q) {
+#pragma unroll
+        for (int q = 0; q < JH; ++q) R += z.row[q][lane];
+#pragma unroll
+        for (int q = 0; q < QT; ++q) col += z.col[q][lane];
+#pragma unroll
+        for (int q = 0; q < NTL; ++q) {
+          wi += z.w[q][lane];
+          uj += z.u[q][lane];
+        }
+        step = dec.dt[lane];
+        slope = dec.slope[lane];
+        own = z.diag[lane] + col + uj;
+      }
+      float dot = 0.f, dd = 0.f;
+#pragma unroll
+      for (int q = 0; q < kWaves; ++q) {
+        if (q < NTL) dot += z.dot[q];
+        dd += z.dd[q];
+      }
+      const float gt = wave_suffix_sum(R - col * step + wi) + wave_prefix_before(uj * step) +
+                       dec.total * dot;
+      const bool in = lane < Q && lane < valid;
+      const float draw = in ? (own + a.A[h] * gt) * slope : 0.f;
+      if (lane < rows) a.ddt[((size_t)b * a.H + h) * a.T + t0 + lane] = draw;
+      const float sa = wave_sum(in ? step * gt : 0.f), sb = wave_sum(draw);
+      if (lane == 0) {
+        sums[h] = sa;
+        sums[a.H + h] = dd;
+        sums[2 * a.H + h] = sb;
+      }
+    };
+    float raw;
     {
-      Stage<Q, N, Tin, kThreads> fb, fc;
+      Stage<Q, N, Tin, kThreads, LN> fb, fc;
       fb.fetch((const Tin*)a.Bm + tg * N, valid);
       fc.fetch((const Tin*)a.Cm + tg * N, valid);
       fetch(h0);
-      fb.put(Bs, LN);
-      fc.put(Cs, LN);
+      raw = steps(h0);
+      fb.put(Bs);
+      fc.put(Cs);
     }
+    if (w == kWaves - 1) fill(h0, raw);
+    raw = steps(h0 + 1);
     __syncthreads();
     // scores of the wave's query tile: rows j = 4 (l / 16) + r, column i = l % 16
-    f32x4 CB[QT];
-    if (w < QT) {
+    f32x4 CB[JM];
+    {
       Frag<N, Tin> cf;
-      cf.load(Cs + w * 16 * LN, LN);
+      cf.load(Cs + qi * 16 * LN, LN);
 #pragma unroll
-      for (int jt = 0; jt < QT; ++jt) {
-        CB[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (jt <= w) {
+      for (int m = 0; m < JM; ++m) {
+        const int jt = jh + JH * m;
+        CB[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (jt <= qi) {
           Frag<N, Tin> bf;
           bf.load(Bs + jt * 16 * LN, LN);
-          mma(CB[jt], bf, cf);
+          mma(CB[m], bf, cf);
         }
       }
     }
 
     for (int h = h0; h < h1; ++h) {
       const size_t bh = (size_t)b * a.H + h, th = bh * a.T + t0;
-      const float A = a.A[h], D = a.D ? a.D[h] : 0.f, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+      const float D = a.D ? a.D[h] : 0.f;
+      const ChunkDecay<Q, true>& dec = decs[(h - h0) & 1];
+      Sums& z = acc2[(h - h0) & 1];
       // the previous head's readers of these buffers are behind a barrier
-      fx.put(Xs, LP);
-      fy.put(Ys, LP);
-      const float raw = fdt;
-      float step = 0.f;
-      if (w == 0) {
-        step = lane < Q && lane < valid ? ssm_step(raw, bias, a.softplus) : 0.f;
-        dec.fill(step, step * A);
-      }
-      f32x4 sv[NQ][PTL], dv[NQ][PTL];
+      fx.put(Xs);
+      fy.put(Ys);
+      f32x4 sv[PTL], dv[PTL];
       {
         const float* sf = o.states + (bh * nch + c) * P * N;
         const float* sr = sf + (size_t)BH * nch * P * N;
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          const int nt = q * kWaves + w;
-          if (nt >= NTL) break;
-#pragma unroll
-          for (int pb = 0; pb < PTL; ++pb) {
-            sv[q][pb] = load4(sf + ((pb * NTL + nt) * 64 + lane) * 4);
-            dv[q][pb] = load4(sr + ((pb * NTL + nt) * 64 + lane) * 4);
-          }
+        for (int pb = 0; pb < PTL; ++pb) {
+          sv[pb] = load4(sf + (pb * NTL + nt) * 256 + (unsigned)(lane * 4));
+          dv[pb] = load4(sr + (pb * NTL + nt) * 256 + (unsigned)(lane * 4));
         }
       }
       if (h + 1 < h1) fetch(h + 1);
       __syncthreads();
 
       // scores of dy and x, K and Z, and the pairs' sums
-      if (w < QT) {
+      {
         Frag<P, Tin> yf;
-        yf.load(Ys + w * 16 * LP, LP);
+        yf.load(Ys + qi * 16 * LP, LP);
         float rsum = 0.f;
-        const int i = w * 16 + lc;
+        const int i = qi * 16 + lc;
 #pragma unroll
-        for (int jt = 0; jt < QT; ++jt) {
+        for (int m = 0; m < JM; ++m) {
+          const int jt = jh + JH * m;
           f32x4 kk = {0.f, 0.f, 0.f, 0.f}, zz = {0.f, 0.f, 0.f, 0.f};
-          if (jt <= w) {
-            f32x4 m = {0.f, 0.f, 0.f, 0.f};
+          if (jt >= QT) break;
+          if (jt <= qi) {
+            f32x4 s = {0.f, 0.f, 0.f, 0.f};
             Frag<P, Tin> xf;
             xf.load(Xs + jt * 16 * LP, LP);
-            mma(m, xf, yf);
-            const f32x4 l = pair_decay<Q>(dec, w, jt), dj = tile_steps<Q>(dec, jt);
+            mma(s, xf, yf);
+            const f32x4 l = pair_decay(dec, qi, jt), dj = tile_steps(dec, jt);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const int j = jt * 16 + g4 + r;
-              const float z = m[r] * l[r];
-              kk[r] = CB[jt][r] * l[r] * dj[r];
-              zz[r] = z * dj[r];
-              float v = CB[jt][r] * z;  // the pair without its step
+              const float zl = s[r] * l[r];
+              kk[r] = CB[m][r] * l[r] * dj[r];
+              zz[r] = zl * dj[r];
+              float v = CB[m][r] * zl;  // the pair without its step
               if (j == i) {
-                diag[j] = v;  // no decay between: not part of g
+                z.diag[j] = v;  // no decay between: not part of g
                 v = 0.f;
               }
               rsum += v * dj[r];
               const float cs = row16_sum(v);
-              if (lc == 0) colv[w][j] = cs;
+              if (lc == 0) z.col[qi][j] = cs;
             }
           } else if (lc == 0) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) colv[w][jt * 16 + g4 + r] = 0.f;
+            for (int r = 0; r < 4; ++r) z.col[qi][jt * 16 + g4 + r] = 0.f;
           }
           store4(Ks + i * LQ + jt * 16 + g4, kk);
           store4(Zs + i * LQ + jt * 16 + g4, zz);
         }
         rsum = add_swap32(add_swap16(rsum));
-        if (lane < 16) rowv[i] = rsum;
+        if (lane < 16) z.row[jh][i] = rsum;
       }
-      float dot = 0.f;
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        const int nt = q * kWaves + w;
-        if (nt >= NTL) break;
+      if (tn == 0) {
+        // <dS, S> as a tree over the lane's values: its error is shared by
+        // every token of the chunk
+        float dot[PTL];
 #pragma unroll
         for (int pb = 0; pb < PTL; ++pb) {
-          store4(dSs + (nt * 16 + lc) * LP + pb * 16 + g4, dv[q][pb]);
+          store4(dSs + (nt * 16 + lc) * LP + pb * 16 + g4, dv[pb]);
+          dot[pb] = (sv[pb][0] * dv[pb][0] + sv[pb][1] * dv[pb][1]) +
+                    (sv[pb][2] * dv[pb][2] + sv[pb][3] * dv[pb][3]);
+        }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) dot += sv[q][pb][e] * dv[q][pb][e];
+        for (int m = PTL / 2; m > 0; m /= 2)
+#pragma unroll
+          for (int pb = 0; pb < m; ++pb) dot[pb] += dot[pb + m];
+        const float s = wave_sum(dot[0]);
+        if (lane == 0) z.dot[w] = s;
+      }
+      // what the entering state and the leaving adjoint give to dC and dB
+      {
+        Parts<P, Tin> sp;
+        parts_from_acc<P>(sp, sv);
+#pragma unroll
+        for (int m = 0; m < TM; ++m) {
+          const int it = tn + TN * m;
+          if (it >= QT) break;
+          Frag<P, Tin> yf;
+          yf.load_perm(Ys + it * 16 * LP, LP);
+          f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+          mma_parts(acc, sp, yf);
+          const int i = it * 16 + lc;
+          const f32x4 cv = load4(Cs + i * LN + nt * 16 + g4);
+          const float ent = dec.ent[i];
+          float ws = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            acc[e] *= ent;
+            ws += acc[e] * cv[e];
+            dC[m][e] += acc[e];
+          }
+          ws = add_swap32(add_swap16(ws));
+          if (lane < 16) z.w[nt][i] = ws;
+          __builtin_amdgcn_sched_barrier(0);  // one token tile's operands at a time
         }
       }
-      dot = wave_sum(dot);
-      if (lane == 0) dots[w] = dot;
+      {
+        Parts<P, Tin> dp;
+        parts_from_acc<P>(dp, dv);
+#pragma unroll
+        for (int m = 0; m < TM; ++m) {
+          const int jt = tn + TN * m;
+          if (jt >= QT) break;
+          Frag<P, Tin> xf;
+          xf.load_perm(Xs + jt * 16 * LP, LP);
+          f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+          mma_parts(acc, dp, xf);
+          const int j = jt * 16 + lc;
+          const f32x4 bv = load4(Bs + j * LN + nt * 16 + g4);
+          const float ex = dec.ext[j], dtj = dec.dt[j];
+          float us = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            acc[e] *= ex;
+            us += acc[e] * bv[e];
+            dB[m][e] += acc[e] * dtj;
+          }
+          us = add_swap32(add_swap16(us));
+          if (lane < 16) z.u[nt][j] = us;
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      if (w == kWaves - QT && h > h0) finish(h - 1);  // the least of the scores
       __syncthreads();
 
-      // dB, dC over the wave's columns n
-      float ws[QT], us[QT];
-#pragma unroll
-      for (int it = 0; it < QT; ++it) ws[it] = us[it] = 0.f;
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        const int nt = q * kWaves + w;
-        if (nt >= NTL) break;
+      if (w == kWaves - 1 && h + 1 < h1) {
+        fill(h + 1, raw);
+        raw = steps(h + 2);
+      }
+      // dB, dC from the chunk's own pairs, over the wave's columns n
+      {
         Frag<Q, Tin> bT, cT;  // rows n, k = token
         bT.load_kmajor(Bs + nt * 16, LN);
         cT.load_kmajor(Cs + nt * 16, LN);
-        {
-          Parts<P, Tin> sp;
-          parts_from_acc<P>(sp, sv[q]);
 #pragma unroll
-          for (int it = 0; it < QT; ++it) {
-            Frag<P, Tin> yf;
-            yf.load_perm(Ys + it * 16 * LP, LP);
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-            mma_parts(acc, sp, yf);
-            const int i = it * 16 + lc;
-            const f32x4 cv = load4(Cs + i * LN + nt * 16 + g4);
-            const float ent = dec.ent[i];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              acc[e] *= ent;
-              ws[it] += acc[e] * cv[e];
-              dC[q][it][e] += acc[e];
-            }
-            Frag<Q, Tin> zf;
-            zf.load(Zs + it * 16 * LQ, LQ);
-            mma_upto<Q>(dC[q][it], bT, zf, 16 * (it + 1));
-          }
-        }
-        {
-          Parts<P, Tin> dp;
-          parts_from_acc<P>(dp, dv[q]);
-#pragma unroll
-          for (int jt = 0; jt < QT; ++jt) {
-            Frag<P, Tin> xf;
-            xf.load_perm(Xs + jt * 16 * LP, LP);
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-            mma_parts(acc, dp, xf);
-            const int j = jt * 16 + lc;
-            const f32x4 bv = load4(Bs + j * LN + nt * 16 + g4);
-            const float ex = dec.ext[j], dtj = dec.dt[j];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              acc[e] *= ex;
-              us[jt] += acc[e] * bv[e];
-              dB[q][jt][e] += acc[e] * dtj;
-            }
-            Frag<Q, Tin> zf;
-            zf.load_kmajor(Zs + jt * 16, LQ);  // rows j, k = i
-            mma(dB[q][jt], cT, zf);
-          }
-        }
-      }
-#pragma unroll
-      for (int it = 0; it < QT; ++it) {
-        const float x = add_swap32(add_swap16(ws[it])), y = add_swap32(add_swap16(us[it]));
-        if (lane < 16) {
-          wv[w][it * 16 + lane] = x;
-          uv[w][it * 16 + lane] = y;
+        for (int m = 0; m < TM; ++m) {
+          const int it = tn + TN * m;
+          if (it >= QT) break;
+          Frag<Q, Tin> zf;
+          zf.load(Zs + it * 16 * LQ, LQ);
+          mma(dC[m], bT, zf);
+          zf.load_kmajor(Zs + it * 16, LQ);  // rows j, k = i
+          mma(dB[m], cT, zf);
         }
       }
 
-      // dx of token tile jt, and its share of dD
+      // dx of token tile qi, and its share of dD
       float dd = 0.f;
       {
-        const int jt = w % QT, j = jt * 16 + lc;
+        const int j = qi * 16 + lc;
         Frag<N, Tin> bf;
-        bf.load(Bs + jt * 16 * LN, LN);
+        bf.load(Bs + qi * 16 * LN, LN);
         Frag<Q, Tin> kf;
-        kf.load_kmajor(Ks + jt * 16, LQ);  // rows j, k = i
-        const float f = dec.ext[j] * dec.dt[j];
+        kf.load_kmajor(Ks + qi * 16, LQ);  // rows j, k = i
+        const float f = dec.wx[j];
+        const Buffer dxb =
+            make_buffer((Tin*)a.dx + th * P, (long long)rows * P * (int)sizeof(Tin));
 #pragma unroll
-        for (int q = 0; q < PTL / PH + (PTL % PH != 0); ++q) {
-          const int pt = q * PH + w / QT;
+        for (int q = 0; q < (PTL + JH - 1) / JH; ++q) {
+          const int pt = q * JH + jh;
           if (pt >= PTL) break;
           Frag<N, Tin> df;
           df.load_kmajor(dSs + pt * 16, LP);  // rows p, k = n
@@ -478,48 +544,15 @@ __global__ __launch_bounds__(kThreads) void ssm_bwd_chunk_kernel(SsmArgs a, Chun
             dd += yv[e] * xv[e];
             acc[e] = j < valid ? acc[e] + D * yv[e] : 0.f;
           }
-          if (j < rows) store4((Tin*)a.dx + (th + j) * P + pt * 16 + g4, acc);
+          buffer_store4(dxb, j * P + pt * 16 + g4, acc, Tin());
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
       dd = wave_sum(dd);
-      if (lane == 0) dds[w] = dd;
+      if (lane == 0) z.dd[w] = dd;
       __syncthreads();
-
-      // per token: the step's gradient
-      if (w == 0) {
-        float R = 0.f, col = 0.f, wi = 0.f, uj = 0.f, own = 0.f;
-        if (lane < Q) {
-          R = rowv[lane];
-#pragma unroll
-          for (int q = 0; q < kWaves; ++q) {
-            if (q < QT) col += colv[q][lane];
-            if (q < NTL) {
-              wi += wv[q][lane];
-              uj += uv[q][lane];
-            }
-          }
-          own = diag[lane] + col + uj;
-        }
-        float dot4 = 0.f, dd4 = 0.f;
-#pragma unroll
-        for (int q = 0; q < kWaves; ++q) {
-          if (q < NTL) dot4 += dots[q];
-          dd4 += dds[q];
-        }
-        const float gt = wave_suffix_sum(R - col * step + wi) + wave_prefix_before(uj * step) +
-                         dec.total * dot4;
-        const bool in = lane < Q && lane < valid;
-        const float draw =
-            in ? (own + A * gt) * ssm_step_slope(raw, bias, a.softplus) : 0.f;
-        if (lane < rows) a.ddt[th + lane] = draw;
-        const float sa = wave_sum(in ? step * gt : 0.f), sb = wave_sum(draw);
-        if (lane == 0) {
-          sums[h] = sa;
-          sums[a.H + h] = dd4;
-          sums[2 * a.H + h] = sb;
-        }
-      }
     }
+    if (w == 0) finish(h1 - 1);
   } else {
     // a chunk behind its sequence: zeros
     for (int h = h0; h < h1; ++h) {
@@ -533,23 +566,18 @@ __global__ __launch_bounds__(kThreads) void ssm_bwd_chunk_kernel(SsmArgs a, Chun
   }
 
 #pragma unroll
-  for (int q = 0; q < NQ; ++q) {
-    const int nt = q * kWaves + w;
-    if (nt >= NTL) break;
-#pragma unroll
-    for (int it = 0; it < QT; ++it) {
-      const int t = it * 16 + lc;
-      if (t >= rows) continue;
-      const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-      const f32x4 vb = t < valid ? dB[q][it] : zero, vc = t < valid ? dC[q][it] : zero;
-      const size_t at = (tg + t) * N + nt * 16 + g4;
-      if (o.parts == 1) {
-        store4((Tin*)a.dB + at, vb);
-        store4((Tin*)a.dC + at, vc);
-      } else {
-        store4(o.dBp + part * GTN + at, vb);
-        store4(o.dCp + part * GTN + at, vc);
-      }
+  for (int m = 0; m < TM; ++m) {
+    const int it = tn + TN * m, t = it * 16 + lc;
+    if (it >= QT || t >= rows) continue;
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+    const f32x4 vb = t < valid ? dB[m] : zero, vc = t < valid ? dC[m] : zero;
+    const size_t at = (tg + t) * N + nt * 16 + g4;
+    if (o.parts == 1) {
+      store4((Tin*)a.dB + at, vb);
+      store4((Tin*)a.dC + at, vc);
+    } else {
+      store4(o.dBp + part * GTN + at, vb);
+      store4(o.dCp + part * GTN + at, vc);
     }
   }
 }
@@ -611,7 +639,7 @@ int run_bwd(const SsmArgs& a, hipStream_t s) {
   const int BH = a.B * a.H, PN = P * N;
   const Plan p = make_plan(a.B, a.H, a.G, a.T, P, N, bwd_q<Tin>());
   float* ws = (float*)a.ws;
-  constexpr int NT = 64 * (P / 16 < kWaves ? P / 16 : kWaves);
+  constexpr int NT = 4 * walk_rows<P>(), SL = P / walk_rows<P>();
   float *slots = ws + p.slots, *logs = ws + p.logs, *states = ws + p.states;
   if (BH == 0)  // an empty batch: zeros for the parameters
     return launch_column_sum(ws, 0, 3 * a.H, a.H, 1, a.dA, a.dD, a.dbias, s);
@@ -619,7 +647,7 @@ int run_bwd(const SsmArgs& a, hipStream_t s) {
   if (p.nseg > 1) {
     tk = ktimer_before(s, "ssm_bwd_state");
     hipLaunchKernelGGL((ssm_walk_kernel<P, N, Tin, false>),
-                       dim3((unsigned)(2 * BH * (p.nseg - 1))), dim3(NT), 0, s, a, p.nseg,
+                       dim3((unsigned)(2 * BH * (p.nseg - 1) * SL)), dim3(NT), 0, s, a, p.nseg,
                        p.segch, slots, logs, states);
     ktimer_after(s, tk);
     tk = ktimer_before(s, "ssm_bwd_chain");
@@ -628,7 +656,7 @@ int run_bwd(const SsmArgs& a, hipStream_t s) {
     ktimer_after(s, tk);
   }
   tk = ktimer_before(s, "ssm_bwd_walk");
-  hipLaunchKernelGGL((ssm_walk_kernel<P, N, Tin, true>), dim3((unsigned)(2 * BH * p.nseg)),
+  hipLaunchKernelGGL((ssm_walk_kernel<P, N, Tin, true>), dim3((unsigned)(2 * BH * p.nseg * SL)),
                      dim3(NT), 0, s, a, p.nseg, p.segch, slots, logs, states);
   ktimer_after(s, tk);
   int rc = (int)hipGetLastError();

@@ -5,15 +5,23 @@
 
 namespace osdn {
 
-// The step size of a token: softplus(raw + bias) (or raw + bias itself).
-// softplus(v) = max(v, 0) + log1p(e^-|v|), exact at both ends.
-__device__ __forceinline__ float ssm_step(float raw, float bias, int softplus) {
+// The step size of a token, softplus(raw + bias) (or raw + bias itself), and
+// its slope by raw. softplus(v) = max(v, 0) + log1p(e), e = exp(-|v|), from the
+// hardware's exp2 and log2 (one unit each): the argument's rounding is put
+// back into e, and log1p(e) = log(1 + e) e / ((1 + e) - 1) makes up for the
+// rounding of 1 + e. slope = 1 / (1 + exp(-v)).
+__device__ __forceinline__ float ssm_step(float raw, float bias, int softplus, float& slope) {
   const float v = raw + bias;
-  return softplus ? fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))) : v;
-}
-// d softplus / dv = 1 / (1 + e^-v).
-__device__ __forceinline__ float ssm_step_slope(float raw, float bias, int softplus) {
-  return softplus ? 1.f / (1.f + expf(-(raw + bias))) : 1.f;
+  slope = 1.f;
+  if (!softplus) return v;
+  const float x = -fabsf(v), t = x * 1.44269504f;
+  const float lost = fmaf(x, 1.44269504f, -t) + x * 1.92596299e-8f;  // of x log2(e)
+  float e = __builtin_amdgcn_exp2f(t);
+  e = fmaf(e, lost * 0.693147181f, e);
+  const float w = 1.f + e, d = w - 1.f;
+  const float l = d > 0.f ? __builtin_amdgcn_logf(w) * 0.693147181f * (e / d) : e;
+  slope = (v >= 0.f ? 1.f : e) / w;
+  return fmaxf(v, 0.f) + l;
 }
 
 // Tokens of batch entry b (lengths null: all T), clamped to [0, T].
@@ -49,20 +57,23 @@ __device__ __forceinline__ float row16_suffix_after(float x) {
 // behind j inside its block, and whole blocks between. No difference of two
 // long sums is taken, so a strong decay early in the chunk costs later pairs
 // no precision; inside one block the difference is of sums over 16 tokens.
-template <int Q>
+template <int Q, bool Grad = false>
 struct ChunkDecay {
   float dt[Q];    // step
   float up[Q];    // log: block start .. token, inclusive
   float eup[Q];   // exp(up)
   float edn[Q];   // exp(log: after token .. block end)
   float ent[Q];   // chunk entry .. token
-  float ext[Q];   // after token .. chunk exit
+  float wx[Q];    // after token .. chunk exit, times dt
+  float ext[Grad ? Q : 4];    // the same without dt
+  float slope[Grad ? Q : 4];  // of the step by its raw value
   float gap[16];  // [a][b], a > b: exp over the blocks strictly between
   float total;    // whole chunk
   float logtot;
 
-  // By one whole wave; lane t (< Q) passes its token's step and log decay.
-  __device__ __forceinline__ void fill(float step, float l) {
+  // By one whole wave; lane t (< Q) passes its token's step, log decay and
+  // slope.
+  __device__ __forceinline__ void fill(float step, float l, float sl) {
     constexpr int NB = Q / 16;
     const int t = threadIdx.x & 63;
     const float u = row16_prefix(l), d = row16_suffix_after(l);
@@ -85,7 +96,12 @@ struct ChunkDecay {
       eup[t] = __expf(u);
       edn[t] = __expf(d);
       ent[t] = __expf(before + u);
-      ext[t] = __expf(d + after);
+      const float x = __expf(d + after);
+      wx[t] = x * step;
+      if constexpr (Grad) {
+        ext[t] = x;
+        slope[t] = sl;
+      }
     }
     if (t < NB * NB) {
       const int x = t / NB, y = t % NB;
@@ -105,8 +121,8 @@ struct ChunkDecay {
 // Decays of one tile of pairs in accumulator layout: lane l holds the factors
 // from the tokens j = 16 jt + 4 (l / 16) + r to i = 16 it + l % 16, zero where
 // j > i.
-template <int Q>
-__device__ __forceinline__ f32x4 pair_decay(const ChunkDecay<Q>& d, int it, int jt) {
+template <int Q, bool G>
+__device__ __forceinline__ f32x4 pair_decay(const ChunkDecay<Q, G>& d, int it, int jt) {
   f32x4 f = {0.f, 0.f, 0.f, 0.f};
   const int i = it * 16 + acc_col(), j = jt * 16 + acc_row(0);
   if (jt < it) {
@@ -124,8 +140,8 @@ __device__ __forceinline__ f32x4 pair_decay(const ChunkDecay<Q>& d, int it, int 
 }
 
 // The steps of the tile's tokens j.
-template <int Q>
-__device__ __forceinline__ f32x4 tile_steps(const ChunkDecay<Q>& d, int jt) {
+template <int Q, bool G>
+__device__ __forceinline__ f32x4 tile_steps(const ChunkDecay<Q, G>& d, int jt) {
   return *reinterpret_cast<const f32x4*>(d.dt + jt * 16 + acc_row(0));
 }
 
@@ -160,17 +176,28 @@ __device__ __forceinline__ void mma_upto(f32x4& acc, const Frag<KEXT, float>& a,
     if (4 * i < kmax) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[i], b.v[i], acc, 0, 0, 0);
 }
 
+// Two values rounded to bf16 by one packed conversion, and back.
+__device__ __forceinline__ unsigned pack_bf16(float x, float y) {
+  typedef __attribute__((ext_vector_type(2))) float f32x2;
+  typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+  return __builtin_bit_cast(unsigned, __builtin_convertvector((f32x2{x, y}), bf16x2));
+}
+__device__ __forceinline__ float low_bf16(unsigned u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float high_bf16(unsigned u) {
+  return __uint_as_float(u & 0xffff0000u);
+}
+
 // A fragment (row = lane % 16) in permuted k order from the accumulator tiles
 // of that k range.
 template <int KEXT>
 __device__ __forceinline__ void frag_from_acc(Frag<KEXT, __bf16>& f, const f32x4 (&t)[KEXT / 16]) {
 #pragma unroll
-  for (int i = 0; i < KEXT / 32; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      f.v[i][e] = (__bf16)t[2 * i][e];
-      f.v[i][4 + e] = (__bf16)t[2 * i + 1][e];
-    }
+  for (int i = 0; i < KEXT / 32; ++i) {
+    const f32x4 &a = t[2 * i], &b = t[2 * i + 1];
+    const u32x4 q = {pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(b[0], b[1]),
+                     pack_bf16(b[2], b[3])};
+    f.v[i] = __builtin_bit_cast(bf16x8, q);
+  }
 }
 template <int KEXT>
 __device__ __forceinline__ void frag_from_acc(Frag<KEXT, float>& f, const f32x4 (&t)[KEXT / 16]) {
@@ -191,11 +218,12 @@ struct Parts {
   Frag<KEXT, Tin> f[M];
 };
 
-__device__ __forceinline__ void split3(float p, __bf16& a, __bf16& b, __bf16& c) {
-  a = (__bf16)p;
-  p -= (float)a;
-  b = (__bf16)p;
-  c = (__bf16)(p - (float)b);
+__device__ __forceinline__ void split3(float x, float y, unsigned& a, unsigned& b, unsigned& c) {
+  a = pack_bf16(x, y);
+  x -= low_bf16(a);
+  y -= high_bf16(a);
+  b = pack_bf16(x, y);
+  c = pack_bf16(x - low_bf16(b), y - high_bf16(b));
 }
 
 // x scaled by w[k] (natural k order, w in LDS).
@@ -205,16 +233,21 @@ __device__ __forceinline__ void scale_parts(const Frag<KEXT, __bf16>& x, const f
   const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
   for (int i = 0; i < KEXT / 32; ++i) {
-    const f32x4 a = *reinterpret_cast<const f32x4*>(w + 32 * i + 8 * g);
-    const f32x4 b = *reinterpret_cast<const f32x4*>(w + 32 * i + 8 * g + 4);
+    const f32x4 f[2] = {*reinterpret_cast<const f32x4*>(w + 32 * i + 8 * g),
+                        *reinterpret_cast<const f32x4*>(w + 32 * i + 8 * g + 4)};
+    const u32x4 u = __builtin_bit_cast(u32x4, x.v[i]);
+    u32x4 q[3];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      __bf16 p0, p1, p2;
-      split3((float)x.v[i][e] * (e < 4 ? a[e & 3] : b[e & 3]), p0, p1, p2);
-      o.f[0].v[i][e] = p0;
-      o.f[1].v[i][e] = p1;
-      o.f[2].v[i][e] = p2;
+    for (int e = 0; e < 4; ++e) {
+      unsigned p0, p1, p2;
+      split3(low_bf16(u[e]) * f[e / 2][2 * (e & 1)], high_bf16(u[e]) * f[e / 2][2 * (e & 1) + 1],
+             p0, p1, p2);
+      q[0][e] = p0;
+      q[1][e] = p1;
+      q[2][e] = p2;
     }
+#pragma unroll
+    for (int m = 0; m < 3; ++m) o.f[m].v[i] = __builtin_bit_cast(bf16x8, q[m]);
   }
 }
 template <int KEXT>
@@ -230,15 +263,19 @@ template <int KEXT>
 __device__ __forceinline__ void parts_from_acc(Parts<KEXT, __bf16>& o,
                                                const f32x4 (&t)[KEXT / 16]) {
 #pragma unroll
-  for (int i = 0; i < KEXT / 32; ++i)
+  for (int i = 0; i < KEXT / 32; ++i) {
+    u32x4 q[3];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      __bf16 p0, p1, p2;
-      split3(t[2 * i + e / 4][e & 3], p0, p1, p2);
-      o.f[0].v[i][e] = p0;
-      o.f[1].v[i][e] = p1;
-      o.f[2].v[i][e] = p2;
+    for (int e = 0; e < 4; ++e) {
+      unsigned p0, p1, p2;
+      split3(t[2 * i + e / 2][2 * (e & 1)], t[2 * i + e / 2][2 * (e & 1) + 1], p0, p1, p2);
+      q[0][e] = p0;
+      q[1][e] = p1;
+      q[2][e] = p2;
     }
+#pragma unroll
+    for (int m = 0; m < 3; ++m) o.f[m].v[i] = __builtin_bit_cast(bf16x8, q[m]);
+  }
 }
 template <int KEXT>
 __device__ __forceinline__ void parts_from_acc(Parts<KEXT, float>& o,
@@ -269,37 +306,63 @@ __device__ __forceinline__ f32x4 load4(const float* p) {
   return *reinterpret_cast<const f32x4*>(p);
 }
 __device__ __forceinline__ void store4(__bf16* p, const f32x4& a) {
-  bf16x4 b;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) b[e] = (__bf16)a[e];
-  *reinterpret_cast<bf16x4*>(p) = b;
+  *reinterpret_cast<uint2*>(p) = uint2{pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3])};
 }
 __device__ __forceinline__ void store4(float* p, const f32x4& a) {
   *reinterpret_cast<f32x4*>(p) = a;
 }
 
+// A buffer descriptor over `bytes` from p (both wave-uniform): reads past the
+// end return zeros and writes past it are dropped, by the hardware's range
+// check, so that the last tile of a sequence takes the same instructions as
+// the others; and a 32-bit offset a lane is the whole address, where a 64-bit
+// pointer a lane would cost the registers that the tiles need.
+typedef __amdgpu_buffer_rsrc_t Buffer;
+__device__ __forceinline__ Buffer make_buffer(const void* p, long long bytes) {
+  const int n = bytes < 0 ? 0 : bytes > 0x7fffffff ? 0x7fffffff : (int)bytes;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, n, 0x00027000);
+}
+__device__ __forceinline__ uint4 buffer_load16(Buffer r, unsigned off) {
+  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+__device__ __forceinline__ float buffer_load_f32(Buffer r, unsigned off) {
+  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+}
+// Four consecutive values, rounded, to element `at`.
+__device__ __forceinline__ void buffer_store4(Buffer r, unsigned at, const f32x4& a, __bf16) {
+  typedef __attribute__((ext_vector_type(2))) unsigned u32x2;
+  __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3])}, r,
+                                        at * 2, 0, 0);
+}
+__device__ __forceinline__ void buffer_store4(Buffer r, unsigned at, const f32x4& a, float) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, a), r, at * 4, 0, 0);
+}
+
 // Staging of a Q x D tile of token rows through registers into LDS by NT
-// threads: fetch() issues the loads (rows from `valid` on are zeros), put()
-// writes them with row stride ld.
-template <int Q, int D, typename Tin, int NT>
+// threads, of rows STRIDE apart in memory and LD in LDS: fetch() issues the
+// loads (rows from `valid` on are zeros), put() writes them.
+template <int Q, int D, typename Tin, int NT, int LD, int STRIDE = D>
 struct Stage {
-  static constexpr int VE = 16 / sizeof(Tin), PER = D / VE, NV = Q * PER / NT;
-  static_assert(Q * PER % NT == 0, "tile divides over the threads");
+  static constexpr int VE = 16 / sizeof(Tin), PER = D / VE, RP = NT / PER;
+  static constexpr int NV = (Q + RP - 1) / RP;
+  static_assert(NT % PER == 0, "threads cover whole rows");
   uint4 v[NV];
+  __device__ __forceinline__ static int row0() { return threadIdx.x / PER; }
   __device__ __forceinline__ void fetch(const Tin* src, int valid) {
+    const Buffer r = make_buffer(src, (long long)min(valid, Q) * STRIDE * (int)sizeof(Tin) -
+                                          (STRIDE - D) * (int)sizeof(Tin));
+    const unsigned off =
+        (unsigned)(row0() * STRIDE + threadIdx.x % PER * VE) * (unsigned)sizeof(Tin);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = i * NT + threadIdx.x, row = e / PER, col = e % PER * VE;
-      v[i] = row < valid ? *reinterpret_cast<const uint4*>(src + (size_t)row * D + col)
-                         : uint4{0u, 0u, 0u, 0u};
-    }
+    for (int i = 0; i < NV; ++i)
+      v[i] = buffer_load16(r, off + i * (unsigned)(RP * STRIDE * sizeof(Tin)));
   }
-  __device__ __forceinline__ void put(Tin* dst, int ld) const {
+  __device__ __forceinline__ void put(Tin* dst) const {
+    Tin* d = dst + row0() * LD + threadIdx.x % PER * VE;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = i * NT + threadIdx.x, row = e / PER, col = e % PER * VE;
-      *reinterpret_cast<uint4*>(dst + row * ld + col) = v[i];
-    }
+    for (int i = 0; i < NV; ++i)
+      if (Q % RP == 0 || row0() + i * RP < Q)
+        *reinterpret_cast<uint4*>(d + i * RP * LD) = v[i];
   }
 };
 

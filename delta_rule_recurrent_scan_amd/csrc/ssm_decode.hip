@@ -31,7 +31,8 @@ __global__ __launch_bounds__(kDecThreads) void ssm_decode_kernel(SsmArgs a) {
     float Bv[NC], Cv[NC];
     load_cols<N, Tin>((const Tin*)a.Bm + (tg + t) * N, cl, Bv);
     load_cols<N, Tin>((const Tin*)a.Cm + (tg + t) * N, cl, Cv);
-    const float dt = ssm_step(a.dt[th + t], bias, a.softplus);
+    float slope;
+    const float dt = ssm_step(a.dt[th + t], bias, a.softplus, slope);
     const float al = expf(dt * A);
     float x[NR], y[NR];
 #pragma unroll
