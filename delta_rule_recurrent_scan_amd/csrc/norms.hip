@@ -11,7 +11,7 @@
 // All are bound by HBM: every input is read and every output written once,
 // 16 bytes a lane, with the sums in 32 bits. A head is 4, 8 or 16 adjacent
 // lanes; a row of the residual norm is one wave (up to 4096 elements, no
-// barrier) or 4 or 16 waves, held in registers between the sum and the scaling.
+// barrier) or four, held in registers between the sum and the scaling.
 //
 // Backward of n = v r, y = n * weight (r the reciprocal root):
 //   dn = dy * weight,  dv = r (dn - n mean(n dn)),  dweight = sum dy n
@@ -42,7 +42,7 @@ __global__ __launch_bounds__(kRowThreads) void gated_norm_kernel(GatedNormArgs a
   if (cg >= ng) return;  // a head's lanes leave together
   const int c = cg * 8, h = c / D, d = c % D;
   float w[8];
-  load8<false>(a.weight + (a.per_head ? c : d), 8, w);
+  load_v<false, 8>(a.weight + (a.per_head ? c : d), 8, w);
   const Tin* z = (const Tin*)a.z;
   float x[kGateRows][8], g[kGateRows][8];
 #pragma unroll
@@ -50,8 +50,8 @@ __global__ __launch_bounds__(kRowThreads) void gated_norm_kernel(GatedNormArgs a
     const long long row = row0 + j * per;
     if (row >= rows) continue;
     const long long b = row / a.T, t = row % a.T;
-    load8<true>((const Tin*)a.x + ((b * a.H + h) * a.T + t) * D + d, 8, x[j]);
-    if (z) load8<ZALN>(z + b * a.zbs + t * a.zts + c, 8, g[j]);
+    load_v<true, 8>((const Tin*)a.x + ((b * a.H + h) * a.T + t) * D + d, 8, x[j]);
+    if (z) load_v<ZALN, 8>(z + b * a.zbs + t * a.zts + c, 8, g[j]);
   }
 #pragma unroll
   for (int j = 0; j < kGateRows; ++j) {
@@ -68,7 +68,7 @@ __global__ __launch_bounds__(kRowThreads) void gated_norm_kernel(GatedNormArgs a
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       x[j][i] = x[j][i] * r * w[i] * (a.gate_first ? 1.f : g[j][i]);
-    store8<true>((Tin*)a.y + row * C + c, 8, x[j]);
+    store_v<true, 8>((Tin*)a.y + row * C + c, 8, x[j]);
   }
 }
 
@@ -84,7 +84,7 @@ __global__ __launch_bounds__(kRowThreads) void gated_norm_bwd_kernel(GatedNormAr
   float dw[8] = {};
   if (cg < ng) {
     float w[8];
-    load8<false>(a.weight + (a.per_head ? c : d), 8, w);
+    load_v<false, 8>(a.weight + (a.per_head ? c : d), 8, w);
     const Tin* z = (const Tin*)a.z;
     const long long step = (long long)nrb * per;
     for (long long row = rb * (long long)per + threadIdx.x / cx; row < rows; row += 2 * step) {
@@ -94,9 +94,9 @@ __global__ __launch_bounds__(kRowThreads) void gated_norm_bwd_kernel(GatedNormAr
         const long long ro = row + j * step;
         if (ro >= rows) continue;
         const long long b = ro / a.T, t = ro % a.T;
-        load8<true>((const Tin*)a.x + ((b * a.H + h) * a.T + t) * D + d, 8, x[j]);
-        if (z) load8<ZALN>(z + b * a.zbs + t * a.zts + c, 8, g[j]);
-        load8<true>((const Tin*)a.dy + ro * C + c, 8, e[j]);
+        load_v<true, 8>((const Tin*)a.x + ((b * a.H + h) * a.T + t) * D + d, 8, x[j]);
+        if (z) load_v<ZALN, 8>(z + b * a.zbs + t * a.zts + c, 8, g[j]);
+        load_v<true, 8>((const Tin*)a.dy + ro * C + c, 8, e[j]);
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -126,8 +126,8 @@ __global__ __launch_bounds__(kRowThreads) void gated_norm_bwd_kernel(GatedNormAr
           dx[i] = a.gate_first ? dv * gate[i] : dv;
           dz[i] = (a.gate_first ? dv * x[j][i] : e[j][i] * n * w[i]) * sl[i];
         }
-        store8<true>((Tin*)a.dx + ((b * a.H + h) * a.T + t) * D + d, 8, dx);
-        if (z) store8<true>((Tin*)a.dz + ro * C + c, 8, dz);
+        store_v<true, 8>((Tin*)a.dx + ((b * a.H + h) * a.T + t) * D + d, 8, dx);
+        if (z) store_v<true, 8>((Tin*)a.dz + ro * C + c, 8, dz);
       }
     }
   }
@@ -164,12 +164,12 @@ int run_gated(const GatedNormArgs& a, hipStream_t s) {
   return (int)hipGetLastError();
 }
 
-// Row blocks of the backward: about 2048 workgroups in all (8 a CU), each
+// Row blocks of the backward: about 1024 workgroups in all (4 a CU), each
 // with one partial row of the weight gradient.
 int gate_row_blocks(int B, int H, int T, int D) {
   const int ng = H * D / 8, cx = row_cx(ng), per = kRowThreads / cx;
   const long long rows = (long long)B * T, ncb = (ng + cx - 1) / cx;
-  long long most = 2048 / ncb, need = (rows + per - 1) / per;
+  long long most = 1024 / ncb, need = (rows + per - 1) / per;
   if (most < 1) most = 1;
   return (int)(need < most ? need : most);
 }
@@ -200,25 +200,8 @@ int run_gated_bwd(const GatedNormArgs& a, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------------------
-// Residual norm: WPR waves a row, each lane NV vectors of V elements. V = 8
-// where every row starts on 16 bytes, else 1.
+// Residual norm: WPR waves a row, each lane NV vectors of 8 elements.
 // ---------------------------------------------------------------------------
-template <typename T, int V>
-__device__ __forceinline__ void load_v(const T* p, float (&v)[V]) {
-  if constexpr (V == 8) {
-    load8<true>(p, 8, v);
-  } else {
-    v[0] = to_f32(*p);
-  }
-}
-template <typename T, int V>
-__device__ __forceinline__ void store_v(T* p, const float (&v)[V]) {
-  if constexpr (V == 8) {
-    store8<true>(p, 8, v);
-  } else {
-    *p = from_f32<T>(v[0]);
-  }
-}
 
 // Sum over the WPR waves of a row (every wave of the workgroup calls it).
 template <int WPR>
@@ -237,27 +220,28 @@ __device__ __forceinline__ float row_total(float s, float* red) {
   return s;
 }
 
-template <typename Tin, typename Tr, int V, int NV, int WPR>
-__global__ __launch_bounds__(WPR == 16 ? 1024 : 256) void residual_norm_kernel(
-    ResidualNormArgs a) {
-  constexpr int RPW = (WPR == 16 ? 16 : 4) / WPR;  // rows of a workgroup
-  __shared__ float red[16];
+constexpr int kResThreads = 256, kResWaves = kResThreads / 64;
+
+template <typename Tin, typename Tr, bool ALN, int NV, int WPR>
+__global__ __launch_bounds__(kResThreads) void residual_norm_kernel(ResidualNormArgs a) {
+  constexpr int RPW = kResWaves / WPR;  // rows of a workgroup
+  __shared__ float red[kResWaves];
   const long long row = blockIdx.x * (long long)RPW + threadIdx.x / (64 * WPR);
   const int l = threadIdx.x % (64 * WPR);
   const bool on = row < a.R;
   const size_t base = (size_t)(on ? row : 0) * a.C;
-  float h[NV][V], s = 0.f;
+  float h[NV][8], s = 0.f;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = (j * 64 * WPR + l) * V;
+    const int c = (j * 64 * WPR + l) * 8;
 #pragma unroll
-    for (int i = 0; i < V; ++i) h[j][i] = 0.f;
+    for (int i = 0; i < 8; ++i) h[j][i] = 0.f;
     if (!on || c >= a.C) continue;
-    float x[V];
-    load_v<Tin, V>((const Tin*)a.x + base + c, x);
-    if (a.residual) load_v<Tr, V>((const Tr*)a.residual + base + c, h[j]);
+    float x[8];
+    load_v<ALN, 8>((const Tin*)a.x + base + c, a.C - c, x);
+    if (a.residual) load_v<ALN, 8>((const Tr*)a.residual + base + c, a.C - c, h[j]);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < 8; ++i) {
       h[j][i] += a.scale * x[i];
       s += h[j][i] * h[j][i];
     }
@@ -265,48 +249,51 @@ __global__ __launch_bounds__(WPR == 16 ? 1024 : 256) void residual_norm_kernel(
   const float r = rsqrtf(row_total<WPR>(s, red) / a.C + a.eps);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = (j * 64 * WPR + l) * V;
+    const int c = (j * 64 * WPR + l) * 8;
     if (!on || c >= a.C) continue;
-    float w[V];
-    load_v<float, V>(a.weight + c, w);
-    if (a.h) store_v<Tr, V>((Tr*)a.h + base + c, h[j]);
+    float w[8];
+    load_v<ALN, 8>(a.weight + c, a.C - c, w);
+    if (a.h) store_v<ALN, 8>((Tr*)a.h + base + c, a.C - c, h[j]);
 #pragma unroll
-    for (int i = 0; i < V; ++i) h[j][i] *= r * w[i];
-    store_v<Tin, V>((Tin*)a.y + base + c, h[j]);
+    for (int i = 0; i < 8; ++i) h[j][i] *= r * w[i];
+    store_v<ALN, 8>((Tin*)a.y + base + c, a.C - c, h[j]);
   }
 }
 
-template <typename Tin, typename Tr, int V, int NV, int WPR>
-__global__ __launch_bounds__(WPR == 16 ? 1024 : 256) void residual_norm_bwd_kernel(
-    ResidualNormArgs a) {
-  constexpr int RPW = (WPR == 16 ? 16 : 4) / WPR;
-  __shared__ float red[16];
+template <typename Tin, typename Tr, bool ALN, int NV, int WPR>
+__global__ __launch_bounds__(kResThreads) void residual_norm_bwd_kernel(ResidualNormArgs a) {
+  constexpr int RPW = kResWaves / WPR;
+  __shared__ float red[kResWaves];
+  __shared__ float wred[RPW > 1 ? NV * 64 * 9 : 1];
   const int l = threadIdx.x % (64 * WPR);
-  float dw[NV][V] = {};
+  float dw[NV][8] = {};
   const long long step = (long long)gridDim.x * RPW;
   // rows of one workgroup run in step (the barriers of row_total)
   for (long long first = blockIdx.x * (long long)RPW; first < a.R; first += step) {
     const long long row = first + threadIdx.x / (64 * WPR);
     const bool on = row < a.R;
     const size_t base = (size_t)(on ? row : 0) * a.C;
-    float h[NV][V], e[NV][V], s = 0.f, q = 0.f;
+    float h[NV][8], e[NV][8], s = 0.f, q = 0.f;
+    Raw<Tr, 8> g[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * 64 * WPR + l) * V;
+      const int c = (j * 64 * WPR + l) * 8;
 #pragma unroll
-      for (int i = 0; i < V; ++i) h[j][i] = e[j][i] = 0.f;
+      for (int i = 0; i < 8; ++i) h[j][i] = e[j][i] = 0.f;
+      g[j].zero();
       if (!on || c >= a.C) continue;
-      load_v<Tr, V>((const Tr*)a.h + base + c, h[j]);
-      load_v<Tin, V>((const Tin*)a.dy + base + c, e[j]);
+      load_v<ALN, 8>((const Tr*)a.h + base + c, a.C - c, h[j]);
+      load_v<ALN, 8>((const Tin*)a.dy + base + c, a.C - c, e[j]);
+      if (a.dh) g[j].template load<ALN>((const Tr*)a.dh + base + c, a.C - c);
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * 64 * WPR + l) * V;
+      const int c = (j * 64 * WPR + l) * 8;
       if (!on || c >= a.C) continue;
-      float w[V];
-      load_v<float, V>(a.weight + c, w);
+      float w[8];
+      load_v<ALN, 8>(a.weight + c, a.C - c, w);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
+      for (int i = 0; i < 8; ++i) {
         s += h[j][i] * h[j][i];
         q += h[j][i] * e[j][i] * w[i];
       }
@@ -315,107 +302,106 @@ __global__ __launch_bounds__(WPR == 16 ? 1024 : 256) void residual_norm_bwd_kern
     const float m = row_total<WPR>(q, red) / a.C * r * r * r;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * 64 * WPR + l) * V;
+      const int c = (j * 64 * WPR + l) * 8;
       if (!on || c >= a.C) continue;
-      float w[V], g[V] = {};
-      load_v<float, V>(a.weight + c, w);
-      if (a.dh) load_v<Tr, V>((const Tr*)a.dh + base + c, g);
-      float dx[V];
+      float w[8], gv[8];
+      load_v<ALN, 8>(a.weight + c, a.C - c, w);
+      g[j].widen(gv);
+      float dx[8];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
+      for (int i = 0; i < 8; ++i) {
         dw[j][i] += e[j][i] * h[j][i] * r;
-        g[i] += r * e[j][i] * w[i] - h[j][i] * m;
-        dx[i] = a.scale * g[i];
+        gv[i] += r * e[j][i] * w[i] - h[j][i] * m;
+        dx[i] = a.scale * gv[i];
       }
-      store_v<Tin, V>((Tin*)a.dx + base + c, dx);
-      if (a.dres) store_v<Tr, V>((Tr*)a.dres + base + c, g);
+      store_v<ALN, 8>((Tin*)a.dx + base + c, a.C - c, dx);
+      if (a.dres) store_v<ALN, 8>((Tr*)a.dres + base + c, a.C - c, gv);
     }
   }
-  // each row lane's partial is a row of the workspace (no two add to one)
-  float* part = (float*)a.ws +
-                ((size_t)blockIdx.x * RPW + threadIdx.x / (64 * WPR)) * a.C;
+  // the workgroup's rows added, one wave after the other: one partial each
+  if constexpr (RPW > 1) {
+    for (int r = RPW - 1; r >= 0; --r) {
+      if (wave_id() == r) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float* p = wred + (j * 64 + l) * 9 + i;
+            if (r < RPW - 1) dw[j][i] += *p;
+            if (r > 0) *p = dw[j][i];
+          }
+      }
+      __syncthreads();
+    }
+    if (wave_id() != 0) return;
+  }
+  float* part = (float*)a.ws + (size_t)blockIdx.x * a.C;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = (j * 64 * WPR + l) * V;
-    if (c >= a.C) continue;
-    store_v<float, V>(part + c, dw[j]);
+    const int c = (j * 64 * WPR + l) * 8;
+    if (c < a.C) store_v<ALN, 8>(part + c, a.C - c, dw[j]);
   }
 }
 
-int rows_per_wg(int wpr) { return (wpr == 16 ? 16 : 4) / wpr; }
-
-// (V, NV, WPR) for a width: the fewest waves a row that hold it in registers.
+// The fewest waves and vectors a row that hold a width in registers.
+constexpr int kMaxWidth = kResWaves * 64 * 8 * 8;  // 16384
 struct Shape {
-  int v, nv, wpr;
+  int nv, wpr;
 };
-bool row_shape(int C, bool aln, Shape* out) {
-  const int v = aln ? 8 : 1;
-  const int nvs[] = {1, 2, 4, 8, 16};
-  for (int wpr : {1, 4, 16})
-    for (int nv : nvs) {
-      if (v == 8 && nv > 8) continue;
-      if (v == 8 && wpr > 1 && nv < 4) continue;   // not instantiated
-      if (v == 1 && nv < (wpr > 1 ? 16 : 4)) continue;
-      if ((long long)64 * wpr * nv * v >= C) {
-        *out = Shape{v, nv, wpr};
-        return true;
-      }
-    }
-  return false;
+Shape row_shape(int C) {
+  for (int nv = 1; nv <= 8; nv *= 2)
+    if (64 * 8 * nv >= C) return Shape{nv, 1};
+  return Shape{64 * 8 * kResWaves * 4 >= C ? 4 : 8, kResWaves};
 }
 
-constexpr int kMaxWidth = 16384;
-
+// Workgroups of the backward, each a partial row of the weight gradient: two
+// a CU (more partials cost more than the occupancy gives).
 int res_blocks(long long R, int wpr) {
-  const int rpw = rows_per_wg(wpr);
-  const long long need = (R + rpw - 1) / rpw, most = wpr == 16 ? 512 : 1024;
-  return (int)(need < most ? need : most);
+  const int rpw = kResWaves / wpr;
+  const long long need = (R + rpw - 1) / rpw;
+  return (int)(need < 512 ? need : 512);
 }
 
-template <typename Tin, typename Tr, int V, int NV, int WPR>
+template <typename Tin, typename Tr, bool ALN, int NV, int WPR>
 int run_res(const ResidualNormArgs& a, int bwd, hipStream_t s) {
-  const dim3 block(WPR == 16 ? 1024 : 256);
   if (!bwd) {
-    const int rpw = rows_per_wg(WPR);
+    const int rpw = kResWaves / WPR;
     const int tk = ktimer_before(s, "residual_norm");
-    hipLaunchKernelGGL((residual_norm_kernel<Tin, Tr, V, NV, WPR>),
-                       dim3((unsigned)((a.R + rpw - 1) / rpw)), block, 0, s, a);
+    hipLaunchKernelGGL((residual_norm_kernel<Tin, Tr, ALN, NV, WPR>),
+                       dim3((unsigned)((a.R + rpw - 1) / rpw)), dim3(kResThreads), 0, s, a);
     ktimer_after(s, tk);
     return (int)hipGetLastError();
   }
   const int nb = res_blocks(a.R, WPR);
   if (nb) {
     const int tk = ktimer_before(s, "residual_norm_bwd");
-    hipLaunchKernelGGL((residual_norm_bwd_kernel<Tin, Tr, V, NV, WPR>), dim3(nb), block, 0, s,
-                       a);
+    hipLaunchKernelGGL((residual_norm_bwd_kernel<Tin, Tr, ALN, NV, WPR>), dim3(nb),
+                       dim3(kResThreads), 0, s, a);
     ktimer_after(s, tk);
     const int rc = (int)hipGetLastError();
     if (rc) return rc;
   }
-  return launch_column_sum((const float*)a.ws, nb * rows_per_wg(WPR), a.C, a.C, 1, a.dweight,
-                           nullptr, nullptr, s);
+  return launch_column_sum((const float*)a.ws, nb, a.C, a.C, 1, a.dweight, nullptr, nullptr, s);
+}
+
+template <typename Tin, typename Tr, bool ALN>
+int run_res_n(const ResidualNormArgs& a, int bwd, hipStream_t s) {
+  const Shape p = row_shape(a.C);
+  if (p.wpr == 1) {
+    switch (p.nv) {
+      case 1: return run_res<Tin, Tr, ALN, 1, 1>(a, bwd, s);
+      case 2: return run_res<Tin, Tr, ALN, 2, 1>(a, bwd, s);
+      case 4: return run_res<Tin, Tr, ALN, 4, 1>(a, bwd, s);
+      case 8: return run_res<Tin, Tr, ALN, 8, 1>(a, bwd, s);
+    }
+  }
+  return p.nv == 4 ? run_res<Tin, Tr, ALN, 4, kResWaves>(a, bwd, s)
+                   : run_res<Tin, Tr, ALN, 8, kResWaves>(a, bwd, s);
 }
 
 template <typename Tin, typename Tr>
 int run_res_t(const ResidualNormArgs& a, bool aln, int bwd, hipStream_t s) {
-  Shape p;
-  if (!row_shape(a.C, aln, &p)) return -1;
-#define OSDN_RES(V, NV, WPR)                     \
-  if (p.v == V && p.nv == NV && p.wpr == WPR)    \
-    return run_res<Tin, Tr, V, NV, WPR>(a, bwd, s);
-  OSDN_RES(8, 1, 1)
-  OSDN_RES(8, 2, 1)
-  OSDN_RES(8, 4, 1)
-  OSDN_RES(8, 8, 1)
-  OSDN_RES(8, 4, 4)
-  OSDN_RES(8, 8, 4)
-  OSDN_RES(1, 4, 1)
-  OSDN_RES(1, 8, 1)
-  OSDN_RES(1, 16, 1)
-  OSDN_RES(1, 16, 4)
-  OSDN_RES(1, 16, 16)
-#undef OSDN_RES
-  return -1;
+  return aln ? run_res_n<Tin, Tr, true>(a, bwd, s) : run_res_n<Tin, Tr, false>(a, bwd, s);
 }
 
 int run_res_any(const ResidualNormArgs& a, bool aln, int bwd, hipStream_t s) {
@@ -450,15 +436,7 @@ int launch_residual_norm(const ResidualNormArgs& a, hipStream_t s) {
 
 size_t residual_norm_backward_ws(long long R, int C) {
   if (C > kMaxWidth) return 0;
-  // either access width may be taken: room for the larger number of partials
-  size_t n = 0;
-  for (bool aln : {true, false}) {
-    Shape p;
-    if (!row_shape(C, aln, &p)) continue;
-    const size_t k = (size_t)res_blocks(R, p.wpr) * rows_per_wg(p.wpr);
-    n = k > n ? k : n;
-  }
-  return n * C * sizeof(float);
+  return (size_t)res_blocks(R, row_shape(C).wpr) * C * sizeof(float);
 }
 
 int launch_residual_norm_backward(const ResidualNormArgs& a, hipStream_t s) {

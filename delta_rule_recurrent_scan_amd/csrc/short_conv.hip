@@ -30,11 +30,10 @@
 namespace osdn {
 namespace {
 
-// Tokens a thread fetches before it works on them: 8 rows of 16 bytes in
-// flight a lane.
-constexpr int kBatch = 8;
+// Channels of a thread and tokens it fetches ahead.
+constexpr int kFwdV = 8, kFwdBatch = 8, kBwdV = 4, kBwdBatch = 4;
 
-template <typename T>
+template <typename T, int V>
 struct ConvIn {
   const T* x;
   long long xts;
@@ -42,23 +41,23 @@ struct ConvIn {
   int C, W, c, nv;
   // row t of the inputs, t < 0 reading the state before them
   template <bool ALN>
-  __device__ __forceinline__ void row(int t, float (&v)[8]) const {
+  __device__ __forceinline__ void row(int t, float (&v)[V]) const {
     if (t >= 0) {
-      load8<ALN>(x + t * xts + c, nv, v);
+      load_v<ALN, V>(x + t * xts + c, nv, v);
     } else if (st) {
-      load8<ALN>(st + (size_t)(W - 1 + t) * C + c, nv, v);
+      load_v<ALN, V>(st + (size_t)(W - 1 + t) * C + c, nv, v);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+      for (int i = 0; i < V; ++i) v[i] = 0.f;
     }
   }
 };
 
-template <int W>
+template <int W, int V>
 __device__ __forceinline__ void load_weights(const float* weight, const float* bias, int c,
-                                             int nv, float (&w)[W][8], float (&bi)[8]) {
+                                             int nv, float (&w)[W][V], float (&bi)[V]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < V; ++i) {
     const bool ok = i < nv;
     bi[i] = ok && bias ? bias[c + i] : 0.f;
 #pragma unroll
@@ -66,121 +65,134 @@ __device__ __forceinline__ void load_weights(const float* weight, const float* b
   }
 }
 
-template <typename T, bool ALN>
-__device__ __forceinline__ void store_heads(T* y, long long bh0, int Tn, int D, int t, int c,
-                                            int nv, const float (&v)[8]) {
-  if constexpr (ALN) {
-    store8<true>(y + ((bh0 + c / D) * Tn + t) * (long long)D + c % D, 8, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < nv)
-        y[((bh0 + (c + i) / D) * Tn + t) * (long long)D + (c + i) % D] = from_f32<T>(v[i]);
+// A thread's channels in the heads [B,H,T,D]: one pointer that advances by D a
+// token where its channels lie in one head, else an address an element.
+template <typename T, int V, bool ALN>
+struct Heads {
+  T* p;  // channel c of token 0 (ALN)
+  T* y;
+  long long bh0;
+  int Tn, D, c, nv;
+  __device__ __forceinline__ Heads(T* base, long long bh, int T_, int D_, int c_, int nv_)
+      : y(base), bh0(bh), Tn(T_), D(D_), c(c_), nv(nv_) {
+    p = base + (bh + c_ / D_) * T_ * (long long)D_ + c_ % D_;
   }
-}
-
-template <typename T, bool ALN>
-__device__ __forceinline__ void load_heads(const T* y, long long bh0, int Tn, int D, int t,
-                                           int c, int nv, float (&v)[8]) {
-  if constexpr (ALN) {
-    load8<true>(y + ((bh0 + c / D) * Tn + t) * (long long)D + c % D, 8, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      v[i] = i < nv ? to_f32(y[((bh0 + (c + i) / D) * Tn + t) * (long long)D + (c + i) % D])
-                    : 0.f;
+  __device__ __forceinline__ T* at(int t, int i) const {
+    return y + ((bh0 + (c + i) / D) * Tn + t) * (long long)D + (c + i) % D;
   }
-}
+  __device__ __forceinline__ void store(int t, const float (&v)[V]) const {
+    if constexpr (ALN) {
+      store_v<true, V>(p + t * (long long)D, V, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i < nv) *at(t, i) = from_f32<T>(v[i]);
+    }
+  }
+  __device__ __forceinline__ void load(int t, Raw<T, V>& r) const {
+    if constexpr (ALN) {
+      r.template load<true>(p + t * (long long)D, V);
+    } else {
+      float v[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = i < nv ? to_f32(*at(t, i)) : 0.f;
+      r.narrow(v);
+    }
+  }
+};
 
 template <typename Tin, int W, bool ALN>
 __global__ __launch_bounds__(kRowThreads) void conv_kernel(ConvArgs a, int cx, int seg,
                                                            int nseg) {
-  const int C = a.H * a.D, ng = (C + 7) / 8;
+  constexpr int V = kFwdV, NB = kFwdBatch;
+  const int C = a.H * a.D, ng = (C + V - 1) / V;
   const int ncb = (ng + cx - 1) / cx, cb = blockIdx.x % ncb, rb = blockIdx.x / ncb;
   const int cg = cb * cx + (threadIdx.x & (cx - 1));
   const long long by = rb * (long long)(kRowThreads / cx) + threadIdx.x / cx;
   const int sg = (int)(by % nseg);
   const long long b = by / nseg;
   if (cg >= ng || b >= a.B) return;  // a head's lanes leave together
-  const int c = cg * 8, nv = C - c;
+  const int c = cg * V, nv = C - c;
   int n = a.lengths ? a.lengths[b] : a.T;
   n = n < 0 ? 0 : n > a.T ? a.T : n;
-  ConvIn<Tin> in{(const Tin*)a.x + b * a.xbs, a.xts,
-                 a.state0 ? (const Tin*)a.state0 + b * (W - 1) * C : nullptr, C, W, c, nv};
-  float w[W][8], bi[8];
-  load_weights<W>(a.weight, a.bias, c, nv, w, bi);
+  ConvIn<Tin, V> in{(const Tin*)a.x + b * a.xbs, a.xts,
+                    a.state0 ? (const Tin*)a.state0 + b * (W - 1) * C : nullptr, C, W, c, nv};
+  float w[W][V], bi[V];
+  load_weights<W, V>(a.weight, a.bias, c, nv, w, bi);
 
   const int t0 = sg * seg, t1 = min(t0 + seg, a.T), tn = min(t1, n);
-  const int L = a.D / 8;  // lanes of a head (l2 only)
-  Tin* y = (Tin*)a.y;
-  float h[W][8];  // h[k] = input t - W + 1 + k
+  const int L = a.D / V;  // lanes of a head (l2 only)
+  const Heads<Tin, V, ALN> y((Tin*)a.y, b * a.H, a.T, a.D, c, nv);
+  // h[0 .. W - 2]: the inputs before the batch; h[W - 1 + j]: the batch's
+  float h[W - 1 + NB][V];
 #pragma unroll
-  for (int k = 0; k < W - 1; ++k) in.template row<ALN>(t0 - (W - 1) + k, h[k + 1]);
-  auto token = [&](int t) {
-    float u[8];
+  for (int k = 0; k < W - 1; ++k) in.template row<ALN>(t0 - (W - 1) + k, h[k]);
+  auto token = [&](int t, int j) {
+    float u[V];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < V; ++i) {
       u[i] = bi[i];
 #pragma unroll
-      for (int k = 0; k < W; ++k) u[i] += w[k][i] * h[k][i];
+      for (int k = 0; k < W; ++k) u[i] += w[k][i] * h[j + k][i];
     }
     if (a.act) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] *= sigmoid_f(u[i]);
+      for (int i = 0; i < V; ++i) u[i] *= sigmoid_f(u[i]);
     }
     if (a.l2) {
       float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += u[i] * u[i];
+      for (int i = 0; i < V; ++i) s += u[i] * u[i];
       const float r = rsqrtf(head_sum(s, L) + a.eps);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] *= r;
+      for (int i = 0; i < V; ++i) u[i] *= r;
     }
-    store_heads<Tin, ALN>(y, b * a.H, a.T, a.D, t, c, nv, u);
+    y.store(t, u);
   };
   int t = t0;
-  for (; t + kBatch <= tn; t += kBatch) {
-    float f[kBatch][8];
+  const Tin* xp = in.x + t0 * in.xts + c;
+  for (; t + NB <= tn; t += NB) {
+    Raw<Tin, V> f[NB];
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) in.template row<ALN>(t + j, f[j]);
+    for (int j = 0; j < NB; ++j, xp += in.xts) f[j].template load<ALN>(xp, nv);
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-#pragma unroll
-        for (int k = 0; k < W - 1; ++k) h[k][i] = h[k + 1][i];
-        h[W - 1][i] = f[j][i];
-      }
-      token(t + j);
+    for (int j = 0; j < NB; ++j) {
+      f[j].widen(h[W - 1 + j]);
+      token(t + j, j);
     }
-  }
-  for (; t < tn; ++t) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int k = 0; k < W - 1; ++k)
 #pragma unroll
-      for (int k = 0; k < W - 1; ++k) h[k][i] = h[k + 1][i];
-    in.template row<ALN>(t, h[W - 1]);
-    token(t);
+      for (int i = 0; i < V; ++i) h[k][i] = h[NB + k][i];
   }
-  const float zero[8] = {};
-  for (; t < t1; ++t) store_heads<Tin, ALN>(y, b * a.H, a.T, a.D, t, c, nv, zero);
+  for (; t < tn; ++t, xp += in.xts) {
+    load_v<ALN, V>(xp, nv, h[W - 1]);
+    token(t, 0);
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) h[k][i] = h[k + 1][i];
+  }
+  const float zero[V] = {};
+  for (; t < t1; ++t) y.store(t, zero);
 
   if (sg == 0 && a.stateT) {
     // all rows read before any is written: state_T may be state0
-    float f[W][8];
+    float f[W][V];
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) in.template row<ALN>(n - (W - 1) + k, f[k]);
     Tin* st = (Tin*)a.stateT + b * (W - 1) * C + c;
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) store8<ALN>(st + (size_t)k * C, nv, f[k]);
+    for (int k = 0; k < W - 1; ++k) store_v<ALN, V>(st + (size_t)k * C, nv, f[k]);
   }
 }
 
 template <typename Tin, typename Tdy, int W, bool ALN>
 __global__ __launch_bounds__(kRowThreads) void conv_bwd_kernel(ConvBackwardArgs p, int cx,
                                                                int seg, int nseg) {
+  constexpr int V = kBwdV, NB = kBwdBatch;
   const ConvArgs& a = p.f;
-  const int C = a.H * a.D, ng = (C + 7) / 8;
+  const int C = a.H * a.D, ng = (C + V - 1) / V;
   const int lx = threadIdx.x & (cx - 1), ly = threadIdx.x / cx;
   const int ncb = (ng + cx - 1) / cx, cb = blockIdx.x % ncb, rb = blockIdx.x / ncb;
   const int cg = cb * cx + lx;
@@ -188,179 +200,198 @@ __global__ __launch_bounds__(kRowThreads) void conv_bwd_kernel(ConvBackwardArgs 
   const int sg = (int)(by % nseg);
   const long long b = by / nseg;
   const bool on = cg < ng && b < a.B;
-  const int c = cg * 8, nv = C - c;
-  float dw[W + 1][8] = {};  // weight gradients, then the bias'
+  const int c = cg * V, nv = C - c;
+  float dw[W + 1][V] = {};  // weight gradients, then the bias'
   if (on) {
     int n = a.lengths ? a.lengths[b] : a.T;
     n = n < 0 ? 0 : n > a.T ? a.T : n;
-    ConvIn<Tin> in{(const Tin*)a.x + b * a.xbs, a.xts,
-                   a.state0 ? (const Tin*)a.state0 + b * (W - 1) * C : nullptr, C, W, c, nv};
-    float w[W][8], bi[8];
-    load_weights<W>(a.weight, a.bias, c, nv, w, bi);
-    const int L = a.D / 8;
+    ConvIn<Tin, V> in{(const Tin*)a.x + b * a.xbs, a.xts,
+                      a.state0 ? (const Tin*)a.state0 + b * (W - 1) * C : nullptr, C, W, c, nv};
+    float w[W][V], bi[V];
+    load_weights<W, V>(a.weight, a.bias, c, nv, w, bi);
+    const int L = a.D / V;
     // rows [r0, r1) of the T + W - 1 of the inputs with their state
     const int rows = a.T + W - 1;
     const int r0 = sg * seg, r1 = min(r0 + seg, rows);
     const Tin* dst = p.dstateT ? (const Tin*)p.dstateT + b * (W - 1) * C + c : nullptr;
-    float h[W][8], acc[W][8] = {};
+    const Heads<Tdy, V, ALN> dyh((Tdy*)const_cast<void*>(p.dy), b * a.H, a.T, a.D, c, nv);
+    Tin* dx = (Tin*)p.dx + (b * a.T - (W - 1)) * (long long)C + c;  // row t of them
+    // h[0 .. W - 2]: the inputs before the batch; acc[k]: open row t + k
+    float h[W - 1 + NB][V], acc[W][V] = {};
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
       const int t = r0 - 2 * (W - 1) + k;
       if (t >= -(W - 1) && t < n) {
-        in.template row<ALN>(t, h[k + 1]);
+        in.template row<ALN>(t, h[k]);
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[k + 1][i] = 0.f;
+        for (int i = 0; i < V; ++i) h[k][i] = 0.f;
       }
     }
-    // du_t enters rows t .. t + W - 1 (acc[k] = row t + k); row t is then whole
-    auto token = [&](int t, const float (&xt)[8], const float (&dy)[8]) {
+    // du_t of a token inside the sequence enters rows t .. t + W - 1
+    auto inside = [&](int j, const float (&dy)[V], bool mine) {
+      float u[V], d[V], sl[V];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < V; ++i) {
+        u[i] = bi[i];
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k) h[k][i] = h[k + 1][i];
-        h[W - 1][i] = xt[i];
+        for (int k = 0; k < W; ++k) u[i] += w[k][i] * h[j + k][i];
+        d[i] = dy[i];
+        sl[i] = 1.f;
+      }
+      if (a.act) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float sgm = sigmoid_f(u[i]);
+          sl[i] = sgm * (1.f + u[i] * (1.f - sgm));
+          u[i] *= sgm;
+        }
+      }
+      if (a.l2) {
+        float s = 0.f, q = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          s += u[i] * u[i];
+          q += u[i] * d[i];
+        }
+        const float r = rsqrtf(head_sum(s, L) + a.eps);
+        q = head_sum(q, L) * r * r;
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] = r * (d[i] - u[i] * q);
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        d[i] *= sl[i];
+#pragma unroll
+        for (int k = 0; k < W; ++k) acc[k][i] += w[k][i] * d[i];
+        if (mine) {  // earlier tokens: a predecessor's sums
+#pragma unroll
+          for (int k = 0; k < W; ++k) dw[k][i] += d[i] * h[j + k][i];
+          dw[W][i] += d[i];
+        }
+      }
+    };
+    auto close = [&]() {  // row t leaves the open ones
+#pragma unroll
+      for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[k][i] = acc[k + 1][i];
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[W - 1][i] = 0.f;
+    };
+    // one token anywhere: before the sequence, in it or behind it
+    auto any = [&](int t) {
+      float dy[V];
+      if (t >= -(W - 1) && t < n) {
+        in.template row<ALN>(t, h[W - 1]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) h[W - 1][i] = 0.f;
       }
       if (t >= 0 && t < n) {
-        float u[8], d[8], sl[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          u[i] = bi[i];
-#pragma unroll
-          for (int k = 0; k < W; ++k) u[i] += w[k][i] * h[k][i];
-          d[i] = dy[i];
-          sl[i] = 1.f;
-        }
-        if (a.act) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float sgm = sigmoid_f(u[i]);
-            sl[i] = sgm * (1.f + u[i] * (1.f - sgm));
-            u[i] *= sgm;
-          }
-        }
-        if (a.l2) {
-          float s = 0.f, q = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            s += u[i] * u[i];
-            q += u[i] * d[i];
-          }
-          const float r = rsqrtf(head_sum(s, L) + a.eps);
-          q = head_sum(q, L) * r * r;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) d[i] = r * (d[i] - u[i] * q);
-        }
-        const bool mine = t >= r0;  // earlier tokens: a predecessor's sums
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          d[i] *= sl[i];
-          const float dm = mine ? d[i] : 0.f;
-#pragma unroll
-          for (int k = 0; k < W; ++k) {
-            acc[k][i] += w[k][i] * d[i];
-            dw[k][i] += dm * h[k][i];
-          }
-          dw[W][i] += dm;
-        }
+        Raw<Tdy, V> r;
+        dyh.load(t, r);
+        r.widen(dy);
+        inside(0, dy, t >= r0);
       }
       if (t >= r0) {
         if (dst && t >= n && t < n + W - 1) {
-          float f[8];
-          load8<ALN>(dst + (size_t)(t - n) * C, nv, f);
+          float f[V];
+          load_v<ALN, V>(dst + (size_t)(t - n) * C, nv, f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) acc[0][i] += f[i];
+          for (int i = 0; i < V; ++i) acc[0][i] += f[i];
         }
         if (t >= W - 1) {
-          store8<ALN>((Tin*)p.dx + (b * a.T + (t - (W - 1))) * (long long)C + c, nv, acc[0]);
+          store_v<ALN, V>(dx + t * (long long)C, nv, acc[0]);
         } else if (p.dstate0) {
-          store8<ALN>((Tin*)p.dstate0 + (b * (W - 1) + t) * (long long)C + c, nv, acc[0]);
+          store_v<ALN, V>((Tin*)p.dstate0 + (b * (W - 1) + t) * (long long)C + c, nv, acc[0]);
         }
       }
+      close();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int k = 0; k < W - 1; ++k)
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k) acc[k][i] = acc[k + 1][i];
-        acc[W - 1][i] = 0.f;
-      }
+        for (int i = 0; i < V; ++i) h[k][i] = h[k + 1][i];
     };
-    auto fetch = [&](int t, float (&xt)[8], float (&dy)[8]) {
-      if (t >= -(W - 1) && t < n) {
-        in.template row<ALN>(t, xt);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) xt[i] = 0.f;
-      }
-      if (t >= 0 && t < n) {
-        load_heads<Tdy, ALN>((const Tdy*)p.dy, b * a.H, a.T, a.D, t, c, nv, dy);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dy[i] = 0.f;
-      }
-    };
-    constexpr int kB = 4;
     int t = r0 - (W - 1);
-    for (; t + kB <= r1; t += kB) {
-      float xt[kB][8], dy[kB][8];
+    for (; t < max(r0, W - 1) && t < r1; ++t) any(t);
+    // whole batches inside the sequence, every row an output row
+    const Tin* xp = in.x + t * in.xts + c;
+    for (; t + NB <= min(r1, n); t += NB) {
+      Raw<Tin, V> f[NB];
+      Raw<Tdy, V> e[NB];
 #pragma unroll
-      for (int j = 0; j < kB; ++j) fetch(t + j, xt[j], dy[j]);
+      for (int j = 0; j < NB; ++j, xp += in.xts) {
+        f[j].template load<ALN>(xp, nv);
+        dyh.load(t + j, e[j]);
+      }
 #pragma unroll
-      for (int j = 0; j < kB; ++j) token(t + j, xt[j], dy[j]);
+      for (int j = 0; j < NB; ++j) {
+        float dy[V];
+        f[j].widen(h[W - 1 + j]);
+        e[j].widen(dy);
+        inside(j, dy, true);
+        store_v<ALN, V>(dx + (t + j) * (long long)C, nv, acc[0]);
+        close();
+      }
+#pragma unroll
+      for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i) h[k][i] = h[NB + k][i];
     }
-    for (; t < r1; ++t) {
-      float xt[8], dy[8];
-      fetch(t, xt, dy);
-      token(t, xt, dy);
-    }
+    for (; t < r1; ++t) any(t);
   }
   // the workgroup's segments added: one partial row [W + 1][C] a workgroup
-  __shared__ float red[kRowThreads * 9];  // 9: adjacent threads on other banks
+  __shared__ float red[kRowThreads * (V + 1)];  // V + 1: adjacent threads on other banks
   float* part = (float*)p.ws + (size_t)rb * (W + 1) * C;
 #pragma unroll
   for (int k = 0; k <= W; ++k) {
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) red[threadIdx.x * 9 + i] = dw[k][i];
+    for (int i = 0; i < V; ++i) red[threadIdx.x * (V + 1) + i] = dw[k][i];
     __syncthreads();
-    for (int e = threadIdx.x; e < cx * 8; e += kRowThreads) {
-      const int col = (cb * cx + e / 8) * 8 + e % 8;
+    for (int e = threadIdx.x; e < cx * V; e += kRowThreads) {
+      const int col = (cb * cx + e / V) * V + e % V;
       if (col >= C) continue;
       float s = 0.f;
-      for (int r = 0; r < kRowThreads / cx; ++r) s += red[(r * cx + e / 8) * 9 + e % 8];
+      for (int r = 0; r < kRowThreads / cx; ++r) s += red[(r * cx + e / V) * (V + 1) + e % V];
       part[(size_t)k * C + col] = s;
     }
   }
 }
 
-__global__ __launch_bounds__(256) void column_sum_kernel(const float* __restrict__ in, int rows,
-                                                         int cols, int c, int w, float* out0,
-                                                         float* out1, float* out2) {
-  // 32 columns x 8 row lanes; each adds every 8th row, then LDS
-  __shared__ float red[8][33];
+// 32 columns and 32 row lanes a workgroup; a lane adds every 32nd row, eight
+// in flight, then the lanes are added in LDS.
+__global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restrict__ in, int rows,
+                                                          int cols, int c, int w, float* out0,
+                                                          float* out1, float* out2) {
+  __shared__ float red[32][33];
   const int x = threadIdx.x & 31, r0 = threadIdx.x >> 5;
   const int j = blockIdx.x * 32 + x;
-  float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+  float s[8] = {};
   if (j < cols) {
+    const float* p = in + j;
     int r = r0;
-    for (; r + 24 < rows; r += 32) {
-      s0 += in[(size_t)r * cols + j];
-      s1 += in[(size_t)(r + 8) * cols + j];
-      s2 += in[(size_t)(r + 16) * cols + j];
-      s3 += in[(size_t)(r + 24) * cols + j];
-    }
-    for (; r < rows; r += 8) s0 += in[(size_t)r * cols + j];
-  }
-  red[r0][x] = (s0 + s1) + (s2 + s3);
-  __syncthreads();
-  if (r0 == 0 && j < cols) {
-    float s = 0.f;
+    for (; r + 7 * 32 < rows; r += 8 * 32)
 #pragma unroll
-    for (int r = 0; r < 8; ++r) s += red[r][x];
+      for (int i = 0; i < 8; ++i) s[i] += p[(size_t)(r + 32 * i) * cols];
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (r + 32 * i < rows) s[i] += p[(size_t)(r + 32 * i) * cols];
+  }
+  red[r0][x] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+  __syncthreads();
+#pragma unroll
+  for (int m = 16; m > 0; m /= 2) {
+    if (r0 < m) red[r0][x] += red[r0 + m][x];
+    __syncthreads();
+  }
+  if (r0 == 0 && j < cols) {
     const int k = j / c, ch = j % c;
     if (k < w) {
-      out0[(size_t)ch * w + k] = s;
+      out0[(size_t)ch * w + k] = red[0][x];
     } else if (float* o = k == w ? out1 : out2) {
-      o[ch] = s;
+      o[ch] = red[0][x];
     }
   }
 }
@@ -376,7 +407,7 @@ int pick_seg(double per, int T, int least, int most) {
 
 template <typename Tin, int W>
 int run_conv(const ConvArgs& a, hipStream_t s) {
-  const int C = a.H * a.D, ng = (C + 7) / 8, cx = row_cx(ng);
+  const int C = a.H * a.D, ng = (C + kFwdV - 1) / kFwdV, cx = row_cx(ng);
   const int seg = a.whole ? (a.T > 0 ? a.T : 1)
                           : pick_seg((double)a.B * a.T * ng, a.T, 8, 32);
   const int nseg = a.T > 0 ? (a.T + seg - 1) / seg : 1;
@@ -406,7 +437,7 @@ struct BwdGrid {
 };
 BwdGrid bwd_grid(int B, int T, int C, int W) {
   BwdGrid g;
-  g.cx = row_cx((C + 7) / 8);
+  g.cx = row_cx((C + kBwdV - 1) / kBwdV);
   g.nseg = (T + W - 1 + kConvBwdSeg - 1) / kConvBwdSeg;
   g.per = kRowThreads / g.cx;
   g.parts = (int)(((long long)B * g.nseg + g.per - 1) / g.per);
@@ -416,7 +447,7 @@ BwdGrid bwd_grid(int B, int T, int C, int W) {
 template <typename Tin, typename Tdy, int W>
 int run_conv_bwd(const ConvBackwardArgs& p, hipStream_t s) {
   const ConvArgs& a = p.f;
-  const int C = a.H * a.D, ng = (C + 7) / 8;
+  const int C = a.H * a.D, ng = (C + kBwdV - 1) / kBwdV;
   const BwdGrid g = bwd_grid(a.B, a.T, C, W);
   const dim3 grid((unsigned)((ng + g.cx - 1) / g.cx * g.parts));
   const size_t m = 16 - 1, es = sizeof(Tin);
@@ -466,7 +497,7 @@ int run_conv_bwd_w(const ConvBackwardArgs& a, hipStream_t s) {
 int launch_column_sum(const float* in, int rows, int cols, int c, int w, float* out0,
                       float* out1, float* out2, hipStream_t s) {
   const int tk = ktimer_before(s, "column_sum");
-  hipLaunchKernelGGL(column_sum_kernel, dim3((cols + 31) / 32), dim3(256), 0, s, in, rows, cols,
+  hipLaunchKernelGGL(column_sum_kernel, dim3((cols + 31) / 32), dim3(1024), 0, s, in, rows, cols,
                      c, w, out0, out1, out2);
   ktimer_after(s, tk);
   return (int)hipGetLastError();

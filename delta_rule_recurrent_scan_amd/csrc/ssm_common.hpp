@@ -176,17 +176,6 @@ __device__ __forceinline__ void mma_upto(f32x4& acc, const Frag<KEXT, float>& a,
     if (4 * i < kmax) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[i], b.v[i], acc, 0, 0, 0);
 }
 
-// Two values rounded to bf16 by one packed conversion, and back.
-__device__ __forceinline__ unsigned pack_bf16(float x, float y) {
-  typedef __attribute__((ext_vector_type(2))) float f32x2;
-  typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
-  return __builtin_bit_cast(unsigned, __builtin_convertvector((f32x2{x, y}), bf16x2));
-}
-__device__ __forceinline__ float low_bf16(unsigned u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float high_bf16(unsigned u) {
-  return __uint_as_float(u & 0xffff0000u);
-}
-
 // A fragment (row = lane % 16) in permuted k order from the accumulator tiles
 // of that k range.
 template <int KEXT>

