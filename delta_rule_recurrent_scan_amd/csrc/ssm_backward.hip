@@ -58,55 +58,54 @@ __device__ __forceinline__ void state_elem(int e, int ntl, int& p, int& n) {
 // BH .. 2 BH - 1 in reverse (dy, C, weights L_i0, from dS_T). Segment k counts
 // along the direction.
 // ---------------------------------------------------------------------------
-// Rows p of the state a workgroup walks: 16 a wave.
 template <int P>
-constexpr int walk_rows() { return P < 64 ? P : 64; }
+constexpr int walk_waves() { return P / 16 < 4 ? P / 16 : 4; }
 
 template <int P, int N, typename Tin, bool WRITE>
-__global__ __launch_bounds__(4 * walk_rows<P>(), 3) void ssm_walk_kernel(
-    SsmArgs a, int nseg, int segch, float* slots, float* slot_log, float* states) {
-  constexpr int Q = bwd_q<Tin>(), SP = walk_rows<P>(), NW = SP / 16, NT = 64 * NW;
+__global__ __launch_bounds__(64 * walk_waves<P>(), 2) void ssm_walk_kernel(
+    SsmArgs a, int nseg, int segch, const ChunkDecay<bwd_q<Tin>()>* decay, float* slots,
+    float* slot_log, float* states) {
+  constexpr int Q = bwd_q<Tin>(), NW = walk_waves<P>(), NT = 64 * NW, PT = P / 16 / NW;
   constexpr int NTL = N / 16;
-  constexpr int LN = N + 16 / sizeof(Tin), LP = SP + 16 / sizeof(Tin);
+  constexpr int LN = N + 16 / sizeof(Tin), LP = P + 16 / sizeof(Tin);
   __shared__ __attribute__((aligned(16))) Tin Ks[Q * LN];
   __shared__ __attribute__((aligned(16))) Tin Vs[Q * LP];
-  __shared__ __attribute__((aligned(16))) ChunkDecay<Q> decs[2];
+  __shared__ __attribute__((aligned(16))) ChunkDecay<Q> dec;
 
   const int lane = threadIdx.x & 63, w = wave_id();
   const int BH = a.B * a.H, nwg = WRITE ? nseg : nseg - 1;
-  const int ps = blockIdx.x % (P / SP), id = blockIdx.x / (P / SP);
-  const int stream = id / nwg, k = id % nwg;
+  const int stream = blockIdx.x / nwg, k = blockIdx.x % nwg;
   const bool rev = stream >= BH;
   const int bh = rev ? stream - BH : stream;
   const int b = bh / a.H, h = bh % a.H, sg = rev ? nseg - 1 - k : k;
   const int n = ssm_length(a.lengths, b, a.T), nch = (a.T + Q - 1) / Q;
-  const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f;
   const size_t th = (size_t)bh * a.T;
   const size_t tg = ((size_t)b * a.G + h / (a.H / a.G)) * a.T;
-  const Tin* val = (const Tin*)(rev ? a.dy : a.x) + th * P + ps * SP;
+  const Tin* val = (const Tin*)(rev ? a.dy : a.x) + th * P;
   const Tin* key = (const Tin*)(rev ? a.Cm : a.Bm) + tg * N;
-  const float* dt = a.dt + th;
 
-  // S[nt]: rows p = 4 (l / 16) + e of the wave's p tile, column n = l % 16
-  f32x4 S[NTL];
+  // S[pt][nt]: rows p = 4 (l / 16) + e of the wave's p tile, column n = l % 16
+  f32x4 S[PT][NTL];
   const float* from = rev ? a.dST : a.S0;
-  const int tile0 = (ps * NW + w) * NTL;
+  const int tile0 = w * PT * NTL;  // S[0][0] to S[PT - 1][NTL - 1] follow
 #pragma unroll
-  for (int nt = 0; nt < NTL; ++nt) {
-    const int at = ((tile0 + nt) * 64 + lane) * 4;
-    if (!WRITE || (k == 0 && !from)) {
-      S[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    } else if (k > 0) {
-      S[nt] = load4(slots + ((size_t)stream * (nseg - 1) + k - 1) * P * N + at);
-    } else {
+  for (int pt = 0; pt < PT; ++pt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        int p, c;
-        state_elem(at + e, NTL, p, c);
-        S[nt][e] = from[((size_t)bh * P + p) * N + c];
+    for (int nt = 0; nt < NTL; ++nt) {
+      const int at = ((tile0 + pt * NTL + nt) * 64 + lane) * 4;
+      if (!WRITE || (k == 0 && !from)) {
+        S[pt][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+      } else if (k > 0) {
+        S[pt][nt] = load4(slots + ((size_t)stream * (nseg - 1) + k - 1) * P * N + at);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          int p, c;
+          state_elem(at + e, NTL, p, c);
+          S[pt][nt][e] = from[((size_t)bh * P + p) * N + c];
+        }
       }
     }
-  }
   float logsum = 0.f;
 
   const int c0 = sg * segch, c1 = min(c0 + segch, nch);
@@ -114,77 +113,71 @@ __global__ __launch_bounds__(4 * walk_rows<P>(), 3) void ssm_walk_kernel(
   const int count = max(cn - c0, 0);
   auto chunk = [&](int i) { return rev ? cn - 1 - i : c0 + i; };
   Stage<Q, N, Tin, NT, LN> fk;
-  Stage<Q, SP, Tin, NT, LP, P> fv;
+  Stage<Q, P, Tin, NT, LP> fv;
+  StageDecay<Q, NT> fd;
   auto fetch = [&](int i) {
     const int t = chunk(i) * Q, valid = n - t;
     fk.fetch(key + (size_t)t * N, valid);
     fv.fetch(val + (size_t)t * P, valid);
+    fd.fetch(decay + (size_t)bh * nch + chunk(i));
   };
-  // decays a chunk ahead, by wave 0, from steps fetched another chunk earlier
-  auto steps = [&](int i) {
-    const int t = i < count ? chunk(i) * Q : n;
-    return w == 0 ? buffer_load_f32(make_buffer(dt + t, (n - t) * 4ll), lane * 4) : 0.f;
-  };
-  auto fill = [&](ChunkDecay<Q>& d, int i, float raw) {
-    float sl = 0.f, st = 0.f;
-    if (lane < Q && chunk(i) * Q + lane < n) st = ssm_step(raw, bias, a.softplus, sl);
-    d.fill(st, st * A, sl);
-  };
-  float raw = 0.f;
-  if (count) {
-    fetch(0);
-    raw = steps(0);
-    if (w == 0) fill(decs[0], 0, raw);
-    raw = steps(1);
-  }
+  if (count) fetch(0);
   for (int i = 0; i < count; ++i) {
-    const ChunkDecay<Q>& dec = decs[i & 1];
     __syncthreads();
     fk.put(Ks);
     fv.put(Vs);
+    fd.put(dec);
     if (i + 1 < count) fetch(i + 1);
     if constexpr (WRITE) {
       float* out = states + ((size_t)stream * nch + chunk(i)) * P * N;
 #pragma unroll
-      for (int nt = 0; nt < NTL; ++nt) store4(out + (tile0 + nt) * 256 + (unsigned)(lane * 4), S[nt]);
+      for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+        for (int nt = 0; nt < NTL; ++nt)
+          store4(out + (tile0 + pt * NTL + nt) * 256 + (unsigned)(lane * 4), S[pt][nt]);
     }
     __syncthreads();
     const float total = dec.total;
     logsum += dec.logtot;
-    Parts<Q, Tin> vw;
-    {
+    Parts<Q, Tin> vw[PT];
+#pragma unroll
+    for (int pt = 0; pt < PT; ++pt) {
       Frag<Q, Tin> vf;
-      vf.load_kmajor(Vs + w * 16, LP);
-      scale_parts<Q>(vf, rev ? dec.ent : dec.wx, vw);
+      vf.load_kmajor(Vs + (w * PT + pt) * 16, LP);
+      scale_parts<Q>(vf, rev ? dec.ent : dec.wx, vw[pt]);
     }
 #pragma unroll
     for (int nt = 0; nt < NTL; ++nt) {
       Frag<Q, Tin> kf;
       kf.load_kmajor(Ks + nt * 16, LN);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) S[nt][e] *= total;
-      mma_parts(S[nt], vw, kf);
-    }
-    if (w == 0 && i + 1 < count) {
-      fill(decs[(i + 1) & 1], i + 1, raw);
-      raw = steps(i + 2);
+      for (int pt = 0; pt < PT; ++pt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[pt][nt][e] *= total;
+        mma_parts(S[pt][nt], vw[pt], kf);
+      }
     }
   }
 
   if constexpr (!WRITE) {
     float* out = slots + ((size_t)stream * (nseg - 1) + k) * P * N;
 #pragma unroll
-    for (int nt = 0; nt < NTL; ++nt) store4(out + (tile0 + nt) * 256 + (unsigned)(lane * 4), S[nt]);
-    if (threadIdx.x == 0 && ps == 0) slot_log[(size_t)stream * (nseg - 1) + k] = logsum;
+    for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+      for (int nt = 0; nt < NTL; ++nt)
+        store4(out + ((tile0 + pt * NTL + nt) * 64 + lane) * 4, S[pt][nt]);
+    if (threadIdx.x == 0) slot_log[(size_t)stream * (nseg - 1) + k] = logsum;
   } else if (rev && k == nseg - 1 && a.dS0) {
 #pragma unroll
-    for (int nt = 0; nt < NTL; ++nt)
+    for (int pt = 0; pt < PT; ++pt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        int p, c;
-        state_elem(((tile0 + nt) * 64 + lane) * 4 + e, NTL, p, c);
-        a.dS0[((size_t)bh * P + p) * N + c] = S[nt][e];
-      }
+      for (int nt = 0; nt < NTL; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          int p, c;
+          state_elem(((tile0 + pt * NTL + nt) * 64 + lane) * 4 + e, NTL, p, c);
+          a.dS0[((size_t)bh * P + p) * N + c] = S[pt][nt][e];
+        }
   }
 }
 
@@ -227,7 +220,8 @@ struct ChunkOut {
 };
 
 template <int P, int N, typename Tin>
-__global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(SsmArgs a, ChunkOut o) {
+__global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
+    SsmArgs a, ChunkOut o, const ChunkDecay<bwd_q<Tin>()>* decay) {
   constexpr int Q = bwd_q<Tin>(), QT = Q / 16, NTL = N / 16, PTL = P / 16;
   constexpr int PAD = 16 / sizeof(Tin), LN = N + PAD, LP = P + PAD, LQ = Q + PAD;
   // shares of the waves: state columns (n tile, token tiles tn, tn + TN, ..);
@@ -241,7 +235,7 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(SsmArgs a, C
   __shared__ __attribute__((aligned(16))) Tin Ks[Q * LQ];
   __shared__ __attribute__((aligned(16))) Tin Zs[Q * LQ];
   __shared__ __attribute__((aligned(16))) Tin dSs[N * LP];
-  __shared__ __attribute__((aligned(16))) ChunkDecay<Q, true> decs[2];
+  __shared__ __attribute__((aligned(16))) ChunkDecay<Q> decs[2];
   // sums of a head, read while the next one is worked on
   struct Sums {
     float row[JH][Q], diag[Q], col[QT][Q], w[NTL][Q], u[NTL][Q], dot[kWaves], dd[kWaves];
@@ -270,29 +264,17 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(SsmArgs a, C
 
   if (valid > 0) {
     Stage<Q, P, Tin, kThreads, LP> fx, fy;
+    StageDecay<Q, kThreads> fd;
     auto fetch = [&](int h) {
-      const size_t th = ((size_t)b * a.H + h) * a.T + t0;
+      const size_t bh = (size_t)b * a.H + h, th = bh * a.T + t0;
       fx.fetch((const Tin*)a.x + th * P, valid);
       fy.fetch((const Tin*)a.dy + th * P, valid);
     };
-    // decays a head ahead, by the last wave, from steps fetched another head
-    // earlier
-    auto steps = [&](int h) {
-      const size_t th = ((size_t)b * a.H + h) * a.T + t0;
-      return w == kWaves - 1 && h < h1
-                 ? buffer_load_f32(make_buffer(a.dt + th, min(valid, Q) * 4ll), lane * 4)
-                 : 0.f;
-    };
-    auto fill = [&](int h, float raw) {
-      float sl = 0.f, st = 0.f;
-      if (lane < Q && lane < valid)
-        st = ssm_step(raw, a.dt_bias ? a.dt_bias[h] : 0.f, a.softplus, sl);
-      decs[(h - h0) & 1].fill(st, st * a.A[h], sl);
-    };
+    auto fetch_decay = [&](int h) { fd.fetch(decay + ((size_t)b * a.H + h) * nch + c); };
     // the step's gradient of every token, from the sums of head h
     auto finish = [&](int h) {
       const Sums& z = acc2[(h - h0) & 1];
-      const ChunkDecay<Q, true>& dec = decs[(h - h0) & 1];
+      const ChunkDecay<Q>& dec = decs[(h - h0) & 1];
       float R = 0.f, col = 0.f, wi = 0.f, uj = 0.f, own = 0.f, step = 0.f, slope = 0.f;
       if (lane < Q) {
 #pragma unroll
@@ -326,18 +308,15 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(SsmArgs a, C
         sums[2 * a.H + h] = sb;
       }
     };
-    float raw;
     {
       Stage<Q, N, Tin, kThreads, LN> fb, fc;
       fb.fetch((const Tin*)a.Bm + tg * N, valid);
       fc.fetch((const Tin*)a.Cm + tg * N, valid);
       fetch(h0);
-      raw = steps(h0);
+      fetch_decay(h0);
       fb.put(Bs);
       fc.put(Cs);
     }
-    if (w == kWaves - 1) fill(h0, raw);
-    raw = steps(h0 + 1);
     __syncthreads();
     // scores of the wave's query tile: rows j = 4 (l / 16) + r, column i = l % 16
     f32x4 CB[JM];
@@ -359,11 +338,12 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(SsmArgs a, C
     for (int h = h0; h < h1; ++h) {
       const size_t bh = (size_t)b * a.H + h, th = bh * a.T + t0;
       const float D = a.D ? a.D[h] : 0.f;
-      const ChunkDecay<Q, true>& dec = decs[(h - h0) & 1];
+      const ChunkDecay<Q>& dec = decs[(h - h0) & 1];
       Sums& z = acc2[(h - h0) & 1];
       // the previous head's readers of these buffers are behind a barrier
       fx.put(Xs);
       fy.put(Ys);
+      fd.put(decs[(h - h0) & 1]);
       f32x4 sv[PTL], dv[PTL];
       {
         const float* sf = o.states + (bh * nch + c) * P * N;
@@ -492,10 +472,7 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(SsmArgs a, C
       if (w == kWaves - QT && h > h0) finish(h - 1);  // the least of the scores
       __syncthreads();
 
-      if (w == kWaves - 1 && h + 1 < h1) {
-        fill(h + 1, raw);
-        raw = steps(h + 2);
-      }
+      if (h + 1 < h1) fetch_decay(h + 1);
       // dB, dC from the chunk's own pairs, over the wave's columns n
       {
         Frag<Q, Tin> bT, cT;  // rows n, k = token
@@ -638,17 +615,19 @@ template <int P, int N, typename Tin>
 int run_bwd(const SsmArgs& a, hipStream_t s) {
   const int BH = a.B * a.H, PN = P * N;
   const Plan p = make_plan(a.B, a.H, a.G, a.T, P, N, bwd_q<Tin>());
-  float* ws = (float*)a.ws;
-  constexpr int NT = 4 * walk_rows<P>(), SL = P / walk_rows<P>();
+  constexpr int NT = 64 * walk_waves<P>(), Q = bwd_q<Tin>();
+  float* ws = (float*)((char*)a.ws + decay_bytes<Q>(a.B, a.H, a.T));
   float *slots = ws + p.slots, *logs = ws + p.logs, *states = ws + p.states;
+  ChunkDecay<Q>* decay = (ChunkDecay<Q>*)a.ws;
+  launch_decay<Q>(a, decay, s);
   if (BH == 0)  // an empty batch: zeros for the parameters
     return launch_column_sum(ws, 0, 3 * a.H, a.H, 1, a.dA, a.dD, a.dbias, s);
   int tk;
   if (p.nseg > 1) {
     tk = ktimer_before(s, "ssm_bwd_state");
     hipLaunchKernelGGL((ssm_walk_kernel<P, N, Tin, false>),
-                       dim3((unsigned)(2 * BH * (p.nseg - 1) * SL)), dim3(NT), 0, s, a, p.nseg,
-                       p.segch, slots, logs, states);
+                       dim3((unsigned)(2 * BH * (p.nseg - 1))), dim3(NT), 0, s, a, p.nseg,
+                       p.segch, decay, slots, logs, states);
     ktimer_after(s, tk);
     tk = ktimer_before(s, "ssm_bwd_chain");
     hipLaunchKernelGGL(ssm_walk_chain_kernel, dim3((PN / 4 + 255) / 256, 2 * BH), dim3(256), 0, s,
@@ -656,8 +635,8 @@ int run_bwd(const SsmArgs& a, hipStream_t s) {
     ktimer_after(s, tk);
   }
   tk = ktimer_before(s, "ssm_bwd_walk");
-  hipLaunchKernelGGL((ssm_walk_kernel<P, N, Tin, true>), dim3((unsigned)(2 * BH * p.nseg * SL)),
-                     dim3(NT), 0, s, a, p.nseg, p.segch, slots, logs, states);
+  hipLaunchKernelGGL((ssm_walk_kernel<P, N, Tin, true>), dim3((unsigned)(2 * BH * p.nseg)),
+                     dim3(NT), 0, s, a, p.nseg, p.segch, decay, slots, logs, states);
   ktimer_after(s, tk);
   int rc = (int)hipGetLastError();
   if (rc) return rc;
@@ -668,7 +647,7 @@ int run_bwd(const SsmArgs& a, hipStream_t s) {
     tk = ktimer_before(s, "ssm_bwd");
     hipLaunchKernelGGL((ssm_bwd_chunk_kernel<P, N, Tin>),
                        dim3((unsigned)((long long)a.B * a.G * p.nch * p.parts)), dim3(kThreads),
-                       0, s, a, o);
+                       0, s, a, o, decay);
     ktimer_after(s, tk);
     if (p.parts > 1) {
       tk = ktimer_before(s, "ssm_bwd_parts");
@@ -702,7 +681,8 @@ int run_bwd_n(const SsmArgs& a, hipStream_t s) {
 
 size_t ssm_backward_ws(int B, int H, int G, int T, int P, int N, int bf16) {
   return make_plan(B, H, G, T, P, N, bf16 ? bwd_q<__bf16>() : bwd_q<float>()).total *
-         sizeof(float);
+             sizeof(float) +
+         (bf16 ? decay_bytes<bwd_q<__bf16>()>(B, H, T) : decay_bytes<bwd_q<float>()>(B, H, T));
 }
 
 int launch_ssm_backward(const SsmArgs& a, hipStream_t s) {

@@ -2,6 +2,8 @@
 #pragma once
 
 #include "device_common.hpp"
+#include "launch.hpp"
+#include "mixer.hpp"
 
 namespace osdn {
 
@@ -31,24 +33,45 @@ __device__ __forceinline__ int ssm_length(const int* lengths, int b, int T) {
   return n < 0 ? 0 : n > T ? T : n;
 }
 
-// Inclusive prefix and suffix sums over each row of 16 lanes, and the suffix
-// without the lane itself.
-__device__ __forceinline__ float row16_prefix(float x) {
-  x += dpp_f<0x111>(x);  // row_shr:1, :2, :4, :8 (zeros from outside the row)
-  x += dpp_f<0x112>(x);
-  x += dpp_f<0x114>(x);
-  x += dpp_f<0x118>(x);
+// A log decay as an fp32 sum and what its roundings lost. Sums of a few
+// tens would otherwise carry an error of 2^-24 of themselves, absolute, into
+// the exponent: 1e-6 relative on the decays, and the same one for every token
+// behind, which adds up in the gradients of A and of the step's bias.
+struct Log2f {
+  float hi, lo;
+};
+__device__ __forceinline__ Log2f add(Log2f a, Log2f b) {
+  const float s = a.hi + b.hi, t = s - a.hi;
+  return {s, ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo)};
+}
+// exp of it, the rounding of x log2(e) put back as well.
+__device__ __forceinline__ float exp_of(float hi, float lo) {
+  const float t = hi * 1.44269504f;
+  const float lost = fmaf(hi, 1.44269504f, -t) + hi * 1.92596299e-8f;
+  const float e = __builtin_amdgcn_exp2f(t);
+  return fmaf(e, fmaf(lost, 0.693147181f, lo), e);
+}
+__device__ __forceinline__ float exp_of(Log2f x) { return exp_of(x.hi, x.lo); }
+
+template <int CTRL>
+__device__ __forceinline__ Log2f dpp_l(Log2f x) {
+  return {dpp_f<CTRL>(x.hi), dpp_f<CTRL>(x.lo)};
+}
+// Inclusive prefix sums over each row of 16 lanes, and the sums of the lanes
+// behind each one (zeros come in from outside the row).
+__device__ __forceinline__ Log2f row16_prefix(Log2f x) {
+  x = add(x, dpp_l<0x111>(x));  // row_shr:1, :2, :4, :8
+  x = add(x, dpp_l<0x112>(x));
+  x = add(x, dpp_l<0x114>(x));
+  x = add(x, dpp_l<0x118>(x));
   return x;
 }
-__device__ __forceinline__ float row16_suffix(float x) {
-  x += dpp_f<0x101>(x);  // row_shl:1, :2, :4, :8
-  x += dpp_f<0x102>(x);
-  x += dpp_f<0x104>(x);
-  x += dpp_f<0x108>(x);
-  return x;
-}
-__device__ __forceinline__ float row16_suffix_after(float x) {
-  return dpp_f<0x101>(row16_suffix(x));
+__device__ __forceinline__ Log2f row16_suffix_after(Log2f x) {
+  x = add(x, dpp_l<0x101>(x));  // row_shl:1, :2, :4, :8
+  x = add(x, dpp_l<0x102>(x));
+  x = add(x, dpp_l<0x104>(x));
+  x = add(x, dpp_l<0x108>(x));
+  return dpp_l<0x101>(x);
 }
 
 // The decays of one chunk of Q tokens. With l = dt A a token, the factor from
@@ -57,63 +80,62 @@ __device__ __forceinline__ float row16_suffix_after(float x) {
 // behind j inside its block, and whole blocks between. No difference of two
 // long sums is taken, so a strong decay early in the chunk costs later pairs
 // no precision; inside one block the difference is of sums over 16 tokens.
-template <int Q, bool Grad = false>
+template <int Q>
 struct ChunkDecay {
   float dt[Q];    // step
   float up[Q];    // log: block start .. token, inclusive
+  float ul[Q];    // what `up` lost to rounding
   float eup[Q];   // exp(up)
   float edn[Q];   // exp(log: after token .. block end)
   float ent[Q];   // chunk entry .. token
   float wx[Q];    // after token .. chunk exit, times dt
-  float ext[Grad ? Q : 4];    // the same without dt
-  float slope[Grad ? Q : 4];  // of the step by its raw value
+  float ext[Q];   // the same without dt
+  float slope[Q]; // of the step by its raw value
   float gap[16];  // [a][b], a > b: exp over the blocks strictly between
   float total;    // whole chunk
   float logtot;
+  float pad[2];
 
-  // By one whole wave; lane t (< Q) passes its token's step, log decay and
-  // slope.
-  __device__ __forceinline__ void fill(float step, float l, float sl) {
+  // By one whole wave; lane t (< Q) passes its token's step, the step's slope
+  // and A.
+  __device__ __forceinline__ void fill(float step, float sl, float A) {
     constexpr int NB = Q / 16;
     const int t = threadIdx.x & 63;
-    const float u = row16_prefix(l), d = row16_suffix_after(l);
-    float bs[NB], pre[NB + 1];
-    pre[0] = 0.f;
+    const float p = step * A;
+    const Log2f l = {p, fmaf(step, A, -p)};
+    const Log2f u = row16_prefix(l), d = row16_suffix_after(l);
+    Log2f bs[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      bs[b] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(u), 16 * b + 15));
-      pre[b + 1] = pre[b] + bs[b];
+      bs[b].hi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(u.hi), 16 * b + 15));
+      bs[b].lo = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(u.lo), 16 * b + 15));
     }
-    float before = 0.f, after = 0.f;
+    Log2f before = {0.f, 0.f}, after = before, all = before, between = before;
+    const int x = t / NB, y = t % NB;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      if (b < t / 16) before += bs[b];
-      if (b > t / 16) after += bs[b];
+      const Log2f zero = {0.f, 0.f};
+      before = add(before, b < t / 16 ? bs[b] : zero);
+      after = add(after, b > t / 16 ? bs[b] : zero);
+      between = add(between, b > y && b < x ? bs[b] : zero);
+      all = add(all, bs[b]);
     }
     if (t < Q) {
       dt[t] = step;
-      up[t] = u;
-      eup[t] = __expf(u);
-      edn[t] = __expf(d);
-      ent[t] = __expf(before + u);
-      const float x = __expf(d + after);
-      wx[t] = x * step;
-      if constexpr (Grad) {
-        ext[t] = x;
-        slope[t] = sl;
-      }
+      up[t] = u.hi;
+      ul[t] = u.lo;
+      eup[t] = exp_of(u);
+      edn[t] = exp_of(d);
+      ent[t] = exp_of(add(before, u));
+      const float e = exp_of(add(d, after));
+      wx[t] = e * step;
+      ext[t] = e;
+      slope[t] = sl;
     }
-    if (t < NB * NB) {
-      const int x = t / NB, y = t % NB;
-      float g = 0.f;
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-        if (b > y && b < x) g += bs[b];
-      gap[x * 4 + y] = __expf(g);
-    }
+    if (t < NB * NB) gap[x * 4 + y] = exp_of(between);
     if (t == 0) {
-      total = __expf(pre[NB]);
-      logtot = pre[NB];
+      total = exp_of(all);
+      logtot = all.hi;
     }
   }
 };
@@ -121,8 +143,8 @@ struct ChunkDecay {
 // Decays of one tile of pairs in accumulator layout: lane l holds the factors
 // from the tokens j = 16 jt + 4 (l / 16) + r to i = 16 it + l % 16, zero where
 // j > i.
-template <int Q, bool G>
-__device__ __forceinline__ f32x4 pair_decay(const ChunkDecay<Q, G>& d, int it, int jt) {
+template <int Q>
+__device__ __forceinline__ f32x4 pair_decay(const ChunkDecay<Q>& d, int it, int jt) {
   f32x4 f = {0.f, 0.f, 0.f, 0.f};
   const int i = it * 16 + acc_col(), j = jt * 16 + acc_row(0);
   if (jt < it) {
@@ -132,16 +154,17 @@ __device__ __forceinline__ f32x4 pair_decay(const ChunkDecay<Q, G>& d, int it, i
     for (int r = 0; r < 4; ++r) f[r] = g * e[r];
   } else if (jt == it) {
     const f32x4 u = *reinterpret_cast<const f32x4*>(d.up + j);
-    const float v = d.up[i];
+    const f32x4 ul = *reinterpret_cast<const f32x4*>(d.ul + j);
+    const float v = d.up[i], vl = d.ul[i];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) f[r] = j + r <= i ? __expf(v - u[r]) : 0.f;
+    for (int r = 0; r < 4; ++r) f[r] = j + r <= i ? exp_of(v - u[r], vl - ul[r]) : 0.f;
   }
   return f;
 }
 
 // The steps of the tile's tokens j.
-template <int Q, bool G>
-__device__ __forceinline__ f32x4 tile_steps(const ChunkDecay<Q, G>& d, int jt) {
+template <int Q>
+__device__ __forceinline__ f32x4 tile_steps(const ChunkDecay<Q>& d, int jt) {
   return *reinterpret_cast<const f32x4*>(d.dt + jt * 16 + acc_row(0));
 }
 
@@ -354,5 +377,60 @@ struct Stage {
         *reinterpret_cast<uint4*>(d + i * RP * LD) = v[i];
   }
 };
+
+// The decays of a chunk, formed once a call (ssm_decay), on their way through
+// registers into LDS.
+template <int Q, int NT>
+struct StageDecay {
+  static constexpr int N16 = sizeof(ChunkDecay<Q>) / 16, NV = (N16 + NT - 1) / NT;
+  static_assert(sizeof(ChunkDecay<Q>) % 16 == 0, "whole 16-byte pieces");
+  uint4 v[NV];
+  __device__ __forceinline__ void fetch(const ChunkDecay<Q>* src) {
+    const Buffer r = make_buffer(src, sizeof(*src));
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = buffer_load16(r, (threadIdx.x + i * NT) * 16);
+  }
+  __device__ __forceinline__ void put(ChunkDecay<Q>& dst) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (threadIdx.x + i * NT < N16) reinterpret_cast<uint4*>(&dst)[threadIdx.x + i * NT] = v[i];
+  }
+};
+
+namespace {  // each source has its own kernel
+
+// One wave a chunk of a (batch, head): bh = id / nch, chunk = id % nch.
+template <int Q>
+__global__ __launch_bounds__(256) void ssm_decay_kernel(SsmArgs a, int nch, long long n,
+                                                        ChunkDecay<Q>* out) {
+  const long long id = blockIdx.x * 4ll + wave_id();
+  if (id >= n) return;
+  const int lane = threadIdx.x & 63, c = (int)(id % nch);
+  const long long bh = id / nch;
+  const int h = (int)(bh % a.H), t = c * Q + lane;
+  float sl = 0.f, st = 0.f;
+  if (lane < Q && t < ssm_length(a.lengths, (int)(bh / a.H), a.T))
+    st = ssm_step(a.dt[bh * a.T + t], a.dt_bias ? a.dt_bias[h] : 0.f, a.softplus, sl);
+  out[id].fill(st, sl, a.A[h]);
+}
+
+// Bytes of the decays of a call, a multiple of 256.
+template <int Q>
+size_t decay_bytes(int B, int H, int T) {
+  return ((size_t)B * H * ((T + Q - 1) / Q) * sizeof(ChunkDecay<Q>) + 255) / 256 * 256;
+}
+
+template <int Q>
+void launch_decay(const SsmArgs& a, ChunkDecay<Q>* out, hipStream_t s) {
+  const int nch = (a.T + Q - 1) / Q;
+  const long long n = (long long)a.B * a.H * nch;
+  if (n == 0) return;
+  const int tk = ktimer_before(s, "ssm_decay");
+  hipLaunchKernelGGL((ssm_decay_kernel<Q>), dim3((unsigned)((n + 3) / 4)), dim3(256), 0, s, a,
+                     nch, n, out);
+  ktimer_after(s, tk);
+}
+
+}  // namespace
 
 }  // namespace osdn

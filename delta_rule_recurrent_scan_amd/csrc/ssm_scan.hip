@@ -7,9 +7,9 @@
 //   S_out = L_Q0 S_in + sum_j L_Qj dt_j x_j B_j^T
 // as matrix products on MFMA.
 //
-// One workgroup walks a segment of the chunks of one (batch, head) with up to
-// 64 rows p of the state in accumulators: each wave owns 16 of them (all N
-// columns), so that the state never leaves registers between chunks; its tiles, read as
+// One workgroup walks a segment of the chunks of one (batch, head) with the
+// state in accumulators: each wave owns 16 or 32 rows p of it (all N columns),
+// so that the state never leaves registers between chunks; its tiles, read as
 // (row p, k = n) fragments in accumulator order, are the operand of the
 // readout without a trip through LDS. Scores are formed once a chunk, each
 // wave a share of the token rows, and pass through LDS. The next chunk's rows
@@ -30,11 +30,10 @@
 namespace osdn {
 namespace {
 
-// Rows p of the state a workgroup walks: a slice of P, 16 rows a wave.
+// Waves of a workgroup, and 16-row tiles p a wave: two at P = 128, where every
+// key and query fragment read from LDS then serves two products.
 template <int P>
-constexpr int scan_rows() { return P; }
-template <int P>
-constexpr int scan_waves() { return scan_rows<P>() / 16; }
+constexpr int scan_waves() { return P / 16 < 4 ? P / 16 : 4; }
 
 template <typename Tin>
 constexpr int scan_q() { return sizeof(Tin) == 2 ? 64 : 32; }
@@ -45,87 +44,71 @@ struct Segments {
 };
 
 template <int P, int N, typename Tin, bool YOUT>
-__global__ __launch_bounds__(64 * scan_waves<P>(), scan_waves<P>() == 8 ? 4 : YOUT ? 2 : 3) void ssm_scan_kernel(SsmArgs a, int nseg,
-                                                                        int seglen,
-                                                                        float* seg_state,
-                                                                        float* seg_log) {
-  constexpr int Q = scan_q<Tin>(), NW = scan_waves<P>(), NT = 64 * NW, SP = scan_rows<P>();
+__global__ __launch_bounds__(64 * scan_waves<P>(), 2) void ssm_scan_kernel(
+    SsmArgs a, int nseg, int seglen, const ChunkDecay<scan_q<Tin>()>* decay, float* seg_state,
+    float* seg_log) {
+  constexpr int Q = scan_q<Tin>(), NW = scan_waves<P>(), NT = 64 * NW, PT = P / 16 / NW;
   constexpr int QT = Q / 16, NTL = N / 16;
-  constexpr int LN = N + 16 / sizeof(Tin), LP = SP + 16 / sizeof(Tin);
+  constexpr int LN = N + 16 / sizeof(Tin), LP = P + 16 / sizeof(Tin);
   // scores: IM query tiles a wave, or JH waves a query tile
   constexpr int IM = NW < QT ? QT / NW : 1, JH = NW > QT ? NW / QT : 1, JM = (QT + JH - 1) / JH;
   __shared__ __attribute__((aligned(16))) Tin Bs[Q * LN];
   __shared__ __attribute__((aligned(16))) Tin Cs[YOUT ? Q * LN : 16];
   __shared__ __attribute__((aligned(16))) Tin Xs[Q * LP];
   __shared__ __attribute__((aligned(16))) Tin Ms[YOUT ? Q * Q : 16];  // fragment order
-  __shared__ __attribute__((aligned(16))) ChunkDecay<Q> decs[2];
+  __shared__ __attribute__((aligned(16))) ChunkDecay<Q> dec;
 
   const int lane = threadIdx.x & 63, w = wave_id();
   const int nwg = YOUT ? nseg : nseg - 1;  // the last segment hands nothing on
-  const int ps = blockIdx.x % (P / SP);    // slice of the state's rows
-  const int bh = blockIdx.x / (P / SP) / nwg, sg = blockIdx.x / (P / SP) % nwg;
+  const int bh = blockIdx.x / nwg, sg = blockIdx.x % nwg;
   const int b = bh / a.H, h = bh % a.H;
   const int n = ssm_length(a.lengths, b, a.T);
-  const float A = a.A[h], D = a.D ? a.D[h] : 0.f, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+  const float D = a.D ? a.D[h] : 0.f;
   const size_t th = (size_t)bh * a.T;
   const size_t tg = ((size_t)b * a.G + h / (a.H / a.G)) * a.T;
-  const Tin* x = (const Tin*)a.x + th * P + ps * SP;
+  const Tin* x = (const Tin*)a.x + th * P;
   const Tin* Bm = (const Tin*)a.Bm + tg * N;
   const Tin* Cm = (const Tin*)a.Cm + tg * N;
-  Tin* y = (Tin*)a.y + th * P + ps * SP;
-  const float* dt = a.dt + th;
+  Tin* y = (Tin*)a.y + th * P;
+  const ChunkDecay<Q>* dc = decay + (size_t)bh * ((a.T + Q - 1) / Q);
 
   const int t0 = sg * seglen, t1 = min(t0 + seglen, a.T), tn = min(t1, n);
 
-  // S[nt]: rows n = 16 nt + 4 (l / 16) + e of column p = l % 16 of the wave's
-  // 16 rows p
-  f32x4 S[NTL];
+  // S[pt][nt]: rows n = 16 nt + 4 (l / 16) + e of column p = l % 16 of the
+  // wave's p tile
+  f32x4 S[PT][NTL];
   const int n0 = 4 * (lane >> 4);
-  const size_t srow = (size_t)(ps * SP + w * 16 + (lane & 15)) * N + n0;
+  const size_t srow = (size_t)(w * PT * 16 + (lane & 15)) * N + n0;
   const float* in = !YOUT ? nullptr
                     : nseg > 1 ? seg_state + ((size_t)bh * nseg + sg) * P * N
                     : a.S0    ? a.S0 + (size_t)bh * P * N
                               : nullptr;
 #pragma unroll
-  for (int nt = 0; nt < NTL; ++nt)
-    S[nt] = in ? load4(in + srow + 16 * nt) : f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+    for (int nt = 0; nt < NTL; ++nt)
+      S[pt][nt] = in ? load4(in + srow + 16 * (pt * N + nt)) : f32x4{0.f, 0.f, 0.f, 0.f};
   float logsum = 0.f;
 
   Stage<Q, N, Tin, NT, LN> fb, fc;
-  Stage<Q, SP, Tin, NT, LP, P> fx;
+  Stage<Q, P, Tin, NT, LP> fx;
+  StageDecay<Q, NT> fd;
   auto fetch = [&](int t) {
     const int valid = tn - t;
     fb.fetch(Bm + (size_t)t * N, valid);
     if (YOUT) fc.fetch(Cm + (size_t)t * N, valid);
     fx.fetch(x + (size_t)t * P, valid);
+    fd.fetch(dc + t / Q);
   };
-  // the decays of a chunk are formed by wave 0 (whose score tile is the
-  // smallest) while the chunk before it is worked on, from steps fetched
-  // another chunk earlier
-  auto steps = [&](int t) {
-    return w == 0 ? buffer_load_f32(make_buffer(dt + t, (tn - t) * 4ll), lane * 4) : 0.f;
-  };
-  auto fill = [&](ChunkDecay<Q>& d, int t, float raw) {
-    float sl = 0.f, st = 0.f;
-    if (lane < Q && t + lane < tn) st = ssm_step(raw, bias, a.softplus, sl);
-    d.fill(st, st * A, sl);
-  };
-  float raw = 0.f;
-  if (t0 < tn) {
-    fetch(t0);
-    raw = steps(t0);
-    if (w == 0) fill(decs[0], t0, raw);
-    raw = steps(t0 + Q);
-  }
-  int par = 0;
-  for (int t = t0; t < tn; t += Q, par ^= 1) {
+  if (t0 < tn) fetch(t0);
+  for (int t = t0; t < tn; t += Q) {
     const int valid = tn - t;
-    const ChunkDecay<Q>& dec = decs[par];
     __syncthreads();
     fb.put(Bs);
     if (YOUT) fc.put(Cs);
     fx.put(Xs);
-    if (!YOUT && t + Q < tn) fetch(t + Q);
+    fd.put(dec);
+    if (t + Q < tn) fetch(t + Q);
     __syncthreads();
 
     if constexpr (YOUT) {
@@ -151,20 +134,18 @@ __global__ __launch_bounds__(64 * scan_waves<P>(), scan_waves<P>() == 8 ? 4 : YO
           Frag<Q, Tin>::store_acc_kblock(Ms + it * Frag<Q, Tin>::ELEMS, jt, s);
         }
       }
+      __syncthreads();
     }
-    if (w == 0 && t + Q < tn) {
-      fill(decs[par ^ 1], t + Q, raw);
-      raw = steps(t + 2 * Q);
-    }
-    if constexpr (YOUT) __syncthreads();
 
-    Frag<Q, Tin> xf;
-    xf.load_kmajor(Xs + w * 16, LP);
+    Frag<Q, Tin> xf[PT];
+#pragma unroll
+    for (int pt = 0; pt < PT; ++pt) xf[pt].load_kmajor(Xs + (w * PT + pt) * 16, LP);
     if constexpr (YOUT) {
       const Buffer yb =
           make_buffer(y + (size_t)t * P, (long long)min(t1 - t, Q) * P * (int)sizeof(Tin));
-      Frag<N, Tin> sf;
-      frag_from_acc<N>(sf, S);
+      Frag<N, Tin> sf[PT];
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) frag_from_acc<N>(sf[pt], S[pt]);
 #pragma unroll
       for (int it = 0; it < QT; ++it) {
         Frag<N, Tin> cf;
@@ -173,33 +154,37 @@ __global__ __launch_bounds__(64 * scan_waves<P>(), scan_waves<P>() == 8 ? 4 : YO
         mf.load_global(Ms + it * Frag<Q, Tin>::ELEMS);
         const int ti = it * 16 + (lane & 15);
         const float ent = dec.ent[ti];
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-        mma(acc, sf, cf);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] *= ent;
-        mma_upto<Q>(acc, xf, mf, 16 * (it + 1));
-        const int p = w * 16 + n0;
-        const f32x4 xv = load4(Xs + ti * LP + p);
+        for (int pt = 0; pt < PT; ++pt) {
+          f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+          mma(acc, sf[pt], cf);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = ti < valid ? acc[e] + D * xv[e] : 0.f;
-        buffer_store4(yb, ti * P + p, acc, Tin());
-        __builtin_amdgcn_sched_barrier(0);  // one token tile's operands at a time
+          for (int e = 0; e < 4; ++e) acc[e] *= ent;
+          mma_upto<Q>(acc, xf[pt], mf, 16 * (it + 1));
+          const int p = (w * PT + pt) * 16 + n0;
+          const f32x4 xv = load4(Xs + ti * LP + p);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[e] = ti < valid ? acc[e] + D * xv[e] : 0.f;
+          buffer_store4(yb, ti * P + p, acc, Tin());
+        }
       }
     }
 
-    // the next chunk's rows; not before, the readout needs the registers
-    if (YOUT && t + Q < tn) fetch(t + Q);
     const float total = dec.total;
     logsum += dec.logtot;
-    Parts<Q, Tin> xw;
-    scale_parts<Q>(xf, dec.wx, xw);
+    Parts<Q, Tin> xw[PT];
+#pragma unroll
+    for (int pt = 0; pt < PT; ++pt) scale_parts<Q>(xf[pt], dec.wx, xw[pt]);
 #pragma unroll
     for (int nt = 0; nt < NTL; ++nt) {
       Frag<Q, Tin> bf;
       bf.load_kmajor(Bs + nt * 16, LN);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) S[nt][e] *= total;
-      mma_parts(S[nt], bf, xw);
+      for (int pt = 0; pt < PT; ++pt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[pt][nt][e] *= total;
+        mma_parts(S[pt][nt], bf, xw[pt]);
+      }
     }
   }
 
@@ -207,16 +192,17 @@ __global__ __launch_bounds__(64 * scan_waves<P>(), scan_waves<P>() == 8 ? 4 : YO
     // rows behind the sequence's last chunk
     const int from = tn > t0 ? t0 + (tn - t0 + Q - 1) / Q * Q : t0;
     constexpr int VE = 16 / sizeof(Tin);
-    for (int e = threadIdx.x; e < max(t1 - from, 0) * (SP / VE); e += NT)
-      *reinterpret_cast<uint4*>(y + (size_t)(from + e / (SP / VE)) * P + e % (SP / VE) * VE) =
-          uint4{0u, 0u, 0u, 0u};
+    for (int e = threadIdx.x; e < max(t1 - from, 0) * (P / VE); e += NT)
+      *reinterpret_cast<uint4*>(y + (size_t)from * P + (size_t)e * VE) = uint4{0u, 0u, 0u, 0u};
   }
   float* out = YOUT ? (a.ST && sg == nseg - 1 ? a.ST + (size_t)bh * P * N : nullptr)
                     : seg_state + ((size_t)bh * nseg + sg + 1) * P * N;
   if (out) {
 #pragma unroll
-    for (int nt = 0; nt < NTL; ++nt) store4(out + srow + 16 * nt, S[nt]);
-    if (!YOUT && ps == 0 && threadIdx.x == 0) seg_log[(size_t)bh * (nseg - 1) + sg] = logsum;
+    for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+      for (int nt = 0; nt < NTL; ++nt) store4(out + srow + 16 * (pt * N + nt), S[pt][nt]);
+    if (!YOUT && threadIdx.x == 0) seg_log[(size_t)bh * (nseg - 1) + sg] = logsum;
   }
 }
 
@@ -249,7 +235,7 @@ __global__ __launch_bounds__(256) void ssm_chain_kernel(int PN, int nseg, const 
 Segments segments(int B, int H, int T, int Q) {
   const int nch = (T + Q - 1) / Q;
   const long long bh = (long long)B * H;
-  long long want = bh > 0 ? (1024 + bh - 1) / bh : 1;
+  long long want = bh > 0 ? (512 + bh - 1) / bh : 1;
   if (want > nch / 4) want = nch / 4;
   if (want < 1) want = 1;
   const int per = nch > 0 ? (int)((nch + want - 1) / want) : 1;
@@ -263,13 +249,16 @@ template <int P, int N, typename Tin>
 int run_scan(const SsmArgs& a, hipStream_t s) {
   const int BH = a.B * a.H, PN = P * N;
   const Segments g = segments(a.B, a.H, a.T, scan_q<Tin>());
-  float* st = (float*)a.ws;
+  constexpr int Q = scan_q<Tin>();
+  ChunkDecay<Q>* dc = (ChunkDecay<Q>*)a.ws;
+  launch_decay<Q>(a, dc, s);
+  float* st = (float*)((char*)a.ws + decay_bytes<Q>(a.B, a.H, a.T));
   float* lg = st + (size_t)BH * g.n * PN;
   constexpr int NT = 64 * scan_waves<P>();
   if (g.n > 1) {
     int tk = ktimer_before(s, "ssm_state");
-    hipLaunchKernelGGL((ssm_scan_kernel<P, N, Tin, false>), dim3((unsigned)(BH * (g.n - 1) * (P / scan_rows<P>()))),
-                       dim3(NT), 0, s, a, g.n, g.len, st, lg);
+    hipLaunchKernelGGL((ssm_scan_kernel<P, N, Tin, false>), dim3((unsigned)(BH * (g.n - 1))),
+                       dim3(NT), 0, s, a, g.n, g.len, dc, st, lg);
     ktimer_after(s, tk);
     tk = ktimer_before(s, "ssm_chain");
     hipLaunchKernelGGL(ssm_chain_kernel, dim3((PN / 4 + 255) / 256, BH), dim3(256), 0, s, PN,
@@ -277,8 +266,8 @@ int run_scan(const SsmArgs& a, hipStream_t s) {
     ktimer_after(s, tk);
   }
   const int tk = ktimer_before(s, "ssm_scan");
-  hipLaunchKernelGGL((ssm_scan_kernel<P, N, Tin, true>), dim3((unsigned)(BH * g.n * (P / scan_rows<P>()))),
-                     dim3(NT), 0, s, a, g.n, g.len, st, lg);
+  hipLaunchKernelGGL((ssm_scan_kernel<P, N, Tin, true>), dim3((unsigned)(BH * g.n)),
+                     dim3(NT), 0, s, a, g.n, g.len, dc, st, lg);
   ktimer_after(s, tk);
   return (int)hipGetLastError();
 }
@@ -302,7 +291,9 @@ int run_scan_n(const SsmArgs& a, hipStream_t s) {
 
 size_t ssm_forward_ws(int B, int H, int T, int P, int N, int bf16) {
   const Segments g = segments(B, H, T, bf16 ? scan_q<__bf16>() : scan_q<float>());
-  return g.n > 1 ? (size_t)B * H * g.n * ((size_t)P * N + 1) * sizeof(float) : 0;
+  const size_t d = bf16 ? decay_bytes<scan_q<__bf16>()>(B, H, T)
+                        : decay_bytes<scan_q<float>()>(B, H, T);
+  return d + (g.n > 1 ? (size_t)B * H * g.n * ((size_t)P * N + 1) * sizeof(float) : 0);
 }
 
 int launch_ssm_forward(const SsmArgs& a, hipStream_t s) {

@@ -520,8 +520,8 @@ int short_conv_backward(int B, int T, int H, int D, int W, int dtype,
  *            be exactly S0
  * P, N in {32, 64, 128}; any T. Tensors start on 16 bytes
  * (OSDN_ERR_MISALIGNED). workspace: ssm_forward_workspace_bytes(...) bytes,
- * 256-byte aligned: the states between the segments that long sequences of
- * few (batch, head) streams are cut into (0 where they are not).
+ * 256-byte aligned: the chunks' decays, and the states between the segments
+ * that long sequences of few (batch, head) streams are cut into.
  */
 size_t ssm_forward_workspace_bytes(int B, int H, int G, int T, int P, int N,
                                    int dtype);
@@ -553,7 +553,7 @@ int ssm_decode(int B, int H, int G, int T, int P, int N, int dtype,
  *   workspace: ssm_backward_workspace_bytes(...) bytes, 256-byte aligned: the
  *            state and its adjoint at every chunk's ends (2 P N floats for each
  *            64 tokens (bf16) or 32 (fp32) of a (batch, head)), the states
- *            between segments, and partial sums
+ *            between segments, the chunks' decays, and partial sums
  */
 size_t ssm_backward_workspace_bytes(int B, int H, int G, int T, int P, int N,
                                     int dtype);
@@ -648,7 +648,7 @@ void osdn_kernel_timing(int enable);
  * backbone), osdn_decode, gdn2_decode (recurrent decode), osdn_bwd_record,
  * osdn_bwd, osdn_bwd_learner (backward), gated_bwd_record, gated_bwd,
  * gated_bwd_learner, gdn2_bwd_record, gdn2_bwd, gdn2_bwd_out (gate-aware
- * backward), short_conv, short_conv_bwd, ssm_state, ssm_chain, ssm_scan,
+ * backward), short_conv, short_conv_bwd, ssm_decay, ssm_state, ssm_chain, ssm_scan,
  * ssm_decode, ssm_bwd_state, ssm_bwd_chain, ssm_bwd_walk, ssm_bwd,
  * ssm_bwd_parts, gated_norm, gated_norm_bwd, residual_norm, residual_norm_bwd,
  * column_sum (the operators around the recurrences).

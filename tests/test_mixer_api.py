@@ -127,7 +127,7 @@ def test_ssm_refusals():
     L = osdn.load_library()
     need = L.ssm_forward_workspace_bytes(1, 2, 1, 2048, 64, 64, BF16)
     assert need > 0 and need % 256 == 0
-    assert L.ssm_forward_workspace_bytes(1, 2, 1, 16, 64, 64, BF16) == 0
+    assert L.ssm_forward_workspace_bytes(1, 2, 1, 0, 64, 64, BF16) == 0
     assert L.ssm_forward_workspace_bytes(1, 3, 2, 2048, 64, 64, BF16) == 0
 
     def fwd(B=1, H=2, G=1, T=2048, P=64, N=64, dt=BF16, x=X, d=DY, A=WT, Bm=Z,
