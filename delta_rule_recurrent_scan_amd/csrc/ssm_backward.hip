@@ -272,9 +272,9 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
     };
     auto fetch_decay = [&](int h) { fd.fetch(decay + ((size_t)b * a.H + h) * nch + c); };
     // the step's gradient of every token, from the sums of head h
-    auto finish = [&](int h) {
-      const Sums& z = acc2[(h - h0) & 1];
-      const ChunkDecay<Q>& dec = decs[(h - h0) & 1];
+    auto finish = [&](int h, int lane, int zero) {
+      const Sums& z = acc2[((h - h0) & 1) + zero];
+      const ChunkDecay<Q>& dec = decs[((h - h0) & 1) + zero];
       float R = 0.f, col = 0.f, wi = 0.f, uj = 0.f, own = 0.f, step = 0.f, slope = 0.f;
       if (lane < Q) {
 #pragma unroll
@@ -300,7 +300,9 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
                        dec.total * dot;
       const bool in = lane < Q && lane < valid;
       const float draw = in ? (own + a.A[h] * gt) * slope : 0.f;
-      if (lane < rows) a.ddt[((size_t)b * a.H + h) * a.T + t0 + lane] = draw;
+      __builtin_amdgcn_raw_buffer_store_b32(
+          __float_as_uint(draw),
+          make_buffer(a.ddt + ((size_t)b * a.H + h) * a.T + t0, rows * 4), lane * 4, 0, 0);
       const float sa = wave_sum(in ? step * gt : 0.f), sb = wave_sum(draw);
       if (lane == 0) {
         sums[h] = sa;
@@ -335,32 +337,48 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
       }
     }
 
+    // the states of a head over the wave's columns n, in halves of P: the first
+    // is in flight from the middle of the head before it, the second while the
+    // scores are formed
+    constexpr int NH = P >= 64 ? 2 : 1, PH = P / NH, PHL = PH / 16;
+    f32x4 sv[NH][PHL], dv[NH][PHL];
+    auto load_states = [&](int h, int hf) {
+      const float* sf = o.states + (((size_t)b * a.H + h) * nch + c) * P * N;
+      const Buffer rf = make_buffer(sf, P * N * 4),
+                   rr = make_buffer(sf + (size_t)BH * nch * P * N, P * N * 4);
+#pragma unroll
+      for (int pb = 0; pb < PHL; ++pb) {
+        const unsigned at = (((hf * PHL + pb) * NTL + nt) * 64 + lane) * 16;
+        sv[hf][pb] = __builtin_bit_cast(f32x4, buffer_load16(rf, at));
+        dv[hf][pb] = __builtin_bit_cast(f32x4, buffer_load16(rr, at));
+      }
+    };
+    load_states(h0, 0);
     for (int h = h0; h < h1; ++h) {
       const size_t bh = (size_t)b * a.H + h, th = bh * a.T + t0;
       const float D = a.D ? a.D[h] : 0.f;
-      const ChunkDecay<Q>& dec = decs[(h - h0) & 1];
-      Sums& z = acc2[(h - h0) & 1];
+      // an offset of zero that the compiler takes for new in every head: it
+      // would otherwise keep some forty LDS addresses across the loop, spill
+      // them, and wait for every load in flight to reload one
+      int zero = 0, lane_now = threadIdx.x & 63;
+      asm volatile("" : "+s"(zero), "+v"(lane_now));
+      const int lane = lane_now, lc = lane & 15, g4 = 4 * (lane >> 4);
+      Tin *bs = Bs + zero, *cs = Cs + zero, *xs = Xs + zero, *ys = Ys + zero, *ks = Ks + zero,
+          *zs = Zs + zero, *ds = dSs + zero;
+      const ChunkDecay<Q>& dec = decs[((h - h0) & 1) + zero];
+      Sums& z = acc2[((h - h0) & 1) + zero];
       // the previous head's readers of these buffers are behind a barrier
-      fx.put(Xs);
-      fy.put(Ys);
-      fd.put(decs[(h - h0) & 1]);
-      f32x4 sv[PTL], dv[PTL];
-      {
-        const float* sf = o.states + (bh * nch + c) * P * N;
-        const float* sr = sf + (size_t)BH * nch * P * N;
-#pragma unroll
-        for (int pb = 0; pb < PTL; ++pb) {
-          sv[pb] = load4(sf + (pb * NTL + nt) * 256 + (unsigned)(lane * 4));
-          dv[pb] = load4(sr + (pb * NTL + nt) * 256 + (unsigned)(lane * 4));
-        }
-      }
+      fx.put(xs);
+      fy.put(ys);
+      fd.put(decs[((h - h0) & 1) + zero]);
+      if constexpr (NH > 1) load_states(h, 1);
       if (h + 1 < h1) fetch(h + 1);
       __syncthreads();
 
       // scores of dy and x, K and Z, and the pairs' sums
       {
         Frag<P, Tin> yf;
-        yf.load(Ys + qi * 16 * LP, LP);
+        yf.load(ys + qi * 16 * LP, LP);
         float rsum = 0.f;
         const int i = qi * 16 + lc;
 #pragma unroll
@@ -371,7 +389,7 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
           if (jt <= qi) {
             f32x4 s = {0.f, 0.f, 0.f, 0.f};
             Frag<P, Tin> xf;
-            xf.load(Xs + jt * 16 * LP, LP);
+            xf.load(xs + jt * 16 * LP, LP);
             mma(s, xf, yf);
             const f32x4 l = pair_decay(dec, qi, jt), dj = tile_steps(dec, jt);
 #pragma unroll
@@ -386,106 +404,111 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
                 v = 0.f;
               }
               rsum += v * dj[r];
-              const float cs = row16_sum(v);
-              if (lc == 0) z.col[qi][j] = cs;
+              const float sum = row16_sum(v);
+              if (lc == 0) z.col[qi][j] = sum;
             }
           } else if (lc == 0) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) z.col[qi][jt * 16 + g4 + r] = 0.f;
           }
-          store4(Ks + i * LQ + jt * 16 + g4, kk);
-          store4(Zs + i * LQ + jt * 16 + g4, zz);
+          store4(ks + i * LQ + jt * 16 + g4, kk);
+          store4(zs + i * LQ + jt * 16 + g4, zz);
         }
         rsum = add_swap32(add_swap16(rsum));
         if (lane < 16) z.row[jh][i] = rsum;
       }
-      if (tn == 0) {
-        // <dS, S> as a tree over the lane's values: its error is shared by
-        // every token of the chunk
-        float dot[PTL];
+      // what the entering state and the leaving adjoint give to dC and dB, and
+      // <dS, S> as a tree over the lane's values (its error is shared by every
+      // token of the chunk)
+      f32x4 aw[TM], au[TM];
 #pragma unroll
-        for (int pb = 0; pb < PTL; ++pb) {
-          store4(dSs + (nt * 16 + lc) * LP + pb * 16 + g4, dv[pb]);
-          dot[pb] = (sv[pb][0] * dv[pb][0] + sv[pb][1] * dv[pb][1]) +
-                    (sv[pb][2] * dv[pb][2] + sv[pb][3] * dv[pb][3]);
+      for (int m = 0; m < TM; ++m) aw[m] = au[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+      float dot = 0.f;
+#pragma unroll
+      for (int hf = 0; hf < NH; ++hf) {
+        if (tn == 0) {
+          float d[PHL];
+#pragma unroll
+          for (int pb = 0; pb < PHL; ++pb) {
+            const f32x4 &u = sv[hf][pb], &v = dv[hf][pb];
+            store4(ds + (nt * 16 + lc) * LP + (hf * PHL + pb) * 16 + g4, v);
+            d[pb] = (u[0] * v[0] + u[1] * v[1]) + (u[2] * v[2] + u[3] * v[3]);
+          }
+#pragma unroll
+          for (int m = PHL / 2; m > 0; m /= 2)
+#pragma unroll
+            for (int pb = 0; pb < m; ++pb) d[pb] += d[pb + m];
+          dot += d[0];
         }
-#pragma unroll
-        for (int m = PTL / 2; m > 0; m /= 2)
-#pragma unroll
-          for (int pb = 0; pb < m; ++pb) dot[pb] += dot[pb + m];
-        const float s = wave_sum(dot[0]);
-        if (lane == 0) z.dot[w] = s;
-      }
-      // what the entering state and the leaving adjoint give to dC and dB
-      {
-        Parts<P, Tin> sp;
-        parts_from_acc<P>(sp, sv);
+        Parts<PH, Tin> sp, dp;
+        parts_from_acc<PH>(sp, sv[hf]);
 #pragma unroll
         for (int m = 0; m < TM; ++m) {
           const int it = tn + TN * m;
           if (it >= QT) break;
-          Frag<P, Tin> yf;
-          yf.load_perm(Ys + it * 16 * LP, LP);
-          f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-          mma_parts(acc, sp, yf);
-          const int i = it * 16 + lc;
-          const f32x4 cv = load4(Cs + i * LN + nt * 16 + g4);
-          const float ent = dec.ent[i];
-          float ws = 0.f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            acc[e] *= ent;
-            ws += acc[e] * cv[e];
-            dC[m][e] += acc[e];
-          }
-          ws = add_swap32(add_swap16(ws));
-          if (lane < 16) z.w[nt][i] = ws;
-          __builtin_amdgcn_sched_barrier(0);  // one token tile's operands at a time
+          Frag<PH, Tin> f;
+          f.load_perm(ys + it * 16 * LP + hf * PH, LP);
+          mma_parts(aw[m], sp, f);
         }
-      }
-      {
-        Parts<P, Tin> dp;
-        parts_from_acc<P>(dp, dv);
+        __builtin_amdgcn_sched_barrier(0);
+        parts_from_acc<PH>(dp, dv[hf]);
 #pragma unroll
         for (int m = 0; m < TM; ++m) {
-          const int jt = tn + TN * m;
-          if (jt >= QT) break;
-          Frag<P, Tin> xf;
-          xf.load_perm(Xs + jt * 16 * LP, LP);
-          f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-          mma_parts(acc, dp, xf);
-          const int j = jt * 16 + lc;
-          const f32x4 bv = load4(Bs + j * LN + nt * 16 + g4);
-          const float ex = dec.ext[j], dtj = dec.dt[j];
-          float us = 0.f;
+          const int it = tn + TN * m;
+          if (it >= QT) break;
+          Frag<PH, Tin> f;
+          f.load_perm(xs + it * 16 * LP + hf * PH, LP);
+          mma_parts(au[m], dp, f);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (tn == 0) {
+        dot = wave_sum(dot);
+        if (lane == 0) z.dot[w] = dot;
+      }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            acc[e] *= ex;
-            us += acc[e] * bv[e];
-            dB[m][e] += acc[e] * dtj;
-          }
-          us = add_swap32(add_swap16(us));
-          if (lane < 16) z.u[nt][j] = us;
-          __builtin_amdgcn_sched_barrier(0);
+      for (int m = 0; m < TM; ++m) {
+        const int it = tn + TN * m;
+        if (it >= QT) break;
+        const int i = it * 16 + lc;
+        const f32x4 cv = load4(cs + i * LN + nt * 16 + g4), bv = load4(bs + i * LN + nt * 16 + g4);
+        const float ent = dec.ent[i], ex = dec.ext[i], dti = dec.dt[i];
+        float ws = 0.f, us = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float w4 = aw[m][e] * ent, u4 = au[m][e] * ex;
+          ws += w4 * cv[e];
+          us += u4 * bv[e];
+          dC[m][e] += w4;
+          dB[m][e] += u4 * dti;
+        }
+        ws = add_swap32(add_swap16(ws));
+        us = add_swap32(add_swap16(us));
+        if (lane < 16) {
+          z.w[nt][i] = ws;
+          z.u[nt][i] = us;
         }
       }
-      if (w == kWaves - QT && h > h0) finish(h - 1);  // the least of the scores
+      if (w == kWaves - QT && h > h0) finish(h - 1, lane, zero);  // the least of the scores
       __syncthreads();
 
-      if (h + 1 < h1) fetch_decay(h + 1);
+      if (h + 1 < h1) {
+        fetch_decay(h + 1);
+        load_states(h + 1, 0);
+      }
       // dB, dC from the chunk's own pairs, over the wave's columns n
       {
         Frag<Q, Tin> bT, cT;  // rows n, k = token
-        bT.load_kmajor(Bs + nt * 16, LN);
-        cT.load_kmajor(Cs + nt * 16, LN);
+        bT.load_kmajor(bs + nt * 16, LN);
+        cT.load_kmajor(cs + nt * 16, LN);
 #pragma unroll
         for (int m = 0; m < TM; ++m) {
           const int it = tn + TN * m;
           if (it >= QT) break;
           Frag<Q, Tin> zf;
-          zf.load(Zs + it * 16 * LQ, LQ);
+          zf.load(zs + it * 16 * LQ, LQ);
           mma(dC[m], bT, zf);
-          zf.load_kmajor(Zs + it * 16, LQ);  // rows j, k = i
+          zf.load_kmajor(zs + it * 16, LQ);  // rows j, k = i
           mma(dB[m], cT, zf);
         }
       }
@@ -495,9 +518,9 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
       {
         const int j = qi * 16 + lc;
         Frag<N, Tin> bf;
-        bf.load(Bs + qi * 16 * LN, LN);
+        bf.load(bs + qi * 16 * LN, LN);
         Frag<Q, Tin> kf;
-        kf.load_kmajor(Ks + qi * 16, LQ);  // rows j, k = i
+        kf.load_kmajor(ks + qi * 16, LQ);  // rows j, k = i
         const float f = dec.wx[j];
         const Buffer dxb =
             make_buffer((Tin*)a.dx + th * P, (long long)rows * P * (int)sizeof(Tin));
@@ -506,16 +529,16 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
           const int pt = q * JH + jh;
           if (pt >= PTL) break;
           Frag<N, Tin> df;
-          df.load_kmajor(dSs + pt * 16, LP);  // rows p, k = n
+          df.load_kmajor(ds + pt * 16, LP);  // rows p, k = n
           f32x4 acc = {0.f, 0.f, 0.f, 0.f};
           mma(acc, df, bf);
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[e] *= f;
           Frag<Q, Tin> yT;
-          yT.load_kmajor(Ys + pt * 16, LP);  // rows p, k = i
+          yT.load_kmajor(ys + pt * 16, LP);  // rows p, k = i
           mma(acc, yT, kf);
-          const f32x4 yv = load4(Ys + j * LP + pt * 16 + g4);
-          const f32x4 xv = load4(Xs + j * LP + pt * 16 + g4);
+          const f32x4 yv = load4(ys + j * LP + pt * 16 + g4);
+          const f32x4 xv = load4(xs + j * LP + pt * 16 + g4);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             dd += yv[e] * xv[e];
@@ -529,7 +552,7 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
       if (lane == 0) z.dd[w] = dd;
       __syncthreads();
     }
-    if (w == 0) finish(h1 - 1);
+    if (w == 0) finish(h1 - 1, lane, 0);
   } else {
     // a chunk behind its sequence: zeros
     for (int h = h0; h < h1; ++h) {
@@ -587,9 +610,9 @@ Plan make_plan(int B, int H, int G, int T, int P, int N, int Q) {
   Plan p{};
   const long long BH = (long long)B * H;
   p.nch = (T + Q - 1) / Q;
-  // walks: about 1024 workgroups over both directions, segments of 4 chunks
+  // walks: about 512 workgroups over both directions, segments of 4 chunks
   // at least (a second segment costs a pass that writes no states)
-  long long want = BH > 0 ? (1024 + 2 * BH - 1) / (2 * BH) : 1;
+  long long want = BH > 0 ? (512 + 2 * BH - 1) / (2 * BH) : 1;
   if (want > p.nch / 4) want = p.nch / 4;
   if (want < 1) want = 1;
   p.segch = p.nch > 0 ? (int)((p.nch + want - 1) / want) : 1;

@@ -11,7 +11,8 @@ import ctypes
 
 import torch
 
-from . import (_DTYPE_CODE, OsdnError, _check, _ptr, _stream, load_library)
+from . import _DTYPE_CODE, OsdnError, load_library
+from . import _check as _check_slow
 
 __all__ = ["short_conv_forward", "short_conv_decode", "short_conv_backward",
            "short_conv_backward_workspace_bytes", "ssm_forward", "ssm_decode",
@@ -58,6 +59,13 @@ def bind(L):
         f.argtypes, f.restype = args, res
 
 
+# The current stream's handle without the Stream object around it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _raw_stream is None:
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
+
+
 def _begin(t, name):
     """Library, dtype code and device of a call whose leading tensor is t."""
     if not isinstance(t, torch.Tensor):
@@ -69,14 +77,29 @@ def _begin(t, name):
     return load_library(), _DTYPE_CODE[t.dtype], t.device
 
 
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _check(t, name, shape, dtype, device):
+    """A tensor of this shape, dtype and device, contiguous (None passes). The
+    attributes are read once here; what is wrong is found out only then (a
+    single-token call spends as long on its checks as on its kernel)."""
+    if t is None or (isinstance(t, torch.Tensor) and t.shape == shape
+                     and t.dtype is dtype and t.device == device
+                     and t.is_contiguous()):
+        return
+    _check_slow(t, name, shape, dtype, device)
+
+
 def _call(fn, name, dev, *args):
     """The call on dev's current stream, with dev current while it is made (a
     launch goes to the current device)."""
     if torch.cuda.current_device() == dev.index:
-        rc = fn(*args, _stream(dev))
+        rc = fn(*args, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, _stream(dev))
+            rc = fn(*args, _raw_stream(dev.index))
     if rc != 0:
         raise OsdnError(rc, name)
 
@@ -84,15 +107,9 @@ def _call(fn, name, dev, *args):
 def _rows(t, name, B, T, C, dtype, dev):
     """Token rows [B,T,C] with any strides over tokens and batch entries:
     checks them and returns (batch stride, token stride)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if t.device != dev:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
-    if tuple(t.shape) != (B, T, C):
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape),
-                                                           (B, T, C)))
-    if t.dtype != dtype:
-        raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if not (isinstance(t, torch.Tensor) and t.device == dev and t.dtype is dtype
+            and t.shape == (B, T, C)):
+        _check_slow(t, name, (B, T, C), dtype, dev)
     if C > 1 and t.numel() and t.stride(2) != 1:
         raise ValueError("%s must be contiguous along its channels" % name)
     # strides of dimensions of one entry are never used and may be anything
