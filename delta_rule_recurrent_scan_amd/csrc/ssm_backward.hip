@@ -58,126 +58,122 @@ __device__ __forceinline__ void state_elem(int e, int ntl, int& p, int& n) {
 // BH .. 2 BH - 1 in reverse (dy, C, weights L_i0, from dS_T). Segment k counts
 // along the direction.
 // ---------------------------------------------------------------------------
+// Rows p of the state a workgroup walks (a slice of P: the rows do not meet),
+// 16 a wave.
 template <int P>
-constexpr int walk_waves() { return P / 16 < 4 ? P / 16 : 4; }
+constexpr int walk_rows() { return P < 64 ? P : 64; }
 
 template <int P, int N, typename Tin, bool WRITE>
-__global__ __launch_bounds__(64 * walk_waves<P>(), 2) void ssm_walk_kernel(
+__global__ __launch_bounds__(4 * walk_rows<P>(), 3) void ssm_walk_kernel(
     SsmArgs a, int nseg, int segch, const ChunkDecay<bwd_q<Tin>()>* decay, float* slots,
     float* slot_log, float* states) {
-  constexpr int Q = bwd_q<Tin>(), NW = walk_waves<P>(), NT = 64 * NW, PT = P / 16 / NW;
+  constexpr int Q = bwd_q<Tin>(), SP = walk_rows<P>(), NW = SP / 16, NT = 64 * NW;
   constexpr int NTL = N / 16;
-  constexpr int LN = N + 16 / sizeof(Tin), LP = P + 16 / sizeof(Tin);
+  constexpr int LN = N + 16 / sizeof(Tin), LP = SP + 16 / sizeof(Tin);
   __shared__ __attribute__((aligned(16))) Tin Ks[Q * LN];
   __shared__ __attribute__((aligned(16))) Tin Vs[Q * LP];
   __shared__ __attribute__((aligned(16))) ChunkDecay<Q> dec;
 
   const int lane = threadIdx.x & 63, w = wave_id();
   const int BH = a.B * a.H, nwg = WRITE ? nseg : nseg - 1;
-  const int stream = blockIdx.x / nwg, k = blockIdx.x % nwg;
+  const int ps = blockIdx.x % (P / SP), id = blockIdx.x / (P / SP);
+  const int stream = id / nwg, k = id % nwg;
   const bool rev = stream >= BH;
   const int bh = rev ? stream - BH : stream;
   const int b = bh / a.H, h = bh % a.H, sg = rev ? nseg - 1 - k : k;
   const int n = ssm_length(a.lengths, b, a.T), nch = (a.T + Q - 1) / Q;
   const size_t th = (size_t)bh * a.T;
   const size_t tg = ((size_t)b * a.G + h / (a.H / a.G)) * a.T;
-  const Tin* val = (const Tin*)(rev ? a.dy : a.x) + th * P;
+  const Tin* val = (const Tin*)(rev ? a.dy : a.x) + th * P + ps * SP;
   const Tin* key = (const Tin*)(rev ? a.Cm : a.Bm) + tg * N;
 
-  // S[pt][nt]: rows p = 4 (l / 16) + e of the wave's p tile, column n = l % 16
-  f32x4 S[PT][NTL];
+  // S[nt]: rows p = 4 (l / 16) + e of the wave's p tile, column n = l % 16
+  f32x4 S[NTL];
   const float* from = rev ? a.dST : a.S0;
-  const int tile0 = w * PT * NTL;  // S[0][0] to S[PT - 1][NTL - 1] follow
+  const int tile0 = (ps * NW + w) * NTL;
 #pragma unroll
-  for (int pt = 0; pt < PT; ++pt)
+  for (int nt = 0; nt < NTL; ++nt) {
+    const int at = ((tile0 + nt) * 64 + lane) * 4;
+    if (!WRITE || (k == 0 && !from)) {
+      S[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    } else if (k > 0) {
+      S[nt] = load4(slots + ((size_t)stream * (nseg - 1) + k - 1) * P * N + at);
+    } else {
 #pragma unroll
-    for (int nt = 0; nt < NTL; ++nt) {
-      const int at = ((tile0 + pt * NTL + nt) * 64 + lane) * 4;
-      if (!WRITE || (k == 0 && !from)) {
-        S[pt][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
-      } else if (k > 0) {
-        S[pt][nt] = load4(slots + ((size_t)stream * (nseg - 1) + k - 1) * P * N + at);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          int p, c;
-          state_elem(at + e, NTL, p, c);
-          S[pt][nt][e] = from[((size_t)bh * P + p) * N + c];
-        }
+      for (int e = 0; e < 4; ++e) {
+        int p, c;
+        state_elem(at + e, NTL, p, c);
+        S[nt][e] = from[((size_t)bh * P + p) * N + c];
       }
     }
+  }
   float logsum = 0.f;
 
   const int c0 = sg * segch, c1 = min(c0 + segch, nch);
   const int cn = min(c1, (n + Q - 1) / Q);  // chunks with tokens
   const int count = max(cn - c0, 0);
   auto chunk = [&](int i) { return rev ? cn - 1 - i : c0 + i; };
-  Stage<Q, N, Tin, NT, LN> fk;
-  Stage<Q, P, Tin, NT, LP> fv;
-  StageDecay<Q, NT> fd;
-  auto fetch = [&](int i) {
+  // rows two chunks ahead: at one workgroup a CU nothing else hides a fetch
+  Stage<Q, N, Tin, NT, LN> fk[2];
+  Stage<Q, SP, Tin, NT, LP, P> fv[2];
+  StageDecay<Q, NT> fd[2];
+  auto fetch = [&](int i, auto& k, auto& v, auto& d) {
     const int t = chunk(i) * Q, valid = n - t;
-    fk.fetch(key + (size_t)t * N, valid);
-    fv.fetch(val + (size_t)t * P, valid);
-    fd.fetch(decay + (size_t)bh * nch + chunk(i));
+    k.fetch(key + (size_t)t * N, valid);
+    v.fetch(val + (size_t)t * P, valid);
+    d.fetch(decay + (size_t)bh * nch + chunk(i));
   };
-  if (count) fetch(0);
-  for (int i = 0; i < count; ++i) {
+  auto step = [&](int i, auto& k, auto& v, auto& d) {
     __syncthreads();
-    fk.put(Ks);
-    fv.put(Vs);
-    fd.put(dec);
-    if (i + 1 < count) fetch(i + 1);
+    k.put(Ks);
+    v.put(Vs);
+    d.put(dec);
+    if (i + 2 < count) fetch(i + 2, k, v, d);
     if constexpr (WRITE) {
       float* out = states + ((size_t)stream * nch + chunk(i)) * P * N;
 #pragma unroll
-      for (int pt = 0; pt < PT; ++pt)
-#pragma unroll
-        for (int nt = 0; nt < NTL; ++nt)
-          store4(out + (tile0 + pt * NTL + nt) * 256 + (unsigned)(lane * 4), S[pt][nt]);
+      for (int nt = 0; nt < NTL; ++nt)
+        store4(out + (tile0 + nt) * 256 + (unsigned)(lane * 4), S[nt]);
     }
     __syncthreads();
     const float total = dec.total;
     logsum += dec.logtot;
-    Parts<Q, Tin> vw[PT];
-#pragma unroll
-    for (int pt = 0; pt < PT; ++pt) {
+    Parts<Q, Tin> vw;
+    {
       Frag<Q, Tin> vf;
-      vf.load_kmajor(Vs + (w * PT + pt) * 16, LP);
-      scale_parts<Q>(vf, rev ? dec.ent : dec.wx, vw[pt]);
+      vf.load_kmajor(Vs + w * 16, LP);
+      scale_parts<Q>(vf, rev ? dec.ent : dec.wx, vw);
     }
 #pragma unroll
     for (int nt = 0; nt < NTL; ++nt) {
       Frag<Q, Tin> kf;
       kf.load_kmajor(Ks + nt * 16, LN);
 #pragma unroll
-      for (int pt = 0; pt < PT; ++pt) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) S[pt][nt][e] *= total;
-        mma_parts(S[pt][nt], vw[pt], kf);
-      }
+      for (int e = 0; e < 4; ++e) S[nt][e] *= total;
+      mma_parts(S[nt], vw, kf);
     }
+  };
+  if (count > 0) fetch(0, fk[0], fv[0], fd[0]);
+  if (count > 1) fetch(1, fk[1], fv[1], fd[1]);
+  for (int i = 0; i < count; i += 2) {
+    step(i, fk[0], fv[0], fd[0]);
+    if (i + 1 < count) step(i + 1, fk[1], fv[1], fd[1]);
   }
 
   if constexpr (!WRITE) {
     float* out = slots + ((size_t)stream * (nseg - 1) + k) * P * N;
 #pragma unroll
-    for (int pt = 0; pt < PT; ++pt)
-#pragma unroll
-      for (int nt = 0; nt < NTL; ++nt)
-        store4(out + ((tile0 + pt * NTL + nt) * 64 + lane) * 4, S[pt][nt]);
-    if (threadIdx.x == 0) slot_log[(size_t)stream * (nseg - 1) + k] = logsum;
+    for (int nt = 0; nt < NTL; ++nt) store4(out + ((tile0 + nt) * 64 + lane) * 4, S[nt]);
+    if (threadIdx.x == 0 && ps == 0) slot_log[(size_t)stream * (nseg - 1) + k] = logsum;
   } else if (rev && k == nseg - 1 && a.dS0) {
 #pragma unroll
-    for (int pt = 0; pt < PT; ++pt)
+    for (int nt = 0; nt < NTL; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < NTL; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          int p, c;
-          state_elem(((tile0 + pt * NTL + nt) * 64 + lane) * 4 + e, NTL, p, c);
-          a.dS0[((size_t)bh * P + p) * N + c] = S[pt][nt][e];
-        }
+      for (int e = 0; e < 4; ++e) {
+        int p, c;
+        state_elem(((tile0 + nt) * 64 + lane) * 4 + e, NTL, p, c);
+        a.dS0[((size_t)bh * P + p) * N + c] = S[nt][e];
+      }
   }
 }
 
@@ -610,9 +606,10 @@ Plan make_plan(int B, int H, int G, int T, int P, int N, int Q) {
   Plan p{};
   const long long BH = (long long)B * H;
   p.nch = (T + Q - 1) / Q;
-  // walks: about 512 workgroups over both directions, segments of 4 chunks
+  // walks: a workgroup a CU over both directions, segments of 4 chunks
   // at least (a second segment costs a pass that writes no states)
-  long long want = BH > 0 ? (512 + 2 * BH - 1) / (2 * BH) : 1;
+  const long long streams = 2 * BH * (P < 64 ? 1 : P / 64);
+  long long want = streams > 0 ? (256 + streams - 1) / streams : 1;
   if (want > p.nch / 4) want = p.nch / 4;
   if (want < 1) want = 1;
   p.segch = p.nch > 0 ? (int)((p.nch + want - 1) / want) : 1;
@@ -638,7 +635,7 @@ template <int P, int N, typename Tin>
 int run_bwd(const SsmArgs& a, hipStream_t s) {
   const int BH = a.B * a.H, PN = P * N;
   const Plan p = make_plan(a.B, a.H, a.G, a.T, P, N, bwd_q<Tin>());
-  constexpr int NT = 64 * walk_waves<P>(), Q = bwd_q<Tin>();
+  constexpr int NT = 4 * walk_rows<P>(), SL = P / walk_rows<P>(), Q = bwd_q<Tin>();
   float* ws = (float*)((char*)a.ws + decay_bytes<Q>(a.B, a.H, a.T));
   float *slots = ws + p.slots, *logs = ws + p.logs, *states = ws + p.states;
   ChunkDecay<Q>* decay = (ChunkDecay<Q>*)a.ws;
@@ -649,7 +646,7 @@ int run_bwd(const SsmArgs& a, hipStream_t s) {
   if (p.nseg > 1) {
     tk = ktimer_before(s, "ssm_bwd_state");
     hipLaunchKernelGGL((ssm_walk_kernel<P, N, Tin, false>),
-                       dim3((unsigned)(2 * BH * (p.nseg - 1))), dim3(NT), 0, s, a, p.nseg,
+                       dim3((unsigned)(2 * BH * (p.nseg - 1) * SL)), dim3(NT), 0, s, a, p.nseg,
                        p.segch, decay, slots, logs, states);
     ktimer_after(s, tk);
     tk = ktimer_before(s, "ssm_bwd_chain");
@@ -658,7 +655,7 @@ int run_bwd(const SsmArgs& a, hipStream_t s) {
     ktimer_after(s, tk);
   }
   tk = ktimer_before(s, "ssm_bwd_walk");
-  hipLaunchKernelGGL((ssm_walk_kernel<P, N, Tin, true>), dim3((unsigned)(2 * BH * p.nseg)),
+  hipLaunchKernelGGL((ssm_walk_kernel<P, N, Tin, true>), dim3((unsigned)(2 * BH * p.nseg * SL)),
                      dim3(NT), 0, s, a, p.nseg, p.segch, decay, slots, logs, states);
   ktimer_after(s, tk);
   int rc = (int)hipGetLastError();
