@@ -9,7 +9,9 @@ resident in HBM, outputs and workspace preallocated. Other workloads time
 gdn2_forward, osdn_gated_forward or one recurrent decode call the same way.
 With --backward a step is the backward of the workload's forward instead
 (osdn_backward, osdn_gated_backward or gdn2_backward: every input's gradient
-from seeded output adjoints).
+from seeded output adjoints). The layer workloads time the operators of a state
+space layer in a row: residual norm, short convolutions, selective scan (or its
+single-token form) and gated norm, or with --backward their backward calls.
 
 Prints one JSON line: throughput (tokens/s = B*T per step time), the HBM
 roofline of the whole step (algorithmic bytes of the forward per its step
@@ -31,6 +33,7 @@ import numpy as np  # noqa: E402
 import torch  # noqa: E402
 
 import workloads as W  # noqa: E402
+from workloads import layers as WL  # noqa: E402
 
 HBM_PEAK_GBS = 8000.0          # MI355X HBM3E, GB/s
 MFMA_BF16_PEAK_TFLOPS = 2500.0  # dense bf16 MFMA
@@ -511,6 +514,141 @@ def metric_name(w, backward=False):
     return "OSDN forward tokens/s + % HBM/MFMA roofline, H=16 d=128 T=4096, 1 GPU"
 
 
+# ---------------------------------------------------------------------------
+# One state space layer's operators in a row
+# ---------------------------------------------------------------------------
+
+def layer_bytes(w, backward=False):
+    """Algorithmic HBM bytes of one step over a layer workload: every tensor
+    that the operators take or return, once per operator that does (an
+    operator's output is written by it and read by the next one)."""
+    s = 2 if w.dtype == "bf16" else 4
+    rows, C = w.B * w.T, w.channels
+    cx, cb = w.splits[0], w.splits[1]
+    conv = rows * (cx + 2 * cb)
+    state = w.B * w.H * w.P * w.N * 4
+    tail = w.B * (w.taps - 1) * (cx + 2 * cb)
+    steps = w.B * w.H * w.T * 4
+    if backward:
+        return (rows * C * (s + 4 + 4 + s)            # residual norm: dy, h; dh, dx
+                + 3 * conv * s                        # convolutions: x, dy, dx
+                + rows * cx * 5 * s                   # gated norm: x, z, dy; dx, dz
+                + rows * cx * 3 * s + rows * cb * 4 * s + 2 * steps)
+    fwd = rows * C * (s + 4 + 4 + s) + 2 * conv * s + rows * cx * 3 * s
+    scan = rows * cx * 2 * s + rows * cb * 2 * s + steps
+    if w.decode:
+        return fwd + scan + 2 * state + 2 * tail * s
+    return fwd + scan + state
+
+
+def layer_forward(w, a):
+    """The layer's forward on preallocated outputs: returns (step, tensors)."""
+    import delta_rule_recurrent_scan_amd as osdn
+    cx, cb, _, _ = w.splits
+    dev, t = a["proj"].device, a["proj"].dtype
+    cuts = (0, cx, cx + cb, cx + 2 * cb)
+    xs = [a["proj"][:, :, cuts[i]:cuts[i + 1]] for i in range(3)]
+    z = a["proj"][:, :, cuts[3]:]
+    dims = ((w.H, w.P), (w.G, w.N), (w.G, w.N))
+    e = lambda *s, d=t: torch.empty(s, dtype=d, device=dev)
+    o = dict(norm=torch.empty_like(a["block"]), h=torch.empty_like(a["residual"]),
+             conv=[e(w.B, n, w.T, d) for n, d in dims],
+             y=e(w.B, w.H, w.T, w.P), out=e(w.B, w.T, cx), xs=xs, z=z)
+    if not w.decode:
+        o["S"] = e(w.B, w.H, w.P, w.N, d=torch.float32)
+        ws = e(max(osdn.ssm_forward_workspace_bytes(
+            w.B, w.H, w.G, w.T, w.P, w.N, t), 1), d=torch.uint8)
+
+    def step():
+        osdn.residual_norm_forward(a["block"], a["norm"], a["residual"],
+                                   out=(o["norm"], o["h"]))
+        for i, (_, d) in enumerate(dims):
+            if w.decode:
+                osdn.short_conv_decode(xs[i], a["conv_w"][i], a["conv_state"][i],
+                                       a["conv_b"][i], head_dim=d, out=o["conv"][i])
+            else:
+                osdn.short_conv_forward(xs[i], a["conv_w"][i], a["conv_b"][i],
+                                        head_dim=d, out=(o["conv"][i], None))
+        x, b, c = o["conv"]
+        if w.decode:
+            osdn.ssm_decode(x, a["dt"], a["A"], b, c, a["S"], D=a["D"],
+                            dt_bias=a["dt_bias"], out=o["y"])
+        else:
+            osdn.ssm_forward(x, a["dt"], a["A"], b, c, D=a["D"],
+                             dt_bias=a["dt_bias"], out=(o["y"], o["S"]),
+                             workspace=ws)
+        osdn.gated_norm_forward(o["y"], z, a["gate_norm"], out=o["out"])
+    return step, o
+
+
+def layer_backward(w, a, o):
+    """The backward of layer_forward from its tensors: returns (step, the
+    gradients' dict)."""
+    import delta_rule_recurrent_scan_amd as osdn
+    dev, t = a["proj"].device, a["proj"].dtype
+    f32 = torch.float32
+    dims = ((w.H, w.P), (w.G, w.N), (w.G, w.N))
+    e = lambda *s, d=f32: torch.empty(s, dtype=d, device=dev)
+    x, b, c = o["conv"]
+    g = dict(gate=dict(x=torch.empty_like(o["y"]),
+                       z=e(*o["z"].shape, d=t), weight=e(w.H, w.P)),
+             scan=dict(x=torch.empty_like(x), B=torch.empty_like(b),
+                       C=torch.empty_like(c), dt=e(w.B, w.H, w.T), A=e(w.H),
+                       D=e(w.H), dt_bias=e(w.H), S0=None),
+             conv=[dict(x=e(*o["xs"][i].shape, d=t), weight=e(n * d, w.taps),
+                        bias=e(n * d),
+                        state=e(w.B, w.taps - 1, n * d, d=t))
+                   for i, (n, d) in enumerate(dims)],
+             norm=dict(x=torch.empty_like(a["block"]),
+                       residual=torch.empty_like(o["h"]), weight=e(w.channels)))
+    need = max([osdn.gated_norm_backward_workspace_bytes(w.B, w.H, w.T, w.P),
+                osdn.ssm_backward_workspace_bytes(w.B, w.H, w.G, w.T, w.P, w.N, t),
+                osdn.residual_norm_backward_workspace_bytes(w.B * w.T, w.channels)]
+               + [osdn.short_conv_backward_workspace_bytes(w.B, w.T, n, d, w.taps)
+                  for n, d in dims])
+    ws = e(max(need, 1), d=torch.uint8)   # the calls follow one another
+
+    def step():
+        osdn.gated_norm_backward(o["y"], o["z"], a["gate_norm"], a["dy"],
+                                 out=g["gate"], workspace=ws)
+        osdn.ssm_backward(x, a["dt"], a["A"], b, c, g["gate"]["x"], D=a["D"],
+                          dt_bias=a["dt_bias"], out=g["scan"], workspace=ws)
+        for i, (_, d) in enumerate(dims):
+            osdn.short_conv_backward(o["xs"][i], a["conv_w"][i],
+                                     g["scan"]["xBC"[i]], a["conv_b"][i],
+                                     head_dim=d, out=g["conv"][i], workspace=ws)
+        osdn.residual_norm_backward(a["dnorm"], o["h"], a["norm"], out=g["norm"],
+                                    workspace=ws)
+    return step, g
+
+
+def layer_bench(w, args):
+    a = WL.make_layer(w, "cuda:0")
+    step, o = layer_forward(w, a)
+    if args.backward:
+        step()
+        step, _ = layer_backward(w, a, o)
+    ms, per_step, kt, cold = timed_steps(step, args)
+    alg = layer_bytes(w, args.backward)
+    kind = ("backward" if args.backward else
+            "single tokens" if w.decode else "forward")
+    print(json.dumps({
+        "metric": "state space layer operators, %s tokens/s + %% HBM roofline, "
+                  "B=%d H=%d d=%d T=%d, 1 GPU" % (kind, w.B, w.H, w.P, w.T),
+        "value": w.B * w.T / (ms * 1e-3), "unit": "tokens/s", "n_gpus": 1,
+        "steps": args.steps, "warmup": args.warmup, "ms_per_step": ms,
+        "higher_is_better": True, "scaling": "weak", "vs_baseline": None,
+        "dtype": w.dtype, "data": "synthetic",
+        "config": {"workload": w.name, "B": w.B, "H": w.H, "G": w.G, "T": w.T,
+                   "P": w.P, "N": w.N, "taps": w.taps, "channels": w.channels,
+                   "pass": kind},
+        "roofline": {"scope": "whole step", "bound": "hbm",
+                     "achieved": alg / (ms * 1e-3) / 1e9, "peak": HBM_PEAK_GBS,
+                     "unit": "GB/s", "frac": alg / (ms * 1e-3) / 1e9 / HBM_PEAK_GBS,
+                     "alg_bytes": alg, "ms": ms},
+        "step_ms": per_step, "cold_step": cold, "kernels": kt}), flush=True)
+
+
 def calibrate_copy(args):
     n = 512 * 1024 * 1024 // 4
     src = torch.ones(n, dtype=torch.float32, device="cuda:0")
@@ -534,7 +672,7 @@ def main():
     ap.add_argument("--steps", type=int, default=20)
     ap.add_argument("--warmup", type=int, default=30)
     ap.add_argument("--workload", default="osdn-1.3b-apf",
-                    choices=[w.name for w in W.WORKLOADS])
+                    choices=[w.name for w in W.WORKLOADS + WL.LAYERS])
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--backward", action="store_true",
                     help="time the backward of the workload's forward")
@@ -555,11 +693,15 @@ def main():
         calibrate_copy(args)
         return
 
-    w = W.BY_NAME[args.workload]
-    if args.backward and w.state:
+    layer = WL.BY_NAME.get(args.workload)
+    w = layer or W.BY_NAME[args.workload]
+    if args.backward and (w.decode if layer else w.state):
         print("--backward times a whole-sequence backward; pick a forward "
               "workload", file=sys.stderr)
         sys.exit(2)
+    if layer:
+        layer_bench(w, args)
+        return
     inp = W.make_inputs(w)
     cot = W.make_cotangents(w) if args.backward else None
     cpu = (None if args.no_cpu_baseline

@@ -358,7 +358,7 @@ int ssm_backward(int B, int H, int G, int T, int P, int N, int dtype, const void
   const size_t need = ssm_backward_workspace_bytes(B, H, G, T, P, N, dtype);
   if (!workspace_ok(workspace, workspace_bytes, need)) return OSDN_ERR_WORKSPACE;
   if (!aligned16(x) || !aligned16(Bm) || !aligned16(Cm) || !aligned16(dy) || !aligned16(dx) ||
-      !aligned16(dB) || !aligned16(dC))
+      !aligned16(dB) || !aligned16(dC) || !aligned16(S0) || !aligned16(dS_T) || !aligned16(dS0))
     return OSDN_ERR_MISALIGNED;
   const size_t tx = BH * T * P * es, tg = (size_t)B * G * T * N * es, hb = (size_t)H * 4;
   const Range ins[] = {rng(x, tx), rng(dt, BH * T * 4), rng(A, hb), rng(Bm, tg), rng(Cm, tg),

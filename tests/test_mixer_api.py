@@ -158,6 +158,41 @@ def test_ssm_refusals():
     assert dec(T=0, x=None, y=None) == OK
 
 
+@needs_lib
+def test_ssm_backward_refusals():
+    L = osdn.load_library()
+    assert L.ssm_backward_workspace_bytes(1, 3, 2, 256, 64, 64, BF16) == 0
+    assert L.ssm_backward_workspace_bytes(1, 2, 1, 256, 48, 64, BF16) == 0
+    need = L.ssm_backward_workspace_bytes(1, 2, 1, 256, 64, 64, BF16)
+    assert need > 0 and need % 256 == 0
+    at = {n: 0x1000000 * (i + 1) for i, n in enumerate(
+        ("x", "dt", "A", "B", "C", "D", "bias", "S0", "dy", "dST", "gx", "gdt", "gA",
+         "gB", "gC", "gD", "gbias", "gS0", "ws"))}
+
+    def bwd(nb=1, H=2, G=1, T=256, P=64, N=64, code=BF16, wsb=need, le=None, **kw):
+        p = dict(at, **kw)
+        return L.ssm_backward(nb, H, G, T, P, N, code, p["x"], p["dt"], p["A"], p["B"],
+                              p["C"], p["D"], p["bias"], 1, p["S0"], le, p["dy"],
+                              p["dST"], p["gx"], p["gdt"], p["gA"], p["gB"], p["gC"],
+                              p["gD"], p["gbias"], p["gS0"], p["ws"], wsb, None)
+    for n in ("x", "dt", "A", "B", "C", "dy", "gx", "gdt", "gA", "gB", "gC"):
+        assert bwd(**{n: None}) == NULL_ARG, n
+    for bad in (dict(nb=-1), dict(G=0), dict(H=3, G=2), dict(T=-1)):
+        assert bwd(**bad) == BAD_DIMS, bad
+    for bad in (dict(P=16), dict(N=96), dict(code=2)):
+        assert bwd(**bad) == UNSUPPORTED, bad
+    for bad in (dict(ws=None), dict(wsb=need - 1), dict(ws=at["ws"] + 16)):
+        assert bwd(**bad) == WORKSPACE, bad
+    for n in ("x", "B", "C", "S0", "dy", "dST", "gx", "gB", "gC", "gS0"):
+        assert bwd(**{n: at[n] + 4}) == MISALIGNED, n
+    for a, b in (("gx", "x"), ("gx", "dy"), ("gdt", "dt"), ("gB", "B"), ("gC", "gB"),
+                 ("gS0", "dST"), ("gS0", "S0"), ("gA", "A"), ("gD", "gA"),
+                 ("ws", "gx"), ("ws", "C"), ("gbias", "bias")):
+        assert bwd(**{a: at[b]}) == ALIASING, (a, b)
+    assert bwd(le=at["gdt"]) == ALIASING
+    assert bwd(H=0, G=0, x=None, gx=None) == OK
+
+
 def test_binding_refuses_cpu_tensors_and_other_types():
     t = torch.zeros(1, 4, 64)
     w = torch.zeros(64, 4)
