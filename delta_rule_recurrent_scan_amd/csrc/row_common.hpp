@@ -3,6 +3,7 @@
 #pragma once
 
 #include "device_common.hpp"
+#include "pack_common.hpp"
 
 namespace osdn {
 

@@ -4,6 +4,7 @@
 #include "device_common.hpp"
 #include "launch.hpp"
 #include "mixer.hpp"
+#include "pack_common.hpp"
 
 namespace osdn {
 
