@@ -234,7 +234,8 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
   __shared__ __attribute__((aligned(16))) ChunkDecay<Q> decs[2];
   // sums of a head, read while the next one is worked on
   struct Sums {
-    float row[JH][Q], diag[Q], col[QT][Q], w[NTL][Q], u[NTL][Q], dot[kWaves], dd[kWaves];
+    double row[JH][Q], col[QT][Q];
+    float diag[Q], w[NTL][Q], u[NTL][Q], dot[kWaves], dd[kWaves];
   };
   __shared__ Sums acc2[2];
 
@@ -271,7 +272,8 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
     auto finish = [&](int h, int lane, int zero) {
       const Sums& z = acc2[((h - h0) & 1) + zero];
       const ChunkDecay<Q>& dec = decs[((h - h0) & 1) + zero];
-      float R = 0.f, col = 0.f, wi = 0.f, uj = 0.f, own = 0.f, step = 0.f, slope = 0.f;
+      double R = 0., col = 0., wi = 0., uj = 0., own = 0., step = 0.;
+      float slope = 0.f;
       if (lane < Q) {
 #pragma unroll
         for (int q = 0; q < JH; ++q) R += z.row[q][lane];
@@ -286,20 +288,21 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
         slope = dec.slope[lane];
         own = z.diag[lane] + col + uj;
       }
-      float dot = 0.f, dd = 0.f;
+      double dot = 0.;
+      float dd = 0.f;
 #pragma unroll
       for (int q = 0; q < kWaves; ++q) {
         if (q < NTL) dot += z.dot[q];
         dd += z.dd[q];
       }
-      const float gt = wave_suffix_sum(R - col * step + wi) + wave_prefix_before(uj * step) +
-                       dec.total * dot;
+      const double gt = wave_suffix_sum(R - col * step + wi) + wave_prefix_before(uj * step) +
+                        dec.total * dot;
       const bool in = lane < Q && lane < valid;
-      const float draw = in ? (own + a.A[h] * gt) * slope : 0.f;
+      const float draw = in ? (float)((own + a.A[h] * gt) * slope) : 0.f;
       __builtin_amdgcn_raw_buffer_store_b32(
           __float_as_uint(draw),
           make_buffer(a.ddt + ((size_t)b * a.H + h) * a.T + t0, rows * 4), lane * 4, 0, 0);
-      const float sa = wave_sum(in ? step * gt : 0.f), sb = wave_sum(draw);
+      const float sa = wave_sum(in ? (float)(step * gt) : 0.f), sb = wave_sum(draw);
       if (lane == 0) {
         sums[h] = sa;
         sums[a.H + h] = dd;
@@ -371,11 +374,12 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
       if (h + 1 < h1) fetch(h + 1);
       __syncthreads();
 
-      // scores of dy and x, K and Z, and the pairs' sums
+      // scores of dy and x, K and Z, and the pairs' sums (in 64 bits: a token's
+      // decay gradient is the difference of rows' and columns' running sums)
       {
         Frag<P, Tin> yf;
         yf.load(ys + qi * 16 * LP, LP);
-        float rsum = 0.f;
+        double rsum = 0.;
         const int i = qi * 16 + lc;
 #pragma unroll
         for (int m = 0; m < JM; ++m) {
@@ -399,8 +403,8 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
                 z.diag[j] = v;  // no decay between: not part of g
                 v = 0.f;
               }
-              rsum += v * dj[r];
-              const float sum = row16_sum(v);
+              rsum += (double)v * dj[r];
+              const double sum = row16_sum((double)v);
               if (lc == 0) z.col[qi][j] = sum;
             }
           } else if (lc == 0) {
@@ -410,7 +414,8 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
           store4(ks + i * LQ + jt * 16 + g4, kk);
           store4(zs + i * LQ + jt * 16 + g4, zz);
         }
-        rsum = add_swap32(add_swap16(rsum));
+        rsum += __shfl_xor(rsum, 16, 64);
+        rsum += __shfl_xor(rsum, 32, 64);
         if (lane < 16) z.row[jh][i] = rsum;
       }
       // what the entering state and the leaving adjoint give to dC and dB, and

@@ -169,19 +169,44 @@ __device__ __forceinline__ f32x4 tile_steps(const ChunkDecay<Q>& d, int jt) {
   return *reinterpret_cast<const f32x4*>(d.dt + jt * 16 + acc_row(0));
 }
 
-// Inclusive sum of lanes l .. 63, and exclusive sum of lanes 0 .. l - 1.
-__device__ __forceinline__ float wave_suffix_sum(float x) {
+// row16_sum in 64 bits.
+template <int CTRL>
+__device__ __forceinline__ double dpp_d(double x) {
+  const unsigned long long u = __builtin_bit_cast(unsigned long long, x);
+  const unsigned lo = __builtin_amdgcn_update_dpp(0, (int)(unsigned)u, CTRL, 0xf, 0xf, false);
+  const unsigned hi =
+      __builtin_amdgcn_update_dpp(0, (int)(unsigned)(u >> 32), CTRL, 0xf, 0xf, false);
+  return __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
+}
+__device__ __forceinline__ double row16_sum(double x) {
+  x += dpp_d<0xB1>(x);
+  x += dpp_d<0x4E>(x);
+  x += dpp_d<0x141>(x);
+  x += dpp_d<0x140>(x);
+  return x;
+}
+
+// Inclusive sum of lanes l .. 63, and exclusive sum of lanes 0 .. l - 1. In 64
+// bits: what the sums take in cancels in part (a chunk's pairs enter a token's
+// decay gradient as the difference of two running sums).
+__device__ __forceinline__ double wave_suffix_sum(double x) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const float y = __shfl_down(x, d, 64);
+    const double y = __shfl_down(x, d, 64);
     if (lane + d < 64) x += y;
   }
   return x;
 }
-__device__ __forceinline__ float wave_prefix_before(float x) {
-  const float y = __shfl_up(wave_prefix_sum(x), 1, 64);
-  return (threadIdx.x & 63) ? y : 0.f;
+__device__ __forceinline__ double wave_prefix_before(double x) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const double y = __shfl_up(x, d, 64);
+    if (lane >= d) x += y;
+  }
+  const double y = __shfl_up(x, 1, 64);
+  return lane ? y : 0.;
 }
 
 // acc += A * B^T over the first kmax (a multiple of 16) of the K indices.
