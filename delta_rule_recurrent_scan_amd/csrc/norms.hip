@@ -11,13 +11,19 @@
 // All are bound by HBM: every input is read and every output written once,
 // 16 bytes a lane, with the sums in 32 bits. A head is 4, 8 or 16 adjacent
 // lanes; a row of the residual norm is one wave (up to 4096 elements, no
-// barrier) or four, held in registers between the sum and the scaling.
+// barrier) or four, held in registers between the sum and the scaling. In bf16,
+// where a copy of 256 MiB reaches 5.4 TB/s: gated norm of 16384 rows of 16 heads of
+// 128, 201 MB, 43 us (4.7 TB/s); residual norm of 16384 rows of 2048 on a 32-bit
+// stream, 403 MB, 78 us (5.2 TB/s).
 //
 // Backward of n = v r, y = n * weight (r the reciprocal root):
 //   dn = dy * weight,  dv = r (dn - n mean(n dn)),  dweight = sum dy n
 // Weight gradients stay in registers while a workgroup walks its rows, are
 // added over its row lanes in LDS and leave as one partial a workgroup,
-// summed in a fixed order by column_sum.
+// summed in a fixed order by column_sum. Gated: 16384 rows of 8 heads of 64, 84 MB,
+// 19 us and 2 us for the sum; residual: 4097 rows of 1021, 42 MB, 14 us and 2 us
+// (unaligned rows take the same wide accesses as aligned ones; element by element
+// it was 69 us).
 #include "launch.hpp"
 #include "mixer.hpp"
 #include "row_common.hpp"

@@ -6,7 +6,9 @@
 // over 16 lanes in 16-byte pieces, so a load instruction of a lane group covers
 // 256 contiguous bytes, and the readout's row sums are row-of-16 DPP sums with
 // no barrier. The state may be written over itself: every element is read
-// and written by the same thread.
+// and written by the same thread. 2048 states of 128 x 128, 270 MB: 41 us of
+// kernel, 6.6 TB/s (part of the states is still in the memory-side cache from the
+// call before).
 #include "launch.hpp"
 #include "mixer.hpp"
 #include "row_state.hpp"
