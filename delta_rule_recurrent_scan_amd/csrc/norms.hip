@@ -22,8 +22,8 @@
 // added over its row lanes in LDS and leave as one partial a workgroup,
 // summed in a fixed order by column_sum. Gated: 16384 rows of 8 heads of 64, 84 MB,
 // 19 us and 2 us for the sum; residual: 4097 rows of 1021, 42 MB, 14 us and 2 us
-// (unaligned rows take the same wide accesses as aligned ones; element by element
-// it was 69 us).
+// (with a partial a wave and unaligned rows element by element it was 69 us: they
+// take the same wide accesses as aligned ones now).
 #include "launch.hpp"
 #include "mixer.hpp"
 #include "row_common.hpp"

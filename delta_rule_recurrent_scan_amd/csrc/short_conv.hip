@@ -13,9 +13,10 @@
 // of a row; a segment re-reads W - 1 rows of its predecessor (from L2). A
 // head of 32, 64 or 128 channels is 4, 8 or 16 adjacent lanes, and its norm a
 // DPP sum: no LDS. B 4, T 4096, 4096 channels of bf16 with the norm, 268 MB: 63
-// us, 4.3 TB/s, where a copy of 256 MiB reaches 5.4 TB/s; 4 channels a thread
-// with 4 rows in flight took 84 us. A single token is the launch alone (3 us of
-// kernel for 2048 channels).
+// us, 4.3 TB/s, where a copy of 256 MiB reaches 5.4 TB/s. Rows are fetched raw,
+// eight in flight, and addressed by pointers that advance: widened at once, with an
+// address formed a token, they took 84 us. A single token of 2048 channels is the
+// launch alone.
 //
 // Backward, with dv = r (dy - v r^2 <v, dy>) for the norm (r = rsqrt(..)),
 // du = dv * sigmoid(u) (1 + u (1 - sigmoid(u))) and the inputs with their
@@ -26,8 +27,8 @@
 // in registers over the segment, are added over the workgroup's segments in
 // LDS, and leave as one partial a workgroup (summed in a fixed order by
 // column_sum). 8 padded sequences of up to 2048 tokens, 2048 channels of bf16, at
-// most 201 MB: 41 us, with 4 channels a thread (at 8, 82 us: the open rows, the
-// inputs and the weights do not fit the registers of enough waves).
+// most 201 MB: 41 us; with 8 channels a thread and rows widened at once it was 82
+// us (the open rows, the inputs and the weights leave room for few waves).
 #include "launch.hpp"
 #include "mixer.hpp"
 #include "row_common.hpp"

@@ -6,9 +6,10 @@
 // over 16 lanes in 16-byte pieces, so a load instruction of a lane group covers
 // 256 contiguous bytes, and the readout's row sums are row-of-16 DPP sums with
 // no barrier. The state may be written over itself: every element is read
-// and written by the same thread. 2048 states of 128 x 128, 270 MB: 41 us of
-// kernel, 6.6 TB/s (part of the states is still in the memory-side cache from the
-// call before).
+// and written by the same thread. 2048 states of 128 x 128, 270 MB: 41 us
+// when the same states move on call after call (part of them is still in the
+// memory-side cache), 51 us with other states each call, 5.3 TB/s, which is what
+// a copy of that size reaches.
 #include "launch.hpp"
 #include "mixer.hpp"
 #include "row_state.hpp"

@@ -26,6 +26,9 @@ Modules:
   OSDN on a per-channel-decay backbone and of GDN-2 (gate-aware: decay,
   erase and write gates), pinned by central differences of ``osdn_ref``,
   ``osdn_gated_ref`` and ``gdn2_ref`` in ``tests/test_oracle_backward.py``.
+* ``mixer``     the operators around the recurrences in a layer (short
+  convolution, selective scan, gated norm, residual norm) and their adjoints,
+  pinned by central differences and closed forms in ``tests/test_oracle_mixer.py``.
 * ``exact``     the same recurrences in exact rational arithmetic
   (``fractions.Fraction``) plus an independent closed-form unrolling of the
   state as a sum of products of transition matrices, for tiny inputs.
