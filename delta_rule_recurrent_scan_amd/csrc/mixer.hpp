@@ -15,6 +15,12 @@ namespace osdn {
 // times 256 / cx rows.
 constexpr int kRowThreads = 256;
 constexpr int kVec = 8;
+
+// A launch holds fewer than 2^32 threads; a call that needs more is refused.
+inline bool grid_ok(long long blocks, int threads) {
+  return blocks < (1LL << 32) / threads;
+}
+
 inline int row_cx(long long ngroups) {
   int cx = 1;
   while (cx < 64 && cx < ngroups) cx *= 2;

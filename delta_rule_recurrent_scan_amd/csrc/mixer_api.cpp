@@ -15,7 +15,8 @@ int status(int rc) {
   return rc == 0 ? OSDN_OK : OSDN_ERR_HIP;
 }
 
-// Channels and rows that the kernels index with 32 bits.
+// Channels, rows and tokens that the kernels index with 32 bits.
+constexpr int kMaxTokens = 1 << 30;
 bool width_ok(long long c) { return c <= (1 << 28); }
 
 bool workspace_ok(const void* ws, size_t bytes, size_t need) {
@@ -31,7 +32,8 @@ size_t span(int B, int T, long long C, long long bs, long long ts, size_t es) {
 // Sizes of a convolution call; OSDN_OK or the status to return.
 int conv_dims(int B, int T, int H, int D, int W, int dtype, long long xbs, long long xts,
               int l2norm) {
-  if (B < 0 || T < 0 || H < 0 || D < 1 || xbs < 0 || xts < 0) return OSDN_ERR_BAD_DIMS;
+  if (B < 0 || T < 0 || H < 0 || D < 1 || T > kMaxTokens || xbs < 0 || xts < 0)
+    return OSDN_ERR_BAD_DIMS;
   if (!width_ok((long long)H * D)) return OSDN_ERR_BAD_DIMS;
   if (W < 2 || W > 4 || !dtype_ok(dtype) || (l2norm && !dim_ok(D))) return OSDN_ERR_UNSUPPORTED;
   return OSDN_OK;
@@ -83,7 +85,7 @@ int res_dims(long long R, int C, int dtype, int res_dtype) {
 
 int ssm_dims(int B, int H, int G, int T, int P, int N, int dtype) {
   if (B < 0 || H < 0 || G < 0 || T < 0 || (H > 0 && (G == 0 || H % G != 0)) ||
-      (long long)B * H > (1LL << 28))
+      (long long)B * H > (1LL << 28) || T > kMaxTokens)
     return OSDN_ERR_BAD_DIMS;
   if (!dim_ok(P) || !dim_ok(N) || !dtype_ok(dtype)) return OSDN_ERR_UNSUPPORTED;
   return OSDN_OK;

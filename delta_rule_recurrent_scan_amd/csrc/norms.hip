@@ -159,7 +159,9 @@ template <typename Tin>
 int run_gated(const GatedNormArgs& a, hipStream_t s) {
   const int ng = a.H * a.D / 8, cx = row_cx(ng), per = kRowThreads / cx * kGateRows;
   const long long rows = (long long)a.B * a.T;
-  const dim3 grid((unsigned)((ng + cx - 1) / cx * ((rows + per - 1) / per)));
+  const long long wgs = (ng + cx - 1) / cx * ((rows + per - 1) / per);
+  if (!grid_ok(wgs, kRowThreads)) return -1;
+  const dim3 grid((unsigned)wgs);
   const int tk = ktimer_before(s, "gated_norm");
   if (z_aligned(a)) {
     hipLaunchKernelGGL((gated_norm_kernel<Tin, true>), grid, dim3(kRowThreads), 0, s, a, cx);
@@ -173,6 +175,7 @@ int run_gated(const GatedNormArgs& a, hipStream_t s) {
 // Row blocks of the backward: about 1024 workgroups in all (4 a CU), each
 // with one partial row of the weight gradient.
 int gate_row_blocks(int B, int H, int T, int D) {
+  if (H == 0) return 0;
   const int ng = H * D / 8, cx = row_cx(ng), per = kRowThreads / cx;
   const long long rows = (long long)B * T, ncb = (ng + cx - 1) / cx;
   long long most = 1024 / ncb, need = (rows + per - 1) / per;
@@ -372,6 +375,7 @@ template <typename Tin, typename Tr, bool ALN, int NV, int WPR>
 int run_res(const ResidualNormArgs& a, int bwd, hipStream_t s) {
   if (!bwd) {
     const int rpw = kResWaves / WPR;
+    if (!grid_ok((a.R + rpw - 1) / rpw, kResThreads)) return -1;
     const int tk = ktimer_before(s, "residual_norm");
     hipLaunchKernelGGL((residual_norm_kernel<Tin, Tr, ALN, NV, WPR>),
                        dim3((unsigned)((a.R + rpw - 1) / rpw)), dim3(kResThreads), 0, s, a);

@@ -419,7 +419,9 @@ int run_conv(const ConvArgs& a, hipStream_t s) {
   const int nseg = a.T > 0 ? (a.T + seg - 1) / seg : 1;
   const long long rows = (long long)a.B * nseg;
   const int per = kRowThreads / cx;
-  const dim3 grid((unsigned)((ng + cx - 1) / cx * ((rows + per - 1) / per)));
+  const long long wgs = (ng + cx - 1) / cx * ((rows + per - 1) / per);
+  if (!grid_ok(wgs, kRowThreads)) return -1;
+  const dim3 grid((unsigned)wgs);
   const size_t m = 16 - 1, es = sizeof(Tin);
   const bool aln = a.D % 8 == 0 && ((size_t)a.x & m) == 0 && ((size_t)a.y & m) == 0 &&
                    ((size_t)a.state0 & m) == 0 && ((size_t)a.stateT & m) == 0 &&
@@ -462,7 +464,9 @@ int run_conv_bwd(const ConvBackwardArgs& p, hipStream_t s) {
   const ConvArgs& a = p.f;
   const int C = a.H * a.D, ng = (C + kBwdV - 1) / kBwdV;
   const BwdGrid g = bwd_grid(a.B, a.T, C, W);
-  const dim3 grid((unsigned)((ng + g.cx - 1) / g.cx * g.parts));
+  const long long wgs = (ng + g.cx - 1) / g.cx * (long long)g.parts;
+  if (!grid_ok(wgs, kRowThreads)) return -1;
+  const dim3 grid((unsigned)wgs);
   const size_t m = 16 - 1, es = sizeof(Tin);
   const bool aln = a.D % 8 == 0 && ((size_t)a.x & m) == 0 && ((size_t)p.dy & m) == 0 &&
                    ((size_t)a.state0 & m) == 0 && ((size_t)p.dstateT & m) == 0 &&

@@ -654,6 +654,11 @@ int run_bwd(const SsmArgs& a, hipStream_t s) {
   float* ws = (float*)((char*)a.ws + decay_bytes<Q>(a.B, a.H, a.T));
   float *slots = ws + p.slots, *logs = ws + p.logs, *states = ws + p.states;
   ChunkDecay<Q>* decay = (ChunkDecay<Q>*)a.ws;
+  const long long chunks = (long long)BH * p.nch, streams = 2ll * BH * SL;
+  const long long wgs = (long long)a.B * a.G * p.nch * p.parts;
+  if (!grid_ok((chunks + 3) / 4, 256) || !grid_ok(streams * p.nseg, NT) ||
+      !grid_ok(wgs, kThreads))
+    return -1;
   launch_decay<Q>(a, decay, s);
   if (BH == 0)  // an empty batch: zeros for the parameters
     return launch_column_sum(ws, 0, 3 * a.H, a.H, 1, a.dA, a.dD, a.dbias, s);
@@ -661,7 +666,7 @@ int run_bwd(const SsmArgs& a, hipStream_t s) {
   if (p.nseg > 1) {
     tk = ktimer_before(s, "ssm_bwd_state");
     hipLaunchKernelGGL((ssm_walk_kernel<P, N, Tin, false>),
-                       dim3((unsigned)(2 * BH * (p.nseg - 1) * SL)), dim3(NT), 0, s, a, p.nseg,
+                       dim3((unsigned)(streams * (p.nseg - 1))), dim3(NT), 0, s, a, p.nseg,
                        p.segch, decay, slots, logs, states);
     ktimer_after(s, tk);
     tk = ktimer_before(s, "ssm_bwd_chain");
@@ -670,7 +675,7 @@ int run_bwd(const SsmArgs& a, hipStream_t s) {
     ktimer_after(s, tk);
   }
   tk = ktimer_before(s, "ssm_bwd_walk");
-  hipLaunchKernelGGL((ssm_walk_kernel<P, N, Tin, true>), dim3((unsigned)(2 * BH * p.nseg * SL)),
+  hipLaunchKernelGGL((ssm_walk_kernel<P, N, Tin, true>), dim3((unsigned)(streams * p.nseg)),
                      dim3(NT), 0, s, a, p.nseg, p.segch, decay, slots, logs, states);
   ktimer_after(s, tk);
   int rc = (int)hipGetLastError();
@@ -681,7 +686,7 @@ int run_bwd(const SsmArgs& a, hipStream_t s) {
                      ws + p.parts_at + (size_t)p.parts * GTN, p.parts, p.hper};
     tk = ktimer_before(s, "ssm_bwd");
     hipLaunchKernelGGL((ssm_bwd_chunk_kernel<P, N, Tin>),
-                       dim3((unsigned)((long long)a.B * a.G * p.nch * p.parts)), dim3(kThreads),
+                       dim3((unsigned)wgs), dim3(kThreads),
                        0, s, a, o, decay);
     ktimer_after(s, tk);
     if (p.parts > 1) {

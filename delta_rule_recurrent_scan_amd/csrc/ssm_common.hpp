@@ -102,8 +102,10 @@ struct ChunkDecay {
   __device__ __forceinline__ void fill(float step, float sl, float A) {
     constexpr int NB = Q / 16;
     const int t = threadIdx.x & 63;
+    // below -1e4 a decay is zero whatever it is; kept finite there, so that the
+    // sums' rounding errors stay numbers
     const float p = step * A;
-    const Log2f l = {p, fmaf(step, A, -p)};
+    const Log2f l = p < -1e4f ? Log2f{-1e4f, 0.f} : Log2f{p, fmaf(step, A, -p)};
     const Log2f u = row16_prefix(l), d = row16_suffix_after(l);
     Log2f bs[NB];
 #pragma unroll

@@ -62,6 +62,7 @@ __global__ __launch_bounds__(kDecThreads) void ssm_decode_kernel(SsmArgs a) {
 
 template <int P, int N>
 int run_decode(const SsmArgs& a, hipStream_t s) {
+  if (!grid_ok((long long)a.B * a.H, kDecThreads)) return -1;
   const int tk = ktimer_before(s, "ssm_decode");
   if (a.bf16) {
     hipLaunchKernelGGL((ssm_decode_kernel<P, N, __bf16>), dim3(a.B * a.H), dim3(kDecThreads), 0,

@@ -261,11 +261,13 @@ int run_scan(const SsmArgs& a, hipStream_t s) {
   const int BH = a.B * a.H, PN = P * N;
   const Segments g = segments(a.B, a.H, a.T, scan_q<Tin>());
   constexpr int Q = scan_q<Tin>();
+  constexpr int NT = 64 * scan_waves<P>();
+  const long long chunks = (long long)BH * ((a.T + Q - 1) / Q);
+  if (!grid_ok((chunks + 3) / 4, 256) || !grid_ok((long long)BH * g.n, NT)) return -1;
   ChunkDecay<Q>* dc = (ChunkDecay<Q>*)a.ws;
   launch_decay<Q>(a, dc, s);
   float* st = (float*)((char*)a.ws + decay_bytes<Q>(a.B, a.H, a.T));
   float* lg = st + (size_t)BH * g.n * PN;
-  constexpr int NT = 64 * scan_waves<P>();
   if (g.n > 1) {
     int tk = ktimer_before(s, "ssm_state");
     hipLaunchKernelGGL((ssm_scan_kernel<P, N, Tin, false>), dim3((unsigned)(BH * (g.n - 1))),

@@ -163,3 +163,13 @@ def test_residual_norm_in_place_and_empty():
     assert y.shape == (0, 256)
     d = osdn.residual_norm_backward(e, e, w)
     assert not d["weight"].any()
+
+
+@pytest.mark.gpu
+def test_gated_norm_backward_without_heads():
+    """No heads: a shared weight's gradient is zeros."""
+    x, z, dy = (torch.zeros(s, device=DEV) for s in ((2, 0, 3, 64), (2, 3, 0), (2, 3, 0)))
+    for weight in (torch.ones(64, device=DEV), torch.ones(0, 64, device=DEV)):
+        g = osdn.gated_norm_backward(x, z, weight, dy)
+        assert g["weight"].shape == weight.shape and not g["weight"].any()
+    assert osdn.gated_norm_forward(x, z, torch.ones(64, device=DEV)).shape == (2, 3, 0)

@@ -321,3 +321,24 @@ def test_backward_against_differences():
         # noise over 2h, and h^2 times a third derivative of the gradient's size
         scale = float(got[n].double().norm() * d.double().norm())
         assert abs(num - ana) <= 2e-3 * scale + 5e-2, (n, num, ana)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("A", [1e30, 3e38])
+def test_decays_beyond_any_exponent(dt, A):
+    """Products dt A up to the end of fp32's range and past it: every decay is
+    zero, and nothing is NaN."""
+    a, k = inputs(1, 2, 1, 150, 64, 32, dt, seed=11)
+    a["A"] = torch.tensor([-A, -1.0], device=DEV)
+    a["dt"][:, :, ::5] = 30.0
+    got = osdn.ssm_forward(**a, **k)
+    check_forward(a, k, got)
+    dy, dS = adjoints(a, k)
+    g = osdn.ssm_backward(**a, dy=dy, dS_T=dS, **k)
+    assert all(bool(torch.isfinite(t).all()) for t in g.values())
+    assert float(g["A"][0]) == 0.0
+    check_l2({n: g[n] for n in ("x", "B", "C")},
+             M.ssm_backward_ref(**ref_args(a, k)[0], dy=f64(dy), dS_T=f64(dS),
+                                **ref_args(a, k)[1]), ("x", "B", "C"),
+             3 * U[BF] if dt is BF else 1e-5)

@@ -159,6 +159,27 @@ def test_ssm_refusals():
 
 
 @needs_lib
+def test_sizes_beyond_one_launch_are_refused():
+    L = osdn.load_library()
+    P = [i << 44 for i in range(1, 8)]
+    r = lambda R: L.residual_norm_forward(R, 8, BF16, BF16, P[0], P[1], 1.0, P[2], 1e-6,
+                                          P[3], P[4], None)
+    assert r(1 << 26) == UNSUPPORTED and r(1 << 31) == UNSUPPORTED
+    assert r((1 << 31) + 1) == BAD_DIMS
+    big = (1 << 30) + 1
+    assert L.ssm_forward_workspace_bytes(1, 1, 1, big, 32, 32, BF16) == 0
+    assert L.ssm_forward_workspace_bytes(1, 1, 1, (1 << 31) - 1, 32, 32, BF16) == 0
+    assert L.ssm_backward_workspace_bytes(1, 1, 1, big, 32, 32, F32) == 0
+    assert L.short_conv_backward_workspace_bytes(1, (1 << 31) - 1, 1, 32, 4) == 0
+    assert L.ssm_forward(1, 1, 1, big, 32, 32, BF16, P[0], P[1], P[2], P[3], P[4], None,
+                         None, 1, None, None, P[5], None, P[6], 1 << 40, None) == BAD_DIMS
+    assert L.short_conv_forward(1, big, 1, 32, 4, BF16, P[0], 0, 32, P[1], None, None, None,
+                                1, 0, 1e-6, P[2], None, None) == BAD_DIMS
+    assert L.ssm_decode(1 << 14, 1 << 10, 1, 1, 32, 32, BF16, P[0], P[1], P[2], P[3], P[4],
+                        None, None, 1, P[5], P[6], P[5], None) == UNSUPPORTED
+
+
+@needs_lib
 def test_ssm_backward_refusals():
     L = osdn.load_library()
     assert L.ssm_backward_workspace_bytes(1, 3, 2, 256, 64, 64, BF16) == 0
