@@ -30,8 +30,9 @@
 // and no atomics. The wave's share is a token tile for the scores and dx, and
 // tiles of state columns n for dB and dC.
 //
-// Rounding (bf16 inputs): K, Z and dS are rounded to bf16 once where they
-// enter products that leave in bf16; S, dS and the walks' dt x L enter in
+// Rounding (bf16 inputs): dS is rounded to bf16 once for dx, K and Z enter their
+// products in two bf16 parts (16 bits; one part is 2e-3 of each head's terms, and
+// more of the sums where the heads of a group cancel); S, dS and the walks' dt x L enter in
 // three bf16 parts (24 bits) wherever the result reaches an fp32 output.
 //
 // What bounds it: at B 4, H 16, G 2, T 2048, 128 x 128 bf16 the states are 268 MB,
@@ -238,8 +239,9 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
   __shared__ __attribute__((aligned(16))) Tin Cs[Q * LN];
   __shared__ __attribute__((aligned(16))) Tin Xs[Q * LP];
   __shared__ __attribute__((aligned(16))) Tin Ys[Q * LP];
-  __shared__ __attribute__((aligned(16))) Tin Ks[Q * LQ];
-  __shared__ __attribute__((aligned(16))) Tin Zs[Q * LQ];
+  constexpr int M2 = two_parts<Tin>(), QL = Q * LQ;
+  __shared__ __attribute__((aligned(16))) Tin Ks[M2 * QL];
+  __shared__ __attribute__((aligned(16))) Tin Zs[M2 * QL];
   __shared__ __attribute__((aligned(16))) Tin dSs[N * LP];
   __shared__ __attribute__((aligned(16))) ChunkDecay<Q> decs[2];
   // sums of a head, read while the next one is worked on
@@ -421,8 +423,8 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
 #pragma unroll
             for (int r = 0; r < 4; ++r) z.col[qi][jt * 16 + g4 + r] = 0.f;
           }
-          store4(ks + i * LQ + jt * 16 + g4, kk);
-          store4(zs + i * LQ + jt * 16 + g4, zz);
+          store4_two(ks + i * LQ + jt * 16 + g4, QL, kk);
+          store4_two(zs + i * LQ + jt * 16 + g4, QL, zz);
         }
         rsum += __shfl_xor(rsum, 16, 64);
         rsum += __shfl_xor(rsum, 32, 64);
@@ -516,11 +518,14 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
         for (int m = 0; m < TM; ++m) {
           const int it = tn + TN * m;
           if (it >= QT) break;
-          Frag<Q, Tin> zf;
-          zf.load(zs + it * 16 * LQ, LQ);
-          mma(dC[m], bT, zf);
-          zf.load_kmajor(zs + it * 16, LQ);  // rows j, k = i
-          mma(dB[m], cT, zf);
+#pragma unroll
+          for (int q = M2 - 1; q >= 0; --q) {
+            Frag<Q, Tin> zf;
+            zf.load(zs + q * QL + it * 16 * LQ, LQ);
+            mma(dC[m], bT, zf);
+            zf.load_kmajor(zs + q * QL + it * 16, LQ);  // rows j, k = i
+            mma(dB[m], cT, zf);
+          }
         }
       }
 
@@ -530,8 +535,9 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
         const int j = qi * 16 + lc;
         Frag<N, Tin> bf;
         bf.load(bs + qi * 16 * LN, LN);
-        Frag<Q, Tin> kf;
-        kf.load_kmajor(ks + qi * 16, LQ);  // rows j, k = i
+        Frag<Q, Tin> kf[M2];  // rows j, k = i
+#pragma unroll
+        for (int m = 0; m < M2; ++m) kf[m].load_kmajor(ks + m * QL + qi * 16, LQ);
         const float f = dec.wx[j];
         const Buffer dxb =
             make_buffer((Tin*)a.dx + th * P, (long long)rows * P * (int)sizeof(Tin));
@@ -547,7 +553,8 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
           for (int e = 0; e < 4; ++e) acc[e] *= f;
           Frag<Q, Tin> yT;
           yT.load_kmajor(ys + pt * 16, LP);  // rows p, k = i
-          mma(acc, yT, kf);
+#pragma unroll
+          for (int m = M2 - 1; m >= 0; --m) mma(acc, yT, kf[m]);
           const f32x4 yv = load4(ys + j * LP + pt * 16 + g4);
           const f32x4 xv = load4(xs + j * LP + pt * 16 + g4);
 #pragma unroll

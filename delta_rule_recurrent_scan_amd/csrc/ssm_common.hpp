@@ -352,6 +352,19 @@ __device__ __forceinline__ void store4(float* p, const f32x4& a) {
   *reinterpret_cast<f32x4*>(p) = a;
 }
 
+// The same in two parts, the rounded values and what their rounding lost (16
+// bits in all), `part` elements apart; fp32 is one part.
+template <typename Tin>
+constexpr int two_parts() { return sizeof(Tin) == 2 ? 2 : 1; }
+__device__ __forceinline__ void store4_two(__bf16* p, int part, const f32x4& a) {
+  const uint2 hi = {pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3])};
+  *reinterpret_cast<uint2*>(p) = hi;
+  *reinterpret_cast<uint2*>(p + part) =
+      uint2{pack_bf16(a[0] - low_bf16(hi.x), a[1] - high_bf16(hi.x)),
+            pack_bf16(a[2] - low_bf16(hi.y), a[3] - high_bf16(hi.y))};
+}
+__device__ __forceinline__ void store4_two(float* p, int, const f32x4& a) { store4(p, a); }
+
 // A buffer descriptor over `bytes` from p (both wave-uniform): reads past the
 // end return zeros and writes past it are dropped, by the hardware's range
 // check, so that the last tile of a sequence takes the same instructions as
