@@ -628,12 +628,14 @@ Plan make_plan(int B, int H, int G, int T, int P, int N, int Q) {
   Plan p{};
   const long long BH = (long long)B * H;
   p.nch = (T + Q - 1) / Q;
-  // walks: a workgroup a CU over both directions, segments of 4 chunks
-  // at least (a second segment costs a pass that writes no states)
+  // walks: a workgroup a CU over both directions, in segments of 4 chunks at
+  // least (a second segment costs a pass that writes no states and two
+  // launches); not below 12 chunks (64 streams of 64 x 128, 8 chunks of bf16: the
+  // whole backward 55 us in one walk, 60 us in two segments)
   const long long streams = 2 * BH * (P < 64 ? 1 : P / 64);
   long long want = streams > 0 ? (256 + streams - 1) / streams : 1;
   if (want > p.nch / 4) want = p.nch / 4;
-  if (want < 1) want = 1;
+  if (want < 1 || p.nch < 12) want = 1;
   p.segch = p.nch > 0 ? (int)((p.nch + want - 1) / want) : 1;
   p.nseg = p.nch > 0 ? (p.nch + p.segch - 1) / p.segch : 1;
   // chunks: heads of a group are split where the chunks alone leave CUs idle
