@@ -37,8 +37,8 @@
 //
 // What bounds it: at B 4, H 16, G 2, T 2048, 128 x 128 bf16 the states are 268 MB,
 // written by the walk (90 us; 4.9 TB/s with the rows it reads) and read by the
-// chunk kernel (108 us: LDS and VALU each busy a third of it, the matrix units a
-// seventh, two barriers a head). The inputs and gradients alone are 123 MB, 23
+// chunk kernel (116 us: LDS and VALU each busy a third of it, the matrix units a
+// sixth, two barriers a head). The inputs and gradients alone are 123 MB, 23
 // us. Longer chunks would move fewer states, but a chunk's pairs and its rows of
 // four tensors fill the LDS at 64. On the way here: states in whole rows of P and
 // 64-bit lane addresses spilled registers, and every reload waits for all loads in
