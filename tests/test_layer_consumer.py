@@ -3,6 +3,7 @@ layer_consumer.c, host-side paths only), built with the system compiler against
 the library, and with the C ABI source rebuilt under AddressSanitizer and
 UndefinedBehaviorSanitizer (host code; the other objects are the regular
 build's). No GPU is used."""
+import glob
 import os
 import shutil
 import subprocess
@@ -10,9 +11,14 @@ import subprocess
 import pytest
 
 import delta_rule_recurrent_scan_amd as osdn
-import test_sanitizers as S
 
-ROOT = S.ROOT
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "delta_rule_recurrent_scan_amd", "csrc")
+BUILD = os.path.join(ROOT, "_build")
+HIPCC = "/opt/rocm/bin/hipcc"
+CLANG = "/opt/rocm/llvm/bin/clang"
+CLANGXX = "/opt/rocm/llvm/bin/clang++"
+RUNTIME = (glob.glob("/opt/rocm/llvm/lib/clang/*/lib/linux") or [None])[0]
 LIB = osdn.library_path()
 SRC = os.path.join(ROOT, "tests", "c", "layer_consumer.c")
 
@@ -29,26 +35,28 @@ def test_layer_consumer(tmp_path):
     assert "all checks passed" in p.stdout
 
 
-@S.needs_toolchain
-@S.needs_build
+@pytest.mark.skipif(not (os.path.exists(HIPCC) and os.path.exists(CLANG) and RUNTIME),
+                    reason="ROCm clang toolchain with sanitizer runtimes not found")
+@pytest.mark.skipif(not os.path.exists(os.path.join(BUILD, "mixer_api.cpp.o")),
+                    reason="in-tree build objects (_build/) missing")
 def test_layer_consumer_under_sanitizers(tmp_path):
     san = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
            "-fno-omit-frame-pointer"]
     src = "mixer_api.cpp"
     obj = str(tmp_path / (src + ".o"))
-    subprocess.run([S.HIPCC, "-O1", "-g", "-std=c++17", "-fPIC", "-I",
+    subprocess.run([HIPCC, "-O1", "-g", "-std=c++17", "-fPIC", "-I",
                     os.path.join(ROOT, "include")] + san
-                   + ["-c", os.path.join(S.CSRC, src), "-o", obj], check=True,
+                   + ["-c", os.path.join(CSRC, src), "-o", obj], check=True,
                    capture_output=True)
-    rest = [os.path.join(S.BUILD, o) for o in sorted(os.listdir(S.BUILD))
+    rest = [os.path.join(BUILD, o) for o in sorted(os.listdir(BUILD))
             if o.endswith(".o") and o != src + ".o"]
-    rt, lib = S._runtime_dir(), str(tmp_path / "liblayer_san.so")
-    subprocess.run([S.CLANGXX, "-shared", "-fPIC", "-fsanitize=address,undefined",
+    rt, lib = RUNTIME, str(tmp_path / "liblayer_san.so")
+    subprocess.run([CLANGXX, "-shared", "-fPIC", "-fsanitize=address,undefined",
                     "-shared-libsan", "-o", lib, obj] + rest
                    + ["-L/opt/rocm/lib", "-lamdhip64", "-Wl,-rpath,/opt/rocm/lib",
                       "-Wl,-rpath," + rt], check=True, capture_output=True)
     exe = str(tmp_path / "layer_consumer_san")
-    subprocess.run([S.CLANG, "-std=c99", "-Wall", "-Werror", "-O1", "-g",
+    subprocess.run([CLANG, "-std=c99", "-Wall", "-Werror", "-O1", "-g",
                     "-fsanitize=address,undefined", "-shared-libsan",
                     "-fno-omit-frame-pointer", "-I", os.path.join(ROOT, "include"), SRC,
                     "-o", exe, "-L", str(tmp_path), "-llayer_san",
