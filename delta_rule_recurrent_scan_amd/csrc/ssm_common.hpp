@@ -356,6 +356,14 @@ __device__ __forceinline__ void store4(float* p, const f32x4& a) {
 // bits in all), `part` elements apart; fp32 is one part.
 template <typename Tin>
 constexpr int two_parts() { return sizeof(Tin) == 2 ? 2 : 1; }
+// What rounding to the type loses.
+__device__ __forceinline__ f32x4 rounding_rest(const f32x4& a, __bf16) {
+  const unsigned x = pack_bf16(a[0], a[1]), y = pack_bf16(a[2], a[3]);
+  return f32x4{a[0] - low_bf16(x), a[1] - high_bf16(x), a[2] - low_bf16(y), a[3] - high_bf16(y)};
+}
+__device__ __forceinline__ f32x4 rounding_rest(const f32x4&, float) {
+  return f32x4{0.f, 0.f, 0.f, 0.f};
+}
 __device__ __forceinline__ void store4_two(__bf16* p, int part, const f32x4& a) {
   const uint2 hi = {pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3])};
   *reinterpret_cast<uint2*>(p) = hi;

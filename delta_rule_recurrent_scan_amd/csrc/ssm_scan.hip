@@ -19,21 +19,24 @@
 // a first pass forms each segment's own contribution to the state (keys and
 // values only), a small kernel chains them, and the segments then run at once.
 //
-// Rounding (bf16 inputs): scores and the state are rounded to bf16 once where
-// they enter the two products of y, which is rounded to bf16 itself; the
-// state's own update takes dt x L in three bf16 parts (24 bits), and is
-// accumulated in fp32. fp32 inputs use fp32 MFMA throughout (Q = 32).
+// Rounding (bf16 inputs): the state is rounded to bf16 once where it enters y,
+// which is rounded to bf16 itself (y 1.70e-3 relative L2 of the exact result; the
+// last rounding alone 1.66e-3; the state in two parts spills: scan 107 us). The
+// scores enter in two bf16 parts (in one, y 2.1e-3, up to 2.7e-3 for the few sums
+// of short sequences; 4 us less). The state's own update takes dt x L in three
+// bf16 parts (24 bits), and is accumulated in fp32. fp32 inputs use fp32 MFMA
+// throughout (Q = 32).
 //
 // What bounds it: at B 4, H 16, G 2, T 4096, 128 x 128 bf16 the products, with
 // the state's update in three parts and formed twice (by the first pass and by
 // the scan), are 64 GFLOP, 56 us at the 1150 TFLOP/s that a large matrix product
-// reaches; the kernels take 116 us (decays 6, first pass 33, chain 10, scan 67).
+// reaches; the kernels take 120 us (decays 6, first pass 33, chain 10, scan 71).
 // The 156 MB of inputs and outputs alone would be 29 us. In the scan the matrix
 // units, the VALU (splitting, decays) and LDS are each busy a third of the time,
 // one after the other within a chunk, with two waves a SIMD to overlap them.
-// Measured beside it: one part instead of three 59 us, without the readout 36,
-// without the update 49; 8 waves of one p tile each 94 us (LDS reads twice as
-// often); row strides of 72 or 76 words instead of 68 no change.
+// Measured beside it, scores in one part (67 us): the update in one part instead
+// of three 59 us, no readout 36, no update 49; 8 waves of one p tile each 94 us (LDS
+// reads twice as often); row strides of 72 or 76 words instead of 68 no change.
 #include "launch.hpp"
 #include "mixer.hpp"
 #include "ssm_common.hpp"
@@ -66,7 +69,8 @@ __global__ __launch_bounds__(64 * scan_waves<P>(), 2) void ssm_scan_kernel(
   __shared__ __attribute__((aligned(16))) Tin Bs[Q * LN];
   __shared__ __attribute__((aligned(16))) Tin Cs[YOUT ? Q * LN : 16];
   __shared__ __attribute__((aligned(16))) Tin Xs[Q * LP];
-  __shared__ __attribute__((aligned(16))) Tin Ms[YOUT ? Q * Q : 16];  // fragment order
+  constexpr int M2 = two_parts<Tin>();  // of the scores
+  __shared__ __attribute__((aligned(16))) Tin Ms[YOUT ? M2 * Q * Q : 16];  // fragment order
   __shared__ __attribute__((aligned(16))) ChunkDecay<Q> dec;
 
   const int lane = threadIdx.x & 63, w = wave_id();
@@ -143,6 +147,9 @@ __global__ __launch_bounds__(64 * scan_waves<P>(), 2) void ssm_scan_kernel(
             for (int r = 0; r < 4; ++r) s[r] *= l[r] * dj[r];
           }
           Frag<Q, Tin>::store_acc_kblock(Ms + it * Frag<Q, Tin>::ELEMS, jt, s);
+          if constexpr (M2 == 2)
+            Frag<Q, Tin>::store_acc_kblock(Ms + Q * Q + it * Frag<Q, Tin>::ELEMS, jt,
+                                           rounding_rest(s, Tin()));
         }
       }
       __syncthreads();
@@ -161,8 +168,9 @@ __global__ __launch_bounds__(64 * scan_waves<P>(), 2) void ssm_scan_kernel(
       for (int it = 0; it < QT; ++it) {
         Frag<N, Tin> cf;
         cf.load_perm(Cs + it * 16 * LN, LN);
-        Frag<Q, Tin> mf;
-        mf.load_global(Ms + it * Frag<Q, Tin>::ELEMS);
+        Frag<Q, Tin> mf[M2];
+#pragma unroll
+        for (int m = 0; m < M2; ++m) mf[m].load_global(Ms + m * Q * Q + it * Frag<Q, Tin>::ELEMS);
         const int ti = it * 16 + (lane & 15);
         const float ent = dec.ent[ti];
 #pragma unroll
@@ -171,7 +179,8 @@ __global__ __launch_bounds__(64 * scan_waves<P>(), 2) void ssm_scan_kernel(
           mma(acc, sf[pt], cf);
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[e] *= ent;
-          mma_upto<Q>(acc, xf[pt], mf, 16 * (it + 1));
+#pragma unroll
+          for (int m = M2 - 1; m >= 0; --m) mma_upto<Q>(acc, xf[pt], mf[m], 16 * (it + 1));
           const int p = (w * PT + pt) * 16 + n0;
           const f32x4 xv = load4(Xs + ti * LP + p);
 #pragma unroll
