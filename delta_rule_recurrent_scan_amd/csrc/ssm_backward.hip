@@ -314,7 +314,7 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
       __builtin_amdgcn_raw_buffer_store_b32(
           __float_as_uint(draw),
           make_buffer(a.ddt + ((size_t)b * a.H + h) * a.T + t0, rows * 4), lane * 4, 0, 0);
-      const float sa = wave_sum(in ? (float)(step * gt) : 0.f), sb = wave_sum(draw);
+      const float sa = (float)wave_sum(in ? step * gt : 0.), sb = wave_sum(draw);
       if (lane == 0) {
         sums[h] = sa;
         sums[a.H + h] = dd;

@@ -188,6 +188,12 @@ __device__ __forceinline__ double row16_sum(double x) {
   return x;
 }
 
+__device__ __forceinline__ double wave_sum(double x) {
+  x = row16_sum(x);
+  x += __shfl_xor(x, 16, 64);
+  return x + __shfl_xor(x, 32, 64);
+}
+
 // Inclusive sum of lanes l .. 63, and exclusive sum of lanes 0 .. l - 1. In 64
 // bits: what the sums take in cancels in part (a chunk's pairs enter a token's
 // decay gradient as the difference of two running sums).
