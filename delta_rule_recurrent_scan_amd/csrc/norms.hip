@@ -10,18 +10,18 @@
 //
 // All are bound by HBM: every input is read and every output written once,
 // 16 bytes a lane, with the sums in 32 bits. A head is 4, 8 or 16 adjacent
-// lanes; a row of the residual norm is one wave (up to 4096 elements, no
+// lanes; a row of the residual norm is one wave (up to 1536 elements, no
 // barrier) or four, held in registers between the sum and the scaling. In bf16,
 // where a copy of 256 MiB reaches 5.4 TB/s: gated norm of 16384 rows of 16 heads of
-// 128, 201 MB, 43 us (4.7 TB/s); residual norm of 16384 rows of 2048 on a 32-bit
-// stream, 403 MB, 78 us (5.2 TB/s).
+// 128, 201 MB, 36 us (5.6 TB/s); residual norm of 16384 rows of 2048 on a 32-bit
+// stream, 403 MB, 71 us (5.7 TB/s).
 //
 // Backward of n = v r, y = n * weight (r the reciprocal root):
 //   dn = dy * weight,  dv = r (dn - n mean(n dn)),  dweight = sum dy n
 // Weight gradients stay in registers while a workgroup walks its rows, are
 // added over its row lanes in LDS and leave as one partial a workgroup,
 // summed in a fixed order by column_sum. Gated: 16384 rows of 8 heads of 64, 84 MB,
-// 19 us and 2 us for the sum; residual: 4097 rows of 1021, 42 MB, 14 us and 2 us
+// 16 us and 2 us for the sum; residual: 4097 rows of 1021, 42 MB, 14 us and 2 us
 // (with a partial a wave and unaligned rows element by element it was 69 us: they
 // take the same wide accesses as aligned ones now).
 #include "launch.hpp"
@@ -335,15 +335,22 @@ __global__ __launch_bounds__(kResThreads) void residual_norm_bwd_kernel(Residual
   }
 }
 
-// The fewest waves and vectors a row that hold a width in registers.
+// Waves and vectors a row. One wave (no barrier) while a row is 3 vectors a lane;
+// above, the four waves of a workgroup, which leave fewer registers a lane and more
+// rows in flight. bf16 on fp32: 16384 rows of 2048, 79 us at 4 vectors of one wave
+// and 69 us at 1 of four, backward 84 and 74 us; of 4096, 164 and 143 us (8 against
+// 2 vectors), backward 211 and 172 us; 4097 rows of 1501, where a quarter of the
+// four waves' lanes is idle, 11 and 12 us.
 constexpr int kMaxWidth = kResWaves * 64 * 8 * 8;  // 16384
 struct Shape {
   int nv, wpr;
 };
 Shape row_shape(int C) {
-  for (int nv = 1; nv <= 8; nv *= 2)
+  for (int nv = 1; nv <= 3; ++nv)
     if (64 * 8 * nv >= C) return Shape{nv, 1};
-  return Shape{64 * 8 * kResWaves * 4 >= C ? 4 : 8, kResWaves};
+  for (int nv = 1; nv <= 4; nv *= 2)
+    if (64 * 8 * kResWaves * nv >= C) return Shape{nv, kResWaves};
+  return Shape{8, kResWaves};
 }
 
 // Workgroups of the backward, each a partial row of the weight gradient: two
@@ -380,16 +387,16 @@ int run_res(const ResidualNormArgs& a, int bwd, hipStream_t s) {
 template <typename Tin, typename Tr, bool ALN>
 int run_res_n(const ResidualNormArgs& a, int bwd, hipStream_t s) {
   const Shape p = row_shape(a.C);
-  if (p.wpr == 1) {
-    switch (p.nv) {
-      case 1: return run_res<Tin, Tr, ALN, 1, 1>(a, bwd, s);
-      case 2: return run_res<Tin, Tr, ALN, 2, 1>(a, bwd, s);
-      case 4: return run_res<Tin, Tr, ALN, 4, 1>(a, bwd, s);
-      case 8: return run_res<Tin, Tr, ALN, 8, 1>(a, bwd, s);
-    }
+  switch (p.nv + (p.wpr == 1 ? 0 : 10)) {
+    case 1: return run_res<Tin, Tr, ALN, 1, 1>(a, bwd, s);
+    case 2: return run_res<Tin, Tr, ALN, 2, 1>(a, bwd, s);
+    case 3: return run_res<Tin, Tr, ALN, 3, 1>(a, bwd, s);
+    case 11: return run_res<Tin, Tr, ALN, 1, kResWaves>(a, bwd, s);
+    case 12: return run_res<Tin, Tr, ALN, 2, kResWaves>(a, bwd, s);
+    case 14: return run_res<Tin, Tr, ALN, 4, kResWaves>(a, bwd, s);
+    case 18: return run_res<Tin, Tr, ALN, 8, kResWaves>(a, bwd, s);
   }
-  return p.nv == 4 ? run_res<Tin, Tr, ALN, 4, kResWaves>(a, bwd, s)
-                   : run_res<Tin, Tr, ALN, 8, kResWaves>(a, bwd, s);
+  return -1;
 }
 
 template <typename Tin, typename Tr>

@@ -437,8 +437,8 @@ int gdn2_backward(int B, int H, int T, int Dk, int Dv, int dtype,
  *    states are those after the last token inside. Values are clamped to
  *    [0, T].
  *  - T up to 2^30 (more: OSDN_ERR_BAD_DIMS). A call that would need 2^32 threads
- *    in one launch (2^26 rows of up to 4096 elements in residual_norm_forward)
- *    is refused with OSDN_ERR_UNSUPPORTED.
+ *    in one launch (in residual_norm_forward 2^26 rows, or 2^24 of more than
+ *    1536 elements) is refused with OSDN_ERR_UNSUPPORTED.
  *  - Backward: adjoints and gradients of activations and of the convolution's
  *    state are in the activation's dtype (each rounded once, at the end), so
  *    that one operator's gradient is the next one's adjoint; gradients of

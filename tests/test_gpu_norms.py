@@ -105,6 +105,11 @@ RES = [
     (1100, 260, BF, BF, 1.0),
     (2100, 129, F32, F32, 1.0),        # more rows than one pass of the backward
     (6, 4000, F32, None, 1.0),
+    (1030, 1300, BF, F32, 0.5),        # three vectors a lane of one wave
+    (7, 1537, F32, F32, 1.0),          # the first width of four waves
+    (600, 2500, BF, BF, 1.0),
+    (3, 6001, BF, F32, 0.3),
+    (3, 8193, F32, None, 1.0),
 ]
 
 
