@@ -21,7 +21,7 @@
 // Weight gradients stay in registers while a workgroup walks its rows, are
 // added over its row lanes in LDS and leave as one partial a workgroup,
 // summed in a fixed order by column_sum. Gated: 16384 rows of 8 heads of 64, 84 MB,
-// 16 us and 2 us for the sum; residual: 4097 rows of 1021, 42 MB, 14 us and 2 us
+// 16 us and 2 us for the sum; residual: 4097 rows of 1021, 42 MB, 11 us and 3 us
 // (with a partial a wave and unaligned rows element by element it was 69 us: they
 // take the same wide accesses as aligned ones now).
 #include "launch.hpp"
@@ -353,12 +353,15 @@ Shape row_shape(int C) {
   return Shape{8, kResWaves};
 }
 
-// Workgroups of the backward, each a partial row of the weight gradient: two
-// a CU (more partials cost more than the occupancy gives).
+// Workgroups of the backward, each a partial row of the weight gradient: four a
+// CU for rows of one wave, two for the wider ones, whose partials cost more. With
+// the column sum: 4097 rows of 1021 bf16 14 us with 1024 partials and 16 with 512;
+// 65536 of 512 75 and 79; 16384 of 2048 on fp32 79 and 76; of 8192 338 and 328.
 int res_blocks(long long R, int wpr) {
   const int rpw = kResWaves / wpr;
   const long long need = (R + rpw - 1) / rpw;
-  return (int)(need < 512 ? need : 512);
+  const long long most = wpr == 1 ? 1024 : 512;
+  return (int)(need < most ? need : most);
 }
 
 template <typename Tin, typename Tr, bool ALN, int NV, int WPR>
