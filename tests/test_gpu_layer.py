@@ -251,3 +251,22 @@ def test_convolutions_and_gated_norm_around_the_delta_rule():
         close(gc[i]["x"], rp.grad[..., i * C:(i + 1) * C], TOL[F32], "d proj %d" % i)
         close(gc[i]["weight"], rc[i].grad, TOL[F32], "d conv weight %d" % i)
     assert not np.isnan(out.cpu().numpy()).any()
+
+
+def test_lengths_outside_the_sequence_are_clamped():
+    B, T, H, G, P, N = 3, 70, 2, 1, 64, 32
+    g = torch.Generator().manual_seed(13)
+    n = lambda *s: torch.randn(s, generator=g).to(DEV)
+    out = torch.tensor([-5, T + 9, 2 ** 31 - 1], dtype=torch.int32, device=DEV)
+    inside = torch.tensor([0, T, T], dtype=torch.int32, device=DEV)
+    rows, cw, dy = n(B, T, H * P), n(H * P, 4), n(B, H, T, P)
+    a = (n(B, H, T), -(1 + n(H).abs()), n(B, G, T, N), n(B, G, T, N))
+    got = []
+    for lens in (out, inside):
+        x, tail = osdn.short_conv_forward(rows, cw, lengths=lens, head_dim=P)
+        y, S = osdn.ssm_forward(x, *a, lengths=lens)
+        gs = osdn.ssm_backward(x, *a, dy, lengths=lens)
+        gc = osdn.short_conv_backward(rows, cw, gs["x"], lengths=lens, head_dim=P)
+        got.append([x, tail, y, S] + list(gs.values()) + list(gc.values()))
+    for u, v in zip(*got):
+        assert torch.equal(u, v)
