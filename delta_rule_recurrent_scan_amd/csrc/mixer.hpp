@@ -14,7 +14,6 @@ namespace osdn {
 // workgroup of 256 threads covers `cx` groups (a power of two, at most 64)
 // times 256 / cx rows.
 constexpr int kRowThreads = 256;
-constexpr int kVec = 8;
 
 // A launch holds fewer than 2^32 threads; a call that needs more is refused.
 inline bool grid_ok(long long blocks, int threads) {

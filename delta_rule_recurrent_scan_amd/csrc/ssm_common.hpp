@@ -392,9 +392,6 @@ __device__ __forceinline__ Buffer make_buffer(const void* p, long long bytes) {
 __device__ __forceinline__ uint4 buffer_load16(Buffer r, unsigned off) {
   return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
-__device__ __forceinline__ float buffer_load_f32(Buffer r, unsigned off) {
-  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
-}
 // Four consecutive values, rounded, to element `at`.
 __device__ __forceinline__ void buffer_store4(Buffer r, unsigned at, const f32x4& a, __bf16) {
   typedef __attribute__((ext_vector_type(2))) unsigned u32x2;
