@@ -307,8 +307,11 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
         if (q < NTL) dot += z.dot[q];
         dd += z.dd[q];
       }
-      const double gt = wave_suffix_sum(R - col * step + wi) + wave_prefix_before(uj * step) +
-                        dec.total * dot;
+      double gt = wave_suffix_sum(R - col * step + wi) + wave_prefix_before(uj * step) +
+                  dec.total * dot;
+      // nothing crosses a token whose decay is zero in fp32; the sums' rest of
+      // 2^-53 would count where the step that empties the state is 1e20 or more
+      if (step * a.A[h] < -104.) gt = 0.;
       const bool in = lane < Q && lane < valid;
       const float draw = in ? (float)((own + a.A[h] * gt) * slope) : 0.f;
       __builtin_amdgcn_raw_buffer_store_b32(

@@ -12,12 +12,16 @@ namespace osdn {
 // its slope by raw. softplus(v) = max(v, 0) + log1p(e), e = exp(-|v|), from the
 // hardware's exp2 and log2 (one unit each): the argument's rounding is put
 // back into e, and log1p(e) = log(1 + e) e / ((1 + e) - 1) makes up for the
-// rounding of 1 + e. slope = 1 / (1 + exp(-v)).
+// rounding of 1 + e. slope = 1 / (1 + exp(-v)). Behind |v| = 128 e is zero in
+// fp32; the argument stops there, so that its product with log2(e) and what that
+// lost are numbers also for infinite v and at the ends of the range, where they
+// would be inf - inf: a raw step of -inf or of the lowest value is a step of zero
+// with a slope of zero. A NaN compares false and stays.
 __device__ __forceinline__ float ssm_step(float raw, float bias, int softplus, float& slope) {
   const float v = raw + bias;
   slope = 1.f;
   if (!softplus) return v;
-  const float x = -fabsf(v), t = x * 1.44269504f;
+  const float m = -fabsf(v), x = m < -128.f ? -128.f : m, t = x * 1.44269504f;
   const float lost = fmaf(x, 1.44269504f, -t) + x * 1.92596299e-8f;  // of x log2(e)
   float e = __builtin_amdgcn_exp2f(t);
   e = fmaf(e, lost * 0.693147181f, e);

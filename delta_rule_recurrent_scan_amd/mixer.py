@@ -282,7 +282,8 @@ def ssm_forward(x, dt, A, B, C, D=None, dt_bias=None, S0=None, lengths=None,
     [H] fp32 (negative: a decay), D, dt_bias [H] fp32 (None: zeros); S0
     [B,H,P,N] fp32 (None: zeros); lengths [B] int32 of a padded batch. With
     s = softplus(dt + dt_bias) (``softplus=False``: the sum itself),
-    S <- exp(s A) S + s x B^T and y = S C + D x. P, N in {32, 64, 128}.
+    S <- exp(s A) S + s x B^T and y = S C + D x. P, N in {32, 64, 128}. A dt of
+    -inf or the lowest fp32 value switches its token off.
     ``out`` may pass preallocated (y, S_T) (S_T may be None to skip it, or S0
     itself) and ``workspace`` a uint8 device buffer of
     ssm_forward_workspace_bytes().

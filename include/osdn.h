@@ -511,7 +511,8 @@ int short_conv_backward(int B, int T, int H, int D, int W, int dtype,
  * Selective state space scan: a recurrence with one decay per token and head
  * and no erase, its keys and queries shared by the H / G heads of a group (g =
  * h / (H / G); G divides H). Per (batch, head), with
- * dt_t = softplus(dt[t] + dt_bias_h) (softplus == 0: the sum itself):
+ * dt_t = softplus(dt[t] + dt_bias_h) (softplus == 0: the sum itself; a raw dt of
+ * -inf or fp32's lowest value is a step of zero and switches the token off):
  *   S_t = exp(dt_t A_h) S_{t-1} + dt_t x_t B_t^T     (P x N)
  *   y_t = S_t C_t + D_h x_t                          (after token t's update)
  *
