@@ -49,12 +49,14 @@ __device__ __forceinline__ Log2f add(Log2f a, Log2f b) {
   const float s = a.hi + b.hi, t = s - a.hi;
   return {s, ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo)};
 }
-// exp of it, the rounding of x log2(e) put back as well.
+// exp of it, the rounding of x log2(e) put back as well (into numbers: a factor
+// past fp32's range is inf, where inf times what was lost would be NaN).
 __device__ __forceinline__ float exp_of(float hi, float lo) {
   const float t = hi * 1.44269504f;
   const float lost = fmaf(hi, 1.44269504f, -t) + hi * 1.92596299e-8f;
   const float e = __builtin_amdgcn_exp2f(t);
-  return fmaf(e, fmaf(lost, 0.693147181f, lo), e);
+  const float r = fmaf(e, fmaf(lost, 0.693147181f, lo), e);
+  return e == INFINITY ? e : r;
 }
 __device__ __forceinline__ float exp_of(Log2f x) { return exp_of(x.hi, x.lo); }
 

@@ -522,6 +522,9 @@ int short_conv_backward(int B, int T, int H, int D, int W, int dtype,
  *   S0       [B,H,P,N] fp32 (NULL: zeros)
  *   y        [B,H,T,P] dtype;  S_T [B,H,P,N] fp32 (NULL: not written); S_T may
  *            be exactly S0
+ * Growth (dt A > 0) is taken while its product over 512 tokens stays in fp32's
+ * range, and so do the products (C_i . B_j) dt_j; past it results are inf or NaN,
+ * also where the tokens one by one would stay finite.
  * P, N in {32, 64, 128}; any T. Tensors of P or N columns start on 16 bytes, in
  * this call and the next two (OSDN_ERR_MISALIGNED). workspace: ssm_forward_workspace_bytes(...) bytes,
  * 256-byte aligned: the chunks' decays, and the states between the segments
