@@ -11,32 +11,32 @@
 // state in accumulators: each wave owns 16 or 32 rows p of it (all N columns),
 // so that the state never leaves registers between chunks; its tiles, read as
 // (row p, k = n) fragments in accumulator order, are the operand of the
-// readout without a trip through LDS. Scores are formed once a chunk, each
-// wave a share of the token rows, and pass through LDS. The next chunk's rows
-// are in flight while one is worked on.
+// readout without a trip through LDS, 32 columns at a time. Scores are formed once
+// a chunk, each wave a share of the token rows, and pass through LDS. The next
+// chunk's rows are in flight while one is worked on.
 //
 // A (batch, head) is cut into segments where B * H alone leaves CUs idle:
 // a first pass forms each segment's own contribution to the state (keys and
 // values only), a small kernel chains them, and the segments then run at once.
 //
-// Rounding (bf16 inputs): the state is rounded to bf16 once where it enters y,
-// which is rounded to bf16 itself (y 1.70e-3 relative L2 of the exact result; the
-// last rounding alone 1.66e-3; the state in two parts spills: scan 107 us). The
-// scores enter in two bf16 parts (in one, y 2.1e-3, up to 2.7e-3 for the few sums
-// of short sequences; 4 us less). The state's own update takes dt x L in three
-// bf16 parts (24 bits), and is accumulated in fp32. fp32 inputs use fp32 MFMA
-// throughout (Q = 32).
+// Rounding (bf16 inputs): y is rounded to bf16 once, at the end, and its error is
+// that rounding (1.66e-3 relative L2): the state and the scores enter it in two bf16
+// parts (16 bits). With the state in one part y is off by 1.70e-3 over long prompts and
+// by 2.0e-3 to 2.5e-3 where few tokens follow a state that came in, and the scan takes
+// 71 us instead of 78; with the scores in one part 2.1e-3 to 2.7e-3, 4 us less. The state's own update takes
+// dt x L in three bf16 parts (24 bits), and is accumulated in fp32. fp32 inputs use
+// fp32 MFMA throughout (Q = 32).
 //
 // What bounds it: at B 4, H 16, G 2, T 4096, 128 x 128 bf16 the products, with
 // the state's update in three parts and formed twice (by the first pass and by
-// the scan), are 64 GFLOP, 56 us at the 1150 TFLOP/s that a large matrix product
-// reaches; the kernels take 120 us (decays 6, first pass 33, chain 10, scan 71).
+// the scan), are 73 GFLOP, 63 us at the 1150 TFLOP/s that a large matrix product
+// reaches; the kernels take 127 us (decays 6, first pass 33, chain 10, scan 78).
 // The 156 MB of inputs and outputs alone would be 29 us. In the scan the matrix
 // units, the VALU (splitting, decays) and LDS are each busy a third of the time,
 // one after the other within a chunk, with two waves a SIMD to overlap them.
-// Measured beside it, scores in one part (67 us): the update in one part instead
-// of three 59 us, no readout 36, no update 49; 8 waves of one p tile each 94 us (LDS
-// reads twice as often); row strides of 72 or 76 words instead of 68 no change.
+// Measured beside it, scores and state in one part (67 us): the update in one part
+// instead of three 59 us, no readout 36, no update 49; 8 waves of one p tile each 94 us
+// (LDS reads twice as often); row strides of 72 or 76 words instead of 68 no change.
 #include "launch.hpp"
 #include "mixer.hpp"
 #include "ssm_common.hpp"
@@ -155,19 +155,45 @@ __global__ __launch_bounds__(64 * scan_waves<P>(), 2) void ssm_scan_kernel(
       __syncthreads();
     }
 
+    f32x4 acc[QT][PT];
+    if constexpr (YOUT) {
+      // S C of every query tile, a 32-wide block of n at a time: of the state's two
+      // parts only a block's fragments are held
+#pragma unroll
+      for (int it = 0; it < QT; ++it)
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) acc[it][pt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < N / 32; ++i) {
+        Frag<32, Tin> sf[PT][M2];
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) {
+          const f32x4 s[2] = {S[pt][2 * i], S[pt][2 * i + 1]};
+          frag_from_acc<32>(sf[pt][0], s);
+          if constexpr (M2 == 2) {
+            const f32x4 r[2] = {rounding_rest(s[0], Tin()), rounding_rest(s[1], Tin())};
+            frag_from_acc<32>(sf[pt][1], r);
+          }
+        }
+#pragma unroll
+        for (int it = 0; it < QT; ++it) {
+          Frag<32, Tin> cf;
+          cf.load_perm(Cs + it * 16 * LN + 32 * i, LN);
+#pragma unroll
+          for (int m = M2 - 1; m >= 0; --m)
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) mma(acc[it][pt], sf[pt][m], cf);
+        }
+      }
+    }
     Frag<Q, Tin> xf[PT];
 #pragma unroll
     for (int pt = 0; pt < PT; ++pt) xf[pt].load_kmajor(Xs + (w * PT + pt) * 16, LP);
     if constexpr (YOUT) {
       const Buffer yb =
           make_buffer(y + (size_t)t * P, (long long)min(t1 - t, Q) * P * (int)sizeof(Tin));
-      Frag<N, Tin> sf[PT];
-#pragma unroll
-      for (int pt = 0; pt < PT; ++pt) frag_from_acc<N>(sf[pt], S[pt]);
 #pragma unroll
       for (int it = 0; it < QT; ++it) {
-        Frag<N, Tin> cf;
-        cf.load_perm(Cs + it * 16 * LN, LN);
         Frag<Q, Tin> mf[M2];
 #pragma unroll
         for (int m = 0; m < M2; ++m) mf[m].load_global(Ms + m * Q * Q + it * Frag<Q, Tin>::ELEMS);
@@ -175,17 +201,16 @@ __global__ __launch_bounds__(64 * scan_waves<P>(), 2) void ssm_scan_kernel(
         const float ent = dec.ent[ti];
 #pragma unroll
         for (int pt = 0; pt < PT; ++pt) {
-          f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-          mma(acc, sf[pt], cf);
+          f32x4& o = acc[it][pt];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[e] *= ent;
+          for (int e = 0; e < 4; ++e) o[e] *= ent;
 #pragma unroll
-          for (int m = M2 - 1; m >= 0; --m) mma_upto<Q>(acc, xf[pt], mf[m], 16 * (it + 1));
+          for (int m = M2 - 1; m >= 0; --m) mma_upto<Q>(o, xf[pt], mf[m], 16 * (it + 1));
           const int p = (w * PT + pt) * 16 + n0;
           const f32x4 xv = load4(Xs + ti * LP + p);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[e] = ti < valid ? acc[e] + D * xv[e] : 0.f;
-          buffer_store4(yb, ti * P + p, acc, Tin());
+          for (int e = 0; e < 4; ++e) o[e] = ti < valid ? o[e] + D * xv[e] : 0.f;
+          buffer_store4(yb, ti * P + p, o, Tin());
         }
       }
     }
