@@ -259,6 +259,49 @@ __device__ __forceinline__ void frag_from_acc(Frag<KEXT, float>& f, const f32x4 
     for (int e = 0; e < 4; ++e) f.v[4 * b + e] = t[b][e];
 }
 
+// Values that are inf or NaN. The test of a whole fragment is the largest exponent
+// of the wave's elements, two operations a register, and the same for every lane.
+__device__ __forceinline__ bool strange(__bf16 x) {
+  return (__builtin_bit_cast(unsigned short, x) & 0x7f80) == 0x7f80;
+}
+__device__ __forceinline__ bool strange(float x) {
+  return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u;
+}
+template <int KEXT>
+__device__ __forceinline__ bool any_strange(const Frag<KEXT, __bf16>& f) {
+  typedef __attribute__((ext_vector_type(2))) unsigned short u16x2;
+  u16x2 m = {0, 0};
+#pragma unroll
+  for (int i = 0; i < KEXT / 32; ++i) {
+    const u32x4 u = __builtin_bit_cast(u32x4, f.v[i]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, u[e] & 0x7fff7fffu));
+  }
+  return __ballot(max(m[0], m[1]) >= 0x7f80) != 0;
+}
+template <int KEXT>
+__device__ __forceinline__ bool any_strange(const Frag<KEXT, float>& f) {
+  unsigned m = 0;
+#pragma unroll
+  for (int i = 0; i < KEXT / 4; ++i) m = max(m, __float_as_uint(f.v[i]) & 0x7fffffffu);
+  return __ballot(m >= 0x7f800000u) != 0;
+}
+template <int KEXT>
+__device__ __forceinline__ void drop_strange(Frag<KEXT, __bf16>& f) {
+#pragma unroll
+  for (int i = 0; i < KEXT / 32; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (strange(f.v[i][e])) f.v[i][e] = (__bf16)0.f;
+}
+template <int KEXT>
+__device__ __forceinline__ void drop_strange(Frag<KEXT, float>& f) {
+#pragma unroll
+  for (int i = 0; i < KEXT / 4; ++i)
+    if (strange(f.v[i])) f.v[i] = 0.f;
+}
+
 // An fp32 operand as bf16 fragments that add up to it: the rounded value, what
 // its rounding lost, and what that one's lost (24 bits in all, an error of
 // some 6e-8). Used where a product's sum leaves in fp32 (states, step and

@@ -22,15 +22,18 @@
 // Rounding (bf16 inputs): y is rounded to bf16 once, at the end, and its error is
 // that rounding (1.66e-3 relative L2): the state and the scores enter it in two bf16
 // parts (16 bits). With the state in one part y is off by 1.70e-3 over long prompts and
-// by 2.0e-3 to 2.5e-3 where few tokens follow a state that came in, and the scan takes
-// 71 us instead of 78; with the scores in one part 2.1e-3 to 2.7e-3, 4 us less. The state's own update takes
+// by 2.0e-3 to 2.5e-3 where few tokens follow a state that came in, and the scan takes 7
+// us less; with the scores in one part 2.1e-3 to 2.7e-3, 4 us less. The state's own update takes
 // dt x L in three bf16 parts (24 bits), and is accumulated in fp32. fp32 inputs use
 // fp32 MFMA throughout (Q = 32).
+//
+// Masked pairs are zeros that the products still take; what is not a number in x is
+// taken out before and put back behind (3 us of the scan for finding none).
 //
 // What bounds it: at B 4, H 16, G 2, T 4096, 128 x 128 bf16 the products, with
 // the state's update in three parts and formed twice (by the first pass and by
 // the scan), are 73 GFLOP, 63 us at the 1150 TFLOP/s that a large matrix product
-// reaches; the kernels take 127 us (decays 6, first pass 33, chain 10, scan 78).
+// reaches; the kernels take 130 us (decays 6, first pass 33, chain 10, scan 81).
 // The 156 MB of inputs and outputs alone would be 29 us. In the scan the matrix
 // units, the VALU (splitting, decays) and LDS are each busy a third of the time,
 // one after the other within a chunk, with two waves a SIMD to overlap them.
@@ -145,6 +148,11 @@ __global__ __launch_bounds__(64 * scan_waves<P>(), 2) void ssm_scan_kernel(
             const f32x4 l = pair_decay(dec, it, jt), dj = tile_steps(dec, jt);
 #pragma unroll
             for (int r = 0; r < 4; ++r) s[r] *= l[r] * dj[r];
+            if (jt == it) {  // zeros ahead of the query whatever the key holds
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (acc_row(r) > acc_col()) s[r] = 0.f;
+            }
           }
           Frag<Q, Tin>::store_acc_kblock(Ms + it * Frag<Q, Tin>::ELEMS, jt, s);
           if constexpr (M2 == 2)
@@ -190,6 +198,16 @@ __global__ __launch_bounds__(64 * scan_waves<P>(), 2) void ssm_scan_kernel(
 #pragma unroll
     for (int pt = 0; pt < PT; ++pt) xf[pt].load_kmajor(Xs + (w * PT + pt) * 16, LP);
     if constexpr (YOUT) {
+      // an inf or NaN of x would reach earlier tokens as its product with their
+      // zero scores: it is left out of the products, and its channel made NaN from
+      // its token on
+      bool odd = false;
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) odd |= any_strange(xf[pt]);
+      if (odd) {
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) drop_strange(xf[pt]);
+      }
       const Buffer yb =
           make_buffer(y + (size_t)t * P, (long long)min(t1 - t, Q) * P * (int)sizeof(Tin));
 #pragma unroll
@@ -207,11 +225,22 @@ __global__ __launch_bounds__(64 * scan_waves<P>(), 2) void ssm_scan_kernel(
 #pragma unroll
           for (int m = M2 - 1; m >= 0; --m) mma_upto<Q>(o, xf[pt], mf[m], 16 * (it + 1));
           const int p = (w * PT + pt) * 16 + n0;
+          if (odd) {
+#pragma unroll 1
+            for (int j = 0; j <= ti; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (strange(Xs[j * LP + p + e])) o[e] = NAN;
+          }
           const f32x4 xv = load4(Xs + ti * LP + p);
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[e] = ti < valid ? o[e] + D * xv[e] : 0.f;
           buffer_store4(yb, ti * P + p, o, Tin());
         }
+      }
+      if (odd) {  // the state takes them
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) xf[pt].load_kmajor(Xs + (w * PT + pt) * 16, LP);
       }
     }
 

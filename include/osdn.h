@@ -522,9 +522,10 @@ int short_conv_backward(int B, int T, int H, int D, int W, int dtype,
  *   S0       [B,H,P,N] fp32 (NULL: zeros)
  *   y        [B,H,T,P] dtype;  S_T [B,H,P,N] fp32 (NULL: not written); S_T may
  *            be exactly S0
- * Growth (dt A > 0) is taken while its product over 512 tokens stays in fp32's
- * range, and so do the products (C_i . B_j) dt_j; past it results are inf or NaN,
- * also where the tokens one by one would stay finite.
+ * A token reaches itself and later tokens alone, also where it holds an inf or a
+ * NaN. Growth (dt A > 0) is taken while its product over the sequence stays in
+ * fp32's range, and so do the products (C_i . B_j) dt_j; past it results are inf or
+ * NaN, also where the tokens one by one would stay finite.
  * P, N in {32, 64, 128}; any T. Tensors of P or N columns start on 16 bytes, in
  * this call and the next two (OSDN_ERR_MISALIGNED). workspace: ssm_forward_workspace_bytes(...) bytes,
  * 256-byte aligned: the chunks' decays, and the states between the segments
@@ -557,6 +558,9 @@ int ssm_decode(int B, int H, int G, int T, int P, int N, int dtype,
  *   ddt      [B,H,T] fp32 OUT (required): of the raw dt, through the softplus
  *   dA       [H] fp32 OUT (required);  dD, ddt_bias [H], dS0 [B,H,P,N] fp32 OUT
  *            (NULL: not written)
+ * An inf or NaN inside a sequence may make any gradient of its head in that batch
+ * entry NaN, dB and dC of its group there, and the parameters' gradients of its head;
+ * other heads, groups and batch entries keep theirs.
  *   workspace: ssm_backward_workspace_bytes(...) bytes, 256-byte aligned: the
  *            state and its adjoint at every chunk's ends (2 P N floats for each
  *            64 tokens (bf16) or 32 (fp32) of a (batch, head)), the states
