@@ -20,6 +20,9 @@ inline bool grid_ok(long long blocks, int threads) {
   return blocks < (1LL << 32) / threads;
 }
 
+// The column sum below: 32 columns a workgroup of 1024 threads.
+inline bool column_sum_ok(long long cols) { return grid_ok((cols + 31) / 32, 1024); }
+
 inline int row_cx(long long ngroups) {
   int cx = 1;
   while (cx < 64 && cx < ngroups) cx *= 2;

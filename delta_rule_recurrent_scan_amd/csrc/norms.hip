@@ -170,6 +170,7 @@ template <typename Tin>
 int run_gated_bwd(const GatedNormArgs& a, hipStream_t s) {
   const int ng = a.H * a.D / 8, cx = row_cx(ng);
   const int nrb = gate_row_blocks(a.B, a.H, a.T, a.D);
+  if (!column_sum_ok(a.per_head ? (long long)a.H * a.D : a.D)) return -1;
   const dim3 grid((unsigned)((ng + cx - 1) / cx * nrb));
   const int tk = ktimer_before(s, "gated_norm_bwd");
   if (nrb == 0) {

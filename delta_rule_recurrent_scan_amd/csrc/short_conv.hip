@@ -465,7 +465,7 @@ int run_conv_bwd(const ConvBackwardArgs& p, hipStream_t s) {
   const int C = a.H * a.D, ng = (C + kBwdV - 1) / kBwdV;
   const BwdGrid g = bwd_grid(a.B, a.T, C, W);
   const long long wgs = (ng + g.cx - 1) / g.cx * (long long)g.parts;
-  if (!grid_ok(wgs, kRowThreads)) return -1;
+  if (!grid_ok(wgs, kRowThreads) || !column_sum_ok((W + 1ll) * C)) return -1;
   const dim3 grid((unsigned)wgs);
   const size_t m = 16 - 1, es = sizeof(Tin);
   const bool aln = a.D % 8 == 0 && ((size_t)a.x & m) == 0 && ((size_t)p.dy & m) == 0 &&

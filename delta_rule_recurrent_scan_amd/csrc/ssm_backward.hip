@@ -669,7 +669,7 @@ int run_bwd(const SsmArgs& a, hipStream_t s) {
   const long long chunks = (long long)BH * p.nch, streams = 2ll * BH * SL;
   const long long wgs = (long long)a.B * a.G * p.nch * p.parts;
   if (!grid_ok((chunks + 3) / 4, 256) || !grid_ok(streams * p.nseg, NT) ||
-      !grid_ok(wgs, kThreads))
+      !grid_ok(wgs, kThreads) || !column_sum_ok(3ll * a.H))
     return -1;
   launch_decay<Q>(a, decay, s);
   if (BH == 0)  // an empty batch: zeros for the parameters
