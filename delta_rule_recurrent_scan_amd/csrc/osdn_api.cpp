@@ -56,10 +56,12 @@ const char* osdn_strerror(int status) {
   switch (status) {
     case OSDN_OK: return "ok";
     case OSDN_ERR_NULL_ARG: return "a required pointer argument is NULL";
-    case OSDN_ERR_BAD_DIMS: 
-      return "bad dimensions: sizes and strides must be >= 0, groups divide the heads";
+    case OSDN_ERR_BAD_DIMS:
+      return "bad dimensions: B, H and T must be >= 0 (as other sizes and strides; "
+             "groups divide the heads)";
     case OSDN_ERR_UNSUPPORTED:
-      return "unsupported combination of sizes and dtype";
+      return "unsupported combination of Dk, Dv, chunk and dtype (around the "
+             "recurrences: of sizes and dtype)";
     case OSDN_ERR_WORKSPACE: return "workspace missing or too small";
     case OSDN_ERR_ALIASING:
       return "an output overlaps an input or another output";
