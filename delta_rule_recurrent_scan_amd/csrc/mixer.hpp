@@ -136,8 +136,8 @@ size_t ssm_backward_ws(int B, int H, int G, int T, int P, int N, int bf16);
 
 // Column sums of fp32 partials [rows][cols]; column j goes to
 // out0[(j % c) * w + j / c] while j / c < w, then to out1[j % c] and out2[j %
-// c] (null: dropped). Parameter gradients are summed this way, in a fixed order, so
-// that a call gives the same bits every time.
+// c] (null: dropped). Parameter gradients are summed this way, in 64 bits and a fixed
+// order, so that a call gives the same bits every time.
 int launch_column_sum(const float* in, int rows, int cols, int c, int w,
                       float* out0, float* out1, float* out2, hipStream_t s);
 

@@ -367,14 +367,15 @@ __global__ __launch_bounds__(kRowThreads) void conv_bwd_kernel(ConvBackwardArgs 
 }
 
 // 32 columns and 32 row lanes a workgroup; a lane adds every 32nd row, eight
-// in flight, then the lanes are added in LDS.
+// in flight, then the lanes are added in LDS. In 64 bits, rounded once: the kernel
+// waits for its rows, not for its sums.
 __global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restrict__ in, int rows,
                                                           int cols, int c, int w, float* out0,
                                                           float* out1, float* out2) {
-  __shared__ float red[32][33];
+  __shared__ double red[32][33];
   const int x = threadIdx.x & 31, r0 = threadIdx.x >> 5;
   const int j = blockIdx.x * 32 + x;
-  float s[8] = {};
+  double s[8] = {};
   if (j < cols) {
     const float* p = in + j;
     int r = r0;
@@ -395,9 +396,9 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restric
   if (r0 == 0 && j < cols) {
     const int k = j / c, ch = j % c;
     if (k < w) {
-      out0[(size_t)ch * w + k] = red[0][x];
+      out0[(size_t)ch * w + k] = (float)red[0][x];
     } else if (float* o = k == w ? out1 : out2) {
-      o[ch] = red[0][x];
+      o[ch] = (float)red[0][x];
     }
   }
 }
