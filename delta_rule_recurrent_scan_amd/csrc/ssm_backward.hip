@@ -30,17 +30,20 @@
 // and no atomics. The wave's share is a token tile for the scores and dx, and
 // tiles of state columns n for dB and dC.
 //
-// Rounding (bf16 inputs): dS is rounded to bf16 once for dx, K and Z enter their
-// products in two bf16 parts (16 bits; one part is 2e-3 of each head's terms, and
-// more of the sums where the heads of a group cancel); S, dS and the walks' dt x L enter in
-// three bf16 parts (24 bits) wherever the result reaches an fp32 output.
+// Rounding (bf16 inputs): dS enters dx, and K and Z their products, in two bf16 parts
+// (16 bits; one part is 2e-3 of each head's terms, and more of the sums where the
+// heads of a group cancel); S, dS and the walks' dt x L enter in three bf16 parts (24
+// bits) wherever the result reaches an fp32 output. The errors of dx, dB and dC are
+// the results' own rounding. dS in one part left dx 1.9e-3 to 2.0e-3 off where dS makes
+// up most of it, and the chunk kernel took 116 us instead of 127: at 128 x 128 both
+// parts fit into LDS for one half of P after the other, two barriers a head more.
 //
 // What bounds it: at B 4, H 16, G 2, T 2048, 128 x 128 bf16 the states are 268 MB,
-// written by the walk (90 us; 4.9 TB/s with the rows it reads) and read by the
-// chunk kernel (116 us: LDS and VALU each busy a third of it, the matrix units a
-// sixth, two barriers a head). The inputs and gradients alone are 123 MB, 23
-// us. Longer chunks would move fewer states, but a chunk's pairs and its rows of
-// four tensors fill the LDS at 64. On the way here: states in whole rows of P and
+// written by the walk (92 us; 4.8 TB/s with the rows it reads) and read by the
+// chunk kernel (127 us: one workgroup a CU by its LDS, four barriers a head; LDS and
+// VALU each busy a third of it, two fifths of the LDS cycles bank conflicts). The
+// inputs and gradients alone are 123 MB, 23 us. Longer chunks would move fewer states,
+// but a chunk's pairs and its rows of four tensors fill the LDS at 64. On the way here: states in whole rows of P and
 // 64-bit lane addresses spilled registers, and every reload waits for all loads in
 // flight (chunk kernel 338 us); a workgroup walking all P rows 106 us, slices of
 // 32 rows 107 us, of 64 rows 90 us.
@@ -242,7 +245,11 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
   constexpr int M2 = two_parts<Tin>(), QL = Q * LQ;
   __shared__ __attribute__((aligned(16))) Tin Ks[M2 * QL];
   __shared__ __attribute__((aligned(16))) Tin Zs[M2 * QL];
-  __shared__ __attribute__((aligned(16))) Tin dSs[N * LP];
+  // dS in its parts, over all of P or (128 x 128, where LDS has no room for both
+  // parts of all of it) over one half after the other
+  constexpr int NS = M2 == 2 && P * N >= 128 * 128 ? 2 : 1, PS = P / NS, LS = PS + PAD,
+                DL = N * LS;
+  __shared__ __attribute__((aligned(16))) Tin dSs[M2 * DL];
   __shared__ __attribute__((aligned(16))) ChunkDecay<Q> decs[2];
   // sums of a head, read while the next one is worked on
   struct Sums {
@@ -355,6 +362,7 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
     // is in flight from the middle of the head before it, the second while the
     // scores are formed
     constexpr int NH = P >= 64 ? 2 : 1, PH = P / NH, PHL = PH / 16;
+    static_assert(NS == 1 || NS == NH, "dS by the halves that are loaded");
     f32x4 sv[NH][PHL], dv[NH][PHL];
     auto load_states = [&](int h, int hf) {
       const float* sf = o.states + (((size_t)b * a.H + h) * nch + c) * P * N;
@@ -447,7 +455,8 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
 #pragma unroll
           for (int pb = 0; pb < PHL; ++pb) {
             const f32x4 &u = sv[hf][pb], &v = dv[hf][pb];
-            store4(ds + (nt * 16 + lc) * LP + (hf * PHL + pb) * 16 + g4, v);
+            if (NS == 1 || hf == 0)
+              store4_two(ds + (nt * 16 + lc) * LS + (hf * PHL + pb) * 16 + g4, DL, v);
             d[pb] = (u[0] * v[0] + u[1] * v[1]) + (u[2] * v[2] + u[3] * v[3]);
           }
 #pragma unroll
@@ -513,7 +522,7 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
         load_states(h + 1, 0);
       }
       // dB, dC from the chunk's own pairs, over the wave's columns n
-      {
+      auto own_pairs = [&]() {
         Frag<Q, Tin> bT, cT;  // rows n, k = token
         bT.load_kmajor(bs + nt * 16, LN);
         cT.load_kmajor(cs + nt * 16, LN);
@@ -530,11 +539,11 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
             mma(dB[m], cT, zf);
           }
         }
-      }
+      };
 
-      // dx of token tile qi, and its share of dD
+      // dx of token tile qi over the p of dS that lie in LDS, and its share of dD
       float dd = 0.f;
-      {
+      auto inputs = [&](int s) {
         const int j = qi * 16 + lc;
         Frag<N, Tin> bf;
         bf.load(bs + qi * 16 * LN, LN);
@@ -545,13 +554,16 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
         const Buffer dxb =
             make_buffer((Tin*)a.dx + th * P, (long long)rows * P * (int)sizeof(Tin));
 #pragma unroll
-        for (int q = 0; q < (PTL + JH - 1) / JH; ++q) {
-          const int pt = q * JH + jh;
-          if (pt >= PTL) break;
-          Frag<N, Tin> df;
-          df.load_kmajor(ds + pt * 16, LP);  // rows p, k = n
+        for (int q = 0; q < (PTL / NS + JH - 1) / JH; ++q) {
+          const int pl = q * JH + jh, pt = s * (PTL / NS) + pl;
+          if (pl >= PTL / NS) break;
           f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-          mma(acc, df, bf);
+#pragma unroll
+          for (int m = M2 - 1; m >= 0; --m) {
+            Frag<N, Tin> df;
+            df.load_kmajor(ds + m * DL + pl * 16, LS);  // rows p, k = n
+            mma(acc, df, bf);
+          }
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[e] *= f;
           Frag<Q, Tin> yT;
@@ -568,6 +580,21 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_bwd_chunk_kernel(
           buffer_store4(dxb, j * P + pt * 16 + g4, acc, Tin());
           __builtin_amdgcn_sched_barrier(0);
         }
+      };
+      if constexpr (NS == 1) {
+        own_pairs();
+        inputs(0);
+      } else {
+        inputs(0);
+        __syncthreads();
+        if (tn == 0) {
+#pragma unroll
+          for (int pb = 0; pb < PHL; ++pb)
+            store4_two(ds + (nt * 16 + lc) * LS + pb * 16 + g4, DL, dv[1][pb]);
+        }
+        own_pairs();
+        __syncthreads();
+        inputs(1);
       }
       dd = wave_sum(dd);
       if (lane == 0) z.dd[w] = dd;
