@@ -658,14 +658,18 @@ Plan make_plan(int B, int H, int G, int T, int P, int N, int Q) {
   Plan p{};
   const long long BH = (long long)B * H;
   p.nch = (T + Q - 1) / Q;
-  // walks: a workgroup a CU over both directions, in segments of 4 chunks at
-  // least (a second segment costs a pass that writes no states and two
-  // launches); not below 12 chunks (64 streams of 64 x 128, 8 chunks of bf16: the
-  // whole backward 55 us in one walk, 60 us in two segments)
+  // walks: a workgroup a CU over both directions, in segments of 4 chunks at least,
+  // and none at all if that makes fewer than 4: a pass that writes no states and two
+  // more launches then cost what the shorter walk gives. The whole backward in one walk
+  // and in segments, bf16: 8 pairs of 64 x 128, 8 chunks 41 and 45 us, 12 chunks 48.5
+  // and 48, 16 chunks 57 and 48, 48 chunks 120 and 62; of 32 x 32, 12 chunks 29 and 34,
+  // 16 chunks 33 and 34, 24 chunks 39 and 35; 32 pairs of 64 x 128 (4 segments), 24
+  // chunks 116 and 102; 64 pairs (2 segments), 16 chunks 86 and 89; 100 pairs (2), 16
+  // chunks 112 and 122, 48 chunks 416 and 437.
   const long long streams = 2 * BH * (P < 64 ? 1 : P / 64);
   long long want = streams > 0 ? (256 + streams - 1) / streams : 1;
   if (want > p.nch / 4) want = p.nch / 4;
-  if (want < 1 || p.nch < 12) want = 1;
+  if (want < 4) want = 1;
   p.segch = p.nch > 0 ? (int)((p.nch + want - 1) / want) : 1;
   p.nseg = p.nch > 0 ? (p.nch + p.segch - 1) / p.segch : 1;
   // chunks: heads of a group are split where the chunks alone leave CUs idle
