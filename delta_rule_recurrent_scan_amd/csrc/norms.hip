@@ -13,17 +13,17 @@
 // lanes; a row of the residual norm is one wave (up to 1536 elements, no
 // barrier) or four, held in registers between the sum and the scaling. In bf16,
 // where a copy of 256 MiB reaches 5.4 TB/s: gated norm of 16384 rows of 16 heads of
-// 128, 201 MB, 36 us (5.6 TB/s); residual norm of 16384 rows of 2048 on a 32-bit
-// stream, 403 MB, 71 us (5.7 TB/s).
+// 128, 201 MB, 36 to 38 us (5.3 to 5.6 TB/s); residual norm of 16384 rows of 2048 on a 32-bit
+// stream, 403 MB, 68 to 72 us (5.6 to 5.9 TB/s).
 //
 // Backward of n = v r, y = n * weight (r the reciprocal root):
 //   dn = dy * weight,  dv = r (dn - n mean(n dn)),  dweight = sum dy n
 // Weight gradients stay in registers while a workgroup walks its rows, are
 // added over its row lanes in LDS and leave as one partial a workgroup,
 // summed in a fixed order by column_sum. Gated: 16384 rows of 8 heads of 64, 84 MB,
-// 16 us and 2 us for the sum; residual: 4097 rows of 1021, 42 MB, 11 us and 3 us
-// (with a partial a wave and unaligned rows element by element it was 69 us: they
-// take the same wide accesses as aligned ones now).
+// 16 to 19 us and 2 to 4 us for the sum; residual: 4097 rows of 1021, 42 MB, 11 to 14
+// us and 3 to 5 us (with a partial a wave and unaligned rows element by element it was
+// 69 us: they take the same wide accesses as aligned ones now).
 #include "launch.hpp"
 #include "mixer.hpp"
 #include "row_common.hpp"
@@ -35,8 +35,8 @@ namespace {
 // Gated head norm
 // ---------------------------------------------------------------------------
 
-// A thread takes 8 channels of one row: 201 MB of bf16 in 37 us, where 2 rows a
-// thread take 39 and 4 take 43 (fewer workgroups, each longer).
+// A thread takes 8 channels of one row: of 201 MB of bf16, in turn, 1 row a thread
+// takes 37 us, 2 take 39 and 4 take 43 (fewer workgroups, each longer).
 template <typename Tin, bool ZALN>
 __global__ __launch_bounds__(kRowThreads) void gated_norm_kernel(GatedNormArgs a, int cx) {
   const int D = a.D, C = a.H * D, ng = C / 8, L = D / 8;

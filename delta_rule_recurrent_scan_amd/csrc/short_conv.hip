@@ -15,8 +15,8 @@
 // DPP sum: no LDS. B 4, T 4096, 4096 channels of bf16 with the norm, 268 MB: 63
 // us, 4.3 TB/s, where a copy of 256 MiB reaches 5.4 TB/s. Rows are fetched raw,
 // eight in flight, and addressed by pointers that advance: widened at once, with an
-// address formed a token, they took 84 us. A single token of 2048 channels is the
-// launch alone.
+// address formed a token, they took 84 us. A single token takes 4 to 8 us whether one
+// sequence or 128, 256 channels or 2048: loads of weights, state and row in turn.
 //
 // Backward, with dv = r (dy - v r^2 <v, dy>) for the norm (r = rsqrt(..)),
 // du = dv * sigmoid(u) (1 + u (1 - sigmoid(u))) and the inputs with their
@@ -423,6 +423,10 @@ int run_conv(const ConvArgs& a, hipStream_t s) {
   const long long wgs = (ng + cx - 1) / cx * ((rows + per - 1) / per);
   if (!grid_ok(wgs, kRowThreads)) return -1;
   const dim3 grid((unsigned)wgs);
+  // Rows of 16-byte pieces, or element by element where any tensor's rows start
+  // elsewhere or heads end inside a thread's 8 channels: B 4, T 4096, 4096 channels of
+  // bf16 (fp32) in 59 (119) us aligned, 120 (226) us with rows of 4101, 209 (282) us
+  // with heads of 20; the backward of 8 x 2048 x 2048 in 52 (88), 106 (110) and 116 (123) us.
   const size_t m = 16 - 1, es = sizeof(Tin);
   const bool aln = a.D % 8 == 0 && ((size_t)a.x & m) == 0 && ((size_t)a.y & m) == 0 &&
                    ((size_t)a.state0 & m) == 0 && ((size_t)a.stateT & m) == 0 &&

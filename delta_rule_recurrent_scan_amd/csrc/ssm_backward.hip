@@ -35,13 +35,14 @@
 // heads of a group cancel); S, dS and the walks' dt x L enter in three bf16 parts (24
 // bits) wherever the result reaches an fp32 output. The errors of dx, dB and dC are
 // the results' own rounding. dS in one part left dx 1.9e-3 to 2.0e-3 off where dS makes
-// up most of it, and the chunk kernel took 116 us instead of 127: at 128 x 128 both
+// up most of it, and the chunk kernel took 116 us instead of 128: at 128 x 128 both
 // parts fit into LDS for one half of P after the other, two barriers a head more.
 //
 // What bounds it: at B 4, H 16, G 2, T 2048, 128 x 128 bf16 the states are 268 MB,
-// written by the walk (92 us; 4.8 TB/s with the rows it reads) and read by the
-// chunk kernel (127 us: one workgroup a CU by its LDS, four barriers a head; LDS and
-// VALU each busy a third of it, two fifths of the LDS cycles bank conflicts). The
+// written by the walk (92 to 96 us; 4.7 TB/s with the rows it reads) and read by the
+// chunk kernel (128 us: one workgroup a CU by its LDS, four barriers a head; LDS and
+// VALU each busy two fifths of it, the matrix units a fifth; 44 % of the LDS cycles are
+// bank conflicts, 33 % in the walk). The
 // inputs and gradients alone are 123 MB, 23 us. Longer chunks would move fewer states,
 // but a chunk's pairs and its rows of four tensors fill the LDS at 64. On the way here: states in whole rows of P and
 // 64-bit lane addresses spilled registers, and every reload waits for all loads in
