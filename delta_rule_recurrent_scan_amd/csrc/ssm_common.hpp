@@ -108,10 +108,12 @@ struct ChunkDecay {
   __device__ __forceinline__ void fill(float step, float sl, float A) {
     constexpr int NB = Q / 16;
     const int t = threadIdx.x & 63;
-    // below -1e4 a decay is zero whatever it is; kept finite there, so that the
-    // sums' rounding errors stay numbers
+    // below -256 a decay is zero whatever it is (and stays it over any growth that
+    // fp32 holds); cut there, so that the sums' rounding errors are numbers, and
+    // small enough to enter the exponential to first order: behind 15 tokens of -1e4
+    // a pair's factor was off by 3e-5
     const float p = step * A;
-    const Log2f l = p < -1e4f ? Log2f{-1e4f, 0.f} : Log2f{p, fmaf(step, A, -p)};
+    const Log2f l = p < -256.f ? Log2f{-256.f, 0.f} : Log2f{p, fmaf(step, A, -p)};
     const Log2f u = row16_prefix(l), d = row16_suffix_after(l);
     Log2f bs[NB];
 #pragma unroll
