@@ -33,8 +33,8 @@
 // What bounds it: at B 4, H 16, G 2, T 4096, 128 x 128 bf16 the products, with
 // the state's update in three parts and formed twice (by the first pass and by
 // the scan), are 73 GFLOP, 63 us at the 1150 TFLOP/s that a large matrix product
-// reaches; the kernels take 130 us (decays 6, first pass 33, chain 10, scan 81).
-// The 156 MB of inputs and outputs alone would be 29 us. In the scan the matrix
+// reaches; the kernels take 131 to 134 us (decays 6, first pass 34, chain 10, scan 81
+// to 84). The 156 MB of inputs and outputs alone would be 29 us. In the scan the matrix
 // units, the VALU (splitting, decays) and LDS are each busy a third of the time,
 // one after the other within a chunk, with two waves a SIMD to overlap them.
 // Measured beside it, scores and state in one part (67 us): the update in one part
