@@ -42,12 +42,12 @@
 // written by the walk (92 to 96 us; 4.7 TB/s with the rows it reads) and read by the
 // chunk kernel (128 us: one workgroup a CU by its LDS, four barriers a head; LDS and
 // VALU each busy two fifths of it, the matrix units a fifth; 44 % of the LDS cycles are
-// bank conflicts, 33 % in the walk). The
-// inputs and gradients alone are 123 MB, 23 us. Longer chunks would move fewer states,
-// but a chunk's pairs and its rows of four tensors fill the LDS at 64. On the way here: states in whole rows of P and
-// 64-bit lane addresses spilled registers, and every reload waits for all loads in
-// flight (chunk kernel 338 us); a workgroup walking all P rows 106 us, slices of
-// 32 rows 107 us, of 64 rows 90 us.
+// bank conflicts, 33 % in the walk). The inputs and gradients alone are 123 MB, 23 us.
+// Longer chunks would move fewer states, but a chunk's pairs and its rows of four
+// tensors fill the LDS at 64. On the way here: states in whole rows of P and 64-bit
+// lane addresses spilled registers, and every reload waits for all loads in flight
+// (chunk kernel 338 us); a workgroup walking all P rows 106 us, slices of 32 rows 107
+// us, of 64 rows 90 us.
 #include "launch.hpp"
 #include "mixer.hpp"
 #include "ssm_common.hpp"
