@@ -111,6 +111,7 @@ def load_library():
     L.osdn_kernel_times.argtypes = [I, P, P, P]
     L.osdn_kernel_times.restype = I
     mixer.bind(L)
+    layer.bind(L)
     _lib = L
     return L
 
@@ -663,5 +664,7 @@ def osdn_gated_forward(q, k, v, beta, log_alpha, r=None, eta=0.1, d0=None,
 
 from . import mixer  # noqa: E402  (uses the helpers above)
 from .mixer import *  # noqa: E402,F401,F403
+from . import layer  # noqa: E402  (uses the helpers above and the mixer's)
+from .layer import *  # noqa: E402,F401,F403
 
-__all__ += mixer.__all__
+__all__ += mixer.__all__ + layer.__all__

@@ -1,0 +1,697 @@
+// Gated linear recurrence, one decay per channel and token:
+//   rho = sigmoid(r),  la = A rho,  a = exp(la),  m = sqrt(1 - a^2) (or 1)
+//   h_t = a_t h_{t-1} + m_t sigmoid(i_t) x_t,     y_t = h_t
+// and its adjoint. With g_t = dy_t + a_{t+1} g_{t+1}:
+//   dx = g m sigmoid(i),  di = g m x sigmoid'(i)
+//   dla = g (a h_{t-1} - (a^2 / m) sigmoid(i) x),  dr = dla la (1 - rho),
+//   dA = sum dla rho.
+//
+// A workgroup walks the tokens of one sequence (or a segment of it) for 64
+// channels, a tile of 128 tokens at a time: a thread holds 8 tokens of 2
+// channels, two threads a wave's half each, eight waves a tile. Every thread
+// runs its own tokens from zero, the ends are joined over the waves through
+// LDS with one barrier a tile, and a second run over the registers from the
+// joined state gives the results: every input is read once and every output
+// written once. Where the sequences and channels alone leave CUs idle the
+// tokens are cut into segments, whose sums a first launch forms.
+//
+// Decays lie close to one and act over thousands of tokens. A product of
+// rounded decays would be off by their common rounding times the number of
+// tokens, so what carries a state over 8 tokens and more is the exponential of
+// a sum of the logarithms; only inside 8 tokens are the decays themselves used.
+// 1 - a^2 comes from a series where it is small.
+#include "launch.hpp"
+#include "layer.hpp"
+#include "row_common.hpp"
+
+namespace osdn {
+namespace {
+
+constexpr int kThreads = 512, kWaves = 8;
+constexpr int kK = 8;                      // tokens a thread
+constexpr int kTile = 2 * kWaves * kK;     // 128 tokens
+constexpr int kCols = 64;                  // channels a workgroup
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
+
+// Two channels of one token as they lie in memory. The base is the same in
+// all lanes and the byte offset 32 bits.
+template <typename T>
+struct Pair;
+template <>
+struct Pair<__bf16> {
+  unsigned u;
+  template <bool ALN>
+  __device__ __forceinline__ void load(const char* base, unsigned o0, unsigned o1) {
+    if constexpr (ALN) {
+      u = *(const unsigned*)(base + o0);
+    } else {
+      u = (unsigned)*(const unsigned short*)(base + o0) |
+          (unsigned)*(const unsigned short*)(base + o1) << 16;
+    }
+  }
+  __device__ __forceinline__ float get(int j) const { return j ? high_bf16(u) : low_bf16(u); }
+};
+template <>
+struct Pair<float> {
+  float v[2];
+  template <bool ALN>
+  __device__ __forceinline__ void load(const char* base, unsigned o0, unsigned o1) {
+    if constexpr (ALN) {
+      const float2 t = *(const float2*)(base + o0);
+      v[0] = t.x; v[1] = t.y;
+    } else {
+      v[0] = *(const float*)(base + o0);
+      v[1] = *(const float*)(base + o1);
+    }
+  }
+  __device__ __forceinline__ float get(int j) const { return v[j]; }
+};
+
+template <bool ALN, typename T>
+__device__ __forceinline__ void store_pair(T* p, float v0, float v1, int n) {
+  if constexpr (ALN) {
+    if (n <= 0) return;
+    if constexpr (sizeof(T) == 2) {
+      *(unsigned*)p = pack_bf16(v0, v1);
+    } else {
+      *(float2*)p = float2{v0, v1};
+    }
+  } else {
+    if (n > 0) p[0] = from_f32<T>(v0);
+    if (n > 1) p[1] = from_f32<T>(v1);
+  }
+}
+
+// A thread's place: tokens first .. first + 7 of the tile and channels c, c + 1.
+struct Place {
+  int seg, c, n;        // n: how many of the two channels exist
+  int c0, c1;           // the channels it reads (the last ones where there are none)
+};
+template <bool ALN>
+__device__ __forceinline__ Place place(int cb, int C) {
+  Place p;
+  const int lane = threadIdx.x & 63;
+  p.seg = 2 * wave_id() + (lane >> 5);
+  p.c = cb * kCols + 2 * (lane & 31);
+  p.n = C - p.c;
+  p.c0 = min(p.c, ALN ? C - 2 : C - 1);
+  p.c1 = min(p.c + 1, C - 1);
+  return p;
+}
+
+// One input's rows of a tile.
+template <typename Tin, bool ALN>
+struct Rows {
+  Pair<Tin> v[kK];
+  // tokens t .. t + 7 (t: the thread's first) of rows at p with stride ts;
+  // tokens from n on read token n - 1.
+  __device__ __forceinline__ void load(const Tin* p, long long ts, int tile, int seg, int n,
+                                       const Place& pl) {
+    const char* base = (const char*)(p + (long long)tile * ts);
+    const unsigned row = (unsigned)ts * (unsigned)sizeof(Tin);
+    const unsigned b0 = pl.c0 * (unsigned)sizeof(Tin), b1 = pl.c1 * (unsigned)sizeof(Tin);
+    if (tile + kTile <= n) {
+      const unsigned o = row * (unsigned)(seg * kK);
+#pragma unroll
+      for (int k = 0; k < kK; ++k)
+        v[k].template load<ALN>(base + (size_t)row * k, o + b0, o + b1);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kK; ++k) {
+        const unsigned o = row * (unsigned)min(seg * kK + k, n - 1 - tile);
+        v[k].template load<ALN>(base, o + b0, o + b1);
+      }
+    }
+  }
+};
+
+// 1 - exp(z) for z <= 0 where e is exp(z): a series where the difference would
+// lose digits (from -0.35 on its eighth term is under half a step).
+__device__ __forceinline__ float one_minus_exp(float z, float e) {
+  float p = 1.f / 5040.f;
+  p = fmaf(p, z, 1.f / 720.f);
+  p = fmaf(p, z, 1.f / 120.f);
+  p = fmaf(p, z, 1.f / 24.f);
+  p = fmaf(p, z, 1.f / 6.f);
+  p = fmaf(p, z, 0.5f);
+  p = fmaf(p, z, 1.f);
+  return z > -0.35f ? -z * p : 1.f - e;
+}
+
+// Decay and input factor of one token and channel: A2 = A log2(e).
+template <bool NORM>
+__device__ __forceinline__ void factors(float r, float A2, float& rho, float& l2, float& a,
+                                        float& m) {
+  rho = sigmoid_f(r);
+  l2 = A2 * rho;
+  a = __builtin_amdgcn_exp2f(l2);
+  m = NORM ? __builtin_amdgcn_sqrtf(one_minus_exp(2.f * kLn2 * l2, a * a)) : 1.f;
+}
+
+// The value of lane l ^ 32.
+__device__ __forceinline__ float other_half(float x) {
+  const unsigned u = __float_as_uint(x);
+  const auto s = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const unsigned lo = s[0], hi = s[1];
+  return __uint_as_float((threadIdx.x & 32) ? lo : hi);
+}
+
+// Joins the threads' ends over a tile. A run of tokens maps the state c that
+// enters it to exp2(L) c + H; in front of a thread's tokens stand the other half
+// of its wave and the waves before (FWD: 0 .. 7 in turn, else 7 .. 0). Returns
+// the state that enters this thread's tokens in `in` and carries the tile's.
+//
+// The carried state is updated as c + (H - (1 - exp2(L)) c): the factor's
+// distance from one keeps its digits, so that steps of long memory do not add up
+// the factors' roundings.
+template <bool FWD>
+__device__ __forceinline__ void join(const float (&L)[2], const float (&H)[2], float (&carry)[2],
+                                     float (&in)[2], float4* buf) {
+  const int lane = threadIdx.x & 63, w = wave_id();
+  const bool first = FWD ? lane < 32 : lane >= 32;
+  float p[2], po[2], Ho[2], Q[2], E[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    p[j] = __builtin_amdgcn_exp2f(L[j]);
+    po[j] = other_half(p[j]);
+    Ho[j] = other_half(H[j]);
+    const float l = L[j] + other_half(L[j]);
+    Q[j] = one_minus_exp(kLn2 * l, p[j] * po[j]);
+    E[j] = fmaf(p[j], Ho[j], H[j]);
+  }
+  if (!first) buf[w * 32 + (lane & 31)] = float4{Q[0], E[0], Q[1], E[1]};
+  __syncthreads();
+  float c0 = carry[0], c1 = carry[1], m0 = c0, m1 = c1;
+#pragma unroll
+  for (int q = 0; q < kWaves; ++q) {
+    const int v = FWD ? q : kWaves - 1 - q;
+    const float4 t = buf[v * 32 + (lane & 31)];
+    if (v == w) {
+      m0 = c0;
+      m1 = c1;
+    }
+    c0 += fmaf(-t.x, c0, t.y);
+    c1 += fmaf(-t.z, c1, t.w);
+  }
+  carry[0] = c0;
+  carry[1] = c1;
+  in[0] = first ? m0 : fmaf(po[0], m0, Ho[0]);
+  in[1] = first ? m1 : fmaf(po[1], m1, Ho[1]);
+}
+
+__device__ __forceinline__ int seq_len(const GlrArgs& a, int b) {
+  return a.lengths ? max(0, min(a.lengths[b], a.T)) : a.T;
+}
+
+// A segment's map, (L, H) of each channel: [B][S][2][C].
+__device__ __forceinline__ float* seg_map(float* ws, int b, int S, int q, int C) {
+  return ws + ((size_t)b * S + q) * 2 * C;
+}
+
+// The state that enters segment q: h0 (or dh_T) through the segments before
+// it (FWD) or behind it.
+template <bool FWD>
+__device__ __forceinline__ void enter(const float* start, const float* ws, int b, int S, int q,
+                                      int C, const Place& pl, float (&c)[2]) {
+  c[0] = start ? start[(size_t)b * C + pl.c0] : 0.f;
+  c[1] = start ? start[(size_t)b * C + pl.c1] : 0.f;
+  for (int j = FWD ? 0 : S - 1; FWD ? j < q : j > q; j += FWD ? 1 : -1) {
+    const float* m = ws + ((size_t)b * S + j) * 2 * C;
+    c[0] = fmaf(__builtin_amdgcn_exp2f(m[pl.c0]), c[0], m[C + pl.c0]);
+    c[1] = fmaf(__builtin_amdgcn_exp2f(m[pl.c1]), c[1], m[C + pl.c1]);
+  }
+}
+
+// Tokens of segment q of S of a sequence of n, whole tiles.
+__device__ __forceinline__ void seg_range(int n, int S, int q, int& t0, int& t1) {
+  const int tiles = (n + kTile - 1) / kTile, per = (tiles + S - 1) / S;
+  t0 = min(n, q * per * kTile);
+  t1 = min(n, (q + 1) * per * kTile);
+}
+
+// ---------------------------------------------------------------------------
+// Forward. PART: only the segments' maps (the first launch).
+// ---------------------------------------------------------------------------
+
+template <typename Tin, bool ALN, bool GATE, bool NORM, bool PART>
+__global__ __launch_bounds__(kThreads) void glr_kernel(GlrArgs a, int ncb, int S) {
+  __shared__ float4 buf[2][kWaves * 32];
+  const int cb = blockIdx.x % ncb, bq = blockIdx.x / ncb;
+  const int nq = PART ? S - 1 : S, q = bq % nq, b = bq / nq;
+  const Place pl = place<ALN>(cb, a.C);
+  const int n = seq_len(a, b);
+  int t0, t1;
+  seg_range(n, S, q, t0, t1);
+  const Tin* x = (const Tin*)a.x + b * a.xbs;
+  const Tin* r = (const Tin*)a.r + b * a.rbs;
+  const Tin* gi = GATE ? (const Tin*)a.i + b * a.ibs : nullptr;
+  float A2[2] = {a.A[pl.c0] * kLog2e, a.A[pl.c1] * kLog2e};
+  float carry[2] = {0.f, 0.f}, Ltot[2] = {0.f, 0.f};
+  if constexpr (!PART) enter<true>(a.h0, (const float*)a.ws, b, S, q, a.C, pl, carry);
+
+  Rows<Tin, ALN> rx, rr, ri;
+  if (t0 < t1) {
+    rx.load(x, a.xts, t0, pl.seg, n, pl);
+    rr.load(r, a.rts, t0, pl.seg, n, pl);
+    if constexpr (GATE) ri.load(gi, a.its, t0, pl.seg, n, pl);
+  }
+  int par = 0;
+  for (int tile = t0; tile < t1; tile += kTile, par ^= 1) {
+    float dec[kK][2], in[kK][2], L[2] = {0.f, 0.f}, H[2] = {0.f, 0.f};
+    const int t = tile + pl.seg * kK;
+#pragma unroll
+    for (int k = 0; k < kK; ++k)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float rho, l2, m;
+        factors<NORM>(rr.v[k].get(j), A2[j], rho, l2, dec[k][j], m);
+        float u = rx.v[k].get(j);
+        if constexpr (GATE) u *= sigmoid_f(ri.v[k].get(j));
+        in[k][j] = m * u;
+        if (tile + kTile > n && t + k >= n) {
+          dec[k][j] = 1.f;
+          in[k][j] = l2 = 0.f;
+        }
+        L[j] += l2;
+        H[j] = fmaf(dec[k][j], H[j], in[k][j]);
+      }
+    const int next = min(tile + kTile, t1 - 1) / kTile * kTile;
+    rx.load(x, a.xts, next, pl.seg, n, pl);
+    rr.load(r, a.rts, next, pl.seg, n, pl);
+    if constexpr (GATE) ri.load(gi, a.its, next, pl.seg, n, pl);
+    float h[2];
+    join<true>(L, H, carry, h, buf[par]);
+    if constexpr (PART) {
+      Ltot[0] += L[0];
+      Ltot[1] += L[1];
+    } else {
+      if (a.states && t % kGlrInterval == 0 && t < a.T) {
+        float* st = a.states + ((size_t)b * ((a.T + kGlrInterval - 1) / kGlrInterval) +
+                                t / kGlrInterval) * a.C + pl.c;
+        store_pair<ALN>(st, h[0], h[1], pl.n);
+      }
+      Tin* y = (Tin*)a.y + ((size_t)b * a.T + t) * a.C + pl.c;
+#pragma unroll
+      for (int k = 0; k < kK; ++k) {
+        h[0] = fmaf(dec[k][0], h[0], in[k][0]);
+        h[1] = fmaf(dec[k][1], h[1], in[k][1]);
+        if (a.y && t + k < n) store_pair<ALN>(y + (size_t)k * a.C, h[0], h[1], pl.n);
+      }
+    }
+  }
+  if constexpr (PART) {
+    // the threads' logarithms added over the 16 of a channel
+    __syncthreads();
+    float* red = (float*)buf;
+    red[pl.seg * kCols + 2 * (threadIdx.x & 31)] = Ltot[0];
+    red[pl.seg * kCols + 2 * (threadIdx.x & 31) + 1] = Ltot[1];
+    __syncthreads();
+    if (threadIdx.x < 32 && pl.n > 0) {
+      float* m = seg_map((float*)a.ws, b, S, q, a.C);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (j >= pl.n) continue;
+        float s = 0.f;
+        for (int w = 0; w < 2 * kWaves; ++w) s += red[w * kCols + 2 * threadIdx.x + j];
+        m[pl.c + j] = s;
+        m[a.C + pl.c + j] = carry[j];
+      }
+    }
+  } else {
+    // the last segment leaves the state, the rows behind the sequence and
+    // their states
+    if (q == S - 1) {
+      if (a.hT && threadIdx.x < 32)
+        store_pair<ALN>(a.hT + (size_t)b * a.C + pl.c, carry[0], carry[1], pl.n);
+      const int ns = (a.T + kGlrInterval - 1) / kGlrInterval;
+      const int s0 = (n + kTile - 1) / kTile * (kTile / kGlrInterval);
+      if (a.states)
+        for (int t = s0 + pl.seg; t < ns; t += 2 * kWaves)
+          store_pair<ALN>(a.states + ((size_t)b * ns + t) * a.C + pl.c, carry[0], carry[1], pl.n);
+      if (a.y)
+        for (int t = n + pl.seg; t < a.T; t += 2 * kWaves)
+          store_pair<ALN>((Tin*)a.y + ((size_t)b * a.T + t) * a.C + pl.c, 0.f, 0.f, pl.n);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Single tokens: two channels a thread, tokens in turn.
+// ---------------------------------------------------------------------------
+
+template <typename Tin, bool ALN, bool GATE, bool NORM>
+__global__ __launch_bounds__(256) void glr_decode_kernel(GlrArgs a) {
+  const int np = (a.C + 1) / 2;
+  const long long at = blockIdx.x * 256LL + threadIdx.x;
+  if (at >= (long long)a.B * np) return;
+  const int b = (int)(at / np), c = (int)(at % np) * 2, n = a.C - c;
+  const int c1 = min(c + 1, a.C - 1);
+  const float A2[2] = {a.A[c] * kLog2e, a.A[c1] * kLog2e};
+  float h[2] = {a.h0[(size_t)b * a.C + c], a.h0[(size_t)b * a.C + c1]};
+  for (int t = 0; t < a.T; ++t) {
+    Pair<Tin> x, r, g;
+    const unsigned o = (unsigned)(c1 - c) * (unsigned)sizeof(Tin);
+    x.template load<ALN>((const char*)((const Tin*)a.x + b * a.xbs + t * a.xts + c), 0, o);
+    r.template load<ALN>((const char*)((const Tin*)a.r + b * a.rbs + t * a.rts + c), 0, o);
+    if constexpr (GATE)
+      g.template load<ALN>((const char*)((const Tin*)a.i + b * a.ibs + t * a.its + c), 0, o);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float rho, l2, d, m, u = x.get(j);
+      factors<NORM>(r.get(j), A2[j], rho, l2, d, m);
+      if constexpr (GATE) u *= sigmoid_f(g.get(j));
+      h[j] = fmaf(d, h[j], m * u);
+    }
+    store_pair<ALN>((Tin*)a.y + ((size_t)b * a.T + t) * a.C + c, h[0], h[1], n);
+  }
+  store_pair<ALN>(a.hT + (size_t)b * a.C + c, h[0], h[1], n);
+}
+
+// ---------------------------------------------------------------------------
+// Backward: tiles from the last to the first. What passes from token t to t - 1
+// is c_t = a_t g_t = a_t (dy_t + c_{t+1}).
+// ---------------------------------------------------------------------------
+
+template <typename Tin, bool ALN>
+__global__ __launch_bounds__(kThreads) void glr_bwd_part_kernel(GlrArgs a, int ncb, int S) {
+  __shared__ float4 buf[2][kWaves * 32];
+  const int cb = blockIdx.x % ncb, bq = blockIdx.x / ncb;
+  const int q = 1 + bq % (S - 1), b = bq / (S - 1);
+  const Place pl = place<ALN>(cb, a.C);
+  const int n = seq_len(a, b);
+  int t0, t1;
+  seg_range(n, S, q, t0, t1);
+  const Tin* r = (const Tin*)a.r + b * a.rbs;
+  const Tin* dy = (const Tin*)a.dy + (size_t)b * a.T * a.C;
+  const float A2[2] = {a.A[pl.c0] * kLog2e, a.A[pl.c1] * kLog2e};
+  float carry[2] = {0.f, 0.f}, Ltot[2] = {0.f, 0.f};
+  Rows<Tin, ALN> rr, rd;
+  int par = 0;
+  for (int tile = t0 < t1 ? (t1 - 1) / kTile * kTile : -1; tile >= t0; tile -= kTile, par ^= 1) {
+    rr.load(r, a.rts, tile, pl.seg, n, pl);
+    rd.load(dy, a.C, tile, pl.seg, n, pl);
+    float L[2] = {0.f, 0.f}, H[2] = {0.f, 0.f};
+    const int t = tile + pl.seg * kK;
+#pragma unroll
+    for (int k = kK - 1; k >= 0; --k)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float l2 = A2[j] * sigmoid_f(rr.v[k].get(j)), d = rd.v[k].get(j);
+        float dec = __builtin_amdgcn_exp2f(l2);
+        if (tile + kTile > n && t + k >= n) {
+          dec = 1.f;
+          l2 = d = 0.f;
+        }
+        L[j] += l2;
+        H[j] = dec * (H[j] + d);
+      }
+    float in[2];
+    join<false>(L, H, carry, in, buf[par]);
+    Ltot[0] += L[0];
+    Ltot[1] += L[1];
+  }
+  __syncthreads();
+  float* red = (float*)buf;
+  red[pl.seg * kCols + 2 * (threadIdx.x & 31)] = Ltot[0];
+  red[pl.seg * kCols + 2 * (threadIdx.x & 31) + 1] = Ltot[1];
+  __syncthreads();
+  if (threadIdx.x < 32 && pl.n > 0) {
+    float* m = seg_map((float*)a.ws, b, S, q, a.C);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (j >= pl.n) continue;
+      float s = 0.f;
+      for (int w = 0; w < 2 * kWaves; ++w) s += red[w * kCols + 2 * threadIdx.x + j];
+      m[pl.c + j] = s;
+      m[a.C + pl.c + j] = carry[j];
+    }
+  }
+}
+
+// parts: [B * S][C], the segments' parts of dA.
+template <typename Tin, bool ALN, bool GATE, bool NORM>
+__global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrArgs a, int ncb, int S,
+                                                           float* parts) {
+  __shared__ float4 buf[2][kWaves * 32];
+  __shared__ double red[2 * kWaves][kCols];
+  const int cb = blockIdx.x % ncb, bq = blockIdx.x / ncb, q = bq % S, b = bq / S;
+  const Place pl = place<ALN>(cb, a.C);
+  const int n = seq_len(a, b), ns = (a.T + kGlrInterval - 1) / kGlrInterval;
+  int t0, t1;
+  seg_range(n, S, q, t0, t1);
+  const Tin* x = (const Tin*)a.x + b * a.xbs;
+  const Tin* r = (const Tin*)a.r + b * a.rbs;
+  const Tin* gi = GATE ? (const Tin*)a.i + b * a.ibs : nullptr;
+  const Tin* dy = (const Tin*)a.dy + (size_t)b * a.T * a.C;
+  const float A2[2] = {a.A[pl.c0] * kLog2e, a.A[pl.c1] * kLog2e};
+  float carry[2];
+  enter<false>(a.dhT, (const float*)a.ws, b, S, q, a.C, pl, carry);
+  double dA[2] = {0.0, 0.0};
+  const int lane = threadIdx.x & 63;
+
+  Rows<Tin, ALN> rx, rr, ri, rd;
+  float s0 = 0.f, s1 = 0.f;
+  auto fetch = [&](int tile) {
+    rr.load(r, a.rts, tile, pl.seg, n, pl);
+    rd.load(dy, a.C, tile, pl.seg, n, pl);
+    rx.load(x, a.xts, tile, pl.seg, n, pl);
+    if constexpr (GATE) ri.load(gi, a.its, tile, pl.seg, n, pl);
+    const int si = min((tile + pl.seg * kK) / kGlrInterval, ns - 1);
+    const float* st = a.states + ((size_t)b * ns + si) * a.C;
+    s0 = st[pl.c0];
+    s1 = st[pl.c1];
+  };
+  const int last = t0 < t1 ? (t1 - 1) / kTile * kTile : -1;
+  int par = 0;
+  for (int tile = last; tile >= t0; tile -= kTile, par ^= 1) {
+    fetch(tile);
+    const int t = tile + pl.seg * kK;
+    float rho[kK][2], l2[kK][2], dec[kK][2], m[kK][2], sg[kK][2], u[kK][2], d[kK][2];
+    float L[2] = {0.f, 0.f}, H[2] = {0.f, 0.f}, F[2] = {lane < 32 ? s0 : 0.f, lane < 32 ? s1 : 0.f};
+    float st[2] = {s0, s1};
+#pragma unroll
+    for (int k = 0; k < kK; ++k)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        factors<NORM>(rr.v[k].get(j), A2[j], rho[k][j], l2[k][j], dec[k][j], m[k][j]);
+        sg[k][j] = GATE ? sigmoid_f(ri.v[k].get(j)) : 1.f;
+        u[k][j] = rx.v[k].get(j) * sg[k][j];
+        d[k][j] = rd.v[k].get(j);
+        if (tile + kTile > n && t + k >= n) {
+          dec[k][j] = 1.f;
+          rho[k][j] = m[k][j] = l2[k][j] = d[k][j] = u[k][j] = 0.f;
+        }
+        L[j] += l2[k][j];
+        F[j] = fmaf(dec[k][j], F[j], m[k][j] * u[k][j]);
+      }
+#pragma unroll
+    for (int k = kK - 1; k >= 0; --k)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) H[j] = dec[k][j] * (H[j] + d[k][j]);
+    // the state before the second half's tokens is the first half's end
+    const float f0 = other_half(F[0]), f1 = other_half(F[1]);
+    float h[2] = {lane < 32 ? st[0] : f0, lane < 32 ? st[1] : f1};
+    float before[kK][2];
+#pragma unroll
+    for (int k = 0; k < kK; ++k)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        before[k][j] = h[j];
+        h[j] = fmaf(dec[k][j], h[j], m[k][j] * u[k][j]);
+      }
+    float c[2], sA[2] = {0.f, 0.f};
+    join<false>(L, H, carry, c, buf[par]);
+    const size_t at = ((size_t)b * a.T + t) * a.C + pl.c;
+#pragma unroll
+    for (int k = kK - 1; k >= 0; --k) {
+      float ox[2], orr[2], oi[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float g = d[k][j] + c[j];
+        c[j] = dec[k][j] * g;
+        const float du = g * m[k][j];
+        ox[j] = du * sg[k][j];
+        oi[j] = du * u[k][j] * (1.f - sg[k][j]);
+        float dla = c[j] * before[k][j];
+        if constexpr (NORM) {
+          // (where a is one no gradient passes through m)
+          const float w = m[k][j] > 0.f
+                              ? dec[k][j] * u[k][j] * __builtin_amdgcn_rcpf(m[k][j])
+                              : 0.f;
+          dla = fmaf(-c[j], w, dla);
+        }
+        orr[j] = dla * (kLn2 * l2[k][j]) * (1.f - rho[k][j]);
+        sA[j] = fmaf(dla, rho[k][j], sA[j]);
+      }
+      if (t + k < n) {
+        store_pair<ALN>((Tin*)a.dx + at + (size_t)k * a.C, ox[0], ox[1], pl.n);
+        store_pair<ALN>((Tin*)a.dr + at + (size_t)k * a.C, orr[0], orr[1], pl.n);
+        if constexpr (GATE)
+          store_pair<ALN>((Tin*)a.di + at + (size_t)k * a.C, oi[0], oi[1], pl.n);
+      }
+    }
+    dA[0] += (double)sA[0];
+    dA[1] += (double)sA[1];
+  }
+  const int lc = 2 * (threadIdx.x & 31);
+  red[pl.seg][lc] = dA[0];
+  red[pl.seg][lc + 1] = dA[1];
+  __syncthreads();
+  if (threadIdx.x < kCols && cb * kCols + (int)threadIdx.x < a.C) {
+    double s = 0.0;
+    for (int w = 0; w < 2 * kWaves; ++w) s += red[w][threadIdx.x];
+    parts[((size_t)b * S + q) * a.C + cb * kCols + threadIdx.x] = (float)s;
+  }
+  if (q == 0 && a.dh0 && threadIdx.x < 32)
+    store_pair<ALN>(a.dh0 + (size_t)b * a.C + pl.c, carry[0], carry[1], pl.n);
+  if (q == S - 1)
+    for (int t = n + pl.seg; t < a.T; t += 2 * kWaves) {
+      const size_t at = ((size_t)b * a.T + t) * a.C + pl.c;
+      store_pair<ALN>((Tin*)a.dx + at, 0.f, 0.f, pl.n);
+      store_pair<ALN>((Tin*)a.dr + at, 0.f, 0.f, pl.n);
+      if constexpr (GATE) store_pair<ALN>((Tin*)a.di + at, 0.f, 0.f, pl.n);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Launches
+// ---------------------------------------------------------------------------
+
+int col_blocks(int C) { return (C + kCols - 1) / kCols; }
+
+// Segments of a sequence: one while the sequences and channels alone give two
+// workgroups a CU or nearly so; otherwise as many as reach that, of two tiles at
+// least.
+int segments(int B, int T, int C) {
+  const long long wgs = (long long)B * col_blocks(C);
+  if (wgs >= 192 || wgs == 0) return 1;
+  const int tiles = (T + kTile - 1) / kTile;
+  long long S = 512 / wgs;
+  if (S > tiles / 2) S = tiles / 2;
+  return S < 2 ? 1 : (int)S;
+}
+
+size_t map_bytes(int B, int T, int C) {
+  const int S = segments(B, T, C);
+  return S > 1 ? ((size_t)B * S * 2 * C * sizeof(float) + 255) / 256 * 256 : 0;
+}
+
+bool even(const void* p, size_t es) { return ((size_t)p & (2 * es - 1)) == 0; }
+
+template <typename Tin, bool ALN, bool GATE, bool NORM>
+int run_forward(const GlrArgs& a, hipStream_t s) {
+  const int ncb = col_blocks(a.C), S = segments(a.B, a.T, a.C);
+  if (!grid_ok((long long)ncb * a.B * S, kThreads)) return -1;
+  if (S > 1) {
+    const int tk = ktimer_before(s, "glr_part");
+    hipLaunchKernelGGL((glr_kernel<Tin, ALN, GATE, NORM, true>),
+                       dim3((unsigned)ncb * a.B * (S - 1)), dim3(kThreads), 0, s, a, ncb, S);
+    ktimer_after(s, tk);
+    const int rc = (int)hipGetLastError();
+    if (rc) return rc;
+  }
+  const int tk = ktimer_before(s, "glr");
+  hipLaunchKernelGGL((glr_kernel<Tin, ALN, GATE, NORM, false>), dim3((unsigned)ncb * a.B * S),
+                     dim3(kThreads), 0, s, a, ncb, S);
+  ktimer_after(s, tk);
+  return (int)hipGetLastError();
+}
+
+template <typename Tin, bool ALN, bool GATE, bool NORM>
+int run_decode(const GlrArgs& a, hipStream_t s) {
+  const long long wgs = ((long long)a.B * ((a.C + 1) / 2) + 255) / 256;
+  if (!grid_ok(wgs, 256)) return -1;
+  const int tk = ktimer_before(s, "glr_decode");
+  hipLaunchKernelGGL((glr_decode_kernel<Tin, ALN, GATE, NORM>), dim3((unsigned)wgs), dim3(256), 0,
+                     s, a);
+  ktimer_after(s, tk);
+  return (int)hipGetLastError();
+}
+
+template <typename Tin, bool ALN, bool GATE, bool NORM>
+int run_backward(const GlrArgs& a0, hipStream_t s) {
+  GlrArgs a = a0;
+  const int ncb = col_blocks(a.C), S = segments(a.B, a.T, a.C);
+  if (!grid_ok((long long)ncb * a.B * S, kThreads) || !column_sum_ok(a.C)) return -1;
+  const size_t maps = map_bytes(a.B, a.T, a.C);
+  float* parts = (float*)((char*)a.ws + maps);
+  if (!a.states && a.T > 0) {
+    // the states that a forward would have left, behind the partial sums
+    a.states = parts + ((size_t)a.B * S * a.C + 63) / 64 * 64;
+    GlrArgs f = a;
+    f.y = nullptr;
+    f.hT = nullptr;
+    const int rc = run_forward<Tin, ALN, GATE, NORM>(f, s);
+    if (rc) return rc;
+  }
+  if (S > 1) {
+    const int tk = ktimer_before(s, "glr_bwd_part");
+    hipLaunchKernelGGL((glr_bwd_part_kernel<Tin, ALN>), dim3((unsigned)ncb * a.B * (S - 1)),
+                       dim3(kThreads), 0, s, a, ncb, S);
+    ktimer_after(s, tk);
+    const int rc = (int)hipGetLastError();
+    if (rc) return rc;
+  }
+  if (a.B > 0) {
+    const int tk = ktimer_before(s, "glr_bwd");
+    hipLaunchKernelGGL((glr_bwd_kernel<Tin, ALN, GATE, NORM>), dim3((unsigned)ncb * a.B * S),
+                       dim3(kThreads), 0, s, a, ncb, S, parts);
+    ktimer_after(s, tk);
+    const int rc = (int)hipGetLastError();
+    if (rc) return rc;
+  }
+  return launch_column_sum(parts, a.B * S, a.C, a.C, 1, a.dA, nullptr, nullptr, s);
+}
+
+// What one launch is instantiated on.
+enum Call { kForward, kDecode, kBackward };
+
+template <Call CALL, typename Tin, bool ALN, bool GATE>
+int run_norm(const GlrArgs& a, hipStream_t s) {
+  if constexpr (CALL == kForward)
+    return a.normalize ? run_forward<Tin, ALN, GATE, true>(a, s)
+                       : run_forward<Tin, ALN, GATE, false>(a, s);
+  if constexpr (CALL == kDecode)
+    return a.normalize ? run_decode<Tin, ALN, GATE, true>(a, s)
+                       : run_decode<Tin, ALN, GATE, false>(a, s);
+  return a.normalize ? run_backward<Tin, ALN, GATE, true>(a, s)
+                     : run_backward<Tin, ALN, GATE, false>(a, s);
+}
+
+template <Call CALL, typename Tin>
+int run_t(const GlrArgs& a, hipStream_t s) {
+  const size_t es = sizeof(Tin);
+  // every pair of channels starts on the size of a pair
+  const bool aln = a.C % 2 == 0 && a.xbs % 2 == 0 && a.xts % 2 == 0 && a.rbs % 2 == 0 &&
+                   a.rts % 2 == 0 && a.ibs % 2 == 0 && a.its % 2 == 0 && even(a.x, es) &&
+                   even(a.r, es) && even(a.i, es) && even(a.y, es) && even(a.dy, es) &&
+                   even(a.dx, es) && even(a.dr, es) && even(a.di, es) && even(a.h0, 4) &&
+                   even(a.hT, 4) && even(a.states, 4) && even(a.dh0, 4);
+  if (aln) return a.i ? run_norm<CALL, Tin, true, true>(a, s) : run_norm<CALL, Tin, true, false>(a, s);
+  return a.i ? run_norm<CALL, Tin, false, true>(a, s) : run_norm<CALL, Tin, false, false>(a, s);
+}
+
+}  // namespace
+
+size_t glr_forward_ws(int B, int T, int C) { return map_bytes(B, T, C); }
+
+int launch_glr_forward(const GlrArgs& a, hipStream_t s) {
+  return a.bf16 ? run_t<kForward, __bf16>(a, s) : run_t<kForward, float>(a, s);
+}
+
+int launch_glr_decode(const GlrArgs& a, hipStream_t s) {
+  return a.bf16 ? run_t<kDecode, __bf16>(a, s) : run_t<kDecode, float>(a, s);
+}
+
+size_t glr_backward_ws(int B, int T, int C, int have_states) {
+  const size_t parts = ((size_t)B * segments(B, T, C) * C + 63) / 64 * 64 * sizeof(float);
+  const size_t st = have_states ? 0
+                                : (size_t)B * ((T + kGlrInterval - 1) / kGlrInterval) * C * sizeof(float);
+  return map_bytes(B, T, C) + parts + st;
+}
+
+int launch_glr_backward(const GlrArgs& a, hipStream_t s) {
+  return a.bf16 ? run_t<kBackward, __bf16>(a, s) : run_t<kBackward, float>(a, s);
+}
+
+}  // namespace osdn

@@ -637,6 +637,159 @@ int residual_norm_backward(long long R, int C, int dtype, int res_dtype,
                            void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Operators that complete a block: the gated linear recurrence (one decay per
+ * channel), the norm and rotation of queries and keys, and the gated feed-forward
+ * product. The conventions of the operators around the recurrences hold here too
+ * (lengths, gradients' types, order of sums); row strides are in elements.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Gated linear recurrence. Per batch entry and channel c, on token rows:
+ *   rho_t = sigmoid(r_t),  a_t = exp(A_c rho_t),  u_t = sigmoid(i_t) x_t
+ *   m_t = sqrt(1 - a_t^2)  (normalize != 0, else 1)
+ *   h_t = a_t h_{t-1} + m_t u_t,   y_t = h_t
+ *
+ *   x, r, i  [B,T,C] dtype: element (b,t,c) at x[b*x_batch_stride +
+ *            t*x_token_stride + c] (strides >= 0), each a channel range of a wider
+ *            projection or not; i NULL: no input gate (u_t = x_t)
+ *   A        [C] fp32, <= 0 (required; with normalize a positive one gives NaN)
+ *   h0       [B,C] fp32 (NULL: zeros)
+ *   y        [B,T,C] dtype (NULL: not written);  h_T [B,C] fp32 (NULL: not written)
+ *   states   [B,ceil(T/16),C] fp32: h before tokens 0, 16, 32, ..., for the backward
+ *            pass; those behind a sequence's end hold h_T (NULL: not written)
+ * The state is held in 32 bits; what carries it over 8 tokens and more is formed
+ * from sums of log a, so that decays close to one keep their memory. C and token
+ * strides up to 2^22 (more: OSDN_ERR_UNSUPPORTED). No output may overlap an input
+ * (h_T not h0 either). workspace: glr_forward_workspace_bytes(...) bytes, 256-byte
+ * aligned: the maps of the segments that long sequences of few channels are cut
+ * into.
+ */
+#define OSDN_GLR_INTERVAL 16
+size_t glr_forward_workspace_bytes(int B, int T, int C);
+int glr_forward(int B, int T, int C, int dtype, const void* x,
+                long long x_batch_stride, long long x_token_stride, const void* r,
+                long long r_batch_stride, long long r_token_stride, const void* i,
+                long long i_batch_stride, long long i_token_stride, const float* A,
+                const float* h0, const int* lengths, int normalize, void* y,
+                float* h_T, float* states, void* workspace, size_t workspace_bytes,
+                void* stream);
+
+/* T tokens (usually 1) of the same recurrence with the state read from h and
+ * written to h_out ([B,C] fp32, both required), which may be exactly h. */
+int glr_decode(int B, int T, int C, int dtype, const void* x,
+               long long x_batch_stride, long long x_token_stride, const void* r,
+               long long r_batch_stride, long long r_token_stride, const void* i,
+               long long i_batch_stride, long long i_token_stride, const float* A,
+               const float* h, int normalize, void* y, float* h_out, void* stream);
+
+/*
+ * Backward of glr_forward: the gradient of sum <dy, y> + <dh_T, h_T>.
+ *   states   what the forward left (NULL: formed here, from h0, with one more pass
+ *            over x, r and i)
+ *   dy       [B,T,C] dtype (required);  dh_T [B,C] fp32 (NULL: zero)
+ *   dx, dr, di  [B,T,C] dtype OUT, contiguous (di required with i)
+ *   dA       [C] fp32 OUT (required);  dh0 [B,C] fp32 OUT (NULL: not written)
+ * Where a_t is exactly one, no gradient passes through m_t (its slope is infinite
+ * there). workspace: glr_backward_workspace_bytes(...) bytes, 256-byte aligned:
+ * the segments' maps and parts of dA, and without `states` those.
+ */
+size_t glr_backward_workspace_bytes(int B, int T, int C, int have_states);
+int glr_backward(int B, int T, int C, int dtype, const void* x,
+                 long long x_batch_stride, long long x_token_stride, const void* r,
+                 long long r_batch_stride, long long r_token_stride, const void* i,
+                 long long i_batch_stride, long long i_token_stride, const float* A,
+                 const float* h0, const int* lengths, int normalize,
+                 const float* states, const void* dy, const float* dh_T, void* dx,
+                 void* dr, void* di, float* dA, float* dh0, void* workspace,
+                 size_t workspace_bytes, void* stream);
+
+/*
+ * Norm of each query's and key's row with the rotation of its position, from token
+ * rows to heads. Per head of D channels of a token at position p:
+ *   n = x * rsqrt(mean_D x^2 + eps)  (OSDN_NORM_RMS),
+ *       x * rsqrt(sum_D x^2 + eps)   (OSDN_NORM_L2),  x (OSDN_NORM_NONE)
+ *   v = n * weight
+ *   (y_a, y_b) = (v_a cos w - v_b sin w, v_b cos w + v_a sin w),  w = p inv_freq[j]
+ * for j < rot / 2 and the channels (a, b) = (j, j + rot/2), or (2j, 2j + 1) with
+ * `interleaved`; channels from rot on pass through (y = v).
+ *
+ *   q        [B,T,Hq*D], k [B,T,Hk*D] dtype rows with strides as above (Hq or Hk 0:
+ *            none)
+ *   q_weight, k_weight  [D] fp32 (NULL: ones)
+ *   inv_freq [rot/2] fp32 (required if rot > 0);  rot a multiple of 16, <= D
+ *   positions [B,T] int32 (NULL: 0 .. T - 1). Angles are formed in 64 bits.
+ *   q_out    [B,Hq,T,D], k_out [B,Hk,T,D] dtype
+ * D in {32, 64, 128}. Outputs, adjoints and gradients of rows start on 16 bytes.
+ */
+enum { OSDN_NORM_NONE = 0, OSDN_NORM_RMS = 1, OSDN_NORM_L2 = 2 };
+int qk_rotary_forward(int B, int T, int Hq, int Hk, int D, int rot, int dtype,
+                      const void* q, long long q_batch_stride,
+                      long long q_token_stride, const void* k,
+                      long long k_batch_stride, long long k_token_stride,
+                      const float* q_weight, const float* k_weight, int norm,
+                      float eps, const float* inv_freq, int interleaved,
+                      const int* positions, const int* lengths, void* q_out,
+                      void* k_out, void* stream);
+
+/*
+ * Its backward: dq_out, dk_out in dy_dtype (the dtype of q and k, or fp32: what the
+ * recurrences' backward returns). dq [B,T,Hq*D], dk [B,T,Hk*D] dtype OUT,
+ * contiguous; dq_weight, dk_weight [D] fp32 OUT (NULL: not written). workspace:
+ * qk_rotary_backward_workspace_bytes(...) bytes, partial sums of the weights'
+ * gradients.
+ */
+size_t qk_rotary_backward_workspace_bytes(int B, int T, int D);
+int qk_rotary_backward(int B, int T, int Hq, int Hk, int D, int rot, int dtype,
+                       int dy_dtype, const void* q, long long q_batch_stride,
+                       long long q_token_stride, const void* k,
+                       long long k_batch_stride, long long k_token_stride,
+                       const float* q_weight, const float* k_weight, int norm,
+                       float eps, const float* inv_freq, int interleaved,
+                       const int* positions, const int* lengths,
+                       const void* dq_out, const void* dk_out, void* dq, void* dk,
+                       float* dq_weight, float* dk_weight, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * Gated feed-forward product of R rows:
+ *   g = x w_gate^T,  u = x w_up^T,  h = act(g) * u
+ * with both products, the activation and their product in one kernel. act is SiLU, or
+ * GELU by the error function, or by tanh: g / 2 (1 + tanh(sqrt(2/pi) (g + 0.044715
+ * g^3))).
+ *   x        [R,C] dtype, rows x_row_stride apart;  w_gate, w_up [F,C] dtype
+ *   h        [R,F] dtype;  gate, up [R,F] dtype: g and u for the backward pass (both
+ *            or neither)
+ * h is formed from the 32-bit sums. C, F and the row stride up to 2^21 (more:
+ * OSDN_ERR_UNSUPPORTED). workspace: gated_ffn_forward_workspace_bytes(...) bytes,
+ * 256-byte aligned: the parts of sums that are split where the rows are few.
+ */
+enum { OSDN_ACT_SILU = 0, OSDN_ACT_GELU = 1, OSDN_ACT_GELU_TANH = 2 };
+size_t gated_ffn_forward_workspace_bytes(long long R, int C, int F, int dtype);
+int gated_ffn_forward(long long R, int C, int F, int dtype, const void* x,
+                      long long x_row_stride, const void* w_gate, const void* w_up,
+                      int activation, void* h, void* gate, void* up,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Its backward from the stored gate and up:
+ *   dg = dh * u * act'(g),  du = dh * act(g)
+ *   dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x
+ * dx [R,C], dw_gate, dw_up [F,C] dtype OUT (contiguous). dg and du enter the products
+ * in dtype (rounded once in bf16), sums are held in 32 bits. workspace:
+ * gated_ffn_backward_workspace_bytes(...) bytes, 256-byte aligned: dg and du, and
+ * parts of sums.
+ */
+size_t gated_ffn_backward_workspace_bytes(long long R, int C, int F, int dtype);
+int gated_ffn_backward(long long R, int C, int F, int dtype, const void* x,
+                       long long x_row_stride, const void* w_gate,
+                       const void* w_up, const void* gate, const void* up,
+                       int activation, const void* dh, void* dx, void* dw_gate,
+                       void* dw_up, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/*
  * Per-kernel timing for measurement harnesses. While enabled, every entry
  * point records a HIP event on its stream before and after each kernel it
  * launches (two event records per kernel; events are created on first use
@@ -662,7 +815,9 @@ void osdn_kernel_timing(int enable);
  * backward), short_conv, short_conv_bwd, ssm_decay, ssm_state, ssm_chain, ssm_scan,
  * ssm_decode, ssm_bwd_state, ssm_bwd_chain, ssm_bwd_walk, ssm_bwd,
  * ssm_bwd_parts, gated_norm, gated_norm_bwd, residual_norm, residual_norm_bwd,
- * column_sum (the operators around the recurrences).
+ * column_sum (the operators around the recurrences), glr_part, glr, glr_decode,
+ * glr_bwd_part, glr_bwd, qk_rotary, qk_rotary_bwd, ffn, ffn_join, ffn_rows, ffn_grad,
+ * ffn_dx, ffn_dw, ffn_sum (the operators that complete a block).
  */
 int osdn_kernel_times(int max, const char** names, int* counts, float* mean_ms);
 
