@@ -615,7 +615,7 @@ int run_backward(const GlrArgs& a0, hipStream_t s) {
   if (!grid_ok((long long)ncb * a.B * S, kThreads) || !column_sum_ok(a.C)) return -1;
   const size_t maps = map_bytes(a.B, a.T, a.C);
   float* parts = (float*)((char*)a.ws + maps);
-  if (!a.states && a.T > 0) {
+  if (!a.states && a.T > 0 && a.B > 0) {
     // the states that a forward would have left, behind the partial sums
     a.states = parts + ((size_t)a.B * S * a.C + 63) / 64 * 64;
     GlrArgs f = a;
