@@ -49,10 +49,14 @@ struct InputSrc {
     second = t < full ? t >= half : t > full;
     return (t < full ? t - (second ? half : 0) : half) * kTileK<T>;
   }
-  __device__ __forceinline__ void direct(int t, char* a, char* b) const {
+  __device__ __forceinline__ void direct_a(int t, char* a) const {
     bool second;
     const int k = place(t, second);
     SA::direct(a, (second ? du : dg) + k, oa);
+  }
+  __device__ __forceinline__ void direct_b(int t, char* b) const {
+    bool second;
+    const int k = place(t, second);
     StageB::direct(b, (second ? wu : wg) + (long long)k * C, ob);
   }
   __device__ __forceinline__ void fetch(int t) {
@@ -80,10 +84,11 @@ struct WeightSrc {
   int F, rows, cols, full;
   unsigned oa[SA::PER], ob[StageB::PER];
   uint4 va[SA::PER], vb[StageB::PER];
-  __device__ __forceinline__ void direct(int t, char* a, char* b) const {
-    const long long k = (long long)t * kTileK<T>;
-    SA::direct(a, d + k * F, oa);
-    StageB::direct(b, x + k * xs, ob);
+  __device__ __forceinline__ void direct_a(int t, char* a) const {
+    SA::direct(a, d + (long long)t * kTileK<T> * F, oa);
+  }
+  __device__ __forceinline__ void direct_b(int t, char* b) const {
+    StageB::direct(b, x + (long long)t * kTileK<T> * xs, ob);
   }
   __device__ __forceinline__ void fetch(int t) {
     const long long k = (long long)t * kTileK<T>;

@@ -30,7 +30,21 @@ constexpr int kUnit = 16 / (int)sizeof(T);       // elements of 16 bytes
 template <typename T>
 constexpr int kTileK = kRowBytes / (int)sizeof(T);
 
-typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(3))) char lds_char;
+
+// 16 bytes a lane from the buffer r at the lane's byte offset to LDS, 1 KB from `lds`
+// on. The load writes no register; the compiler does not know of it (of the builtin's
+// it would wait for all before every transpose load), so the waits are written out,
+// wait_loads() below. Memory past the LDS address register takes one cycle to use it.
+__device__ __forceinline__ void load_lds(u32x4 r, unsigned offset, unsigned lds) {
+  asm volatile(
+      "s_mov_b32 m0, %2\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %0, %1, 0 offen lds"
+      :
+      : "v"(offset), "s"(r), "s"(lds)
+      : "m0", "memory");
+}
 
 // One 16-byte unit of each operand a lane: 32 of k for bf16, 16 for fp32.
 __device__ __forceinline__ void mma(f32x4& acc, const uint4& a, const uint4& b, __bf16) {
@@ -80,11 +94,10 @@ struct Stage {
   }
   // A whole tile of k, global memory to LDS. p: its first element.
   __device__ __forceinline__ static void direct(char* lds, const T* p, const unsigned (&o)[PER]) {
-    const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(p), 0, -1, 0x00027000);
+    const u32x4 r = {(unsigned)(size_t)p, (unsigned)((size_t)p >> 32) & 0xffffu, ~0u, 0x00027000u};
 #pragma unroll
     for (int j = 0; j < PER; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          r, (lds_void*)(lds + (wave_id() * PER + j) * 1024), 16, (int)o[j], 0, 0, 0);
+      load_lds(r, o[j], (unsigned)(size_t)(lds_char*)lds + (wave_id() * PER + j) * 1024);
   }
   // Any tile through registers: nk of k exist, `rows` rows.
   __device__ __forceinline__ static void fetch(uint4 (&v)[PER], const T* p, long long ld, int rows,
@@ -165,51 +178,119 @@ __device__ __forceinline__ TileAt tile_at(int tm, int tn, int splits) {
   return TileAt{m0 + w % h, w / h, s};
 }
 
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
 // The products of a wave over the tiles of k from t0 to t1, in the order of `src`:
-// those of a whole tile's length, src.full of them, before the ends. src.direct(t, a,
-// b) sends a whole tile to LDS, src.fetch(t) and src.put(a, b) take any through
-// registers; src.fragb(b, j, step) is the wave's j-th 16 columns.
+// those of a whole tile's length, src.full of them, before the ends. src.direct_a(t, a)
+// and src.direct_b(t, b) send a whole tile's operand to LDS, src.fetch(t) and
+// src.put(a, b) take any through registers; src.fragb(b, j, step) is the wave's j-th 16
+// columns.
+//
+// Whole tiles pass through five buffers in turn, A and B of one tile after the other:
+// while tile t is used, t + 1 and A of t + 2 are on their way, and B of t + 2 and A of
+// t + 3 follow as soon as every wave has read tile t, so that the memory pipes never
+// run empty. A wave works off a tile in four parts (two steps of k, two halves of its
+// rows) and fetches each part's operands while the one before is multiplied; the
+// barrier stands before a tile's last part, whose operands are in registers.
 template <typename T, class S, bool AK, bool DIRECT, class Src>
 __device__ __forceinline__ void products(f32x4 (&acc)[S::TM][S::TN], Src& src, int t0, int t1) {
-  __shared__ __attribute__((aligned(1024))) char a0[S::BM * kRowBytes], b0[S::BN * kRowBytes];
-  __shared__ __attribute__((aligned(1024))) char a1[S::BM * kRowBytes], b1[S::BN * kRowBytes];
+  constexpr int BUF = (S::BM > S::BN ? S::BM : S::BN) * kRowBytes;
+  __shared__ __attribute__((aligned(1024))) char u0[BUF], u1[BUF], u2[BUF], u3[BUF], u4[BUF];
   typedef Stage<T, S::BM, AK, S::NT> SA;
+  constexpr int NA = SA::PER, NB = S::BN * kRowBytes / 16 / S::NT, HM = S::TM / 2;
   const int wm = wave_id() / S::WN * (S::BM / S::WM);
 #pragma unroll
   for (int i = 0; i < S::TM; ++i)
 #pragma unroll
     for (int j = 0; j < S::TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto run = [&](const char* la, const char* lb) {
+
+  auto read_a = [&](uint4 (&f)[HM], const char* la, int step, int half) {
 #pragma unroll
-    for (int step = 0; step < 2; ++step) {
-      uint4 fa[S::TM], fb[S::TN];
-#pragma unroll
-      for (int j = 0; j < S::TN; ++j) fb[j] = src.fragb(lb, j, step);
-#pragma unroll
-      for (int i = 0; i < S::TM; ++i) fa[i] = SA::frag(la, wm + 16 * i, step);
-      // (columns first: a lane then holds four consecutive n of one m)
-#pragma unroll
-      for (int i = 0; i < S::TM; ++i)
-#pragma unroll
-        for (int j = 0; j < S::TN; ++j) mma(acc[i][j], fb[j], fa[i], T());
-    }
+    for (int i = 0; i < HM; ++i) f[i] = SA::frag(la, wm + 16 * (half * HM + i), step);
   };
+  auto read_b = [&](uint4 (&f)[S::TN], const char* lb, int step) {
+#pragma unroll
+    for (int j = 0; j < S::TN; ++j) f[j] = src.fragb(lb, j, step);
+  };
+  // (columns first: a lane then holds four consecutive n of one m)
+  auto multiply = [&](const uint4 (&fa)[HM], const uint4 (&fb)[S::TN], int half) {
+#pragma unroll
+    for (int i = 0; i < HM; ++i)
+#pragma unroll
+      for (int j = 0; j < S::TN; ++j) mma(acc[half * HM + i][j], fb[j], fa[i], T());
+  };
+
   if constexpr (DIRECT) {
-    // what is on its way to LDS has arrived, and every wave has read the other stage
-    auto turn = [&]() {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();
-    };
     const int tf = min(t1, src.full);
-    if (t0 < tf) src.direct(t0, a0, b0);
-    for (int t = t0; t < tf; t += 2) {
-      turn();
-      if (t + 1 < tf) src.direct(t + 1, a1, b1);
-      run(a0, b0);
-      if (t + 1 >= tf) break;
-      turn();
-      if (t + 2 < tf) src.direct(t + 2, a0, b0);
-      run(a1, b1);
+    uint4 fa[2][HM], fb[2][S::TN];
+    auto fence = [&]() {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    };
+    // tile t in buffers a, b; the next one's are an, bn
+    auto tile = [&](int t, char* a, char* b, const char* an, const char* bn) {
+      read_a(fa[1], a, 0, 1);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(fa[0], fb[0], 0);
+      __builtin_amdgcn_sched_barrier(0);
+      read_b(fb[1], b, 1);
+      read_a(fa[0], a, 1, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(fa[1], fb[0], 1);
+      __builtin_amdgcn_sched_barrier(0);
+      read_a(fa[1], a, 1, 1);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(fa[0], fb[1], 0);
+      __builtin_amdgcn_sched_barrier(0);
+      if (t + 1 < tf) {
+        // the next tile has arrived, A of the one behind it may be on its way
+        if (t + 2 < tf) {
+          wait_loads<NA>();
+        } else {
+          wait_loads<0>();
+        }
+        fence();
+        if (t + 2 < tf) src.direct_b(t + 2, a);
+        if (t + 3 < tf) src.direct_a(t + 3, b);
+        read_b(fb[0], bn, 0);
+        read_a(fa[0], an, 0, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(fa[1], fb[1], 1);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    if (t0 < tf) {
+      src.direct_a(t0, u0);
+      src.direct_b(t0, u1);
+      if (t0 + 1 < tf) {
+        src.direct_a(t0 + 1, u2);
+        src.direct_b(t0 + 1, u3);
+      }
+      if (t0 + 2 < tf) {
+        src.direct_a(t0 + 2, u4);
+        wait_loads<2 * NA + NB>();
+      } else {
+        wait_loads<0>();
+      }
+      fence();
+      read_b(fb[0], u1, 0);
+      read_a(fa[0], u0, 0, 0);
+      for (int t = t0;;) {
+        tile(t, u0, u1, u2, u3);
+        if (++t >= tf) break;
+        tile(t, u2, u3, u4, u0);
+        if (++t >= tf) break;
+        tile(t, u4, u0, u1, u2);
+        if (++t >= tf) break;
+        tile(t, u1, u2, u3, u4);
+        if (++t >= tf) break;
+        tile(t, u3, u4, u0, u1);
+        if (++t >= tf) break;
+      }
     }
     t0 = max(t0, tf);
   }
@@ -217,10 +298,19 @@ __device__ __forceinline__ void products(f32x4 (&acc)[S::TM][S::TN], Src& src, i
   if (t0 < t1) src.fetch(t0);
   for (int t = t0; t < t1; ++t) {
     __syncthreads();
-    src.put(a0, b0);
+    src.put(u0, u1);
     __syncthreads();
     if (t + 1 < t1) src.fetch(t + 1);
-    run(a0, b0);
+#pragma unroll
+    for (int step = 0; step < 2; ++step) {
+      uint4 fa[HM], fb[S::TN];
+      read_b(fb, u1, step);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        read_a(fa, u0, step, half);
+        multiply(fa, fb, half);
+      }
+    }
   }
 }
 

@@ -26,9 +26,11 @@ struct ForwardSrc {
   unsigned oa[SA::PER], ob[StageB::PER];
   uint4 va[SA::PER], vg[StageB::PER], vu[StageB::PER];
 
-  __device__ __forceinline__ void direct(int t, char* a, char* b) const {
+  __device__ __forceinline__ void direct_a(int t, char* a) const {
+    SA::direct(a, x + t * kTileK<T>, oa);
+  }
+  __device__ __forceinline__ void direct_b(int t, char* b) const {
     const int k = t * kTileK<T>;
-    SA::direct(a, x + k, oa);
     StageB::direct(b, wg + k, ob);
     StageB::direct(b + HALF, wu + k, ob);
   }
