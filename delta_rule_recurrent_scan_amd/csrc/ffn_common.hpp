@@ -16,6 +16,7 @@
 #pragma once
 
 #include "device_common.hpp"
+#include "launch.hpp"
 #include "layer.hpp"
 #include "pack_common.hpp"
 #include "row_common.hpp"
@@ -57,11 +58,23 @@ __device__ __forceinline__ void mma(f32x4& acc, const uint4& a, const uint4& b, 
   for (int i = 0; i < 4; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i], y[i], acc, 0, 0, 0);
 }
 
-// Swizzle of an MN-major row.
-__device__ __forceinline__ int mn_swizzle(int k) { return ((k & 3) | ((k >> 3) & 1) << 2) << 1; }
+// The thread's number, worked out anew: what depends on it is not kept in registers
+// over the products of an item, whose accumulators and operands take them all.
+__device__ __forceinline__ int fresh_thread() {
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
+__device__ __forceinline__ int wave_of(int thread) {
+  return __builtin_amdgcn_readfirstlane(thread >> 6);
+}
 
-// ROWS rows (m or n) of an operand, one tile of k, in LDS. NT threads stage it.
-template <typename T, int ROWS, bool KMAJ, int NT>
+// Swizzle of rows that are read in runs of four, eight apart.
+__device__ __forceinline__ int runs_swizzle(int r) { return (r & 3) | ((r >> 3) & 1) << 2; }
+
+// ROWS rows (m or n) of an operand, one tile of k, in LDS. NT threads stage it. RUNS
+// (K-major): fragments take rows in runs of four, eight apart.
+template <typename T, int ROWS, bool KMAJ, int NT, bool RUNS = false>
 struct Stage {
   static constexpr int BYTES = ROWS * kRowBytes;
   static constexpr int UNITS = BYTES / 16, PER = UNITS / NT;   // units a thread
@@ -69,21 +82,22 @@ struct Stage {
   static_assert(UNITS % NT == 0 && NT % 64 == 0, "whole waves stage a tile");
 
   __device__ __forceinline__ static int swizzle(int row) {
-    return KMAJ ? row & 7 : mn_swizzle(row) & (UPR - 1);
+    return KMAJ ? (RUNS ? runs_swizzle(row) : row & 7) : runs_swizzle(row) * 2 & (UPR - 1);
   }
-  // LDS row and logical unit of the thread's j-th unit.
-  __device__ __forceinline__ static void where(int j, int& row, int& u) {
-    const int at = (wave_id() * PER + j) * 64 + (threadIdx.x & 63);
+  // LDS row and logical unit of a thread's j-th unit.
+  __device__ __forceinline__ static void where(int thread, int j, int& row, int& u) {
+    const int at = (wave_of(thread) * PER + j) * 64 + (thread & 63);
     row = at / UPR;
     u = (at % UPR) ^ swizzle(row);
   }
   // Byte offsets of the thread's units from the tile's first element; `rows` of
   // the operand exist from there on (a multiple of a unit when MN-major).
   __device__ __forceinline__ static void offsets(unsigned (&o)[PER], long long ld, int rows) {
+    const int thread = fresh_thread();
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       int row, u;
-      where(j, row, u);
+      where(thread, j, row, u);
       if constexpr (KMAJ) {
         o[j] = (unsigned)min(row, rows - 1) * (unsigned)ld * (unsigned)sizeof(T) + u * 16;
       } else {
@@ -102,10 +116,11 @@ struct Stage {
   // Any tile through registers: nk of k exist, `rows` rows.
   __device__ __forceinline__ static void fetch(uint4 (&v)[PER], const T* p, long long ld, int rows,
                                                int nk) {
+    const int thread = fresh_thread();
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       int row, u;
-      where(j, row, u);
+      where(thread, j, row, u);
       const int m = KMAJ ? row : u * kUnit<T>, k = KMAJ ? u * kUnit<T> : row;
       const int have = KMAJ ? (m < rows ? nk - k : 0) : (k < nk ? rows - m : 0);
       v[j] = uint4{0u, 0u, 0u, 0u};
@@ -130,7 +145,9 @@ struct Stage {
   __device__ __forceinline__ static uint4 frag(const char* lds, int row0, int step) {
     const int lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
     if constexpr (KMAJ) {
-      return *(const uint4*)(lds + (row0 + l) * kRowBytes + (((4 * step + g) ^ (l & 7)) << 4));
+      // RUNS: row0 is 8 h of a block of 32 rows' first, or 8 h + 4
+      const int r = row0 + (RUNS ? 8 * (l >> 2) + (l & 3) : l);
+      return *(const uint4*)(lds + r * kRowBytes + (((4 * step + g) ^ swizzle(r)) << 4));
     } else if constexpr (sizeof(T) == 2) {
       typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
       const int k = 32 * step + 8 * g + (l >> 2);
@@ -162,20 +179,53 @@ struct Shape {
 typedef Shape<256, 256, 2, 4> Large;
 typedef Shape<128, 128, 2, 2> Middle;
 typedef Shape<64, 64, 2, 2> Small;
+typedef Shape<64, 64, 2, 1> SmallPairs;    // column tiles in pairs, for two products
 
-// Where a workgroup's tile lies: runs of eight tiles of m for each of n, and
-// consecutive ones on the same XCD (workgroups go to the eight in turn), so that
-// the workgroups of an XCD share their operands' rows in its L2.
-struct TileAt {
-  int m, n, split;
+// How a product is cut: tm x tn tiles over nt tiles of k. The first `whole` tiles
+// (full rounds of the workgroups that are on the card at once) are formed whole, the
+// rest in `splits` parts of `per` tiles of k each, which a second launch adds.
+struct Plan {
+  int shape;                       // 0 large, 1 middle, 2 small
+  int tm, tn, nt, whole, splits, per;
+  __host__ __device__ int rest() const { return tm * tn - whole; }
+  __host__ __device__ int items() const { return whole + rest() * splits; }
 };
-__device__ __forceinline__ TileAt tile_at(int tm, int tn, int splits) {
-  const int total = tm * tn * splits, id = blockIdx.x;
-  const int x = id % 8, i = id / 8;
-  const int at = x * (total / 8) + min(x, total % 8) + i;
-  const int per = tm * tn, s = at / per, r = at % per;
-  const int width = 8 * tn, g = r / width, m0 = g * 8, h = min(tm - m0, 8), w = r % width;
-  return TileAt{m0 + w % h, w / h, s};
+
+struct Item {
+  int m, n, split, t0, t1;
+  int tile;                        // of the rest
+};
+// Consecutive numbers on one XCD (workgroups go to the eight in turn): number id of
+// `total`.
+__device__ __forceinline__ int on_xcd(int id, int total) {
+  const int x = id % 8;
+  return x * (total / 8) + min(x, total % 8) + id / 8;
+}
+// Tiles run over eight of m for each of n, so that the workgroups of an XCD share their
+// operands' rows in its L2.
+__device__ __forceinline__ void tile_place(const Plan& p, int r, int& m, int& n) {
+  const int width = 8 * p.tn, m0 = r / width * 8, h = min(p.tm - m0, 8), w = r % width;
+  m = m0 + w % h;
+  n = w / h;
+}
+__device__ __forceinline__ Item item_at(const Plan& p, int id) {
+  Item it;
+  int r;
+  if (id < p.whole) {
+    r = on_xcd(id, p.whole);
+    it.split = it.tile = 0;
+    it.t0 = 0;
+    it.t1 = p.nt;
+  } else {
+    const int rest = p.rest(), j = on_xcd(id - p.whole, rest * p.splits);
+    it.split = j / rest;
+    it.tile = j % rest;
+    r = p.whole + it.tile;
+    it.t0 = it.split * p.per;
+    it.t1 = min(p.nt, it.t0 + p.per);
+  }
+  tile_place(p, r, it.m, it.n);
+  return it;
 }
 
 template <int N>
@@ -183,37 +233,35 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// The products of a wave over the tiles of k from t0 to t1, in the order of `src`:
-// those of a whole tile's length, src.full of them, before the ends. src.direct_a(t, a)
-// and src.direct_b(t, b) send a whole tile's operand to LDS, src.fetch(t) and
-// src.put(a, b) take any through registers; src.fragb(b, j, step) is the wave's j-th 16
-// columns.
+// One item of a product. Op is the product:
+//   place(a, item)       the operands' tile
+//   direct_a(t, lds), direct_b  tile t of k of an operand to LDS, whole tiles (t < full)
+//   fetch(t), put(a, b)  any tile through registers
+//   fragb(lds, j, step)  the wave's j-th 16 columns
+//   store_row(a, i, row) the wave's i-th 16 rows of results
 //
-// Whole tiles pass through five buffers in turn, A and B of one tile after the other:
-// while tile t is used, t + 1 and A of t + 2 are on their way, and B of t + 2 and A of
-// t + 3 follow as soon as every wave has read tile t, so that the memory pipes never
-// run empty. A wave works off a tile in four parts (two steps of k, two halves of its
-// rows) and fetches each part's operands while the one before is multiplied; the
+// Whole tiles of k pass through five buffers in turn, A and B of one tile after the
+// other: while tile t is used, t + 1 and A of t + 2 are on their way, and B of t + 2 and
+// A of t + 3 follow as soon as every wave has read tile t, so that the memory pipes
+// never run empty. A wave works off a tile in four parts (two steps of k, two halves of
+// its rows) and fetches each part's operands while the one before is multiplied; the
 // barrier stands before a tile's last part, whose operands are in registers.
-template <typename T, class S, bool AK, bool DIRECT, class Src>
-__device__ __forceinline__ void products(f32x4 (&acc)[S::TM][S::TN], Src& src, int t0, int t1) {
+template <typename T, class S, class Op, bool DIRECT>
+__device__ __forceinline__ void products(const FfnArgs& a, const Plan& p) {
   constexpr int BUF = (S::BM > S::BN ? S::BM : S::BN) * kRowBytes;
   __shared__ __attribute__((aligned(1024))) char u0[BUF], u1[BUF], u2[BUF], u3[BUF], u4[BUF];
-  typedef Stage<T, S::BM, AK, S::NT> SA;
+  typedef typename Op::StageA SA;
   constexpr int NA = SA::PER, NB = S::BN * kRowBytes / 16 / S::NT, HM = S::TM / 2;
   const int wm = wave_id() / S::WN * (S::BM / S::WM);
+
+  f32x4 acc[S::TM][S::TN];
 #pragma unroll
   for (int i = 0; i < S::TM; ++i)
 #pragma unroll
     for (int j = 0; j < S::TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
   auto read_a = [&](uint4 (&f)[HM], const char* la, int step, int half) {
 #pragma unroll
     for (int i = 0; i < HM; ++i) f[i] = SA::frag(la, wm + 16 * (half * HM + i), step);
-  };
-  auto read_b = [&](uint4 (&f)[S::TN], const char* lb, int step) {
-#pragma unroll
-    for (int j = 0; j < S::TN; ++j) f[j] = src.fragb(lb, j, step);
   };
   // (columns first: a lane then holds four consecutive n of one m)
   auto multiply = [&](const uint4 (&fa)[HM], const uint4 (&fb)[S::TN], int half) {
@@ -223,26 +271,34 @@ __device__ __forceinline__ void products(f32x4 (&acc)[S::TM][S::TN], Src& src, i
       for (int j = 0; j < S::TN; ++j) mma(acc[half * HM + i][j], fb[j], fa[i], T());
   };
 
+  const Item it = item_at(p, blockIdx.x);
+  Op op;
+  op.place(a, it);
+  int t = it.t0;
   if constexpr (DIRECT) {
-    const int tf = min(t1, src.full);
+    const int tf = min(it.t1, op.full);
     uint4 fa[2][HM], fb[2][S::TN];
+    auto read_b = [&](uint4 (&f)[S::TN], const char* lb, int step) {
+#pragma unroll
+      for (int j = 0; j < S::TN; ++j) f[j] = op.fragb(lb, j, step);
+    };
     auto fence = [&]() {
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
     };
-    // tile t in buffers a, b; the next one's are an, bn
-    auto tile = [&](int t, char* a, char* b, const char* an, const char* bn) {
-      read_a(fa[1], a, 0, 1);
+    // tile t in buffers la, lb; the next one's are an, bn
+    auto tile = [&](char* la, char* lb, const char* an, const char* bn) {
+      read_a(fa[1], la, 0, 1);
       __builtin_amdgcn_sched_barrier(0);
       multiply(fa[0], fb[0], 0);
       __builtin_amdgcn_sched_barrier(0);
-      read_b(fb[1], b, 1);
-      read_a(fa[0], a, 1, 0);
+      read_b(fb[1], lb, 1);
+      read_a(fa[0], la, 1, 0);
       __builtin_amdgcn_sched_barrier(0);
       multiply(fa[1], fb[0], 1);
       __builtin_amdgcn_sched_barrier(0);
-      read_a(fa[1], a, 1, 1);
+      read_a(fa[1], la, 1, 1);
       __builtin_amdgcn_sched_barrier(0);
       multiply(fa[0], fb[1], 0);
       __builtin_amdgcn_sched_barrier(0);
@@ -254,8 +310,8 @@ __device__ __forceinline__ void products(f32x4 (&acc)[S::TM][S::TN], Src& src, i
           wait_loads<0>();
         }
         fence();
-        if (t + 2 < tf) src.direct_b(t + 2, a);
-        if (t + 3 < tf) src.direct_a(t + 3, b);
+        if (t + 2 < tf) op.direct_b(t + 2, la);
+        if (t + 3 < tf) op.direct_a(t + 3, lb);
         read_b(fb[0], bn, 0);
         read_a(fa[0], an, 0, 0);
       }
@@ -263,15 +319,15 @@ __device__ __forceinline__ void products(f32x4 (&acc)[S::TM][S::TN], Src& src, i
       multiply(fa[1], fb[1], 1);
       __builtin_amdgcn_sched_barrier(0);
     };
-    if (t0 < tf) {
-      src.direct_a(t0, u0);
-      src.direct_b(t0, u1);
-      if (t0 + 1 < tf) {
-        src.direct_a(t0 + 1, u2);
-        src.direct_b(t0 + 1, u3);
+    if (t < tf) {
+      op.direct_a(t, u0);
+      op.direct_b(t, u1);
+      if (t + 1 < tf) {
+        op.direct_a(t + 1, u2);
+        op.direct_b(t + 1, u3);
       }
-      if (t0 + 2 < tf) {
-        src.direct_a(t0 + 2, u4);
+      if (t + 2 < tf) {
+        op.direct_a(t + 2, u4);
         wait_loads<2 * NA + NB>();
       } else {
         wait_loads<0>();
@@ -279,32 +335,32 @@ __device__ __forceinline__ void products(f32x4 (&acc)[S::TM][S::TN], Src& src, i
       fence();
       read_b(fb[0], u1, 0);
       read_a(fa[0], u0, 0, 0);
-      for (int t = t0;;) {
-        tile(t, u0, u1, u2, u3);
+      for (;;) {
+        tile(u0, u1, u2, u3);
         if (++t >= tf) break;
-        tile(t, u2, u3, u4, u0);
+        tile(u2, u3, u4, u0);
         if (++t >= tf) break;
-        tile(t, u4, u0, u1, u2);
+        tile(u4, u0, u1, u2);
         if (++t >= tf) break;
-        tile(t, u1, u2, u3, u4);
+        tile(u1, u2, u3, u4);
         if (++t >= tf) break;
-        tile(t, u3, u4, u0, u1);
+        tile(u3, u4, u0, u1);
         if (++t >= tf) break;
       }
     }
-    t0 = max(t0, tf);
   }
   // through registers, a tile ahead of the one that is being used
-  if (t0 < t1) src.fetch(t0);
-  for (int t = t0; t < t1; ++t) {
+  if (t < it.t1) op.fetch(t);
+  for (; t < it.t1; ++t) {
     __syncthreads();
-    src.put(u0, u1);
+    op.put(u0, u1);
     __syncthreads();
-    if (t + 1 < t1) src.fetch(t + 1);
+    if (t + 1 < it.t1) op.fetch(t + 1);
 #pragma unroll
     for (int step = 0; step < 2; ++step) {
       uint4 fa[HM], fb[S::TN];
-      read_b(fb, u1, step);
+#pragma unroll
+      for (int j = 0; j < S::TN; ++j) fb[j] = op.fragb(u1, j, step);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         read_a(fa, u0, step, half);
@@ -312,6 +368,68 @@ __device__ __forceinline__ void products(f32x4 (&acc)[S::TM][S::TN], Src& src, i
       }
     }
   }
+
+  if (p.splits > 1 && (int)blockIdx.x >= p.whole) {
+    f32x4* part = (f32x4*)a.parts +
+                  (size_t)(it.tile * p.splits + it.split) * (S::BM * S::BN / 4) + fresh_thread();
+#pragma unroll
+    for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+      for (int j = 0; j < S::TN; ++j) part[(i * S::TN + j) * S::NT] = acc[i][j];
+  } else {
+#pragma unroll
+    for (int i = 0; i < S::TM; ++i) op.store_row(a, i, acc[i]);
+  }
+}
+
+// The parts of one tile's i-th rows added in order, and stored.
+template <class S, class Op>
+__device__ __forceinline__ void join_parts(const FfnArgs& a, const Plan& p) {
+  const int tile = blockIdx.x / S::TM, i = blockIdx.x % S::TM;
+  Item it;
+  it.t0 = it.t1 = it.split = 0;
+  it.tile = tile;
+  tile_place(p, p.whole + tile, it.m, it.n);
+  Op op;
+  op.place(a, it);
+  const f32x4* part = (const f32x4*)a.parts + (size_t)tile * p.splits * (S::BM * S::BN / 4) +
+                      i * S::TN * S::NT + threadIdx.x;
+  f32x4 row[S::TN];
+#pragma unroll
+  for (int j = 0; j < S::TN; ++j) row[j] = part[j * S::NT];
+  for (int s = 1; s < p.splits; ++s) {
+    part += S::BM * S::BN / 4;
+#pragma unroll
+    for (int j = 0; j < S::TN; ++j) row[j] += part[j * S::NT];
+  }
+  op.store_row(a, i, row);
+}
+
+template <typename T, class S, class Op, bool DIRECT>
+__global__ __launch_bounds__(S::NT) void ffn_kernel(FfnArgs a, Plan p) {
+  products<T, S, Op, DIRECT>(a, p);
+}
+template <class S, class Op>
+__global__ __launch_bounds__(S::NT) void ffn_join_kernel(FfnArgs a, Plan p) {
+  join_parts<S, Op>(a, p);
+}
+
+template <typename T, class S, class Op>
+int launch_products(const FfnArgs& a, const Plan& p, bool direct, const char* name,
+                    const char* join_name, hipStream_t s) {
+  int tk = ktimer_before(s, name);
+  if (direct) {
+    hipLaunchKernelGGL((ffn_kernel<T, S, Op, true>), dim3(p.items()), dim3(S::NT), 0, s, a, p);
+  } else {
+    hipLaunchKernelGGL((ffn_kernel<T, S, Op, false>), dim3(p.items()), dim3(S::NT), 0, s, a, p);
+  }
+  ktimer_after(s, tk);
+  const int rc = (int)hipGetLastError();
+  if (rc || p.splits == 1) return rc;
+  tk = ktimer_before(s, join_name);
+  hipLaunchKernelGGL((ffn_join_kernel<S, Op>), dim3(p.rest() * S::TM), dim3(S::NT), 0, s, a, p);
+  ktimer_after(s, tk);
+  return (int)hipGetLastError();
 }
 
 // Four consecutive elements of a row, n of them inside; vec: rows start on 16 bytes
@@ -328,6 +446,18 @@ __device__ __forceinline__ void store4(T* p, const f32x4& v, int n, bool vec) {
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = from_f32<T>(v[i]);
+  }
+}
+
+// Eight of them; vec: rows hold whole eights.
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8], int n, bool vec) {
+  if (vec) {
+    if (n > 0) store_v<true, 8>(p, 8, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
       if (i < n) p[i] = from_f32<T>(v[i]);
   }
 }
@@ -356,15 +486,9 @@ __device__ __forceinline__ void activated(float g, int act, float& f, float& slo
   }
 }
 
-// How a product of M x N (in tiles of k: nt) is cut: the shape (0 large, 1 middle, 2
-// small) and the parts that its k is split into.
-struct Cut {
-  int shape, splits;
-};
-Cut cut_of(long long M, long long N, int nt);
-
-// out[i] = the sum over the splits of part[s][i] of n elements, in order.
-int launch_ffn_sum(const float* part, int splits, long long n, void* out, int bf16, hipStream_t s);
+// The plan of `sets` products of M x N over K, and the bytes of its parts.
+bool make_plan(Plan& p, int sets, long long M, long long N, long long K, int bf16, bool direct);
+size_t parts_bytes(const Plan& p);
 
 }  // namespace ffn
 }  // namespace osdn

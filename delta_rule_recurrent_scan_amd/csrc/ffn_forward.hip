@@ -8,26 +8,43 @@
 // workgroup, its eight waves taking tiles of k in turn straight from memory into
 // registers, their sums joined in LDS.
 #include "ffn_common.hpp"
-#include "launch.hpp"
 
 namespace osdn {
 namespace ffn {
 namespace {
 
-// Rows of x by rows of both weights, all K-major.
+// Rows of x by rows of both weights, all K-major. The wave's first half of column tiles
+// is of the gate, the second of the other; two column tiles of 16 take their columns in
+// turns of four, so that a lane's results are eight consecutive ones.
 template <typename T, class S>
-struct ForwardSrc {
-  typedef Stage<T, S::BM, true, S::NT> SA;
-  typedef Stage<T, S::BN / 2, true, S::NT> StageB;
-  static constexpr int HALF = S::BN / 2 * kRowBytes;
+struct Forward {
+  typedef Stage<T, S::BM, true, S::NT> StageA;
+  typedef Stage<T, S::BN / 2, true, S::NT, true> StageB;
+  static constexpr int BF = S::BN / 2, TH = S::TN / 2, HALF = BF * kRowBytes;
+  static_assert(TH % 2 == 0, "column tiles in pairs");
   const T *x, *wg, *wu;
+  long long m0;
+  int f0, rows, cols, full, C;
   long long xs;
-  int C, rows, cols, full;    // rows of x and of each weight from the tile on
-  unsigned oa[SA::PER], ob[StageB::PER];
-  uint4 va[SA::PER], vg[StageB::PER], vu[StageB::PER];
+  unsigned oa[StageA::PER], ob[StageB::PER];
+  uint4 va[StageA::PER], vg[StageB::PER], vu[StageB::PER];
 
+  __device__ __forceinline__ void place(const FfnArgs& a, const Item& it) {
+    m0 = (long long)it.m * S::BM;
+    f0 = it.n * BF;
+    xs = a.xs;
+    C = a.C;
+    x = (const T*)a.x + m0 * a.xs;
+    wg = (const T*)a.wg + (long long)f0 * a.C;
+    wu = (const T*)a.wu + (long long)f0 * a.C;
+    rows = (int)min((long long)S::BM, a.R - m0);
+    cols = min(BF, a.F - f0);
+    full = a.C / kTileK<T>;
+    StageA::offsets(oa, a.xs, rows);
+    StageB::offsets(ob, a.C, cols);
+  }
   __device__ __forceinline__ void direct_a(int t, char* a) const {
-    SA::direct(a, x + t * kTileK<T>, oa);
+    StageA::direct(a, x + t * kTileK<T>, oa);
   }
   __device__ __forceinline__ void direct_b(int t, char* b) const {
     const int k = t * kTileK<T>;
@@ -36,92 +53,51 @@ struct ForwardSrc {
   }
   __device__ __forceinline__ void fetch(int t) {
     const int k = t * kTileK<T>;
-    SA::fetch(va, x + k, xs, rows, C - k);
+    StageA::fetch(va, x + k, xs, rows, C - k);
     StageB::fetch(vg, wg + k, C, cols, C - k);
     StageB::fetch(vu, wu + k, C, cols, C - k);
   }
   __device__ __forceinline__ void put(char* a, char* b) const {
-    SA::put(a, va);
+    StageA::put(a, va);
     StageB::put(b, vg);
     StageB::put(b + HALF, vu);
   }
-  // gate columns, then up columns of the wave
+  // Column tile j: the first row of its run of fours within the wave's columns.
+  __device__ __forceinline__ static int column(int wave, int j) {
+    return wave % S::WN * (16 * TH) + 32 * (j / 2) + 4 * (j % 2);
+  }
   __device__ __forceinline__ uint4 fragb(const char* lb, int j, int step) const {
-    constexpr int TH = S::TN / 2;
-    const int w = wave_id() % S::WN * (16 * TH);
-    return StageB::frag(j < TH ? lb : lb + HALF, w + 16 * (j % TH), step);
+    return StageB::frag(j < TH ? lb : lb + HALF, column(wave_id(), j % TH), step);
   }
-};
-
-template <typename T, class S, bool DIRECT>
-__global__ __launch_bounds__(S::NT) void ffn_kernel(FfnArgs a, int tm, int tn, int splits, int per,
-                                                    int vec) {
-  constexpr int BF = S::BN / 2, TH = S::TN / 2;
-  const TileAt at = tile_at(tm, tn, splits);
-  const long long m0 = (long long)at.m * S::BM;
-  const int f0 = at.n * BF;
-  ForwardSrc<T, S> src;
-  src.xs = a.xs;
-  src.C = a.C;
-  src.x = (const T*)a.x + m0 * a.xs;
-  src.wg = (const T*)a.wg + (long long)f0 * a.C;
-  src.wu = (const T*)a.wu + (long long)f0 * a.C;
-  src.rows = (int)min((long long)S::BM, a.R - m0);
-  src.cols = min(BF, a.F - f0);
-  src.full = a.C / kTileK<T>;
-  if constexpr (DIRECT) {
-    decltype(src)::SA::offsets(src.oa, a.xs, src.rows);
-    decltype(src)::StageB::offsets(src.ob, a.C, src.cols);
+  static __device__ __forceinline__ bool vectors(const FfnArgs& a) {
+    constexpr int E = 8;
+    return a.F % E == 0 && (((size_t)a.h | (size_t)a.gate | (size_t)a.up) & 15) == 0;
   }
-  const int t0 = at.split * per, nt = (a.C + kTileK<T> - 1) / kTileK<T>;
-  f32x4 acc[S::TM][S::TN];
-  products<T, S, true, DIRECT>(acc, src, t0, min(t0 + per, nt));
-
-  const int l = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-  const int wm = wave_id() / S::WN * (S::BM / S::WM), wn = wave_id() % S::WN * (16 * TH);
+  __device__ __forceinline__ void store_row(const FfnArgs& a, int i,
+                                            const f32x4 (&row)[S::TN]) const {
+    const int thread = fresh_thread(), lane = thread & 63, wave = wave_of(thread);
+    const long long m = m0 + wave / S::WN * (S::BM / S::WM) + 16 * i + (lane & 15);
+    if (m >= a.R) return;
+    const bool vec = vectors(a);
 #pragma unroll
-  for (int i = 0; i < S::TM; ++i) {
-    const long long m = m0 + wm + 16 * i + l;
-    if (m >= a.R) continue;
+    for (int j = 0; j < TH; j += 2) {
+      const int f = f0 + column(wave, j) + 8 * (lane >> 4);
+      float x[8], u[8], h[8];
 #pragma unroll
-    for (int j = 0; j < TH; ++j) {
-      const int f = f0 + wn + 16 * j + 4 * g, n = a.F - f;
-      const long long to = m * a.F + f;
-      const f32x4 &x = acc[i][j], &u = acc[i][j + TH];
-      if (splits > 1) {
-        float* p = (float*)a.ws + (long long)at.split * 2 * a.R * a.F;
-        store4(p + to, x, n, vec);
-        store4(p + a.R * a.F + to, u, n, vec);
-        continue;
+      for (int k = 0; k < 8; ++k) {
+        x[k] = row[j + k / 4][k % 4];
+        u[k] = row[TH + j + k / 4][k % 4];
+        h[k] = activated(x[k], a.act) * u[k];
       }
-      f32x4 h;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) h[k] = activated(x[k], a.act) * u[k];
-      store4((T*)a.h + to, h, n, vec);
+      const long long to = m * a.F + f;
+      store8((T*)a.h + to, h, a.F - f, vec);
       if (a.gate) {
-        store4((T*)a.gate + to, x, n, vec);
-        store4((T*)a.up + to, u, n, vec);
+        store8((T*)a.gate + to, x, a.F - f, vec);
+        store8((T*)a.up + to, u, a.F - f, vec);
       }
     }
   }
-}
-
-// The activation over sums that were split: part [splits][2][R F].
-template <typename T>
-__global__ __launch_bounds__(256) void ffn_join_kernel(FfnArgs a, int splits) {
-  const long long n = a.R * a.F, at = blockIdx.x * 256LL + threadIdx.x;
-  if (at >= n) return;
-  float g = 0.f, u = 0.f;
-  for (int s = 0; s < splits; ++s) {
-    g += ((const float*)a.ws)[(long long)s * 2 * n + at];
-    u += ((const float*)a.ws)[((long long)s * 2 + 1) * n + at];
-  }
-  ((T*)a.h)[at] = from_f32<T>(activated(g, a.act) * u);
-  if (a.gate) {
-    ((T*)a.gate)[at] = from_f32<T>(g);
-    ((T*)a.up)[at] = from_f32<T>(u);
-  }
-}
+};
 
 // ---------------------------------------------------------------------------
 // Few rows: NR fragments of 16 rows.
@@ -221,31 +197,16 @@ int run_rows(const FfnArgs& a, hipStream_t s) {
   return (int)hipGetLastError();
 }
 
-template <typename T, class S, bool DIRECT>
-int run_tiles(const FfnArgs& a, int splits, hipStream_t s) {
-  const int nt = (a.C + kTileK<T> - 1) / kTileK<T>, per = (nt + splits - 1) / splits;
-  const long long tm = (a.R + S::BM - 1) / S::BM, tn = (a.F + S::BN / 2 - 1) / (S::BN / 2);
-  if (!grid_ok(tm * tn * splits, S::NT)) return -1;
-  const int vec = a.F % 4 == 0 && on16(a.h) && on16(a.gate) && on16(a.up);
-  int tk = ktimer_before(s, "ffn");
-  hipLaunchKernelGGL((ffn_kernel<T, S, DIRECT>), dim3((unsigned)(tm * tn * splits)), dim3(S::NT), 0,
-                     s, a, (int)tm, (int)tn, splits, per, vec);
-  ktimer_after(s, tk);
-  int rc = (int)hipGetLastError();
-  if (rc || splits == 1) return rc;
-  tk = ktimer_before(s, "ffn_join");
-  hipLaunchKernelGGL((ffn_join_kernel<T>), dim3((unsigned)((a.R * a.F + 255) / 256)), dim3(256), 0,
-                     s, a, splits);
-  ktimer_after(s, tk);
-  return (int)hipGetLastError();
-}
-
 template <typename T, class S>
-int run_shape(const FfnArgs& a, int splits, hipStream_t s) {
+int run_shape(const FfnArgs& a, const Plan& p, hipStream_t s) {
   const size_t es = sizeof(T);
   const bool direct = on16(a.x) && on16(a.wg) && on16(a.wu) && a.xs * es % 16 == 0 &&
                       a.C * es % 16 == 0;
-  return direct ? run_tiles<T, S, true>(a, splits, s) : run_tiles<T, S, false>(a, splits, s);
+  return launch_products<T, S, Forward<T, S>>(a, p, direct, "ffn", "ffn_join", s);
+}
+
+bool forward_plan(Plan& p, long long R, int C, int F, int bf16) {
+  return make_plan(p, 1, R, 2LL * F, C, bf16, C % (bf16 ? 8 : 4) == 0);
 }
 
 template <typename T>
@@ -253,79 +214,66 @@ int run(const FfnArgs& a, hipStream_t s) {
   if (a.R <= 16) return run_rows<T, 1>(a, s);
   if (a.R <= 32) return run_rows<T, 2>(a, s);
   if (a.R <= kFewRows) return run_rows<T, 4>(a, s);
-  const Cut c = cut_of(a.R, 2LL * a.F, (a.C + kTileK<T> - 1) / kTileK<T>);
-  switch (c.shape) {
-    case 0: return run_shape<T, Large>(a, c.splits, s);
-    case 1: return run_shape<T, Middle>(a, c.splits, s);
+  Plan p;
+  if (!forward_plan(p, a.R, a.C, a.F, a.bf16)) return -1;
+  FfnArgs b = a;
+  b.parts = (float*)a.ws;
+  switch (p.shape) {
+    case 0: return run_shape<T, Large>(b, p, s);
+    case 1: return run_shape<T, Middle>(b, p, s);
   }
-  return run_shape<T, Small>(a, c.splits, s);
+  return run_shape<T, SmallPairs>(b, p, s);
 }
 
 }  // namespace
 
-// The share of a CU's rate that a shape reaches, and how many of its workgroups a
-// CU holds.
-Cut cut_of(long long M, long long N, int nt) {
-  const int bm[] = {256, 128, 64}, at_once[] = {1, 2, 4};
-  const double rate[] = {1.0, 0.7, 0.4};
-  Cut best{2, 1};
-  nt = nt < 1 ? 1 : nt;
+// What a tile of k costs a workgroup that has a CU to itself or shares it with as many
+// as fit, in microseconds, by shape: bf16 is bound by operands from L2 and LDS, the more
+// the smaller the tile; fp32 by the matrix units.
+bool make_plan(Plan& best, int sets, long long M, long long N, long long K, int bf16,
+               bool direct) {
+  const int bm[] = {256, 128, 64}, kt = bf16 ? kTileK<__bf16> : kTileK<float>;
+  const int at_once[] = {1, 2, 4};
+  const double cost[2][3] = {{7.0, 1.75, 0.45}, {1.46, 0.5, 0.2}};
+  const long long nt = K > 0 ? (K + kt - 1) / kt : 1;
   double least = 1e300;
-  for (int k = 0; k < 3; ++k) {
-    const double tiles = (double)((M + bm[k] - 1) / bm[k]) * (double)((N + bm[k] - 1) / bm[k]);
-    for (int s = 1; s <= 16 && (s == 1 || nt / s >= 4); ++s) {
-      const int per = (nt + s - 1) / s;
+  if (nt > (1 << 26)) return false;
+  for (int k = direct ? 0 : 1; k < 3; ++k) {
+    const long long tm = sets * ((M + bm[k] - 1) / bm[k]), tn = (N + bm[k] - 1) / bm[k];
+    const long long tiles = tm * tn, full = 256 * at_once[k];
+    if (!grid_ok(16 * tiles, 512)) continue;
+    const long long whole = tiles / full * full, rest = tiles - whole;
+    for (int s = 1; s <= 16 && (s == 1 || (rest > 0 && nt / s >= 4)); ++s) {
+      const long long per = (nt + s - 1) / s;
       if ((nt + per - 1) / per != s) continue;     // (no empty part)
-      // rounds of the workgroups that are there at once, at a whole tile's cost each
-      const double wgs = tiles * s, full = 256.0 * at_once[k];
-      const double rounds = wgs <= 256 ? 1.0 / at_once[k] : (double)(long long)((wgs + full - 1) / full);
-      double t = rounds * at_once[k] * ((double)bm[k] * bm[k] / 65536) / rate[k] * (per + 3);
-      // the parts written and read, and the launch that adds them
-      if (s > 1) t += 8 + (double)s * (double)M * (double)N * 8 / 5e6 / 1.0;
+      // a round costs its tiles of k and the start and end of a tile; one of fewer
+      // workgroups than CUs runs each of them alone
+      const double each = bf16 ? 8 : 2, wgs = (double)(rest * s);
+      const double last = wgs <= 256 ? (wgs > 0) : at_once[k] * (double)((rest * s + full - 1) / full);
+      double t = cost[bf16][k] * (at_once[k] * (double)(whole / full) * (nt + each) +
+                                  last * (per + each));
+      // parts written and read, and the launch that adds them
+      if (s > 1) t += 5 + wgs * bm[k] * bm[k] * 8 / 4e6;
       if (t < least) {
         least = t;
-        best = Cut{k, s};
+        best = Plan{k, (int)tm, (int)tn, (int)nt, (int)whole, s, (int)per};
       }
     }
   }
-  return best;
+  return least < 1e300;
 }
 
-namespace {
-
-template <typename T>
-__global__ __launch_bounds__(256) void ffn_sum_kernel(const float* part, int splits, long long n,
-                                                      T* out) {
-  const long long at = blockIdx.x * 256LL + threadIdx.x;
-  if (at >= n) return;
-  float v = 0.f;
-  for (int s = 0; s < splits; ++s) v += part[s * n + at];
-  out[at] = from_f32<T>(v);
-}
-
-}  // namespace
-
-int launch_ffn_sum(const float* part, int splits, long long n, void* out, int bf16, hipStream_t s) {
-  const int tk = ktimer_before(s, "ffn_sum");
-  const dim3 grid((unsigned)((n + 255) / 256));
-  if (bf16) {
-    hipLaunchKernelGGL((ffn_sum_kernel<__bf16>), grid, dim3(256), 0, s, part, splits, n,
-                       (__bf16*)out);
-  } else {
-    hipLaunchKernelGGL((ffn_sum_kernel<float>), grid, dim3(256), 0, s, part, splits, n,
-                       (float*)out);
-  }
-  ktimer_after(s, tk);
-  return (int)hipGetLastError();
+size_t parts_bytes(const Plan& p) {
+  const int b[] = {256, 128, 64};
+  return p.splits > 1 ? (size_t)p.rest() * p.splits * b[p.shape] * b[p.shape] * sizeof(float) : 0;
 }
 
 }  // namespace ffn
 
 size_t ffn_forward_ws(long long R, int C, int F, int bf16) {
   if (R <= ffn::kFewRows) return 0;
-  const int kt = bf16 ? ffn::kTileK<__bf16> : ffn::kTileK<float>;
-  const ffn::Cut c = ffn::cut_of(R, 2LL * F, (C + kt - 1) / kt);
-  return c.splits > 1 ? (size_t)c.splits * 2 * R * F * sizeof(float) : 0;
+  ffn::Plan p;
+  return F > 0 && ffn::forward_plan(p, R, C, F, bf16) ? ffn::parts_bytes(p) : 0;
 }
 
 int launch_ffn_forward(const FfnArgs& a, hipStream_t s) {

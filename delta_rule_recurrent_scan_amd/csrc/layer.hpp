@@ -73,6 +73,9 @@ struct FfnArgs {
   // backward
   const void* dh;               // [R,F]
   void *dx, *dwg, *dwu;         // [R,C], [F,C], [F,C]
+  // within ws
+  void *dg, *du;                // [R,F]
+  float* parts;
 };
 
 size_t ffn_forward_ws(long long R, int C, int F, int bf16);
