@@ -188,12 +188,15 @@ struct Plan {
   int shape;                       // 0 large, 1 middle, 2 small
   int tm, tn, nt, whole, splits, per;
   __host__ __device__ int rest() const { return tm * tn - whole; }
+  // Items of the rest that go before the whole tiles: the workgroups that begin with a
+  // part store their results while the others multiply, and the other way about.
+  __host__ __device__ int lead() const { return whole ? splits / 2 * rest() : 0; }
   __host__ __device__ int items() const { return whole + rest() * splits; }
 };
 
 struct Item {
   int m, n, split, t0, t1;
-  int tile;                        // of the rest
+  int tile;                        // of the rest (-1: a whole tile)
 };
 // Consecutive numbers on one XCD (workgroups go to the eight in turn): number id of
 // `total`.
@@ -211,13 +214,15 @@ __device__ __forceinline__ void tile_place(const Plan& p, int r, int& m, int& n)
 __device__ __forceinline__ Item item_at(const Plan& p, int id) {
   Item it;
   int r;
-  if (id < p.whole) {
-    r = on_xcd(id, p.whole);
-    it.split = it.tile = 0;
+  const int lead = p.lead();
+  if (id >= lead && id < lead + p.whole) {
+    r = on_xcd(id - lead, p.whole);
+    it.split = it.tile = -1;
     it.t0 = 0;
     it.t1 = p.nt;
   } else {
-    const int rest = p.rest(), j = on_xcd(id - p.whole, rest * p.splits);
+    const int rest = p.rest(), k = id < lead ? id : id - p.whole;
+    const int j = id < lead ? on_xcd(k, lead) : lead + on_xcd(k - lead, rest * p.splits - lead);
     it.split = j / rest;
     it.tile = j % rest;
     r = p.whole + it.tile;
@@ -369,7 +374,7 @@ __device__ __forceinline__ void products(const FfnArgs& a, const Plan& p) {
     }
   }
 
-  if (p.splits > 1 && (int)blockIdx.x >= p.whole) {
+  if (p.splits > 1 && it.tile >= 0) {
     f32x4* part = (f32x4*)a.parts +
                   (size_t)(it.tile * p.splits + it.split) * (S::BM * S::BN / 4) + fresh_thread();
 #pragma unroll
@@ -463,10 +468,16 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8], int n, bool ve
 }
 
 // The activation of g, and its slope.
-__device__ __forceinline__ float activated(float g, int act) {
-  if (act == OSDN_ACT_SILU) return g * sigmoid_f(g);
-  if (act == OSDN_ACT_GELU) return g * (0.5f * erfcf(-0.707106781186547524f * g));
+template <int ACT>
+__device__ __forceinline__ float activated(float g) {
+  if constexpr (ACT == OSDN_ACT_SILU) return g * sigmoid_f(g);
+  if constexpr (ACT == OSDN_ACT_GELU) return g * (0.5f * erfcf(-0.707106781186547524f * g));
   return g * sigmoid_f(1.59576912160573071f * fmaf(0.044715f * g * g, g, g));
+}
+__device__ __forceinline__ float activated(float g, int act) {
+  return act == OSDN_ACT_SILU   ? activated<OSDN_ACT_SILU>(g)
+         : act == OSDN_ACT_GELU ? activated<OSDN_ACT_GELU>(g)
+                                : activated<OSDN_ACT_GELU_TANH>(g);
 }
 __device__ __forceinline__ void activated(float g, int act, float& f, float& slope) {
   if (act == OSDN_ACT_SILU) {

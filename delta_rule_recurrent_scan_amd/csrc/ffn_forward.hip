@@ -75,6 +75,16 @@ struct Forward {
   }
   __device__ __forceinline__ void store_row(const FfnArgs& a, int i,
                                             const f32x4 (&row)[S::TN]) const {
+    // (the branch around whole rows: one for every element costs as much as its work)
+    switch (a.act) {
+      case OSDN_ACT_SILU: return store_row<OSDN_ACT_SILU>(a, i, row);
+      case OSDN_ACT_GELU: return store_row<OSDN_ACT_GELU>(a, i, row);
+      default: return store_row<OSDN_ACT_GELU_TANH>(a, i, row);
+    }
+  }
+  template <int ACT>
+  __device__ __forceinline__ void store_row(const FfnArgs& a, int i,
+                                            const f32x4 (&row)[S::TN]) const {
     const int thread = fresh_thread(), lane = thread & 63, wave = wave_of(thread);
     const long long m = m0 + wave / S::WN * (S::BM / S::WM) + 16 * i + (lane & 15);
     if (m >= a.R) return;
@@ -87,7 +97,7 @@ struct Forward {
       for (int k = 0; k < 8; ++k) {
         x[k] = row[j + k / 4][k % 4];
         u[k] = row[TH + j + k / 4][k % 4];
-        h[k] = activated(x[k], a.act) * u[k];
+        h[k] = activated<ACT>(x[k]) * u[k];
       }
       const long long to = m * a.F + f;
       store8((T*)a.h + to, h, a.F - f, vec);
