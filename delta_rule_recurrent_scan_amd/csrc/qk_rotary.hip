@@ -22,24 +22,15 @@ namespace osdn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 8;     // tokens of a workgroup's tile
-constexpr int kMaxPairs = 64;     // D / 2 at most
+constexpr int kBatch = 4;         // rows that a lane has on their way
 
 struct Turns {
-  float2 cs[kMaxTokens * kMaxPairs];   // [token][pair] (cos, sin)
-  int b[kMaxTokens], t[kMaxTokens], on[kMaxTokens];
+  float2 cs[kThreads * 4];        // [token][pair] (cos, sin), 4 L pairs at most
 };
 
-// The tile's tokens with their cosines and sines; the caller's barrier follows.
+// The cosines and sines of the tile's tokens; the caller's barrier follows.
 __device__ __forceinline__ void fill_turns(const QkArgs& a, Turns& s, long long tok, int nt) {
   const unsigned np = a.rot / 2;
-  if ((int)threadIdx.x < nt) {
-    const long long at = tok + threadIdx.x;
-    const int b = (int)(at / a.T), t = (int)(at % a.T);
-    s.b[threadIdx.x] = b;
-    s.t[threadIdx.x] = t;
-    s.on[threadIdx.x] = !a.lengths || t < a.lengths[b];
-  }
   for (unsigned e = threadIdx.x; e < nt * np; e += kThreads) {
     const unsigned i = e / np, j = e % np;
     const long long at = tok + i;
@@ -52,36 +43,73 @@ __device__ __forceinline__ void fill_turns(const QkArgs& a, Turns& s, long long 
   }
 }
 
-// The rotation of a lane's channels d .. d + 7 of a head (L lanes); sign -1
-// turns back. Every lane of the head calls it.
+// A lane's place in a tile: 8 channels from d on of one token, and the heads first,
+// first + step, ... of it. Neighbouring rows of lanes take neighbouring tokens, whose
+// rows lie side by side in the heads.
+struct Place {
+  bool in, on;           // the token exists; it lies inside its sequence
+  int d, first, step;
+  long long b, t;
+  int partner;           // the lane that holds the other members of its pairs
+  bool turned;
+};
 template <int L>
-__device__ __forceinline__ void turn(float (&v)[8], const float2* cs, int d, int rot,
-                                     int interleaved, float sign) {
-  if (rot == 0) return;
-  if (interleaved) {
-    if (d < rot) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 w = cs[d / 2 + i];
-        const float x = v[2 * i], y = v[2 * i + 1], s = w.y * sign;
-        v[2 * i] = x * w.x - y * s;
-        v[2 * i + 1] = y * w.x + x * s;
-      }
-    }
-    return;
-  }
-  // the other member of a pair is rot / 2 channels away, rot / 16 lanes
-  const int hr = rot / 16, l = d / 8, lane = threadIdx.x & 63;
-  const int other = l < hr ? lane + hr : l < 2 * hr ? lane - hr : lane;
-  const float s = l < hr ? -sign : sign;
+__device__ __forceinline__ Place place(const QkArgs& a, long long tok, int per, long long tokens) {
+  Place p;
+  const int row = threadIdx.x / L, l = threadIdx.x % L, lane = threadIdx.x & 63;
+  const long long at = tok + row % per;
+  p.in = at < tokens;
+  p.b = p.in ? at / a.T : 0;
+  p.t = p.in ? at % a.T : 0;
+  p.on = p.in && (!a.lengths || p.t < a.lengths[p.b]);
+  p.d = 8 * l;
+  p.first = row / per;
+  p.step = kThreads / L / per;    // (per is a power of two up to kThreads / L)
+  p.turned = p.d < a.rot;
+  // (rot / 2 channels away are rot / 16 lanes)
+  const int hr = a.rot / 16;
+  p.partner = a.interleaved || !p.turned ? lane : l < hr ? lane + hr : lane - hr;
+  return p;
+}
+
+// A lane's part of the rotation, y_i = v_i c_i + w_i s_i with w the other members of the
+// pairs; turning back, s changes its sign.
+struct Rotation {
+  float c[8], s[8];
+};
+__device__ __forceinline__ void rotation(const QkArgs& a, const Turns& t, const Place& p, int token,
+                                         Rotation& r) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float o = __shfl(v[i], other, 64);
-    if (l < 2 * hr) {
-      const float2 w = cs[(l < hr ? d : d - rot / 2) + i];
-      v[i] = v[i] * w.x + o * (w.y * s);
-    }
+    r.c[i] = 1.f;
+    r.s[i] = 0.f;
   }
+  if (!p.turned) return;
+  const int np = a.rot / 2, half = p.d < np ? 0 : np;
+  const float2* cs = t.cs + token * np;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 w = cs[a.interleaved ? p.d / 2 + i / 2 : p.d - half + i];
+    r.c[i] = w.x;
+    r.s[i] = (a.interleaved ? i % 2 == 0 : half == 0) ? -w.y : w.y;
+  }
+}
+
+// The other members of a lane's pairs, as they lie in memory.
+template <typename T>
+__device__ __forceinline__ void others(const Raw<T, 8>& x, const QkArgs& a, const Place& p,
+                                       float (&o)[8]) {
+  if (a.interleaved) {
+    float v[8];
+    x.widen(v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = v[i ^ 1];
+    return;
+  }
+  Raw<T, 8> y;
+#pragma unroll
+  for (int i = 0; i < Raw<T, 8>::W; ++i) y.u[i] = __shfl(x.u[i], p.partner, 64);
+  y.widen(o);
 }
 
 template <int L>
@@ -90,31 +118,47 @@ __device__ __forceinline__ float root(const QkArgs& a, float ss) {
   return a.norm == 0 ? 1.f : rsqrtf((a.norm == 1 ? m / (8 * L) : m) + a.eps);
 }
 
-// One input (queries or keys): H heads of every token of the tile.
+// One input (queries or keys): H heads of the lane's token. The weights of both members
+// of a pair are multiplied into the rotation, which all heads share.
 template <typename Tin, int L, bool ALN>
-__device__ __forceinline__ void forward_rows(const QkArgs& a, const Turns& s, long long tok, int nt,
+__device__ __forceinline__ void forward_rows(const QkArgs& a, const Place& p, const Rotation& r,
                                              int H, const Tin* x, long long bs, long long ts,
                                              const float* weight, Tin* y) {
-  constexpr int D = 8 * L, per = kThreads / L;
-  const int d = (threadIdx.x % L) * 8, np = a.rot / 2;
-  float w[8];
+  constexpr int D = 8 * L;
+  float c[8], s[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = weight ? weight[d + i] : 1.f;
-  for (unsigned e = threadIdx.x / L; e < (unsigned)(nt * H); e += per) {
-    const unsigned i = e / (unsigned)H, h = e % (unsigned)H;
-    const long long b = s.b[i], t = s.t[i];
-    float v[8];
+  for (int i = 0; i < 8; ++i) {
+    const int o = a.interleaved ? p.d + (i ^ 1) : 8 * (p.partner % L) + i;
+    c[i] = r.c[i] * (weight ? weight[p.d + i] : 1.f);
+    s[i] = r.s[i] * (weight ? weight[o] : 1.f);
+  }
+  if (!p.in) return;
+  x += p.b * bs + p.t * ts + p.d;
+  y += (p.b * H * a.T + p.t) * D + p.d;
+  const long long hs = (long long)a.T * D;
+  for (int h = p.first; h < H; h += kBatch * p.step) {
+    Raw<Tin, 8> v[kBatch];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = 0.f;
-    if (s.on[i]) load_v<ALN, 8>(x + b * bs + t * ts + h * D + d, 8, v);
-    float ss = 0.f;
+    for (int k = 0; k < kBatch; ++k) {
+      v[k].zero();
+      if (p.on && h + k * p.step < H) v[k].template load<ALN>(x + (h + k * p.step) * D, 8);
+    }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) ss += v[k] * v[k];
-    const float r = root<L>(a, ss);
+    for (int k = 0; k < kBatch; ++k) {
+      if (h + k * p.step >= H) break;      // (a head's lanes leave together)
+      float w[8], o[8], ss = 0.f;
+      v[k].widen(w);
+      others(v[k], a, p, o);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] *= r * w[k];
-    turn<L>(v, s.cs + i * np, d, a.rot, a.interleaved, 1.f);
-    store_v<true, 8>(y + ((b * H + h) * (long long)a.T + t) * D + d, 8, v);
+      for (int i = 0; i < 8; ++i) ss = fmaf(w[i], w[i], ss);
+      const float n = root<L>(a, ss);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float t = w[i] * c[i];
+        w[i] = (p.turned ? fmaf(o[i], s[i], t) : t) * n;
+      }
+      store_v<true, 8>(y + (h + k * p.step) * hs, 8, w);
+    }
   }
 }
 
@@ -122,49 +166,65 @@ template <typename Tin, int L, bool ALN>
 __global__ __launch_bounds__(kThreads) void qk_rotary_kernel(QkArgs a, int per) {
   __shared__ Turns s;
   const long long tok = blockIdx.x * (long long)per, tokens = (long long)a.B * a.T;
-  const int nt = (int)min((long long)per, tokens - tok);
-  fill_turns(a, s, tok, nt);
+  fill_turns(a, s, tok, (int)min((long long)per, tokens - tok));
   __syncthreads();
-  forward_rows<Tin, L, ALN>(a, s, tok, nt, a.Hq, (const Tin*)a.q, a.qbs, a.qts, a.wq, (Tin*)a.yq);
-  forward_rows<Tin, L, ALN>(a, s, tok, nt, a.Hk, (const Tin*)a.k, a.kbs, a.kts, a.wk, (Tin*)a.yk);
+  const Place p = place<L>(a, tok, per, tokens);
+  Rotation r;
+  rotation(a, s, p, threadIdx.x / L % per, r);
+  forward_rows<Tin, L, ALN>(a, p, r, a.Hq, (const Tin*)a.q, a.qbs, a.qts, a.wq, (Tin*)a.yq);
+  forward_rows<Tin, L, ALN>(a, p, r, a.Hk, (const Tin*)a.k, a.kbs, a.kts, a.wk, (Tin*)a.yk);
 }
 
 template <typename Tin, typename Tdy, int L, bool ALN>
-__device__ __forceinline__ void backward_rows(const QkArgs& a, const Turns& s, long long tok,
-                                              int nt, int H, const Tin* x, long long bs,
-                                              long long ts, const float* weight, const Tdy* dy,
-                                              Tin* dx, float (&dw)[8]) {
-  constexpr int D = 8 * L, per = kThreads / L;
-  const int d = (threadIdx.x % L) * 8, np = a.rot / 2;
+__device__ __forceinline__ void backward_rows(const QkArgs& a, const Place& p, const Rotation& r,
+                                              int H, const Tin* x, long long bs, long long ts,
+                                              const float* weight, const Tdy* dy, Tin* dx,
+                                              float (&dw)[8]) {
+  constexpr int D = 8 * L, B = kBatch / 2;
   float w[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = weight ? weight[d + i] : 1.f;
-  for (unsigned e = threadIdx.x / L; e < (unsigned)(nt * H); e += per) {
-    const unsigned i = e / (unsigned)H, h = e % (unsigned)H;
-    const long long b = s.b[i], t = s.t[i];
-    float v[8], g[8];
+  for (int i = 0; i < 8; ++i) w[i] = weight ? weight[p.d + i] : 1.f;
+  if (!p.in) return;
+  x += p.b * bs + p.t * ts + p.d;
+  dx += (p.b * a.T + p.t) * ((long long)H * D) + p.d;
+  dy += (p.b * H * a.T + p.t) * D + p.d;
+  const long long hs = (long long)a.T * D;
+  for (int h = p.first; h < H; h += B * p.step) {
+    Raw<Tin, 8> xs[B];
+    Raw<Tdy, 8> gs[B];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = g[k] = 0.f;
-    if (s.on[i]) {
-      load_v<ALN, 8>(x + b * bs + t * ts + h * D + d, 8, v);
-      load_v<true, 8>(dy + ((b * H + h) * (long long)a.T + t) * D + d, 8, g);
+    for (int k = 0; k < B; ++k) {
+      xs[k].zero();
+      gs[k].zero();
+      if (p.on && h + k * p.step < H) {
+        xs[k].template load<ALN>(x + (h + k * p.step) * D, 8);
+        gs[k].template load<true>(dy + (h + k * p.step) * hs, 8);
+      }
     }
-    turn<L>(g, s.cs + i * np, d, a.rot, a.interleaved, -1.f);
-    float ss = 0.f, q = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      ss += v[k] * v[k];
-      q += v[k] * g[k] * w[k];
-    }
-    const float r = root<L>(a, ss);
-    // n (n . f): r^2 x (x . f), over D for the mean
-    const float m = a.norm == 0 ? 0.f : group_sum<L>(q) * r * r * (a.norm == 1 ? 1.f / D : 1.f);
+    for (int k = 0; k < B; ++k) {
+      if (h + k * p.step >= H) break;
+      float v[8], e[8], o[8], ss = 0.f, q = 0.f;
+      xs[k].widen(v);
+      gs[k].widen(e);
+      others(gs[k], a, p, o);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      dw[k] += g[k] * v[k] * r;
-      v[k] = r * (g[k] * w[k] - v[k] * m);
+      for (int i = 0; i < 8; ++i) {
+        const float t = e[i] * r.c[i];
+        e[i] = p.turned ? fmaf(-o[i], r.s[i], t) : t;
+        ss = fmaf(v[i], v[i], ss);
+        q = fmaf(v[i], e[i] * w[i], q);
+      }
+      const float n = root<L>(a, ss);
+      // n (n . f): n^2 x (x . f), over D for the mean
+      const float m = a.norm == 0 ? 0.f : group_sum<L>(q) * n * n * (a.norm == 1 ? 1.f / D : 1.f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        dw[i] = fmaf(e[i] * v[i], n, dw[i]);
+        v[i] = n * (e[i] * w[i] - v[i] * m);
+      }
+      store_v<true, 8>(dx + (h + k * p.step) * D, 8, v);
     }
-    store_v<true, 8>(dx + (tok + i) * ((long long)H * D) + h * D + d, 8, v);
   }
 }
 
@@ -178,13 +238,15 @@ __global__ __launch_bounds__(kThreads) void qk_rotary_bwd_kernel(QkArgs a, int p
   float dwq[8] = {}, dwk[8] = {};
   for (long long tok = blockIdx.x * (long long)per; tok < tokens;
        tok += (long long)gridDim.x * per) {
-    const int nt = (int)min((long long)per, tokens - tok);
     __syncthreads();   // the last tile's turns are read
-    fill_turns(a, s, tok, nt);
+    fill_turns(a, s, tok, (int)min((long long)per, tokens - tok));
     __syncthreads();
-    backward_rows<Tin, Tdy, L, ALN>(a, s, tok, nt, a.Hq, (const Tin*)a.q, a.qbs, a.qts, a.wq,
+    const Place p = place<L>(a, tok, per, tokens);
+    Rotation r;
+    rotation(a, s, p, threadIdx.x / L % per, r);
+    backward_rows<Tin, Tdy, L, ALN>(a, p, r, a.Hq, (const Tin*)a.q, a.qbs, a.qts, a.wq,
                                     (const Tdy*)a.dyq, (Tin*)a.dq, dwq);
-    backward_rows<Tin, Tdy, L, ALN>(a, s, tok, nt, a.Hk, (const Tin*)a.k, a.kbs, a.kts, a.wk,
+    backward_rows<Tin, Tdy, L, ALN>(a, p, r, a.Hk, (const Tin*)a.k, a.kbs, a.kts, a.wk,
                                     (const Tdy*)a.dyk, (Tin*)a.dk, dwk);
   }
   float* part = (float*)a.ws + (size_t)blockIdx.x * 2 * D;
@@ -202,16 +264,18 @@ __global__ __launch_bounds__(kThreads) void qk_rotary_bwd_kernel(QkArgs a, int p
   }
 }
 
-// Tokens a workgroup: as many as leave four workgroups a CU, up to eight.
-int tile_tokens(long long tokens) {
-  int per = kMaxTokens;
+// Tokens a workgroup: as many as leave four workgroups a CU. All its rows of lanes on
+// tokens of their own give the longest runs of memory: 16384 tokens of 32 heads of 128
+// take 57 us at 16 tokens a tile and 62 at 8.
+int tile_tokens(long long tokens, int L) {
+  int per = kThreads / L;
   while (per > 1 && tokens / per < 1024) per /= 2;
   return per;
 }
 
 // Workgroups of the backward, each a partial row: four a CU at most.
-int bwd_blocks(long long tokens) {
-  const int per = tile_tokens(tokens);
+int bwd_blocks(long long tokens, int L) {
+  const int per = tile_tokens(tokens, L);
   const long long need = (tokens + per - 1) / per;
   return (int)(need < 1024 ? need : 1024);
 }
@@ -219,7 +283,7 @@ int bwd_blocks(long long tokens) {
 template <typename Tin, int L, bool ALN>
 int run_forward(const QkArgs& a, hipStream_t s) {
   const long long tokens = (long long)a.B * a.T;
-  const int per = tile_tokens(tokens);
+  const int per = tile_tokens(tokens, L);
   const long long wgs = (tokens + per - 1) / per;
   if (!grid_ok(wgs, kThreads)) return -1;
   const int tk = ktimer_before(s, "qk_rotary");
@@ -232,11 +296,11 @@ int run_forward(const QkArgs& a, hipStream_t s) {
 template <typename Tin, typename Tdy, int L, bool ALN>
 int run_backward(const QkArgs& a, hipStream_t s) {
   const long long tokens = (long long)a.B * a.T;
-  const int nb = bwd_blocks(tokens);
+  const int nb = bwd_blocks(tokens, L);
   if (nb > 0) {
     const int tk = ktimer_before(s, "qk_rotary_bwd");
     hipLaunchKernelGGL((qk_rotary_bwd_kernel<Tin, Tdy, L, ALN>), dim3(nb), dim3(kThreads), 0, s, a,
-                       tile_tokens(tokens));
+                       tile_tokens(tokens, L));
     ktimer_after(s, tk);
     const int rc = (int)hipGetLastError();
     if (rc) return rc;
@@ -281,7 +345,7 @@ int launch_qk_rotary(const QkArgs& a, hipStream_t s) {
 }
 
 size_t qk_rotary_backward_ws(int B, int T, int D) {
-  return (size_t)bwd_blocks((long long)B * T) * 2 * D * sizeof(float);
+  return (size_t)bwd_blocks((long long)B * T, D / 8) * 2 * D * sizeof(float);
 }
 
 int launch_qk_rotary_backward(const QkArgs& a, hipStream_t s) {
