@@ -7,8 +7,8 @@
 //   dA = sum dla rho.
 //
 // A workgroup walks the tokens of one sequence (or a segment of it) for 64
-// channels, a tile of 128 tokens at a time: a thread holds 8 tokens of 2
-// channels, two threads a wave's half each, eight waves a tile. Every thread
+// channels, a tile of 128 or 256 tokens at a time: a thread holds 8 or 16
+// tokens of 2 channels, two threads a wave's half each, eight waves a tile. Every thread
 // runs its own tokens from zero, the ends are joined over the waves through
 // LDS with one barrier a tile, and a second run over the registers from the
 // joined state gives the results: every input is read once and every output
@@ -17,8 +17,8 @@
 //
 // Decays lie close to one and act over thousands of tokens. A product of
 // rounded decays would be off by their common rounding times the number of
-// tokens, so what carries a state over 8 tokens and more is the exponential of
-// a sum of the logarithms; only inside 8 tokens are the decays themselves used.
+// tokens, so what carries a state from thread to thread is the exponential of
+// a sum of the logarithms; only inside a thread are the decays themselves used.
 // 1 - a^2 comes from a series where it is small.
 #include "launch.hpp"
 #include "layer.hpp"
@@ -28,9 +28,10 @@ namespace osdn {
 namespace {
 
 constexpr int kThreads = 512, kWaves = 8;
-constexpr int kK = 8;                      // tokens a thread
-constexpr int kTile = 2 * kWaves * kK;     // 128 tokens
 constexpr int kCols = 64;                  // channels a workgroup
+// K tokens a thread, 16 K a tile.
+template <int K>
+constexpr int kTile = 2 * kWaves * K;
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 
 // Two channels of one token as they lie in memory. The base is the same in
@@ -82,7 +83,7 @@ __device__ __forceinline__ void store_pair(T* p, float v0, float v1, int n) {
   }
 }
 
-// A thread's place: tokens first .. first + 7 of the tile and channels c, c + 1.
+// A thread's place: the seg-th run of tokens of the tile and channels c, c + 1.
 struct Place {
   int seg, c, n;        // n: how many of the two channels exist
   int c0, c1;           // the channels it reads (the last ones where there are none)
@@ -100,40 +101,38 @@ __device__ __forceinline__ Place place(int cb, int C) {
 }
 
 // One input's rows of a tile.
-template <typename Tin, bool ALN>
+template <typename Tin, bool ALN, int K>
 struct Rows {
-  Pair<Tin> v[kK];
-  // tokens t .. t + 7 (t: the thread's first) of rows at p with stride ts;
-  // tokens from n on read token n - 1.
+  Pair<Tin> v[K];
+  // the thread's tokens of the tile's rows at p with stride ts; tokens from n on read
+  // token n - 1.
   __device__ __forceinline__ void load(const Tin* p, long long ts, int tile, int seg, int n,
                                        const Place& pl) {
     const char* base = (const char*)(p + (long long)tile * ts);
     const unsigned row = (unsigned)ts * (unsigned)sizeof(Tin);
     const unsigned b0 = pl.c0 * (unsigned)sizeof(Tin), b1 = pl.c1 * (unsigned)sizeof(Tin);
-    if (tile + kTile <= n) {
-      const unsigned o = row * (unsigned)(seg * kK);
+    if (tile + kTile<K> <= n) {
+      const unsigned o = row * (unsigned)(seg * K);
 #pragma unroll
-      for (int k = 0; k < kK; ++k)
+      for (int k = 0; k < K; ++k)
         v[k].template load<ALN>(base + (size_t)row * k, o + b0, o + b1);
     } else {
 #pragma unroll
-      for (int k = 0; k < kK; ++k) {
-        const unsigned o = row * (unsigned)min(seg * kK + k, n - 1 - tile);
+      for (int k = 0; k < K; ++k) {
+        const unsigned o = row * (unsigned)min(seg * K + k, n - 1 - tile);
         v[k].template load<ALN>(base, o + b0, o + b1);
       }
     }
   }
 };
 
-// 1 - exp(z) for z <= 0 where e is exp(z): a series where the difference would
-// lose digits (from -0.35 on its eighth term is under half a step).
+// 1 - exp(z) for z <= 0 where e is exp(z): from -0.35 on, where the difference would
+// lose digits, z times the polynomial of degree 4 through the Chebyshev nodes of that
+// range (1.5e-8 off, 1.1e-7 with its roundings).
 __device__ __forceinline__ float one_minus_exp(float z, float e) {
-  float p = 1.f / 5040.f;
-  p = fmaf(p, z, 1.f / 720.f);
-  p = fmaf(p, z, 1.f / 120.f);
-  p = fmaf(p, z, 1.f / 24.f);
-  p = fmaf(p, z, 1.f / 6.f);
-  p = fmaf(p, z, 0.5f);
+  float p = fmaf(0.0072125504f, z, 0.04133279f);
+  p = fmaf(p, z, 0.1666255f);
+  p = fmaf(p, z, 0.4999982f);
   p = fmaf(p, z, 1.f);
   return z > -0.35f ? -z * p : 1.f - e;
 }
@@ -223,44 +222,46 @@ __device__ __forceinline__ void enter(const float* start, const float* ws, int b
 }
 
 // Tokens of segment q of S of a sequence of n, whole tiles.
-__device__ __forceinline__ void seg_range(int n, int S, int q, int& t0, int& t1) {
-  const int tiles = (n + kTile - 1) / kTile, per = (tiles + S - 1) / S;
-  t0 = min(n, q * per * kTile);
-  t1 = min(n, (q + 1) * per * kTile);
+__device__ __forceinline__ void seg_range(int n, int S, int q, int tile, int& t0, int& t1) {
+  const int tiles = (n + tile - 1) / tile, per = (tiles + S - 1) / S;
+  t0 = min(n, q * per * tile);
+  t1 = min(n, (q + 1) * per * tile);
 }
 
 // ---------------------------------------------------------------------------
 // Forward. PART: only the segments' maps (the first launch).
 // ---------------------------------------------------------------------------
 
-template <typename Tin, bool ALN, bool GATE, bool NORM, bool PART>
+template <typename Tin, int K, bool ALN, bool GATE, bool NORM, bool PART>
 __global__ __launch_bounds__(kThreads) void glr_kernel(GlrArgs a, int ncb, int S) {
+  constexpr int TILE = kTile<K>;
   __shared__ float4 buf[2][kWaves * 32];
   const int cb = blockIdx.x % ncb, bq = blockIdx.x / ncb;
   const int nq = PART ? S - 1 : S, q = bq % nq, b = bq / nq;
   const Place pl = place<ALN>(cb, a.C);
   const int n = seq_len(a, b);
   int t0, t1;
-  seg_range(n, S, q, t0, t1);
+  seg_range(n, S, q, TILE, t0, t1);
   const Tin* x = (const Tin*)a.x + b * a.xbs;
   const Tin* r = (const Tin*)a.r + b * a.rbs;
   const Tin* gi = GATE ? (const Tin*)a.i + b * a.ibs : nullptr;
-  float A2[2] = {a.A[pl.c0] * kLog2e, a.A[pl.c1] * kLog2e};
+  const float A2[2] = {a.A[pl.c0] * kLog2e, a.A[pl.c1] * kLog2e};
   float carry[2] = {0.f, 0.f}, Ltot[2] = {0.f, 0.f};
   if constexpr (!PART) enter<true>(a.h0, (const float*)a.ws, b, S, q, a.C, pl, carry);
 
-  Rows<Tin, ALN> rx, rr, ri;
-  if (t0 < t1) {
-    rx.load(x, a.xts, t0, pl.seg, n, pl);
-    rr.load(r, a.rts, t0, pl.seg, n, pl);
-    if constexpr (GATE) ri.load(gi, a.its, t0, pl.seg, n, pl);
-  }
+  Rows<Tin, ALN, K> rx, rr, ri;
+  auto fetch = [&](int tile) {
+    rx.load(x, a.xts, tile, pl.seg, n, pl);
+    rr.load(r, a.rts, tile, pl.seg, n, pl);
+    if constexpr (GATE) ri.load(gi, a.its, tile, pl.seg, n, pl);
+  };
+  if (t0 < t1) fetch(t0);
   int par = 0;
-  for (int tile = t0; tile < t1; tile += kTile, par ^= 1) {
-    float dec[kK][2], in[kK][2], L[2] = {0.f, 0.f}, H[2] = {0.f, 0.f};
-    const int t = tile + pl.seg * kK;
+  for (int tile = t0; tile < t1; tile += TILE, par ^= 1) {
+    float dec[K][2], in[K][2], L[2] = {0.f, 0.f}, H[2] = {0.f, 0.f};
+    const int t = tile + pl.seg * K;
 #pragma unroll
-    for (int k = 0; k < kK; ++k)
+    for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         float rho, l2, m;
@@ -268,17 +269,27 @@ __global__ __launch_bounds__(kThreads) void glr_kernel(GlrArgs a, int ncb, int S
         float u = rx.v[k].get(j);
         if constexpr (GATE) u *= sigmoid_f(ri.v[k].get(j));
         in[k][j] = m * u;
-        if (tile + kTile > n && t + k >= n) {
-          dec[k][j] = 1.f;
-          in[k][j] = l2 = 0.f;
-        }
         L[j] += l2;
         H[j] = fmaf(dec[k][j], H[j], in[k][j]);
       }
-    const int next = min(tile + kTile, t1 - 1) / kTile * kTile;
-    rx.load(x, a.xts, next, pl.seg, n, pl);
-    rr.load(r, a.rts, next, pl.seg, n, pl);
-    if constexpr (GATE) ri.load(gi, a.its, next, pl.seg, n, pl);
+    if (tile + TILE > n) {
+      // tokens behind the end keep the state: the sums again without them
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        L[j] = H[j] = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          if (t + k >= n) {
+            dec[k][j] = 1.f;
+            in[k][j] = 0.f;
+          } else {
+            L[j] += A2[j] * sigmoid_f(rr.v[k].get(j));
+          }
+          H[j] = fmaf(dec[k][j], H[j], in[k][j]);
+        }
+      }
+    }
+    fetch(min(tile + TILE, t1 - 1) / TILE * TILE);
     float h[2];
     join<true>(L, H, carry, h, buf[par]);
     if constexpr (PART) {
@@ -290,12 +301,25 @@ __global__ __launch_bounds__(kThreads) void glr_kernel(GlrArgs a, int ncb, int S
                                 t / kGlrInterval) * a.C + pl.c;
         store_pair<ALN>(st, h[0], h[1], pl.n);
       }
-      Tin* y = (Tin*)a.y + ((size_t)b * a.T + t) * a.C + pl.c;
+      if (a.y) {
+        // rows of the tile from one base, 32-bit offsets
+        char* y = (char*)((Tin*)a.y + ((size_t)b * a.T + tile) * a.C);
+        const unsigned row = (unsigned)a.C * (unsigned)sizeof(Tin);
+        const unsigned o = row * (unsigned)(pl.seg * K) + pl.c * (unsigned)sizeof(Tin);
+        auto tokens = [&](bool whole) {
 #pragma unroll
-      for (int k = 0; k < kK; ++k) {
-        h[0] = fmaf(dec[k][0], h[0], in[k][0]);
-        h[1] = fmaf(dec[k][1], h[1], in[k][1]);
-        if (a.y && t + k < n) store_pair<ALN>(y + (size_t)k * a.C, h[0], h[1], pl.n);
+          for (int k = 0; k < K; ++k) {
+            h[0] = fmaf(dec[k][0], h[0], in[k][0]);
+            h[1] = fmaf(dec[k][1], h[1], in[k][1]);
+            if (whole || t + k < n)
+              store_pair<ALN>((Tin*)(y + (size_t)row * k + o), h[0], h[1], pl.n);
+          }
+        };
+        if (tile + TILE <= n) {
+          tokens(true);
+        } else {
+          tokens(false);
+        }
       }
     }
   }
@@ -324,7 +348,7 @@ __global__ __launch_bounds__(kThreads) void glr_kernel(GlrArgs a, int ncb, int S
       if (a.hT && threadIdx.x < 32)
         store_pair<ALN>(a.hT + (size_t)b * a.C + pl.c, carry[0], carry[1], pl.n);
       const int ns = (a.T + kGlrInterval - 1) / kGlrInterval;
-      const int s0 = (n + kTile - 1) / kTile * (kTile / kGlrInterval);
+      const int s0 = (n + TILE - 1) / TILE * (TILE / kGlrInterval);
       if (a.states)
         for (int t = s0 + pl.seg; t < ns; t += 2 * kWaves)
           store_pair<ALN>(a.states + ((size_t)b * ns + t) * a.C + pl.c, carry[0], carry[1], pl.n);
@@ -372,39 +396,47 @@ __global__ __launch_bounds__(256) void glr_decode_kernel(GlrArgs a) {
 // is c_t = a_t g_t = a_t (dy_t + c_{t+1}).
 // ---------------------------------------------------------------------------
 
+constexpr int kBK = 8;   // tokens a thread
+
 template <typename Tin, bool ALN>
 __global__ __launch_bounds__(kThreads) void glr_bwd_part_kernel(GlrArgs a, int ncb, int S) {
+  constexpr int K = kBK, TILE = kTile<K>;
   __shared__ float4 buf[2][kWaves * 32];
   const int cb = blockIdx.x % ncb, bq = blockIdx.x / ncb;
   const int q = 1 + bq % (S - 1), b = bq / (S - 1);
   const Place pl = place<ALN>(cb, a.C);
   const int n = seq_len(a, b);
   int t0, t1;
-  seg_range(n, S, q, t0, t1);
+  seg_range(n, S, q, TILE, t0, t1);
   const Tin* r = (const Tin*)a.r + b * a.rbs;
   const Tin* dy = (const Tin*)a.dy + (size_t)b * a.T * a.C;
   const float A2[2] = {a.A[pl.c0] * kLog2e, a.A[pl.c1] * kLog2e};
   float carry[2] = {0.f, 0.f}, Ltot[2] = {0.f, 0.f};
-  Rows<Tin, ALN> rr, rd;
-  int par = 0;
-  for (int tile = t0 < t1 ? (t1 - 1) / kTile * kTile : -1; tile >= t0; tile -= kTile, par ^= 1) {
+  Rows<Tin, ALN, K> rr, rd;
+  auto fetch = [&](int tile) {
     rr.load(r, a.rts, tile, pl.seg, n, pl);
     rd.load(dy, a.C, tile, pl.seg, n, pl);
+  };
+  const int last = t0 < t1 ? (t1 - 1) / TILE * TILE : -1;
+  if (t0 < t1) fetch(last);
+  int par = 0;
+  for (int tile = last; tile >= t0; tile -= TILE, par ^= 1) {
     float L[2] = {0.f, 0.f}, H[2] = {0.f, 0.f};
-    const int t = tile + pl.seg * kK;
+    const int t = tile + pl.seg * K;
 #pragma unroll
-    for (int k = kK - 1; k >= 0; --k)
+    for (int k = K - 1; k >= 0; --k)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         float l2 = A2[j] * sigmoid_f(rr.v[k].get(j)), d = rd.v[k].get(j);
         float dec = __builtin_amdgcn_exp2f(l2);
-        if (tile + kTile > n && t + k >= n) {
+        if (tile + TILE > n && t + k >= n) {
           dec = 1.f;
           l2 = d = 0.f;
         }
         L[j] += l2;
         H[j] = dec * (H[j] + d);
       }
+    fetch(max(tile - TILE, t0));
     float in[2];
     join<false>(L, H, carry, in, buf[par]);
     Ltot[0] += L[0];
@@ -432,13 +464,14 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_part_kernel(GlrArgs a, int n
 template <typename Tin, bool ALN, bool GATE, bool NORM>
 __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrArgs a, int ncb, int S,
                                                            float* parts) {
+  constexpr int K = kBK, TILE = kTile<K>;
   __shared__ float4 buf[2][kWaves * 32];
   __shared__ double red[2 * kWaves][kCols];
   const int cb = blockIdx.x % ncb, bq = blockIdx.x / ncb, q = bq % S, b = bq / S;
   const Place pl = place<ALN>(cb, a.C);
   const int n = seq_len(a, b), ns = (a.T + kGlrInterval - 1) / kGlrInterval;
   int t0, t1;
-  seg_range(n, S, q, t0, t1);
+  seg_range(n, S, q, TILE, t0, t1);
   const Tin* x = (const Tin*)a.x + b * a.xbs;
   const Tin* r = (const Tin*)a.r + b * a.rbs;
   const Tin* gi = GATE ? (const Tin*)a.i + b * a.ibs : nullptr;
@@ -447,53 +480,68 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrArgs a, int ncb, i
   float carry[2];
   enter<false>(a.dhT, (const float*)a.ws, b, S, q, a.C, pl, carry);
   double dA[2] = {0.0, 0.0};
-  const int lane = threadIdx.x & 63;
+  const bool low = (threadIdx.x & 63) < 32;
 
-  Rows<Tin, ALN> rx, rr, ri, rd;
+  Rows<Tin, ALN, K> rx, rr, ri, rd;
   float s0 = 0.f, s1 = 0.f;
   auto fetch = [&](int tile) {
     rr.load(r, a.rts, tile, pl.seg, n, pl);
     rd.load(dy, a.C, tile, pl.seg, n, pl);
     rx.load(x, a.xts, tile, pl.seg, n, pl);
     if constexpr (GATE) ri.load(gi, a.its, tile, pl.seg, n, pl);
-    const int si = min((tile + pl.seg * kK) / kGlrInterval, ns - 1);
+    const int si = min((tile + pl.seg * K) / kGlrInterval, ns - 1);
     const float* st = a.states + ((size_t)b * ns + si) * a.C;
     s0 = st[pl.c0];
     s1 = st[pl.c1];
   };
-  const int last = t0 < t1 ? (t1 - 1) / kTile * kTile : -1;
+  const int last = t0 < t1 ? (t1 - 1) / TILE * TILE : -1;
+  if (t0 < t1) fetch(last);
   int par = 0;
-  for (int tile = last; tile >= t0; tile -= kTile, par ^= 1) {
-    fetch(tile);
-    const int t = tile + pl.seg * kK;
-    float rho[kK][2], l2[kK][2], dec[kK][2], m[kK][2], sg[kK][2], u[kK][2], d[kK][2];
-    float L[2] = {0.f, 0.f}, H[2] = {0.f, 0.f}, F[2] = {lane < 32 ? s0 : 0.f, lane < 32 ? s1 : 0.f};
-    float st[2] = {s0, s1};
+  for (int tile = last; tile >= t0; tile -= TILE, par ^= 1) {
+    const int t = tile + pl.seg * K;
+    float rho[K][2], dec[K][2], m[K][2], sg[K][2], u[K][2], d[K][2];
+    float L[2] = {0.f, 0.f}, H[2] = {0.f, 0.f}, st[2] = {s0, s1};
 #pragma unroll
-    for (int k = 0; k < kK; ++k)
+    for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        factors<NORM>(rr.v[k].get(j), A2[j], rho[k][j], l2[k][j], dec[k][j], m[k][j]);
+        float l2;
+        factors<NORM>(rr.v[k].get(j), A2[j], rho[k][j], l2, dec[k][j], m[k][j]);
         sg[k][j] = GATE ? sigmoid_f(ri.v[k].get(j)) : 1.f;
         u[k][j] = rx.v[k].get(j) * sg[k][j];
         d[k][j] = rd.v[k].get(j);
-        if (tile + kTile > n && t + k >= n) {
-          dec[k][j] = 1.f;
-          rho[k][j] = m[k][j] = l2[k][j] = d[k][j] = u[k][j] = 0.f;
-        }
-        L[j] += l2[k][j];
+      }
+    fetch(max(tile - TILE, t0));
+    if (tile + TILE > n) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (t + k >= n) {
+            dec[k][j] = 1.f;
+            rho[k][j] = m[k][j] = d[k][j] = u[k][j] = 0.f;
+          }
+    }
+    float F[2] = {low ? st[0] : 0.f, low ? st[1] : 0.f};
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        L[j] += rho[k][j];
         F[j] = fmaf(dec[k][j], F[j], m[k][j] * u[k][j]);
       }
+    L[0] *= A2[0];
+    L[1] *= A2[1];
 #pragma unroll
-    for (int k = kK - 1; k >= 0; --k)
+    for (int k = K - 1; k >= 0; --k)
 #pragma unroll
       for (int j = 0; j < 2; ++j) H[j] = dec[k][j] * (H[j] + d[k][j]);
     // the state before the second half's tokens is the first half's end
     const float f0 = other_half(F[0]), f1 = other_half(F[1]);
-    float h[2] = {lane < 32 ? st[0] : f0, lane < 32 ? st[1] : f1};
-    float before[kK][2];
+    float h[2] = {low ? st[0] : f0, low ? st[1] : f1};
+    float before[K][2];
 #pragma unroll
-    for (int k = 0; k < kK; ++k)
+    for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         before[k][j] = h[j];
@@ -501,34 +549,44 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrArgs a, int ncb, i
       }
     float c[2], sA[2] = {0.f, 0.f};
     join<false>(L, H, carry, c, buf[par]);
-    const size_t at = ((size_t)b * a.T + t) * a.C + pl.c;
+    const size_t base = ((size_t)b * a.T + tile) * a.C;
+    const unsigned row = (unsigned)a.C * (unsigned)sizeof(Tin);
+    const unsigned o = row * (unsigned)(pl.seg * K) + pl.c * (unsigned)sizeof(Tin);
+    char *px = (char*)((Tin*)a.dx + base), *pr = (char*)((Tin*)a.dr + base),
+         *pi = GATE ? (char*)((Tin*)a.di + base) : nullptr;
+    auto tokens = [&](bool whole) {
 #pragma unroll
-    for (int k = kK - 1; k >= 0; --k) {
-      float ox[2], orr[2], oi[2];
+      for (int k = K - 1; k >= 0; --k) {
+        float ox[2], orr[2], oi[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float g = d[k][j] + c[j];
-        c[j] = dec[k][j] * g;
-        const float du = g * m[k][j];
-        ox[j] = du * sg[k][j];
-        oi[j] = du * u[k][j] * (1.f - sg[k][j]);
-        float dla = c[j] * before[k][j];
-        if constexpr (NORM) {
+        for (int j = 0; j < 2; ++j) {
+          const float g = d[k][j] + c[j];
+          c[j] = dec[k][j] * g;
+          const float du = g * m[k][j];
+          ox[j] = du * sg[k][j];
+          oi[j] = du * u[k][j] * (1.f - sg[k][j]);
+          float w = before[k][j];
           // (where a is one no gradient passes through m)
-          const float w = m[k][j] > 0.f
-                              ? dec[k][j] * u[k][j] * __builtin_amdgcn_rcpf(m[k][j])
-                              : 0.f;
-          dla = fmaf(-c[j], w, dla);
+          if constexpr (NORM) {
+            const float v = dec[k][j] * u[k][j] * __builtin_amdgcn_rcpf(m[k][j]);
+            w -= m[k][j] > 0.f ? v : 0.f;
+          }
+          const float dla = c[j] * w * rho[k][j];    // of A
+          orr[j] = dla * (kLn2 * A2[j]) * (1.f - rho[k][j]);
+          sA[j] += dla;
         }
-        orr[j] = dla * (kLn2 * l2[k][j]) * (1.f - rho[k][j]);
-        sA[j] = fmaf(dla, rho[k][j], sA[j]);
+        if (whole || t + k < n) {
+          const size_t at = (size_t)row * k + o;
+          store_pair<ALN>((Tin*)(px + at), ox[0], ox[1], pl.n);
+          store_pair<ALN>((Tin*)(pr + at), orr[0], orr[1], pl.n);
+          if constexpr (GATE) store_pair<ALN>((Tin*)(pi + at), oi[0], oi[1], pl.n);
+        }
       }
-      if (t + k < n) {
-        store_pair<ALN>((Tin*)a.dx + at + (size_t)k * a.C, ox[0], ox[1], pl.n);
-        store_pair<ALN>((Tin*)a.dr + at + (size_t)k * a.C, orr[0], orr[1], pl.n);
-        if constexpr (GATE)
-          store_pair<ALN>((Tin*)a.di + at + (size_t)k * a.C, oi[0], oi[1], pl.n);
-      }
+    };
+    if (tile + TILE <= n) {
+      tokens(true);
+    } else {
+      tokens(false);
     }
     dA[0] += (double)sA[0];
     dA[1] += (double)sA[1];
@@ -559,15 +617,17 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrArgs a, int ncb, i
 
 int col_blocks(int C) { return (C + kCols - 1) / kCols; }
 
+// Tokens a thread of the forward: 16 halve the joins, and in bf16 their registers leave
+// room for the tile ahead. Short sequences would leave waves of a tile empty.
+bool long_runs(int T, int bf16) { return bf16 && T >= 512; }
+
 // Segments of a sequence: one while the sequences and channels alone give two
-// workgroups a CU or nearly so; otherwise as many as reach that, of two tiles at
-// least.
+// workgroups a CU or nearly so; otherwise as many as reach that, of 256 tokens at least.
 int segments(int B, int T, int C) {
   const long long wgs = (long long)B * col_blocks(C);
   if (wgs >= 192 || wgs == 0) return 1;
-  const int tiles = (T + kTile - 1) / kTile;
   long long S = 512 / wgs;
-  if (S > tiles / 2) S = tiles / 2;
+  if (S > T / 256) S = T / 256;
   return S < 2 ? 1 : (int)S;
 }
 
@@ -578,23 +638,30 @@ size_t map_bytes(int B, int T, int C) {
 
 bool even(const void* p, size_t es) { return ((size_t)p & (2 * es - 1)) == 0; }
 
-template <typename Tin, bool ALN, bool GATE, bool NORM>
-int run_forward(const GlrArgs& a, hipStream_t s) {
+template <typename Tin, int K, bool ALN, bool GATE, bool NORM>
+int run_walk(const GlrArgs& a, hipStream_t s) {
   const int ncb = col_blocks(a.C), S = segments(a.B, a.T, a.C);
   if (!grid_ok((long long)ncb * a.B * S, kThreads)) return -1;
   if (S > 1) {
     const int tk = ktimer_before(s, "glr_part");
-    hipLaunchKernelGGL((glr_kernel<Tin, ALN, GATE, NORM, true>),
+    hipLaunchKernelGGL((glr_kernel<Tin, K, ALN, GATE, NORM, true>),
                        dim3((unsigned)ncb * a.B * (S - 1)), dim3(kThreads), 0, s, a, ncb, S);
     ktimer_after(s, tk);
     const int rc = (int)hipGetLastError();
     if (rc) return rc;
   }
   const int tk = ktimer_before(s, "glr");
-  hipLaunchKernelGGL((glr_kernel<Tin, ALN, GATE, NORM, false>), dim3((unsigned)ncb * a.B * S),
+  hipLaunchKernelGGL((glr_kernel<Tin, K, ALN, GATE, NORM, false>), dim3((unsigned)ncb * a.B * S),
                      dim3(kThreads), 0, s, a, ncb, S);
   ktimer_after(s, tk);
   return (int)hipGetLastError();
+}
+
+template <typename Tin, bool ALN, bool GATE, bool NORM>
+int run_forward(const GlrArgs& a, hipStream_t s) {
+  if constexpr (sizeof(Tin) == 2 && ALN)
+    if (long_runs(a.T, a.bf16)) return run_walk<Tin, 16, ALN, GATE, NORM>(a, s);
+  return run_walk<Tin, 8, ALN, GATE, NORM>(a, s);
 }
 
 template <typename Tin, bool ALN, bool GATE, bool NORM>

@@ -659,7 +659,7 @@ int residual_norm_backward(long long R, int C, int dtype, int res_dtype,
  *   y        [B,T,C] dtype (NULL: not written);  h_T [B,C] fp32 (NULL: not written)
  *   states   [B,ceil(T/16),C] fp32: h before tokens 0, 16, 32, ..., for the backward
  *            pass; those behind a sequence's end hold h_T (NULL: not written)
- * The state is held in 32 bits; what carries it over 8 tokens and more is formed
+ * The state is held in 32 bits; what carries it over more than 16 tokens is formed
  * from sums of log a, so that decays close to one keep their memory. C and token
  * strides up to 2^22 (more: OSDN_ERR_UNSUPPORTED). No output may overlap an input
  * (h_T not h0 either). workspace: glr_forward_workspace_bytes(...) bytes, 256-byte
