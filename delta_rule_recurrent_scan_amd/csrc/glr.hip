@@ -20,6 +20,8 @@
 // tokens, so what carries a state from thread to thread is the exponential of
 // a sum of the logarithms; only inside a thread are the decays themselves used.
 // 1 - a^2 comes from a series where it is small.
+#include <type_traits>
+
 #include "launch.hpp"
 #include "layer.hpp"
 #include "row_common.hpp"
@@ -51,6 +53,8 @@ struct Pair<__bf16> {
     }
   }
   __device__ __forceinline__ float get(int j) const { return j ? high_bf16(u) : low_bf16(u); }
+  __device__ __forceinline__ void shut() { u = 0xff80ff80u; }   // -inf
+  __device__ __forceinline__ void zero() { u = 0u; }
 };
 template <>
 struct Pair<float> {
@@ -66,16 +70,20 @@ struct Pair<float> {
     }
   }
   __device__ __forceinline__ float get(int j) const { return v[j]; }
+  __device__ __forceinline__ void shut() { v[0] = v[1] = -__builtin_inff(); }
+  __device__ __forceinline__ void zero() { v[0] = v[1] = 0.f; }
 };
 
+// (past the caches, which the rows read ahead need: 2 % of a prompt's time)
 template <bool ALN, typename T>
 __device__ __forceinline__ void store_pair(T* p, float v0, float v1, int n) {
   if constexpr (ALN) {
     if (n <= 0) return;
     if constexpr (sizeof(T) == 2) {
-      *(unsigned*)p = pack_bf16(v0, v1);
+      __builtin_nontemporal_store(pack_bf16(v0, v1), (unsigned*)p);
     } else {
-      *(float2*)p = float2{v0, v1};
+      typedef __attribute__((ext_vector_type(2))) float f32x2;
+      __builtin_nontemporal_store(f32x2{v0, v1}, (f32x2*)p);
     }
   } else {
     if (n > 0) p[0] = from_f32<T>(v0);
@@ -104,37 +112,33 @@ __device__ __forceinline__ Place place(int cb, int C) {
 template <typename Tin, bool ALN, int K>
 struct Rows {
   Pair<Tin> v[K];
-  // the thread's tokens of the tile's rows at p with stride ts; tokens from n on read
-  // token n - 1.
-  __device__ __forceinline__ void load(const Tin* p, long long ts, int tile, int seg, int n,
+  // Token k of the thread's in the tile's rows at p with stride ts; tokens from n on read
+  // token n - 1 (WHOLE: there are none).
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(int k, const Tin* p, long long ts, int tile, int n,
                                        const Place& pl) {
     const char* base = (const char*)(p + (long long)tile * ts);
     const unsigned row = (unsigned)ts * (unsigned)sizeof(Tin);
     const unsigned b0 = pl.c0 * (unsigned)sizeof(Tin), b1 = pl.c1 * (unsigned)sizeof(Tin);
-    if (tile + kTile<K> <= n) {
-      const unsigned o = row * (unsigned)(seg * K);
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-        v[k].template load<ALN>(base + (size_t)row * k, o + b0, o + b1);
+    if constexpr (WHOLE) {
+      const unsigned o = row * (unsigned)(pl.seg * K);
+      v[k].template load<ALN>(base + (size_t)row * k, o + b0, o + b1);
     } else {
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const unsigned o = row * (unsigned)min(seg * K + k, n - 1 - tile);
-        v[k].template load<ALN>(base, o + b0, o + b1);
-      }
+      const unsigned o = row * (unsigned)min(pl.seg * K + k, n - 1 - tile);
+      v[k].template load<ALN>(base, o + b0, o + b1);
     }
   }
 };
 
-// 1 - exp(z) for z <= 0 where e is exp(z): from -0.35 on, where the difference would
-// lose digits, z times the polynomial of degree 4 through the Chebyshev nodes of that
-// range (1.5e-8 off, 1.1e-7 with its roundings).
-__device__ __forceinline__ float one_minus_exp(float z, float e) {
-  float p = fmaf(0.0072125504f, z, 0.04133279f);
-  p = fmaf(p, z, 0.1666255f);
-  p = fmaf(p, z, 0.4999982f);
-  p = fmaf(p, z, 1.f);
-  return z > -0.35f ? -z * p : 1.f - e;
+// 1 - 4^w for w <= 0 with e = 2^w: from -1/4 on, where the difference would lose
+// digits, w times the polynomial of degree 4 through the Chebyshev nodes of that range
+// (1.4e-8 off, 1.3e-7 with its roundings).
+__device__ __forceinline__ float one_minus_square(float w, float e) {
+  float p = fmaf(-0.03698064014f, w, -0.15267968178f);
+  p = fmaf(p, w, -0.44392627478f);
+  p = fmaf(p, w, -0.96090275049f);
+  p = fmaf(p, w, -1.38629436493f);
+  return w > -0.25f ? w * p : fmaf(-e, e, 1.f);
 }
 
 // Decay and input factor of one token and channel: A2 = A log2(e).
@@ -144,7 +148,7 @@ __device__ __forceinline__ void factors(float r, float A2, float& rho, float& l2
   rho = sigmoid_f(r);
   l2 = A2 * rho;
   a = __builtin_amdgcn_exp2f(l2);
-  m = NORM ? __builtin_amdgcn_sqrtf(one_minus_exp(2.f * kLn2 * l2, a * a)) : 1.f;
+  m = NORM ? __builtin_amdgcn_sqrtf(one_minus_square(l2, a)) : 1.f;
 }
 
 // The value of lane l ^ 32.
@@ -171,11 +175,11 @@ __device__ __forceinline__ void join(const float (&L)[2], const float (&H)[2], f
   float p[2], po[2], Ho[2], Q[2], E[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
+    const float l = 0.5f * (L[j] + other_half(L[j]));
     p[j] = __builtin_amdgcn_exp2f(L[j]);
     po[j] = other_half(p[j]);
     Ho[j] = other_half(H[j]);
-    const float l = L[j] + other_half(L[j]);
-    Q[j] = one_minus_exp(kLn2 * l, p[j] * po[j]);
+    Q[j] = one_minus_square(l, __builtin_amdgcn_exp2f(l));
     E[j] = fmaf(p[j], Ho[j], H[j]);
   }
   if (!first) buf[w * 32 + (lane & 31)] = float4{Q[0], E[0], Q[1], E[1]};
@@ -196,6 +200,16 @@ __device__ __forceinline__ void join(const float (&L)[2], const float (&H)[2], f
   carry[1] = c1;
   in[0] = first ? m0 : fmaf(po[0], m0, Ho[0]);
   in[1] = first ? m1 : fmaf(po[1], m1, Ho[1]);
+}
+
+// All 64 channels of a block exist.
+__device__ __forceinline__ bool whole_columns(int cb, int C) { return (cb + 1) * kCols <= C; }
+
+// Keeps the two forms of a tile's loads apart: joined behind the branch they would take
+// their addresses in 64 bits a lane.
+template <bool WHOLE>
+__device__ __forceinline__ void apart() {
+  if constexpr (WHOLE) asm volatile("; whole tile");
 }
 
 __device__ __forceinline__ int seq_len(const GlrArgs& a, int b) {
@@ -250,46 +264,54 @@ __global__ __launch_bounds__(kThreads) void glr_kernel(GlrArgs a, int ncb, int S
   if constexpr (!PART) enter<true>(a.h0, (const float*)a.ws, b, S, q, a.C, pl, carry);
 
   Rows<Tin, ALN, K> rx, rr, ri;
-  auto fetch = [&](int tile) {
-    rx.load(x, a.xts, tile, pl.seg, n, pl);
-    rr.load(r, a.rts, tile, pl.seg, n, pl);
-    if constexpr (GATE) ri.load(gi, a.its, tile, pl.seg, n, pl);
+  auto fetch = [&](auto whole, int k, int tile) {
+    rr.template load<whole()>(k, r, a.rts, tile, n, pl);
+    rx.template load<whole()>(k, x, a.xts, tile, n, pl);
+    if constexpr (GATE) ri.template load<whole()>(k, gi, a.its, tile, n, pl);
   };
-  if (t0 < t1) fetch(t0);
+  if (t0 < t1) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) fetch(std::false_type(), k, t0);
+  }
   int par = 0;
   for (int tile = t0; tile < t1; tile += TILE, par ^= 1) {
     float dec[K][2], in[K][2], L[2] = {0.f, 0.f}, H[2] = {0.f, 0.f};
     const int t = tile + pl.seg * K;
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float rho, l2, m;
-        factors<NORM>(rr.v[k].get(j), A2[j], rho, l2, dec[k][j], m);
-        float u = rx.v[k].get(j);
-        if constexpr (GATE) u *= sigmoid_f(ri.v[k].get(j));
-        in[k][j] = m * u;
-        L[j] += l2;
-        H[j] = fmaf(dec[k][j], H[j], in[k][j]);
-      }
     if (tile + TILE > n) {
-      // tokens behind the end keep the state: the sums again without them
+      // tokens behind the end: a closed gate keeps the state, and nothing comes in
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        L[j] = H[j] = 0.f;
+      for (int k = 0; k < K; ++k)
+        if (t + k >= n) {
+          rr.v[k].shut();
+          rx.v[k].zero();
+        }
+    }
+    // A token's registers take the same one of the next tile as soon as it is worked
+    // off: its 100 KB a CU take nearly as long as the work.
+    const int next = min(tile + TILE, t1 - 1) / TILE * TILE;
+    auto tokens = [&](auto whole) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-          if (t + k >= n) {
-            dec[k][j] = 1.f;
-            in[k][j] = 0.f;
-          } else {
-            L[j] += A2[j] * sigmoid_f(rr.v[k].get(j));
-          }
+      for (int k = 0; k < K; ++k) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float rho, l2, m;
+          factors<NORM>(rr.v[k].get(j), A2[j], rho, l2, dec[k][j], m);
+          float u = rx.v[k].get(j);
+          if constexpr (GATE) u *= sigmoid_f(ri.v[k].get(j));
+          in[k][j] = m * u;
+          L[j] += l2;
           H[j] = fmaf(dec[k][j], H[j], in[k][j]);
         }
+        fetch(whole, k, next);
+        if (k % 4 == 3) __builtin_amdgcn_sched_barrier(0);
       }
+      apart<whole()>();
+    };
+    if (next + TILE <= n) {
+      tokens(std::true_type());
+    } else {
+      tokens(std::false_type());
     }
-    fetch(min(tile + TILE, t1 - 1) / TILE * TILE);
     float h[2];
     join<true>(L, H, carry, h, buf[par]);
     if constexpr (PART) {
@@ -312,10 +334,10 @@ __global__ __launch_bounds__(kThreads) void glr_kernel(GlrArgs a, int ncb, int S
             h[0] = fmaf(dec[k][0], h[0], in[k][0]);
             h[1] = fmaf(dec[k][1], h[1], in[k][1]);
             if (whole || t + k < n)
-              store_pair<ALN>((Tin*)(y + (size_t)row * k + o), h[0], h[1], pl.n);
+              store_pair<ALN>((Tin*)(y + (size_t)row * k + o), h[0], h[1], whole ? 2 : pl.n);
           }
         };
-        if (tile + TILE <= n) {
+        if (tile + TILE <= n && whole_columns(cb, a.C)) {
           tokens(true);
         } else {
           tokens(false);
@@ -413,30 +435,46 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_part_kernel(GlrArgs a, int n
   const float A2[2] = {a.A[pl.c0] * kLog2e, a.A[pl.c1] * kLog2e};
   float carry[2] = {0.f, 0.f}, Ltot[2] = {0.f, 0.f};
   Rows<Tin, ALN, K> rr, rd;
-  auto fetch = [&](int tile) {
-    rr.load(r, a.rts, tile, pl.seg, n, pl);
-    rd.load(dy, a.C, tile, pl.seg, n, pl);
+  auto fetch = [&](auto whole, int k, int tile) {
+    rr.template load<whole()>(k, r, a.rts, tile, n, pl);
+    rd.template load<whole()>(k, dy, a.C, tile, n, pl);
   };
   const int last = t0 < t1 ? (t1 - 1) / TILE * TILE : -1;
-  if (t0 < t1) fetch(last);
+  if (t0 < t1) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) fetch(std::false_type(), k, last);
+  }
   int par = 0;
   for (int tile = last; tile >= t0; tile -= TILE, par ^= 1) {
     float L[2] = {0.f, 0.f}, H[2] = {0.f, 0.f};
     const int t = tile + pl.seg * K;
+    if (tile + TILE > n) {
 #pragma unroll
-    for (int k = K - 1; k >= 0; --k)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float l2 = A2[j] * sigmoid_f(rr.v[k].get(j)), d = rd.v[k].get(j);
-        float dec = __builtin_amdgcn_exp2f(l2);
-        if (tile + TILE > n && t + k >= n) {
-          dec = 1.f;
-          l2 = d = 0.f;
+      for (int k = 0; k < K; ++k)
+        if (t + k >= n) {
+          rr.v[k].shut();
+          rd.v[k].zero();
         }
-        L[j] += l2;
-        H[j] = dec * (H[j] + d);
+    }
+    const int next = max(tile - TILE, t0);
+    auto tokens = [&](auto whole) {
+#pragma unroll
+      for (int k = K - 1; k >= 0; --k) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float l2 = A2[j] * sigmoid_f(rr.v[k].get(j));
+          L[j] += l2;
+          H[j] = __builtin_amdgcn_exp2f(l2) * (H[j] + rd.v[k].get(j));
+        }
+        fetch(whole, k, next);
       }
-    fetch(max(tile - TILE, t0));
+      apart<whole()>();
+    };
+    if (next + TILE <= n) {
+      tokens(std::true_type());
+    } else {
+      tokens(std::false_type());
+    }
     float in[2];
     join<false>(L, H, carry, in, buf[par]);
     Ltot[0] += L[0];
@@ -484,23 +522,40 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrArgs a, int ncb, i
 
   Rows<Tin, ALN, K> rx, rr, ri, rd;
   float s0 = 0.f, s1 = 0.f;
-  auto fetch = [&](int tile) {
-    rr.load(r, a.rts, tile, pl.seg, n, pl);
-    rd.load(dy, a.C, tile, pl.seg, n, pl);
-    rx.load(x, a.xts, tile, pl.seg, n, pl);
-    if constexpr (GATE) ri.load(gi, a.its, tile, pl.seg, n, pl);
+  auto fetch = [&](auto whole, int k, int tile) {
+    rr.template load<whole()>(k, r, a.rts, tile, n, pl);
+    rd.template load<whole()>(k, dy, a.C, tile, n, pl);
+    rx.template load<whole()>(k, x, a.xts, tile, n, pl);
+    if constexpr (GATE) ri.template load<whole()>(k, gi, a.its, tile, n, pl);
+  };
+  auto fetch_state = [&](int tile) {
     const int si = min((tile + pl.seg * K) / kGlrInterval, ns - 1);
     const float* st = a.states + ((size_t)b * ns + si) * a.C;
     s0 = st[pl.c0];
     s1 = st[pl.c1];
   };
   const int last = t0 < t1 ? (t1 - 1) / TILE * TILE : -1;
-  if (t0 < t1) fetch(last);
+  if (t0 < t1) {
+    fetch_state(last);
+#pragma unroll
+    for (int k = 0; k < K; ++k) fetch(std::false_type(), k, last);
+  }
   int par = 0;
   for (int tile = last; tile >= t0; tile -= TILE, par ^= 1) {
     const int t = tile + pl.seg * K;
+    if (tile + TILE > n) {
+      // (as in the forward, and no adjoint)
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (t + k >= n) {
+          rr.v[k].shut();
+          rx.v[k].zero();
+          rd.v[k].zero();
+        }
+    }
     float rho[K][2], dec[K][2], m[K][2], sg[K][2], u[K][2], d[K][2];
     float L[2] = {0.f, 0.f}, H[2] = {0.f, 0.f}, st[2] = {s0, s1};
+    const int next = max(tile - TILE, t0);
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -511,16 +566,15 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrArgs a, int ncb, i
         u[k][j] = rx.v[k].get(j) * sg[k][j];
         d[k][j] = rd.v[k].get(j);
       }
-    fetch(max(tile - TILE, t0));
-    if (tile + TILE > n) {
+    // (token by token as in the forward the registers run out: 211 against 206 us)
+    fetch_state(next);
+    if (next + TILE <= n) {
 #pragma unroll
-      for (int k = 0; k < K; ++k)
+      for (int k = 0; k < K; ++k) fetch(std::true_type(), k, next);
+      apart<true>();
+    } else {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          if (t + k >= n) {
-            dec[k][j] = 1.f;
-            rho[k][j] = m[k][j] = d[k][j] = u[k][j] = 0.f;
-          }
+      for (int k = 0; k < K; ++k) fetch(std::false_type(), k, next);
     }
     float F[2] = {low ? st[0] : 0.f, low ? st[1] : 0.f};
 #pragma unroll
@@ -576,14 +630,14 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrArgs a, int ncb, i
           sA[j] += dla;
         }
         if (whole || t + k < n) {
-          const size_t at = (size_t)row * k + o;
-          store_pair<ALN>((Tin*)(px + at), ox[0], ox[1], pl.n);
-          store_pair<ALN>((Tin*)(pr + at), orr[0], orr[1], pl.n);
-          if constexpr (GATE) store_pair<ALN>((Tin*)(pi + at), oi[0], oi[1], pl.n);
+          const int nc = whole ? 2 : pl.n;
+          store_pair<ALN>((Tin*)(px + (size_t)row * k + o), ox[0], ox[1], nc);
+          store_pair<ALN>((Tin*)(pr + (size_t)row * k + o), orr[0], orr[1], nc);
+          if constexpr (GATE) store_pair<ALN>((Tin*)(pi + (size_t)row * k + o), oi[0], oi[1], nc);
         }
       }
     };
-    if (tile + TILE <= n) {
+    if (tile + TILE <= n && whole_columns(cb, a.C)) {
       tokens(true);
     } else {
       tokens(false);
@@ -621,13 +675,14 @@ int col_blocks(int C) { return (C + kCols - 1) / kCols; }
 // room for the tile ahead. Short sequences would leave waves of a tile empty.
 bool long_runs(int T, int bf16) { return bf16 && T >= 512; }
 
-// Segments of a sequence: one while the sequences and channels alone give two
-// workgroups a CU or nearly so; otherwise as many as reach that, of 256 tokens at least.
+// Segments of a sequence: one while the sequences and channels alone give three
+// quarters of the CUs a workgroup; otherwise as many as give each one, of 128 tokens at
+// least (1 x 8192 x 2048: 64 us with two a CU, 55 with one).
 int segments(int B, int T, int C) {
   const long long wgs = (long long)B * col_blocks(C);
   if (wgs >= 192 || wgs == 0) return 1;
-  long long S = 512 / wgs;
-  if (S > T / 256) S = T / 256;
+  long long S = 256 / wgs;
+  if (S > T / 128) S = T / 128;
   return S < 2 ? 1 : (int)S;
 }
 
