@@ -13,15 +13,23 @@ namespace osdn {
 namespace ffn {
 namespace {
 
+// dg and du in rows of Fp elements, zeros behind F.
 template <typename T>
-__global__ __launch_bounds__(256) void ffn_grad_kernel(FfnArgs a, long long n, T* dg, T* du) {
+__global__ __launch_bounds__(256) void ffn_grad_kernel(FfnArgs a) {
   const long long at = (blockIdx.x * 256LL + threadIdx.x) * 8;
-  if (at >= n) return;
-  const int m = (int)min(8LL, n - at);
+  if (at >= a.R * a.Fp) return;
+  long long from = at;
+  int m = 8;
+  if (a.Fp != a.F) {
+    const long long r = at / a.Fp;
+    const int f = (int)(at % a.Fp);
+    from = r * a.F + f;
+    m = min(8, a.F - f);
+  }
   float g[8], u[8], d[8];
-  load_v<false, 8>((const T*)a.gate + at, m, g);
-  load_v<false, 8>((const T*)a.up + at, m, u);
-  load_v<false, 8>((const T*)a.dh + at, m, d);
+  load_v<false, 8>((const T*)a.gate + from, m, g);
+  load_v<false, 8>((const T*)a.up + from, m, u);
+  load_v<false, 8>((const T*)a.dh + from, m, d);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float f, s;
@@ -29,8 +37,8 @@ __global__ __launch_bounds__(256) void ffn_grad_kernel(FfnArgs a, long long n, T
     g[i] = d[i] * u[i] * s;
     u[i] = d[i] * f;
   }
-  store_v<false, 8>(dg + at, m, g);
-  store_v<false, 8>(du + at, m, u);
+  store_v<true, 8>((T*)a.dg + at, 8, g);
+  store_v<true, 8>((T*)a.du + at, 8, u);
 }
 
 // A wave's i-th 16 rows, from m0 on of M, to columns from n0 on of N.
@@ -56,24 +64,25 @@ struct Input {
   typedef Stage<T, S::BN, false, S::NT> StageB;
   const T *dg, *du, *wg, *wu;
   long long m0;
-  int n0, C, F, rows, cols, full;
+  int n0, C, F, Fp, rows, cols, full;
   unsigned oa[StageA::PER], ob[StageB::PER];
   uint4 va[StageA::PER], vb[StageB::PER];
 
   __device__ __forceinline__ void place(const FfnArgs& a, const Item& it) {
     m0 = (long long)it.m * S::BM;
     n0 = it.n * S::BN;
-    C = a.C;
+    C = a.Cp;
     F = a.F;
-    dg = (const T*)a.dg + m0 * a.F;
-    du = (const T*)a.du + m0 * a.F;
+    Fp = a.Fp;
+    dg = (const T*)a.dg + m0 * Fp;
+    du = (const T*)a.du + m0 * Fp;
     wg = (const T*)a.wg + n0;
     wu = (const T*)a.wu + n0;
     rows = (int)min((long long)S::BM, a.R - m0);
-    cols = min(S::BN, a.C - n0);
+    cols = min(S::BN, C - n0);
     full = 2 * (a.F / kTileK<T>);
-    StageA::offsets(oa, a.F, rows);
-    StageB::offsets(ob, a.C, cols);
+    StageA::offsets(oa, Fp, rows);
+    StageB::offsets(ob, C, cols);
   }
   __device__ __forceinline__ int along(int t, bool& second) const {
     const int half = full / 2;
@@ -93,7 +102,7 @@ struct Input {
   __device__ __forceinline__ void fetch(int t) {
     bool second;
     const int k = along(t, second);
-    StageA::fetch(va, (second ? du : dg) + k, F, rows, F - k);
+    StageA::fetch(va, (second ? du : dg) + k, Fp, rows, F - k);
     StageB::fetch(vb, (second ? wu : wg) + (long long)k * C, C, cols, F - k);
   }
   __device__ __forceinline__ void put(char* a, char* b) const {
@@ -127,16 +136,16 @@ struct Weight {
     const bool second = it.m >= tm;
     m0 = (it.m - (second ? tm : 0)) * S::BM;
     n0 = it.n * S::BN;
-    F = a.F;
+    F = a.Fp;
     R = a.R;
     xs = a.xs;
     full = (int)(a.R / kTileK<T>);
     d = (const T*)(second ? a.du : a.dg) + m0;
     x = (const T*)a.x + n0;
     out = (T*)(second ? a.dwu : a.dwg);
-    rows = min(S::BM, a.F - m0);
-    cols = min(S::BN, a.C - n0);
-    StageA::offsets(oa, a.F, rows);
+    rows = min(S::BM, F - m0);
+    cols = min(S::BN, a.Cp - n0);
+    StageA::offsets(oa, F, rows);
     StageB::offsets(ob, a.xs, cols);
   }
   __device__ __forceinline__ void direct_a(int t, char* a) const {
@@ -168,40 +177,30 @@ struct Weight {
 // Launches
 // ---------------------------------------------------------------------------
 
-bool on16(const void* p) { return ((size_t)p & 15) == 0; }
-
-bool units(int C, int F, int bf16) {
-  const int u = bf16 ? 8 : 4;
-  return C % u == 0 && F % u == 0;
-}
 // (tiles of k: whole ones of each half, then the ends)
 bool input_plan(Plan& p, long long R, int C, int F, int bf16) {
   const long long kt = bf16 ? kTileK<__bf16> : kTileK<float>;
-  return make_plan(p, 1, R, C, 2 * ((F + kt - 1) / kt) * kt, bf16, units(C, F, bf16));
+  return make_plan(p, 1, R, C, 2 * ((F + kt - 1) / kt) * kt, bf16);
 }
 bool weight_plan(Plan& p, long long R, int C, int F, int bf16) {
-  return make_plan(p, 2, F, C, R, bf16, units(C, F, bf16));
+  return make_plan(p, 2, F, C, R, bf16);
 }
 
-size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
-size_t half_bytes(long long R, int F, int bf16) { return round256((size_t)R * F * (bf16 ? 2 : 4)); }
+size_t half_bytes(long long R, int F, int bf16) {
+  return round256((size_t)R * whole_eights(F) * (bf16 ? 2 : 4));
+}
 
 template <typename T, class S>
 int run_shape(const FfnArgs& a, const Plan& p, bool weights, hipStream_t s) {
-  if (!weights) {
-    const bool direct = on16(a.wg) && on16(a.wu) && units(a.C, a.F, a.bf16);
-    return launch_products<T, S, Input<T, S>>(a, p, direct, "ffn_dx", "ffn_dx_join", s);
-  }
-  const bool direct = on16(a.x) && a.xs % kUnit<T> == 0 && units(a.C, a.F, a.bf16);
-  return launch_products<T, S, Weight<T, S>>(a, p, direct, "ffn_dw", "ffn_dw_join", s);
+  return weights ? launch_products<T, S, Weight<T, S>>(a, p, "ffn_dw", "ffn_dw_join", s)
+                 : launch_products<T, S, Input<T, S>>(a, p, "ffn_dx", "ffn_dx_join", s);
 }
 
 template <typename T>
 int run_plan(const FfnArgs& a, const Plan& p, bool weights, hipStream_t s) {
-  switch (p.shape) {
-    case 0: return run_shape<T, Large>(a, p, weights, s);
-    case 1: return run_shape<T, Middle>(a, p, weights, s);
-  }
+  if constexpr (sizeof(T) == 2)
+    if (p.shape == 0) return run_shape<T, Large>(a, p, weights, s);
+  if (p.shape == 1) return run_shape<T, Middle>(a, p, weights, s);
   return run_shape<T, Small>(a, p, weights, s);
 }
 
@@ -211,17 +210,17 @@ int run(const FfnArgs& a0, hipStream_t s) {
   const size_t half = half_bytes(a.R, a.F, a.bf16);
   a.dg = a.ws;
   a.du = (char*)a.ws + half;
-  a.parts = (float*)((char*)a.ws + 2 * half);
-  const long long n = a.R * a.F;
+  char* room = (char*)a.ws + 2 * half;
   Plan x{}, w{};
+  const long long wgs = (a.R * whole_eights(a.F) + 2047) / 2048;
   if ((a.R > 0 && !input_plan(x, a.R, a.C, a.F, a.bf16)) ||
-      (a.F > 0 && !weight_plan(w, a.R, a.C, a.F, a.bf16)) || !grid_ok((n + 2047) / 2048, 256))
+      (a.F > 0 && !weight_plan(w, a.R, a.C, a.F, a.bf16)) || !grid_ok(wgs, 256))
     return -1;
-  int rc = 0;
-  if (n > 0) {
+  int rc = align_operands(a, room, s);
+  a.parts = (float*)(room + aligned_bytes(a.R, a.C, a.F, a.bf16));
+  if (!rc && wgs > 0) {
     const int tk = ktimer_before(s, "ffn_grad");
-    hipLaunchKernelGGL((ffn_grad_kernel<T>), dim3((unsigned)((n + 2047) / 2048)), dim3(256), 0, s,
-                       a, n, (T*)a.dg, (T*)a.du);
+    hipLaunchKernelGGL((ffn_grad_kernel<T>), dim3((unsigned)wgs), dim3(256), 0, s, a);
     ktimer_after(s, tk);
     rc = (int)hipGetLastError();
   }
@@ -237,7 +236,7 @@ size_t ffn_backward_ws(long long R, int C, int F, int bf16) {
   ffn::Plan p;
   const size_t px = R > 0 && C > 0 && ffn::input_plan(p, R, C, F, bf16) ? ffn::parts_bytes(p) : 0;
   const size_t pw = F > 0 && C > 0 && ffn::weight_plan(p, R, C, F, bf16) ? ffn::parts_bytes(p) : 0;
-  return 2 * ffn::half_bytes(R, F, bf16) + (px > pw ? px : pw);
+  return 2 * ffn::half_bytes(R, F, bf16) + ffn::aligned_bytes(R, C, F, bf16) + (px > pw ? px : pw);
 }
 
 int launch_ffn_backward(const FfnArgs& a, hipStream_t s) {

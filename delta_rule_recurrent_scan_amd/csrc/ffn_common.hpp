@@ -10,9 +10,11 @@
 // MN-major row k at u ^ 2 f(k). MN-major bf16 is read by the LDS transpose load,
 // which gives a lane the run of k that a K-major row would.
 //
-// Operands whose rows do not start on 16 bytes, and the last part of k, go through
-// registers, with zeros behind the end of k. Rows behind m and n repeat the last
-// one; their products are not stored.
+// The last part of k goes through registers, with zeros behind the end of k. Rows
+// behind m and n repeat the last one; their products are not stored. All rows start on
+// 16 bytes and hold whole eights of elements: operands that do not are first copied so
+// (777 x 1021 x 2001 in bf16: with rows of any alignment through registers the products
+// took 40 to 97 us).
 #pragma once
 
 #include "device_common.hpp"
@@ -251,7 +253,7 @@ __device__ __forceinline__ void wait_loads() {
 // never run empty. A wave works off a tile in four parts (two steps of k, two halves of
 // its rows) and fetches each part's operands while the one before is multiplied; the
 // barrier stands before a tile's last part, whose operands are in registers.
-template <typename T, class S, class Op, bool DIRECT>
+template <typename T, class S, class Op>
 __device__ __forceinline__ void products(const FfnArgs& a, const Plan& p) {
   constexpr int BUF = (S::BM > S::BN ? S::BM : S::BN) * kRowBytes;
   __shared__ __attribute__((aligned(1024))) char u0[BUF], u1[BUF], u2[BUF], u3[BUF], u4[BUF];
@@ -280,7 +282,7 @@ __device__ __forceinline__ void products(const FfnArgs& a, const Plan& p) {
   Op op;
   op.place(a, it);
   int t = it.t0;
-  if constexpr (DIRECT) {
+  {
     const int tf = min(it.t1, op.full);
     uint4 fa[2][HM], fb[2][S::TN];
     auto read_b = [&](uint4 (&f)[S::TN], const char* lb, int step) {
@@ -410,9 +412,9 @@ __device__ __forceinline__ void join_parts(const FfnArgs& a, const Plan& p) {
   op.store_row(a, i, row);
 }
 
-template <typename T, class S, class Op, bool DIRECT>
+template <typename T, class S, class Op>
 __global__ __launch_bounds__(S::NT) void ffn_kernel(FfnArgs a, Plan p) {
-  products<T, S, Op, DIRECT>(a, p);
+  products<T, S, Op>(a, p);
 }
 template <class S, class Op>
 __global__ __launch_bounds__(S::NT) void ffn_join_kernel(FfnArgs a, Plan p) {
@@ -420,14 +422,10 @@ __global__ __launch_bounds__(S::NT) void ffn_join_kernel(FfnArgs a, Plan p) {
 }
 
 template <typename T, class S, class Op>
-int launch_products(const FfnArgs& a, const Plan& p, bool direct, const char* name,
-                    const char* join_name, hipStream_t s) {
+int launch_products(const FfnArgs& a, const Plan& p, const char* name, const char* join_name,
+                    hipStream_t s) {
   int tk = ktimer_before(s, name);
-  if (direct) {
-    hipLaunchKernelGGL((ffn_kernel<T, S, Op, true>), dim3(p.items()), dim3(S::NT), 0, s, a, p);
-  } else {
-    hipLaunchKernelGGL((ffn_kernel<T, S, Op, false>), dim3(p.items()), dim3(S::NT), 0, s, a, p);
-  }
+  hipLaunchKernelGGL((ffn_kernel<T, S, Op>), dim3(p.items()), dim3(S::NT), 0, s, a, p);
   ktimer_after(s, tk);
   const int rc = (int)hipGetLastError();
   if (rc || p.splits == 1) return rc;
@@ -498,8 +496,17 @@ __device__ __forceinline__ void activated(float g, int act, float& f, float& slo
 }
 
 // The plan of `sets` products of M x N over K, and the bytes of its parts.
-bool make_plan(Plan& p, int sets, long long M, long long N, long long K, int bf16, bool direct);
+bool make_plan(Plan& p, int sets, long long M, long long N, long long K, int bf16);
 size_t parts_bytes(const Plan& p);
+
+inline int whole_eights(int n) { return (n + 7) / 8 * 8; }
+inline size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+inline bool on16(const void* p) { return ((size_t)p & 15) == 0; }
+
+// Bytes of ws behind `used` that copies of x and the weights may take, and the copies
+// made where they are needed: a's pointers and strides are then those of the products.
+size_t aligned_bytes(long long R, int C, int F, int bf16);
+int align_operands(FfnArgs& a, char* room, hipStream_t s);
 
 }  // namespace ffn
 }  // namespace osdn

@@ -33,15 +33,15 @@ struct Forward {
     m0 = (long long)it.m * S::BM;
     f0 = it.n * BF;
     xs = a.xs;
-    C = a.C;
+    C = a.Cp;
     x = (const T*)a.x + m0 * a.xs;
-    wg = (const T*)a.wg + (long long)f0 * a.C;
-    wu = (const T*)a.wu + (long long)f0 * a.C;
+    wg = (const T*)a.wg + (long long)f0 * C;
+    wu = (const T*)a.wu + (long long)f0 * C;
     rows = (int)min((long long)S::BM, a.R - m0);
     cols = min(BF, a.F - f0);
-    full = a.C / kTileK<T>;
+    full = C / kTileK<T>;
     StageA::offsets(oa, a.xs, rows);
-    StageB::offsets(ob, a.C, cols);
+    StageB::offsets(ob, C, cols);
   }
   __device__ __forceinline__ void direct_a(int t, char* a) const {
     StageA::direct(a, x + t * kTileK<T>, oa);
@@ -196,8 +196,6 @@ __global__ __launch_bounds__(64 * kRowsWaves) void ffn_rows_kernel(FfnArgs a) {
 
 constexpr int kFewRows = 64;
 
-bool on16(const void* p) { return ((size_t)p & 15) == 0; }
-
 template <typename T, int NR>
 int run_rows(const FfnArgs& a, hipStream_t s) {
   const int tk = ktimer_before(s, "ffn_rows");
@@ -209,14 +207,11 @@ int run_rows(const FfnArgs& a, hipStream_t s) {
 
 template <typename T, class S>
 int run_shape(const FfnArgs& a, const Plan& p, hipStream_t s) {
-  const size_t es = sizeof(T);
-  const bool direct = on16(a.x) && on16(a.wg) && on16(a.wu) && a.xs * es % 16 == 0 &&
-                      a.C * es % 16 == 0;
-  return launch_products<T, S, Forward<T, S>>(a, p, direct, "ffn", "ffn_join", s);
+  return launch_products<T, S, Forward<T, S>>(a, p, "ffn", "ffn_join", s);
 }
 
 bool forward_plan(Plan& p, long long R, int C, int F, int bf16) {
-  return make_plan(p, 1, R, 2LL * F, C, bf16, C % (bf16 ? 8 : 4) == 0);
+  return make_plan(p, 1, R, 2LL * F, whole_eights(C), bf16);
 }
 
 template <typename T>
@@ -228,42 +223,52 @@ int run(const FfnArgs& a, hipStream_t s) {
   if (!forward_plan(p, a.R, a.C, a.F, a.bf16)) return -1;
   FfnArgs b = a;
   b.parts = (float*)a.ws;
-  switch (p.shape) {
-    case 0: return run_shape<T, Large>(b, p, s);
-    case 1: return run_shape<T, Middle>(b, p, s);
-  }
+  const int rc = align_operands(b, (char*)a.ws + round256(parts_bytes(p)), s);
+  if (rc) return rc;
+  if constexpr (sizeof(T) == 2)
+    if (p.shape == 0) return run_shape<T, Large>(b, p, s);
+  if (p.shape == 1) return run_shape<T, Middle>(b, p, s);
   return run_shape<T, SmallPairs>(b, p, s);
 }
 
 }  // namespace
 
-// What a tile of k costs a workgroup that has a CU to itself or shares it with as many
-// as fit, in microseconds, by shape: bf16 is bound by operands from L2 and LDS, the more
-// the smaller the tile; fp32 by the matrix units.
-bool make_plan(Plan& best, int sets, long long M, long long N, long long K, int bf16,
-               bool direct) {
+// Microseconds of a tile of k, by shape: of one workgroup that has its CU to itself
+// (bound by the way of its operands in bf16, by the matrix units in fp32), and the CU's
+// share of each where as many as fit run at once. Measured with one, two and four
+// workgroups a CU at 176 tiles of k (bf16) and 128 (fp32).
+struct Cost {
+  double alone[3], share[3], each[3];   // each: start and end of a tile
+};
+constexpr Cost kBf16 = {{1.46, 0.73, 0.45}, {1.46, 0.575, 0.25}, {8.0, 4.0, 1.0}};
+constexpr Cost kF32 = {{0.0, 2.5, 0.91}, {0.0, 1.95, 0.64}, {0.0, 4.0, 1.0}};
+
+bool make_plan(Plan& best, int sets, long long M, long long N, long long K, int bf16) {
   const int bm[] = {256, 128, 64}, kt = bf16 ? kTileK<__bf16> : kTileK<float>;
   const int at_once[] = {1, 2, 4};
-  const double cost[2][3] = {{7.0, 1.75, 0.45}, {1.46, 0.5, 0.2}};
+  const Cost& c = bf16 ? kBf16 : kF32;
   const long long nt = K > 0 ? (K + kt - 1) / kt : 1;
   double least = 1e300;
   if (nt > (1 << 26)) return false;
-  for (int k = direct ? 0 : 1; k < 3; ++k) {
+  // (large fp32 tiles gain nothing: the middle ones have the matrix units busy)
+  for (int k = bf16 ? 0 : 1; k < 3; ++k) {
     const long long tm = sets * ((M + bm[k] - 1) / bm[k]), tn = (N + bm[k] - 1) / bm[k];
     const long long tiles = tm * tn, full = 256 * at_once[k];
     if (!grid_ok(16 * tiles, 512)) continue;
+    // workgroups of `len` tiles of k each
+    auto time = [&](long long wgs, long long len) {
+      const long long a_cu = (wgs + 255) / 256, rem = a_cu % at_once[k];
+      const double one = at_once[k] * c.share[k] * len + c.each[k];
+      const double last = rem * c.share[k] > c.alone[k] ? rem * c.share[k] : c.alone[k];
+      return (double)(a_cu / at_once[k]) * one + (rem ? last * len + c.each[k] : 0.0);
+    };
     const long long whole = tiles / full * full, rest = tiles - whole;
     for (int s = 1; s <= 16 && (s == 1 || (rest > 0 && nt / s >= 4)); ++s) {
       const long long per = (nt + s - 1) / s;
       if ((nt + per - 1) / per != s) continue;     // (no empty part)
-      // a round costs its tiles of k and the start and end of a tile; one of fewer
-      // workgroups than CUs runs each of them alone
-      const double each = bf16 ? 8 : 2, wgs = (double)(rest * s);
-      const double last = wgs <= 256 ? (wgs > 0) : at_once[k] * (double)((rest * s + full - 1) / full);
-      double t = cost[bf16][k] * (at_once[k] * (double)(whole / full) * (nt + each) +
-                                  last * (per + each));
+      double t = time(whole, nt) + time(rest * s, per);
       // parts written and read, and the launch that adds them
-      if (s > 1) t += 5 + wgs * bm[k] * bm[k] * 8 / 4e6;
+      if (s > 1) t += 6.5 + (double)(rest * s) * bm[k] * bm[k] * 8 / 4e6;
       if (t < least) {
         least = t;
         best = Plan{k, (int)tm, (int)tn, (int)nt, (int)whole, s, (int)per};
@@ -271,6 +276,63 @@ bool make_plan(Plan& best, int sets, long long M, long long N, long long K, int 
     }
   }
   return least < 1e300;
+}
+
+namespace {
+
+// rows of C elements to rows of Cp, zeros behind C.
+template <typename T>
+__global__ __launch_bounds__(256) void ffn_pad_kernel(const T* in, long long ld, long long rows,
+                                                      int C, int Cp, T* out) {
+  const unsigned per = Cp / 8;
+  const long long at = blockIdx.x * 256LL + threadIdx.x;
+  const long long r = at / per;
+  if (r >= rows) return;
+  const int c = (int)(at % per) * 8;
+  float v[8];
+  load_v<false, 8>(in + r * ld + c, C - c, v);
+  store_v<true, 8>(out + r * Cp + c, 8, v);
+}
+
+template <typename T>
+int pad(const void*& p, long long ld, long long rows, int C, int Cp, char*& room, hipStream_t s) {
+  const long long wgs = (rows * (Cp / 8) + 255) / 256;
+  if (!grid_ok(wgs, 256)) return -1;
+  const int tk = ktimer_before(s, "ffn_pad");
+  hipLaunchKernelGGL((ffn_pad_kernel<T>), dim3((unsigned)wgs), dim3(256), 0, s, (const T*)p, ld,
+                     rows, C, Cp, (T*)room);
+  ktimer_after(s, tk);
+  p = room;
+  room += round256((size_t)rows * Cp * sizeof(T));
+  return (int)hipGetLastError();
+}
+
+template <typename T>
+int align_t(FfnArgs& a, char* room, hipStream_t s) {
+  a.Cp = whole_eights(a.C);
+  a.Fp = whole_eights(a.F);
+  int rc = 0;
+  if (a.R > 0 && a.C > 0 &&
+      (a.Cp != a.C || !on16(a.x) || a.xs * (long long)sizeof(T) % 16 != 0)) {
+    rc = pad<T>(a.x, a.xs, a.R, a.C, a.Cp, room, s);
+    a.xs = a.Cp;
+  }
+  if (a.Cp != a.C && a.F > 0 && a.C > 0) {
+    if (!rc) rc = pad<T>(a.wg, a.C, a.F, a.C, a.Cp, room, s);
+    if (!rc) rc = pad<T>(a.wu, a.C, a.F, a.C, a.Cp, room, s);
+  }
+  return rc;
+}
+
+}  // namespace
+
+size_t aligned_bytes(long long R, int C, int F, int bf16) {
+  const size_t row = (size_t)whole_eights(C) * (bf16 ? 2 : 4);
+  return round256(R * row) + (C % 8 ? 2 * round256(F * row) : 0);
+}
+
+int align_operands(FfnArgs& a, char* room, hipStream_t s) {
+  return a.bf16 ? align_t<__bf16>(a, room, s) : align_t<float>(a, room, s);
 }
 
 size_t parts_bytes(const Plan& p) {
@@ -283,7 +345,8 @@ size_t parts_bytes(const Plan& p) {
 size_t ffn_forward_ws(long long R, int C, int F, int bf16) {
   if (R <= ffn::kFewRows) return 0;
   ffn::Plan p;
-  return F > 0 && ffn::forward_plan(p, R, C, F, bf16) ? ffn::parts_bytes(p) : 0;
+  if (F == 0 || !ffn::forward_plan(p, R, C, F, bf16)) return 0;
+  return ffn::round256(ffn::parts_bytes(p)) + ffn::aligned_bytes(R, C, F, bf16);
 }
 
 int launch_ffn_forward(const FfnArgs& a, hipStream_t s) {

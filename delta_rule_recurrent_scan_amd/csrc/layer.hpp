@@ -73,8 +73,10 @@ struct FfnArgs {
   // backward
   const void* dh;               // [R,F]
   void *dx, *dwg, *dwu;         // [R,C], [F,C], [F,C]
-  // within ws
-  void *dg, *du;                // [R,F]
+  // operands of the tiled products: rows of Cp and Fp elements, multiples of 8 (x and the
+  // weights copied to ws with zeros behind C where theirs are not), dg, du [R,Fp] in ws
+  int Cp, Fp;
+  void *dg, *du;
   float* parts;
 };
 

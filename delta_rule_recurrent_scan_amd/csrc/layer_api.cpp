@@ -94,6 +94,11 @@ int ffn_dims(ll R, int C, int F, int dtype, ll xs, int act) {
   return OSDN_OK;
 }
 
+// Where rows of C are whole eights the weights are read where they lie.
+bool weights_ok(int C, const void* g, const void* u) {
+  return C % 8 != 0 || (aligned16(g) && aligned16(u));
+}
+
 }  // namespace
 
 extern "C" {
@@ -279,6 +284,7 @@ int gated_ffn_forward(ll R, int C, int F, int dtype, const void* x, ll x_row_str
   if (n == 0) return OSDN_OK;
   if (!h || (C > 0 && (!x || !w_gate || !w_up)) || (gate == nullptr) != (up == nullptr))
     return OSDN_ERR_NULL_ARG;
+  if (!weights_ok(C, w_gate, w_up)) return OSDN_ERR_MISALIGNED;
   const size_t need = gated_ffn_forward_workspace_bytes(R, C, F, dtype);
   if (!workspace_ok(workspace, workspace_bytes, need)) return OSDN_ERR_WORKSPACE;
   const Range ins[] = {rng(x, span(1, R, C, 0, x_row_stride, es)), rng(w_gate, nw * es),
@@ -309,6 +315,7 @@ int gated_ffn_backward(ll R, int C, int F, int dtype, const void* x, ll x_row_st
   if ((nx > 0 && (!x || !dx)) || (nw > 0 && (!w_gate || !w_up || !dw_gate || !dw_up)) ||
       (n > 0 && (!gate || !up || !dh)))
     return OSDN_ERR_NULL_ARG;
+  if (!weights_ok(C, w_gate, w_up)) return OSDN_ERR_MISALIGNED;
   const size_t need = gated_ffn_backward_workspace_bytes(R, C, F, dtype);
   if (!workspace_ok(workspace, workspace_bytes, need)) return OSDN_ERR_WORKSPACE;
   const Range ins[] = {rng(x, span(1, R, C, 0, x_row_stride, es)), rng(w_gate, nw * es),

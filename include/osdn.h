@@ -762,8 +762,10 @@ int qk_rotary_backward(int B, int T, int Hq, int Hk, int D, int rot, int dtype,
  *   h        [R,F] dtype;  gate, up [R,F] dtype: g and u for the backward pass (both
  *            or neither)
  * h is formed from the 32-bit sums. C, F and the row stride up to 2^21 (more:
- * OSDN_ERR_UNSUPPORTED). workspace: gated_ffn_forward_workspace_bytes(...) bytes,
- * 256-byte aligned: the parts of sums that are split where the rows are few.
+ * OSDN_ERR_UNSUPPORTED). Where C is a multiple of 8 the weights start on 16 bytes
+ * (OSDN_ERR_MISALIGNED). workspace: gated_ffn_forward_workspace_bytes(...) bytes,
+ * 256-byte aligned: the parts of sums that are split where tiles are few, and room for
+ * rows of x (and of weights whose C is not a multiple of 8) off 16 bytes.
  */
 enum { OSDN_ACT_SILU = 0, OSDN_ACT_GELU = 1, OSDN_ACT_GELU_TANH = 2 };
 size_t gated_ffn_forward_workspace_bytes(long long R, int C, int F, int dtype);
@@ -779,7 +781,7 @@ int gated_ffn_forward(long long R, int C, int F, int dtype, const void* x,
  * dx [R,C], dw_gate, dw_up [F,C] dtype OUT (contiguous). dg and du enter the products
  * in dtype (rounded once in bf16), sums are held in 32 bits. workspace:
  * gated_ffn_backward_workspace_bytes(...) bytes, 256-byte aligned: dg and du, and
- * parts of sums.
+ * what the forward's holds.
  */
 size_t gated_ffn_backward_workspace_bytes(long long R, int C, int F, int dtype);
 int gated_ffn_backward(long long R, int C, int F, int dtype, const void* x,
@@ -816,8 +818,8 @@ void osdn_kernel_timing(int enable);
  * ssm_decode, ssm_bwd_state, ssm_bwd_chain, ssm_bwd_walk, ssm_bwd,
  * ssm_bwd_parts, gated_norm, gated_norm_bwd, residual_norm, residual_norm_bwd,
  * column_sum (the operators around the recurrences), glr_part, glr, glr_decode,
- * glr_bwd_part, glr_bwd, qk_rotary, qk_rotary_bwd, ffn, ffn_join, ffn_rows, ffn_grad,
- * ffn_dx, ffn_dw, ffn_sum (the operators that complete a block).
+ * glr_bwd_part, glr_bwd, qk_rotary, qk_rotary_bwd, ffn, ffn_join, ffn_rows, ffn_pad,
+ * ffn_grad, ffn_dx, ffn_dx_join, ffn_dw, ffn_dw_join (the operators that complete a block).
  */
 int osdn_kernel_times(int max, const char** names, int* counts, float* mean_ms);
 

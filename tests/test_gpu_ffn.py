@@ -87,12 +87,39 @@ def test_row_strides(extra, dt):
     check_backward(80, 128, 64, dt, extra=extra, seed=3)
 
 
+@pytest.mark.parametrize("dt", [F32, BF], ids=["f32", "bf16"])
+def test_rows_off_16_bytes(dt):
+    """x that starts off 16 bytes with rows of whole eights; weights there are refused,
+    and taken where C is none."""
+    for R in (20, 90):
+        x, wg, wu, dh = inputs(R, 72, 40, dt, seed=10)
+        flat = torch.zeros(8192, dtype=dt, device=DEV)
+        y = flat[1:1 + x.numel()].view(R, 72)
+        y.copy_(x)
+        h, g, u = osdn.gated_ffn_forward(x, wg, wu, save=True)
+        assert torch.equal(osdn.gated_ffn_forward(y, wg, wu)[0], h)
+        a, b = (osdn.gated_ffn_backward(t, wg, wu, g, u, dh) for t in (x, y))
+        assert all(torch.equal(a[n], b[n]) for n in a)
+        w = flat[1:1 + wg.numel()].view(40, 72)
+        with pytest.raises(osdn.OsdnError) as e:
+            osdn.gated_ffn_forward(x, w, wu)
+        assert e.value.status == 7
+        with pytest.raises(osdn.OsdnError):
+            osdn.gated_ffn_backward(x, wg, w, g, u, dh)
+    check_backward(90, 71, 40, dt, seed=11)
+    both = torch.randn(80, 71, device=DEV).to(dt)       # one tensor's halves
+    x = torch.randn(90, 71, device=DEV).to(dt)
+    want = osdn.gated_ffn_forward(x, both[:40].clone(), both[40:].clone())[0]
+    assert torch.equal(osdn.gated_ffn_forward(x, both[:40], both[40:])[0], want)
+
+
 @pytest.mark.parametrize("dt,R,C,F", [
     (BF, 8192, 64, 2048),        # large tiles, one of k
     (BF, 4100, 264, 1050),       # their ends
     (BF, 2048, 1024, 1024),
     (BF, 700, 512, 1400),
     (BF, 130, 2048, 512),        # parts of k
+    (BF, 130, 512, 2048),
     (BF, 96, 4096, 128),
     (BF, 2111, 320, 200),
     (F32, 1030, 132, 520),
@@ -104,12 +131,16 @@ def test_shapes(dt, R, C, F):
 
 
 def test_parts_are_used():
-    """The sizes above reach the split products."""
-    assert osdn.gated_ffn_forward_workspace_bytes(96, 4096, 128, BF) > 0
-    assert osdn.gated_ffn_forward_workspace_bytes(8192, 64, 2048, BF) == 0
-    assert osdn.gated_ffn_forward_workspace_bytes(64, 4096, 128, BF) == 0
-    plain = 2 * ((96 * 128 * 2 + 255) // 256 * 256)
-    assert osdn.gated_ffn_backward_workspace_bytes(96, 4096, 128, BF) >= plain
+    """The sizes above reach the split products: their workspace holds more than dg, du
+    and copies of x and the weights."""
+    up = lambda n: (n + 255) // 256 * 256
+    need = osdn.gated_ffn_forward_workspace_bytes
+    assert need(96, 4096, 128, BF) > up(96 * 4096 * 2)
+    assert need(8192, 64, 2048, BF) == up(8192 * 64 * 2)
+    assert need(64, 4096, 128, BF) == 0
+    assert need(4100, 263, 64, BF) >= up(4100 * 264 * 2) + 2 * up(64 * 264 * 2)
+    assert (osdn.gated_ffn_backward_workspace_bytes(130, 512, 2048, BF)
+            > 2 * up(130 * 2048 * 2) + up(130 * 512 * 2))
 
 
 def test_leading_dimensions():

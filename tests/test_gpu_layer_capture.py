@@ -48,7 +48,8 @@ def case(name, dt, seed=0, T=150):
         qk_rotary_backward=((a(B, T, 3 * D), a(B, T, 2 * D), a(B, 3, T, D),
                              a(B, 2, T, D), D), qk,
                             osdn.qk_rotary_backward_workspace_bytes(B, T, D), False),
-        gated_ffn_forward=((x, wg, wu), {}, 0, False),
+        gated_ffn_forward=((x, wg, wu), {}, osdn.gated_ffn_forward_workspace_bytes(
+            R, W, F, dt), False),
         gated_ffn_forward_rows=((x[:9].contiguous(), wg, wu), {}, 0, False),
         gated_ffn_forward_parts=(wide, {}, osdn.gated_ffn_forward_workspace_bytes(
             R, 4096, 64, dt), False),
