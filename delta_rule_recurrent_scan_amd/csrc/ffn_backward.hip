@@ -180,10 +180,10 @@ struct Weight {
 // (tiles of k: whole ones of each half, then the ends)
 bool input_plan(Plan& p, long long R, int C, int F, int bf16) {
   const long long kt = bf16 ? kTileK<__bf16> : kTileK<float>;
-  return make_plan(p, 1, R, C, 2 * ((F + kt - 1) / kt) * kt, bf16);
+  return make_plan(p, kOne, R, C, 2 * ((F + kt - 1) / kt) * kt, bf16);
 }
 bool weight_plan(Plan& p, long long R, int C, int F, int bf16) {
-  return make_plan(p, 2, F, C, R, bf16);
+  return make_plan(p, kTwo, F, C, R, bf16);
 }
 
 size_t half_bytes(long long R, int F, int bf16) {

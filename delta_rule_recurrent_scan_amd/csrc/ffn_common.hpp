@@ -181,7 +181,7 @@ struct Shape {
 typedef Shape<256, 256, 2, 4> Large;
 typedef Shape<128, 128, 2, 2> Middle;
 typedef Shape<64, 64, 2, 2> Small;
-typedef Shape<64, 64, 2, 1> SmallPairs;    // column tiles in pairs, for two products
+typedef Shape<64, 128, 2, 2> SmallPairs;   // the forward's: column tiles in pairs
 
 // How a product is cut: tm x tn tiles over nt tiles of k. The first `whole` tiles
 // (full rounds of the workgroups that are on the card at once) are formed whole, the
@@ -189,6 +189,7 @@ typedef Shape<64, 64, 2, 1> SmallPairs;    // column tiles in pairs, for two pro
 struct Plan {
   int shape;                       // 0 large, 1 middle, 2 small
   int tm, tn, nt, whole, splits, per;
+  int area;                        // elements of a tile
   __host__ __device__ int rest() const { return tm * tn - whole; }
   // Items of the rest that go before the whole tiles: the workgroups that begin with a
   // part store their results while the others multiply, and the other way about.
@@ -495,8 +496,10 @@ __device__ __forceinline__ void activated(float g, int act, float& f, float& slo
   }
 }
 
-// The plan of `sets` products of M x N over K, and the bytes of its parts.
-bool make_plan(Plan& p, int sets, long long M, long long N, long long K, int bf16);
+// The plan of a product of M x N over K, of the two in the weights' gradients or of the
+// forward's, and the bytes of its parts.
+enum Kind { kOne, kTwo, kForwards };
+bool make_plan(Plan& p, Kind kind, long long M, long long N, long long K, int bf16);
 size_t parts_bytes(const Plan& p);
 
 inline int whole_eights(int n) { return (n + 7) / 8 * 8; }

@@ -211,7 +211,7 @@ int run_shape(const FfnArgs& a, const Plan& p, hipStream_t s) {
 }
 
 bool forward_plan(Plan& p, long long R, int C, int F, int bf16) {
-  return make_plan(p, 1, R, 2LL * F, whole_eights(C), bf16);
+  return make_plan(p, kForwards, R, 2LL * F, whole_eights(C), bf16);
 }
 
 template <typename T>
@@ -238,29 +238,31 @@ int run(const FfnArgs& a, hipStream_t s) {
 // share of each where as many as fit run at once. Measured with one, two and four
 // workgroups a CU at 176 tiles of k (bf16) and 128 (fp32).
 struct Cost {
-  double alone[3], share[3], each[3];   // each: start and end of a tile
+  int bm, bn, at_once;
+  double alone, share, each;       // each: start and end of a tile
 };
-constexpr Cost kBf16 = {{1.46, 0.73, 0.45}, {1.46, 0.575, 0.25}, {8.0, 4.0, 1.0}};
-constexpr Cost kF32 = {{0.0, 2.5, 0.91}, {0.0, 1.95, 0.64}, {0.0, 4.0, 1.0}};
+// (large fp32 tiles gain nothing: the middle ones have the matrix units busy)
+constexpr Cost kBf16[] = {{256, 256, 1, 1.46, 1.46, 8.0}, {128, 128, 2, 0.73, 0.575, 4.0},
+                          {64, 64, 4, 0.45, 0.25, 1.0}, {64, 128, 2, 0.55, 0.4, 2.0}};
+constexpr Cost kF32[] = {{0, 0, 0, 0, 0, 0}, {128, 128, 2, 2.5, 1.95, 4.0},
+                         {64, 64, 4, 0.91, 0.64, 1.0}, {64, 128, 2, 1.2, 1.0, 2.0}};
 
-bool make_plan(Plan& best, int sets, long long M, long long N, long long K, int bf16) {
-  const int bm[] = {256, 128, 64}, kt = bf16 ? kTileK<__bf16> : kTileK<float>;
-  const int at_once[] = {1, 2, 4};
-  const Cost& c = bf16 ? kBf16 : kF32;
+bool make_plan(Plan& best, Kind kind, long long M, long long N, long long K, int bf16) {
+  const int kt = bf16 ? kTileK<__bf16> : kTileK<float>;
   const long long nt = K > 0 ? (K + kt - 1) / kt : 1;
   double least = 1e300;
   if (nt > (1 << 26)) return false;
-  // (large fp32 tiles gain nothing: the middle ones have the matrix units busy)
   for (int k = bf16 ? 0 : 1; k < 3; ++k) {
-    const long long tm = sets * ((M + bm[k] - 1) / bm[k]), tn = (N + bm[k] - 1) / bm[k];
-    const long long tiles = tm * tn, full = 256 * at_once[k];
+    const Cost& c = (bf16 ? kBf16 : kF32)[k == 2 && kind == kForwards ? 3 : k];
+    const long long tm = (kind == kTwo ? 2 : 1) * ((M + c.bm - 1) / c.bm);
+    const long long tn = (N + c.bn - 1) / c.bn, tiles = tm * tn, full = 256 * c.at_once;
     if (!grid_ok(16 * tiles, 512)) continue;
     // workgroups of `len` tiles of k each
     auto time = [&](long long wgs, long long len) {
-      const long long a_cu = (wgs + 255) / 256, rem = a_cu % at_once[k];
-      const double one = at_once[k] * c.share[k] * len + c.each[k];
-      const double last = rem * c.share[k] > c.alone[k] ? rem * c.share[k] : c.alone[k];
-      return (double)(a_cu / at_once[k]) * one + (rem ? last * len + c.each[k] : 0.0);
+      const long long a_cu = (wgs + 255) / 256, rem = a_cu % c.at_once;
+      const double one = c.at_once * c.share * len + c.each;
+      const double last = rem * c.share > c.alone ? rem * c.share : c.alone;
+      return (double)(a_cu / c.at_once) * one + (rem ? last * len + c.each : 0.0);
     };
     const long long whole = tiles / full * full, rest = tiles - whole;
     for (int s = 1; s <= 16 && (s == 1 || (rest > 0 && nt / s >= 4)); ++s) {
@@ -268,60 +270,78 @@ bool make_plan(Plan& best, int sets, long long M, long long N, long long K, int 
       if ((nt + per - 1) / per != s) continue;     // (no empty part)
       double t = time(whole, nt) + time(rest * s, per);
       // parts written and read, and the launch that adds them
-      if (s > 1) t += 6.5 + (double)(rest * s) * bm[k] * bm[k] * 8 / 4e6;
+      if (s > 1) t += 6.5 + (double)(rest * s) * c.bm * c.bn * 8 / 4e6;
       if (t < least) {
         least = t;
-        best = Plan{k, (int)tm, (int)tn, (int)nt, (int)whole, s, (int)per};
+        best = Plan{k, (int)tm, (int)tn, (int)nt, (int)whole, s, (int)per, c.bm * c.bn};
       }
     }
   }
   return least < 1e300;
 }
 
-namespace {
-
-// rows of C elements to rows of Cp, zeros behind C.
-template <typename T>
-__global__ __launch_bounds__(256) void ffn_pad_kernel(const T* in, long long ld, long long rows,
-                                                      int C, int Cp, T* out) {
-  const unsigned per = Cp / 8;
-  const long long at = blockIdx.x * 256LL + threadIdx.x;
-  const long long r = at / per;
-  if (r >= rows) return;
-  const int c = (int)(at % per) * 8;
-  float v[8];
-  load_v<false, 8>(in + r * ld + c, C - c, v);
-  store_v<true, 8>(out + r * Cp + c, 8, v);
+size_t parts_bytes(const Plan& p) {
+  return p.splits > 1 ? (size_t)p.rest() * p.splits * p.area * sizeof(float) : 0;
 }
 
+namespace {
+
+// Up to three operands in one launch: rows of C elements to rows of Cp, zeros behind C.
+struct Pads {
+  const void* in[3];
+  void* out[3];
+  long long ld[3], end[3];    // end: of its groups of eight among all
+  int C, Cp;
+};
 template <typename T>
-int pad(const void*& p, long long ld, long long rows, int C, int Cp, char*& room, hipStream_t s) {
-  const long long wgs = (rows * (Cp / 8) + 255) / 256;
-  if (!grid_ok(wgs, 256)) return -1;
-  const int tk = ktimer_before(s, "ffn_pad");
-  hipLaunchKernelGGL((ffn_pad_kernel<T>), dim3((unsigned)wgs), dim3(256), 0, s, (const T*)p, ld,
-                     rows, C, Cp, (T*)room);
-  ktimer_after(s, tk);
-  p = room;
-  room += round256((size_t)rows * Cp * sizeof(T));
-  return (int)hipGetLastError();
+__global__ __launch_bounds__(256) void ffn_pad_kernel(Pads p) {
+  const long long id = blockIdx.x * 256LL + threadIdx.x;
+  if (id >= p.end[2]) return;
+  const int k = id < p.end[0] ? 0 : id < p.end[1] ? 1 : 2;
+  const long long at = id - (k ? p.end[k - 1] : 0);
+  const unsigned per = p.Cp / 8;
+  const long long r = at / per;
+  const int c = (int)(at % per) * 8;
+  float v[8];
+  load_v<false, 8>((const T*)p.in[k] + r * p.ld[k] + c, p.C - c, v);
+  store_v<true, 8>((T*)p.out[k] + r * p.Cp + c, 8, v);
 }
 
 template <typename T>
 int align_t(FfnArgs& a, char* room, hipStream_t s) {
   a.Cp = whole_eights(a.C);
   a.Fp = whole_eights(a.F);
-  int rc = 0;
-  if (a.R > 0 && a.C > 0 &&
-      (a.Cp != a.C || !on16(a.x) || a.xs * (long long)sizeof(T) % 16 != 0)) {
-    rc = pad<T>(a.x, a.xs, a.R, a.C, a.Cp, room, s);
+  const bool px = a.R > 0 && a.C > 0 &&
+                  (a.Cp != a.C || !on16(a.x) || a.xs * (long long)sizeof(T) % 16 != 0);
+  const bool pw = a.Cp != a.C && a.F > 0;
+  if (!px && !pw) return 0;
+  Pads p{};
+  p.C = a.C;
+  p.Cp = a.Cp;
+  long long end = 0;
+  auto take = [&](int k, const void*& in, long long ld, long long rows) {
+    p.in[k] = in;
+    p.out[k] = room;
+    p.ld[k] = ld;
+    end += rows * (a.Cp / 8);
+    in = room;
+    room += round256((size_t)rows * a.Cp * sizeof(T));
+  };
+  if (px) {
+    take(0, a.x, a.xs, a.R);
     a.xs = a.Cp;
   }
-  if (a.Cp != a.C && a.F > 0 && a.C > 0) {
-    if (!rc) rc = pad<T>(a.wg, a.C, a.F, a.C, a.Cp, room, s);
-    if (!rc) rc = pad<T>(a.wu, a.C, a.F, a.C, a.Cp, room, s);
-  }
-  return rc;
+  p.end[0] = end;
+  if (pw) take(1, a.wg, a.C, a.F);
+  p.end[1] = end;
+  if (pw) take(2, a.wu, a.C, a.F);
+  p.end[2] = end;
+  const long long wgs = (end + 255) / 256;
+  if (!grid_ok(wgs, 256)) return -1;
+  const int tk = ktimer_before(s, "ffn_pad");
+  hipLaunchKernelGGL((ffn_pad_kernel<T>), dim3((unsigned)wgs), dim3(256), 0, s, p);
+  ktimer_after(s, tk);
+  return (int)hipGetLastError();
 }
 
 }  // namespace
@@ -333,11 +353,6 @@ size_t aligned_bytes(long long R, int C, int F, int bf16) {
 
 int align_operands(FfnArgs& a, char* room, hipStream_t s) {
   return a.bf16 ? align_t<__bf16>(a, room, s) : align_t<float>(a, room, s);
-}
-
-size_t parts_bytes(const Plan& p) {
-  const int b[] = {256, 128, 64};
-  return p.splits > 1 ? (size_t)p.rest() * p.splits * b[p.shape] * b[p.shape] * sizeof(float) : 0;
 }
 
 }  // namespace ffn
