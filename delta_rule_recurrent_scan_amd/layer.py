@@ -12,7 +12,8 @@ import ctypes
 import torch
 
 from . import _DTYPE_CODE, load_library
-from .mixer import _begin, _call, _check, _ptr, _required, _rows, _workspace
+from .mixer import _begin, _call, _check, _ptr, _required, _rows
+from .mixer import _workspace as _any_workspace
 
 __all__ = ["glr_forward", "glr_decode", "glr_backward",
            "glr_forward_workspace_bytes", "glr_backward_workspace_bytes",
@@ -55,6 +56,15 @@ def bind(L):
     for name, (args, res) in SIGNATURES.items():
         f = getattr(L, name)
         f.argtypes, f.restype = args, res
+
+
+def _workspace(ws, need, dev):
+    """(pointer, bytes, tensor) of a call's workspace; none is made where none is
+    needed (a single-token call would spend a fifth of its time on it)."""
+    if ws is None and need == 0:
+        return None, 0, None
+    ws = _any_workspace(ws, need, dev)
+    return ws.data_ptr(), ws.numel(), ws
 
 
 # ---------------------------------------------------------------------------
@@ -105,12 +115,12 @@ def glr_forward(x, r, A, i=None, h0=None, lengths=None, normalize=True,
         states = torch.empty(kept, dtype=f32, device=dev) if save else None
     else:
         y, h_T, states = out
-    _check(y, "y", (B, T, C), x.dtype, dev)
-    _check(h_T, "h_T", (B, C), f32, dev)
-    _check(states, "states", kept, f32, dev)
-    ws = _workspace(workspace, L.glr_forward_workspace_bytes(B, T, C), dev)
+        _check(y, "y", (B, T, C), x.dtype, dev)
+        _check(h_T, "h_T", (B, C), f32, dev)
+        _check(states, "states", kept, f32, dev)
+    wp, wn, ws = _workspace(workspace, L.glr_forward_workspace_bytes(B, T, C), dev)
     _call(L.glr_forward, "glr_forward", dev, *args, _ptr(h0), _ptr(lengths),
-          int(normalize), _ptr(y), _ptr(h_T), _ptr(states), _ptr(ws), ws.numel())
+          int(normalize), _ptr(y), _ptr(h_T), _ptr(states), wp, wn)
     return y, h_T, states
 
 
@@ -120,11 +130,15 @@ def glr_decode(x, r, A, h, i=None, normalize=True, out=None, h_out=None):
     if h is None:
         raise ValueError("h is required")
     L, dev, (B, T, C), args = _glr_checks(x, r, A, i)
-    ho = h if h_out is None else h_out
-    y = torch.empty((B, T, C), dtype=x.dtype, device=dev) if out is None else out
     _check(h, "h", (B, C), torch.float32, dev)
-    _check(ho, "h_out", (B, C), torch.float32, dev)
-    _check(y, "y", (B, T, C), x.dtype, dev)
+    ho, y = h, out
+    if h_out is not None:
+        ho = h_out
+        _check(ho, "h_out", (B, C), torch.float32, dev)
+    if out is None:
+        y = torch.empty((B, T, C), dtype=x.dtype, device=dev)
+    else:
+        _check(y, "y", (B, T, C), x.dtype, dev)
     _call(L.glr_decode, "glr_decode", dev, *args, _ptr(h), int(normalize), _ptr(y),
           _ptr(ho))
     return y
@@ -163,12 +177,12 @@ def glr_backward(x, r, A, dy, i=None, h0=None, dh_T=None, lengths=None,
         _check(g[n], "out[%s]" % n, (B, T, C), x.dtype, dev)
     _check(g["A"], "out[A]", (C,), f32, dev)
     _check(g.get("h0"), "out[h0]", (B, C), f32, dev)
-    ws = _workspace(workspace, L.glr_backward_workspace_bytes(
+    wp, wn, ws = _workspace(workspace, L.glr_backward_workspace_bytes(
         B, T, C, int(states is not None)), dev)
     _call(L.glr_backward, "glr_backward", dev, *args, _ptr(h0), _ptr(lengths),
           int(normalize), _ptr(states), _ptr(dy), _ptr(dh_T), _ptr(g["x"]),
           _ptr(g["r"]), _ptr(None if i is None else g["i"]), _ptr(g["A"]),
-          _ptr(g.get("h0")), _ptr(ws), ws.numel())
+          _ptr(g.get("h0")), wp, wn)
     return g
 
 
@@ -186,6 +200,7 @@ def _qk_checks(q, k, head_dim, inv_freq, q_weight, k_weight, positions, lengths,
     D = int(head_dim)
     if norm not in _NORM:
         raise ValueError("norm must be one of %s" % sorted(_NORM))
+    dt, f32 = lead.dtype, torch.float32
     heads, rows = [], ()
     for t, name in ((q, "q"), (k, "k")):
         if t is None:
@@ -198,17 +213,21 @@ def _qk_checks(q, k, head_dim, inv_freq, q_weight, k_weight, positions, lengths,
         if D < 1 or C % D:
             raise ValueError("head_dim %d does not divide the %d channels" % (D, C))
         heads.append(C // D)
-        rows += (_ptr(t),) + _rows(t, name, B, T, C, lead.dtype, dev)
+        rows += (t.data_ptr(),) + _rows(t, name, B, T, C, dt, dev)
     rot = 0
     if inv_freq is not None:
         if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
             raise ValueError("inv_freq must be [rot / 2]")
         rot = 2 * inv_freq.shape[0]
-        _check(inv_freq, "inv_freq", (rot // 2,), torch.float32, dev)
-    _check(q_weight, "q_weight", (D,), torch.float32, dev)
-    _check(k_weight, "k_weight", (D,), torch.float32, dev)
-    _check(positions, "positions", (B, T), torch.int32, dev)
-    _check(lengths, "lengths", (B,), torch.int32, dev)
+        _check(inv_freq, "inv_freq", (rot // 2,), f32, dev)
+    if q_weight is not None:
+        _check(q_weight, "q_weight", (D,), f32, dev)
+    if k_weight is not None:
+        _check(k_weight, "k_weight", (D,), f32, dev)
+    if positions is not None:
+        _check(positions, "positions", (B, T), torch.int32, dev)
+    if lengths is not None:
+        _check(lengths, "lengths", (B,), torch.int32, dev)
     dims = (B, T, heads[0], heads[1], D)
     args = rows + (_ptr(q_weight), _ptr(k_weight), _NORM[norm], float(eps),
                    _ptr(inv_freq), int(interleaved), _ptr(positions),
@@ -240,8 +259,8 @@ def qk_rotary_forward(q, k, head_dim, inv_freq=None, q_weight=None, k_weight=Non
                   for t, H in ((q, Hq), (k, Hk)))
     else:
         yq, yk = out
-    _check(yq, "out[0]", (B, Hq, T, D), dt, dev)
-    _check(yk, "out[1]", (B, Hk, T, D), dt, dev)
+        _check(yq, "out[0]", (B, Hq, T, D), dt, dev)
+        _check(yk, "out[1]", (B, Hk, T, D), dt, dev)
     _call(L.qk_rotary_forward, "qk_rotary_forward", dev, B, T, Hq, Hk, D, rot, code,
           *args, _ptr(yq), _ptr(yk))
     return yq, yk
@@ -280,14 +299,14 @@ def qk_rotary_backward(q, k, dq, dk, head_dim, inv_freq=None, q_weight=None,
     _required(g, [n for n, (s, d, t) in shapes.items() if t is not None])
     for n, (s, d, t) in shapes.items():
         _check(g.get(n) if t is not None else None, "out[%s]" % n, s, d, dev)
-    ws = _workspace(workspace, L.qk_rotary_backward_workspace_bytes(B, T, D), dev)
+    wp, wn, ws = _workspace(workspace, L.qk_rotary_backward_workspace_bytes(B, T, D), dev)
 
     def to(n):
         return _ptr(g[n]) if shapes[n][2] is not None else None
     _call(L.qk_rotary_backward, "qk_rotary_backward", dev, B, T, Hq, Hk, D, rot,
           code, _DTYPE_CODE[lead.dtype], *args,
           _ptr(dq) if q is not None else None, _ptr(dk) if k is not None else None,
-          to("q"), to("k"), to("q_weight"), to("k_weight"), _ptr(ws), ws.numel())
+          to("q"), to("k"), to("q_weight"), to("k_weight"), wp, wn)
     return g
 
 
@@ -307,21 +326,20 @@ def _ffn_checks(x, w_gate, w_up, activation):
     R = 1
     for n in x.shape[:-1]:
         R *= n
-    # any rows whose leading dimensions lie one row stride apart
-    stride, want = C, None
-    for n, s in zip(reversed(x.shape[:-1]), reversed(x.stride()[:-1])):
-        if n == 1:
-            continue
-        if want is None:
-            stride = s
-            want = s
-        if s != want:
-            raise ValueError("x must have its rows one stride apart")
-        want = s * n
-    if C > 1 and x.numel() and x.stride(-1) != 1:
-        raise ValueError("x must be contiguous along its channels")
-    if stride < 0 or (R == 0 or C == 0):
-        stride = C
+    stride = C
+    if R and C and not x.is_contiguous():
+        # any rows whose leading dimensions lie one row stride apart
+        want = None
+        for n, s in zip(reversed(x.shape[:-1]), reversed(x.stride()[:-1])):
+            if n == 1:
+                continue
+            if want is None:
+                stride = want = s
+            if s != want:
+                raise ValueError("x must have its rows one stride apart")
+            want = s * n
+        if C > 1 and x.stride(-1) != 1:
+            raise ValueError("x must be contiguous along its channels")
     _check(w_gate, "w_gate", (F, C), x.dtype, dev)
     if w_up is None:
         raise ValueError("w_up is required")
@@ -355,12 +373,12 @@ def gated_ffn_forward(x, w_gate, w_up, activation="silu", save=False, out=None,
                     else (None, None))
     else:
         h, gate, up = out
-    for t, n in ((h, "h"), (gate, "gate"), (up, "up")):
-        _check(t, n, shape, x.dtype, dev)
-    ws = _workspace(workspace, L.gated_ffn_forward_workspace_bytes(R, C, F, code),
+        for t, n in ((h, "h"), (gate, "gate"), (up, "up")):
+            _check(t, n, shape, x.dtype, dev)
+    wp, wn, ws = _workspace(workspace, L.gated_ffn_forward_workspace_bytes(R, C, F, code),
                     dev)
     _call(L.gated_ffn_forward, "gated_ffn_forward", dev, *args, _ACT[activation],
-          _ptr(h), _ptr(gate), _ptr(up), _ptr(ws), ws.numel())
+          _ptr(h), _ptr(gate), _ptr(up), wp, wn)
     return h, gate, up
 
 
@@ -389,9 +407,9 @@ def gated_ffn_backward(x, w_gate, w_up, gate, up, dh, activation="silu", out=Non
     _check(g["x"], "out[x]", tuple(x.shape), dt, dev)
     _check(g["w_gate"], "out[w_gate]", (F, C), dt, dev)
     _check(g["w_up"], "out[w_up]", (F, C), dt, dev)
-    ws = _workspace(workspace, L.gated_ffn_backward_workspace_bytes(R, C, F, code),
+    wp, wn, ws = _workspace(workspace, L.gated_ffn_backward_workspace_bytes(R, C, F, code),
                     dev)
     _call(L.gated_ffn_backward, "gated_ffn_backward", dev, *args, _ptr(gate),
           _ptr(up), _ACT[activation], _ptr(dh), _ptr(g["x"]), _ptr(g["w_gate"]),
-          _ptr(g["w_up"]), _ptr(ws), ws.numel())
+          _ptr(g["w_up"]), wp, wn)
     return g
