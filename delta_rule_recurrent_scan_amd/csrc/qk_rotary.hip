@@ -114,8 +114,9 @@ __device__ __forceinline__ void others(const Raw<T, 8>& x, const QkArgs& a, cons
 
 template <int L>
 __device__ __forceinline__ float root(const QkArgs& a, float ss) {
-  const float m = group_sum<L>(ss);
-  return a.norm == 0 ? 1.f : rsqrtf((a.norm == 1 ? m / (8 * L) : m) + a.eps);
+  const float m = group_sum<L>(ss), s = (a.norm == 1 ? m / (8 * L) : m) + a.eps;
+  // (rows of zeros, those behind a sequence too, keep their zeros with eps = 0)
+  return a.norm == 0 ? 1.f : s == 0.f ? 0.f : rsqrtf(s);
 }
 
 // One input (queries or keys): H heads of the lane's token. The weights of both members

@@ -713,7 +713,8 @@ int glr_backward(int B, int T, int C, int dtype, const void* x,
  *   v = n * weight
  *   (y_a, y_b) = (v_a cos w - v_b sin w, v_b cos w + v_a sin w),  w = p inv_freq[j]
  * for j < rot / 2 and the channels (a, b) = (j, j + rot/2), or (2j, 2j + 1) with
- * `interleaved`; channels from rot on pass through (y = v).
+ * `interleaved`; channels from rot on pass through (y = v). With eps = 0 a row of
+ * zeros gives zeros, and zero gradients.
  *
  *   q        [B,T,Hq*D], k [B,T,Hk*D] dtype rows with strides as above (Hq or Hk 0:
  *            none)

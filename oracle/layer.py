@@ -114,7 +114,9 @@ def _root(x, norm, eps):
     if norm == "none":
         return np.ones_like(x[..., :1]), 0
     count = x.shape[-1] if norm == "rms" else 1
-    return 1 / np.sqrt((x * x).sum(-1, keepdims=True) / count + eps), count
+    s = (x * x).sum(-1, keepdims=True) / count + eps
+    # (rows of zeros keep their zeros with eps = 0)
+    return np.where(s == 0, 0.0, 1 / np.sqrt(np.where(s == 0, 1.0, s))), count
 
 
 def _off(lengths, B, T):

@@ -129,6 +129,20 @@ def test_zero_rows():
     assert not d["q_weight"].any()
 
 
+@pytest.mark.parametrize("norm", ["rms", "l2"])
+@pytest.mark.parametrize("dt", [F32, BF], ids=["f32", "bf16"])
+def test_no_eps(dt, norm):
+    """eps = 0: rows behind a sequence and rows of zeros give zeros, no NaN."""
+    check(3, 9, 2, 1, 64, dt, 32, norm=norm, eps=0.0, lens=[9, 0, 4], seed=7)
+    q, k, dq, dk, kw = inputs(1, 4, 2, 1, 64, dt, 32, seed=8)
+    q = torch.zeros_like(q)
+    y, _ = osdn.qk_rotary_forward(q, k, 64, norm=norm, eps=0.0, **kw)
+    d = osdn.qk_rotary_backward(q, k, dq, dk, 64, norm=norm, eps=0.0, **kw)
+    torch.cuda.synchronize()
+    for t in (y, d["q"], d["q_weight"]):
+        assert (t == 0).all()
+
+
 def test_empty():
     for B, T in ((0, 4), (3, 0)):
         q, k, dq, dk, kw = inputs(B, T, 2, 1, 32, F32, 32)
