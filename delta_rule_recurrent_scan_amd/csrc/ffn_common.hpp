@@ -492,7 +492,9 @@ __device__ __forceinline__ void activated(float g, int act, float& f, float& slo
     // 0.5 (1 + tanh z) = sigmoid(2 z), z = sqrt(2 / pi) (g + 0.044715 g^3)
     const float p = sigmoid_f(1.59576912160573071f * fmaf(0.044715f * g * g, g, g));
     f = g * p;
-    slope = fmaf(g * p * (1.f - p), 1.59576912160573071f * fmaf(0.134145f * g, g, 1.f), p);
+    // (p is 0 or 1 from |g| = 16 on; the factor of 1 - p would be infinite from 1e20 on)
+    const float c = __builtin_amdgcn_fmed3f(g, -16.f, 16.f);
+    slope = fmaf(c * p * (1.f - p), 1.59576912160573071f * fmaf(0.134145f * c, c, 1.f), p);
   }
 }
 

@@ -178,6 +178,22 @@ def test_extremes():
             assert torch.equal(a[keep], b[keep]) and torch.isnan(a[3]).all()
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_huge_gates(act):
+    """Far out every activation is its argument or zero, with a slope of one or zero,
+    up to gates whose square or cube is past the type."""
+    for s in (20.0, 1e4, 1e20, 1e38):
+        g = torch.tensor([s, -s] * 16, device=DEV).repeat(2, 1)
+        z = lambda *n: torch.zeros(n, device=DEV)
+        x, w, one = z(2, 32), torch.eye(32, device=DEV), torch.ones_like(g)
+        # with the identity as the gate's weights dx is dg
+        d = osdn.gated_ffn_backward(x, w, z(32, 32), g, one, one, activation=act)
+        # (slope of silu at -20: -20 exp(-20))
+        assert torch.allclose(d["x"], (g > 0).float(), rtol=0, atol=5e-8), (s, d["x"])
+        h = osdn.gated_ffn_forward(g, w, w, activation=act)[0]
+        assert h[:, 0].isinf().all() if s == 1e38 else torch.allclose(h[:, 0], g[:, 0] ** 2)
+
+
 @pytest.mark.parametrize("R,C,F", [(0, 8, 8), (3, 0, 8), (3, 8, 0), (100, 0, 8)])
 def test_empty(R, C, F):
     x, wg, wu, dh = inputs(R, C, F, F32)
