@@ -126,7 +126,7 @@ def kernel_times():
     """{kernel name: (launches, mean ms)} of the kernels launched while
     timing was enabled (waits for their events)."""
     L = load_library()
-    n = 16
+    n = 128
     names = (ctypes.c_char_p * n)()
     counts = (ctypes.c_int * n)()
     ms = (ctypes.c_float * n)()

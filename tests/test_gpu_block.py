@@ -204,3 +204,18 @@ def test_tokens_after_a_prompt():
         yt = osdn.glr_decode(ct[:, 0], cut(r, t, t + 1), w["A"], h, i=cut(i, t, t + 1))
         assert rel(yt, f64(cut(y, t, t + 1))) <= 1e-5
     assert rel(h, f64(h_T)) <= 1e-5
+
+
+def test_kernel_times_of_both_blocks():
+    """Every kernel of the two blocks is reported, more than 16 of them."""
+    osdn.kernel_timing(True)
+    try:
+        for kind in ("recurrence", "delta"):
+            block(weights(kind), kind)
+        seen = osdn.kernel_times()
+    finally:
+        osdn.kernel_timing(False)
+    print(sorted(seen))
+    assert len(seen) > 16
+    assert {"glr", "glr_bwd", "qk_rotary", "qk_rotary_bwd", "ffn_grad", "residual_norm",
+            "short_conv_bwd"} <= set(seen)
