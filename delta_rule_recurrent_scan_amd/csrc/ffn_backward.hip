@@ -13,9 +13,11 @@ namespace osdn {
 namespace ffn {
 namespace {
 
-// dg and du in rows of Fp elements, zeros behind F.
+// dg and du in rows of Fp elements, zeros behind F; behind the first n workgroups the
+// copies of operands off 16 bytes.
 template <typename T>
-__global__ __launch_bounds__(256) void ffn_grad_kernel(FfnArgs a) {
+__global__ __launch_bounds__(256) void ffn_grad_kernel(FfnArgs a, Pads p, unsigned n) {
+  if (blockIdx.x >= n) return pad_group<T>(p, (blockIdx.x - n) * 256LL + threadIdx.x);
   const long long at = (blockIdx.x * 256LL + threadIdx.x) * 8;
   if (at >= a.R * a.Fp) return;
   long long from = at;
@@ -177,31 +179,50 @@ struct Weight {
 // Launches
 // ---------------------------------------------------------------------------
 
-// (tiles of k: whole ones of each half, then the ends)
-bool input_plan(Plan& p, long long R, int C, int F, int bf16) {
+// How both products are cut. pair: in one launch.
+struct Plans {
+  Plan x, w;
+  bool pair;
+  size_t parts() const {
+    const size_t px = parts_bytes(x), pw = parts_bytes(w);
+    return pair ? px + pw : px > pw ? px : pw;
+  }
+};
+bool make_plans(Plans& p, long long R, int C, int F, int bf16) {
+  p = Plans{};
   const long long kt = bf16 ? kTileK<__bf16> : kTileK<float>;
-  return make_plan(p, kOne, R, C, 2 * ((F + kt - 1) / kt) * kt, bf16);
-}
-bool weight_plan(Plan& p, long long R, int C, int F, int bf16) {
-  return make_plan(p, kTwo, F, C, R, bf16);
+  // (tiles of k of dx: whole ones of each half, then the ends)
+  const long long x[3] = {R, C, 2 * ((F + kt - 1) / kt) * kt}, w[3] = {F, C, R};
+  double tx = 0.0, tw = 0.0;
+  if (C == 0) return true;
+  if (R > 0 && !make_plan(p.x, kOne, x[0], x[1], x[2], bf16, &tx)) return false;
+  if (F > 0 && !make_plan(p.w, kTwo, w[0], w[1], w[2], bf16, &tw)) return false;
+  if (R > 0 && F > 0) p.pair = make_pair(p.x, p.w, x, w, bf16, tx + tw + kLaunch);
+  return true;
 }
 
 size_t half_bytes(long long R, int F, int bf16) {
   return round256((size_t)R * whole_eights(F) * (bf16 ? 2 : 4));
 }
 
+enum What { kDx, kDw, kBoth };
 template <typename T, class S>
-int run_shape(const FfnArgs& a, const Plan& p, bool weights, hipStream_t s) {
-  return weights ? launch_products<T, S, Weight<T, S>>(a, p, "ffn_dw", "ffn_dw_join", s)
-                 : launch_products<T, S, Input<T, S>>(a, p, "ffn_dx", "ffn_dx_join", s);
+int run_shape(const FfnArgs& a, const Plans& p, What what, hipStream_t s) {
+  typedef Input<T, S> X;
+  typedef Weight<T, S> W;
+  if (what == kBoth)
+    return launch_pair<T, S, X, W>(a, p.x, p.w, "ffn_dxdw", "ffn_dxdw_join", s);
+  return what == kDx ? launch_products<T, S, X>(a, p.x, "ffn_dx", "ffn_dx_join", s)
+                     : launch_products<T, S, W>(a, p.w, "ffn_dw", "ffn_dw_join", s);
 }
 
 template <typename T>
-int run_plan(const FfnArgs& a, const Plan& p, bool weights, hipStream_t s) {
+int run_plan(const FfnArgs& a, const Plans& p, What what, hipStream_t s) {
+  const int shape = what == kDw ? p.w.shape : p.x.shape;
   if constexpr (sizeof(T) == 2)
-    if (p.shape == 0) return run_shape<T, Large>(a, p, weights, s);
-  if (p.shape == 1) return run_shape<T, Middle>(a, p, weights, s);
-  return run_shape<T, Small>(a, p, weights, s);
+    if (shape == 0) return run_shape<T, Large>(a, p, what, s);
+  if (shape == 1) return run_shape<T, Middle>(a, p, what, s);
+  return run_shape<T, Small>(a, p, what, s);
 }
 
 template <typename T>
@@ -211,21 +232,23 @@ int run(const FfnArgs& a0, hipStream_t s) {
   a.dg = a.ws;
   a.du = (char*)a.ws + half;
   char* room = (char*)a.ws + 2 * half;
-  Plan x{}, w{};
+  Plans p;
   const long long wgs = (a.R * whole_eights(a.F) + 2047) / 2048;
-  if ((a.R > 0 && !input_plan(x, a.R, a.C, a.F, a.bf16)) ||
-      (a.F > 0 && !weight_plan(w, a.R, a.C, a.F, a.bf16)) || !grid_ok(wgs, 256))
-    return -1;
-  int rc = align_operands(a, room, s);
+  const Pads pads = align_operands(a, room);
+  const long long copies = (pads.end[2] + 255) / 256;
+  if (!make_plans(p, a.R, a.C, a.F, a.bf16) || !grid_ok(wgs + copies, 256)) return -1;
   a.parts = (float*)(room + aligned_bytes(a.R, a.C, a.F, a.bf16));
-  if (!rc && wgs > 0) {
+  int rc = 0;
+  if (wgs + copies > 0) {
     const int tk = ktimer_before(s, "ffn_grad");
-    hipLaunchKernelGGL((ffn_grad_kernel<T>), dim3((unsigned)wgs), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((ffn_grad_kernel<T>), dim3((unsigned)(wgs + copies)), dim3(256), 0, s, a,
+                       pads, (unsigned)wgs);
     ktimer_after(s, tk);
     rc = (int)hipGetLastError();
   }
-  if (!rc && a.R > 0) rc = run_plan<T>(a, x, false, s);
-  if (!rc && a.F > 0) rc = run_plan<T>(a, w, true, s);
+  if (!rc && p.pair) return run_plan<T>(a, p, kBoth, s);
+  if (!rc && a.R > 0) rc = run_plan<T>(a, p, kDx, s);
+  if (!rc && a.F > 0) rc = run_plan<T>(a, p, kDw, s);
   return rc;
 }
 
@@ -233,10 +256,9 @@ int run(const FfnArgs& a0, hipStream_t s) {
 }  // namespace ffn
 
 size_t ffn_backward_ws(long long R, int C, int F, int bf16) {
-  ffn::Plan p;
-  const size_t px = R > 0 && C > 0 && ffn::input_plan(p, R, C, F, bf16) ? ffn::parts_bytes(p) : 0;
-  const size_t pw = F > 0 && C > 0 && ffn::weight_plan(p, R, C, F, bf16) ? ffn::parts_bytes(p) : 0;
-  return 2 * ffn::half_bytes(R, F, bf16) + ffn::aligned_bytes(R, C, F, bf16) + (px > pw ? px : pw);
+  ffn::Plans p;
+  const size_t parts = ffn::make_plans(p, R, C, F, bf16) ? p.parts() : 0;
+  return 2 * ffn::half_bytes(R, F, bf16) + ffn::aligned_bytes(R, C, F, bf16) + parts;
 }
 
 int launch_ffn_backward(const FfnArgs& a, hipStream_t s) {

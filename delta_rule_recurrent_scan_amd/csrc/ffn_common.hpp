@@ -84,7 +84,9 @@ struct Stage {
   static_assert(UNITS % NT == 0 && NT % 64 == 0, "whole waves stage a tile");
 
   __device__ __forceinline__ static int swizzle(int row) {
-    return KMAJ ? (RUNS ? runs_swizzle(row) : row & 7) : runs_swizzle(row) * 2 & (UPR - 1);
+    if constexpr (KMAJ) return RUNS ? runs_swizzle(row) : row & 7;
+    // (fp32: the four rows that a wave reads at once lie four apart, 64 bytes of each)
+    return (sizeof(T) == 2 ? runs_swizzle(row) * 2 : row & 12) & (UPR - 1);
   }
   // LDS row and logical unit of a thread's j-th unit.
   __device__ __forceinline__ static void where(int thread, int j, int& row, int& u) {
@@ -190,6 +192,7 @@ struct Plan {
   int shape;                       // 0 large, 1 middle, 2 small
   int tm, tn, nt, whole, splits, per;
   int area;                        // elements of a tile
+  long long parts_at;              // its parts' place in FfnArgs::parts
   __host__ __device__ int rest() const { return tm * tn - whole; }
   // Items of the rest that go before the whole tiles: the workgroups that begin with a
   // part store their results while the others multiply, and the other way about.
@@ -254,10 +257,13 @@ __device__ __forceinline__ void wait_loads() {
 // never run empty. A wave works off a tile in four parts (two steps of k, two halves of
 // its rows) and fetches each part's operands while the one before is multiplied; the
 // barrier stands before a tile's last part, whose operands are in registers.
+//
+// id: the item's number; u0 .. u4: the buffers.
+template <class S>
+constexpr int kBuffer = (S::BM > S::BN ? S::BM : S::BN) * kRowBytes;
 template <typename T, class S, class Op>
-__device__ __forceinline__ void products(const FfnArgs& a, const Plan& p) {
-  constexpr int BUF = (S::BM > S::BN ? S::BM : S::BN) * kRowBytes;
-  __shared__ __attribute__((aligned(1024))) char u0[BUF], u1[BUF], u2[BUF], u3[BUF], u4[BUF];
+__device__ __forceinline__ void products(const FfnArgs& a, const Plan& p, int id, char* u0,
+                                         char* u1, char* u2, char* u3, char* u4) {
   typedef typename Op::StageA SA;
   constexpr int NA = SA::PER, NB = S::BN * kRowBytes / 16 / S::NT, HM = S::TM / 2;
   const int wm = wave_id() / S::WN * (S::BM / S::WM);
@@ -279,7 +285,7 @@ __device__ __forceinline__ void products(const FfnArgs& a, const Plan& p) {
       for (int j = 0; j < S::TN; ++j) mma(acc[half * HM + i][j], fb[j], fa[i], T());
   };
 
-  const Item it = item_at(p, blockIdx.x);
+  const Item it = item_at(p, id);
   Op op;
   op.place(a, it);
   int t = it.t0;
@@ -378,7 +384,7 @@ __device__ __forceinline__ void products(const FfnArgs& a, const Plan& p) {
   }
 
   if (p.splits > 1 && it.tile >= 0) {
-    f32x4* part = (f32x4*)a.parts +
+    f32x4* part = (f32x4*)(a.parts + p.parts_at) +
                   (size_t)(it.tile * p.splits + it.split) * (S::BM * S::BN / 4) + fresh_thread();
 #pragma unroll
     for (int i = 0; i < S::TM; ++i)
@@ -392,15 +398,16 @@ __device__ __forceinline__ void products(const FfnArgs& a, const Plan& p) {
 
 // The parts of one tile's i-th rows added in order, and stored.
 template <class S, class Op>
-__device__ __forceinline__ void join_parts(const FfnArgs& a, const Plan& p) {
-  const int tile = blockIdx.x / S::TM, i = blockIdx.x % S::TM;
+__device__ __forceinline__ void join_parts(const FfnArgs& a, const Plan& p, int id) {
+  const int tile = id / S::TM, i = id % S::TM;
   Item it;
   it.t0 = it.t1 = it.split = 0;
   it.tile = tile;
   tile_place(p, p.whole + tile, it.m, it.n);
   Op op;
   op.place(a, it);
-  const f32x4* part = (const f32x4*)a.parts + (size_t)tile * p.splits * (S::BM * S::BN / 4) +
+  const f32x4* part = (const f32x4*)(a.parts + p.parts_at) +
+                      (size_t)tile * p.splits * (S::BM * S::BN / 4) +
                       i * S::TN * S::NT + threadIdx.x;
   f32x4 row[S::TN];
 #pragma unroll
@@ -415,11 +422,33 @@ __device__ __forceinline__ void join_parts(const FfnArgs& a, const Plan& p) {
 
 template <typename T, class S, class Op>
 __global__ __launch_bounds__(S::NT) void ffn_kernel(FfnArgs a, Plan p) {
-  products<T, S, Op>(a, p);
+  __shared__ __attribute__((aligned(1024))) char u0[kBuffer<S>], u1[kBuffer<S>], u2[kBuffer<S>],
+      u3[kBuffer<S>], u4[kBuffer<S>];
+  products<T, S, Op>(a, p, blockIdx.x, u0, u1, u2, u3, u4);
 }
 template <class S, class Op>
 __global__ __launch_bounds__(S::NT) void ffn_join_kernel(FfnArgs a, Plan p) {
-  join_parts<S, Op>(a, p);
+  join_parts<S, Op>(a, p, blockIdx.x);
+}
+// Two products in one launch, the items of the first before those of the second.
+template <typename T, class S, class Op1, class Op2>
+__global__ __launch_bounds__(S::NT) void ffn_pair_kernel(FfnArgs a, Plan p, Plan q) {
+  __shared__ __attribute__((aligned(1024))) char u0[kBuffer<S>], u1[kBuffer<S>], u2[kBuffer<S>],
+      u3[kBuffer<S>], u4[kBuffer<S>];
+  const int n = p.items();
+  if ((int)blockIdx.x < n) {
+    products<T, S, Op1>(a, p, blockIdx.x, u0, u1, u2, u3, u4);
+  } else {
+    products<T, S, Op2>(a, q, blockIdx.x - n, u0, u1, u2, u3, u4);
+  }
+}
+template <class S, class Op1, class Op2>
+__global__ __launch_bounds__(S::NT) void ffn_pair_join_kernel(FfnArgs a, Plan p, Plan q, int n) {
+  if ((int)blockIdx.x < n) {
+    join_parts<S, Op1>(a, p, blockIdx.x);
+  } else {
+    join_parts<S, Op2>(a, q, blockIdx.x - n);
+  }
 }
 
 template <typename T, class S, class Op>
@@ -432,6 +461,23 @@ int launch_products(const FfnArgs& a, const Plan& p, const char* name, const cha
   if (rc || p.splits == 1) return rc;
   tk = ktimer_before(s, join_name);
   hipLaunchKernelGGL((ffn_join_kernel<S, Op>), dim3(p.rest() * S::TM), dim3(S::NT), 0, s, a, p);
+  ktimer_after(s, tk);
+  return (int)hipGetLastError();
+}
+
+template <typename T, class S, class Op1, class Op2>
+int launch_pair(const FfnArgs& a, const Plan& p, const Plan& q, const char* name,
+                const char* join_name, hipStream_t s) {
+  int tk = ktimer_before(s, name);
+  hipLaunchKernelGGL((ffn_pair_kernel<T, S, Op1, Op2>), dim3(p.items() + q.items()), dim3(S::NT),
+                     0, s, a, p, q);
+  ktimer_after(s, tk);
+  const int rc = (int)hipGetLastError();
+  const int n = p.splits > 1 ? p.rest() * S::TM : 0, m = q.splits > 1 ? q.rest() * S::TM : 0;
+  if (rc || n + m == 0) return rc;
+  tk = ktimer_before(s, join_name);
+  hipLaunchKernelGGL((ffn_pair_join_kernel<S, Op1, Op2>), dim3(n + m), dim3(S::NT), 0, s, a, p, q,
+                     n);
   ktimer_after(s, tk);
   return (int)hipGetLastError();
 }
@@ -500,18 +546,44 @@ __device__ __forceinline__ void activated(float g, int act, float& f, float& slo
 
 // The plan of a product of M x N over K, of the two in the weights' gradients or of the
 // forward's, and the bytes of its parts.
+constexpr double kLaunch = 4.5;   // microseconds between two launches
 enum Kind { kOne, kTwo, kForwards };
-bool make_plan(Plan& p, Kind kind, long long M, long long N, long long K, int bf16);
+bool make_plan(Plan& p, Kind kind, long long M, long long N, long long K, int bf16,
+               double* microseconds = nullptr);
+// Plans of the products kOne and kTwo of these sizes in one launch, where that takes less
+// time than `microseconds`.
+bool make_pair(Plan& p, Plan& q, const long long (&one)[3], const long long (&two)[3], int bf16,
+               double microseconds);
 size_t parts_bytes(const Plan& p);
 
 inline int whole_eights(int n) { return (n + 7) / 8 * 8; }
 inline size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 inline bool on16(const void* p) { return ((size_t)p & 15) == 0; }
 
-// Bytes of ws behind `used` that copies of x and the weights may take, and the copies
-// made where they are needed: a's pointers and strides are then those of the products.
+// Copies of up to three operands: rows of C elements to rows of Cp, zeros behind C.
+struct Pads {
+  const void* in[3];
+  void* out[3];
+  long long ld[3], end[3];    // end: of its groups of eight among all
+  int C, Cp;
+};
+// The id-th group of eight.
+template <typename T>
+__device__ __forceinline__ void pad_group(const Pads& p, long long id) {
+  if (id >= p.end[2]) return;
+  const int k = id < p.end[0] ? 0 : id < p.end[1] ? 1 : 2;
+  const long long at = id - (k ? p.end[k - 1] : 0);
+  const unsigned per = p.Cp / 8;
+  const long long r = at / per;
+  const int c = (int)(at % per) * 8;
+  float v[8];
+  load_v<false, 8>((const T*)p.in[k] + r * p.ld[k] + c, p.C - c, v);
+  store_v<true, 8>((T*)p.out[k] + r * p.Cp + c, 8, v);
+}
+// Bytes that copies of x and the weights may take, and those that are needed: a's pointers
+// and strides are then the copies'. pads.end[2]: the groups to copy, none if 0.
 size_t aligned_bytes(long long R, int C, int F, int bf16);
-int align_operands(FfnArgs& a, char* room, hipStream_t s);
+Pads align_operands(FfnArgs& a, char* room);
 
 }  // namespace ffn
 }  // namespace osdn

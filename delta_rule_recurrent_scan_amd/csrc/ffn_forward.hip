@@ -215,6 +215,11 @@ bool forward_plan(Plan& p, long long R, int C, int F, int bf16) {
 }
 
 template <typename T>
+__global__ __launch_bounds__(256) void ffn_pad_kernel(Pads p) {
+  pad_group<T>(p, blockIdx.x * 256LL + threadIdx.x);
+}
+
+template <typename T>
 int run(const FfnArgs& a, hipStream_t s) {
   if (a.R <= 16) return run_rows<T, 1>(a, s);
   if (a.R <= 32) return run_rows<T, 2>(a, s);
@@ -223,8 +228,16 @@ int run(const FfnArgs& a, hipStream_t s) {
   if (!forward_plan(p, a.R, a.C, a.F, a.bf16)) return -1;
   FfnArgs b = a;
   b.parts = (float*)a.ws;
-  const int rc = align_operands(b, (char*)a.ws + round256(parts_bytes(p)), s);
-  if (rc) return rc;
+  const Pads pads = align_operands(b, (char*)a.ws + round256(parts_bytes(p)));
+  const long long wgs = (pads.end[2] + 255) / 256;
+  if (!grid_ok(wgs, 256)) return -1;
+  if (wgs > 0) {
+    const int tk = ktimer_before(s, "ffn_pad");
+    hipLaunchKernelGGL((ffn_pad_kernel<T>), dim3((unsigned)wgs), dim3(256), 0, s, pads);
+    ktimer_after(s, tk);
+    const int rc = (int)hipGetLastError();
+    if (rc) return rc;
+  }
   if constexpr (sizeof(T) == 2)
     if (p.shape == 0) return run_shape<T, Large>(b, p, s);
   if (p.shape == 1) return run_shape<T, Middle>(b, p, s);
@@ -247,7 +260,12 @@ constexpr Cost kBf16[] = {{256, 256, 1, 1.46, 1.46, 8.0}, {128, 128, 2, 0.73, 0.
 constexpr Cost kF32[] = {{0, 0, 0, 0, 0, 0}, {128, 128, 2, 2.5, 1.95, 4.0},
                          {64, 64, 4, 0.91, 0.64, 1.0}, {64, 128, 2, 1.2, 1.0, 2.0}};
 
-bool make_plan(Plan& best, Kind kind, long long M, long long N, long long K, int bf16) {
+// A second launch and its parts: written and read, each once.
+constexpr double kJoin = 6.5;
+double parts_time(long long parts, const Cost& c) { return (double)parts * c.bm * c.bn * 8 / 4e6; }
+
+bool make_plan(Plan& best, Kind kind, long long M, long long N, long long K, int bf16,
+               double* microseconds) {
   const int kt = bf16 ? kTileK<__bf16> : kTileK<float>;
   const long long nt = K > 0 ? (K + kt - 1) / kt : 1;
   double least = 1e300;
@@ -269,52 +287,71 @@ bool make_plan(Plan& best, Kind kind, long long M, long long N, long long K, int
       const long long per = (nt + s - 1) / s;
       if ((nt + per - 1) / per != s) continue;     // (no empty part)
       double t = time(whole, nt) + time(rest * s, per);
-      // parts written and read, and the launch that adds them
-      if (s > 1) t += 6.5 + (double)(rest * s) * c.bm * c.bn * 8 / 4e6;
+      if (s > 1) t += kJoin + parts_time(rest * s, c);
       if (t < least) {
         least = t;
-        best = Plan{k, (int)tm, (int)tn, (int)nt, (int)whole, s, (int)per, c.bm * c.bn};
+        best = Plan{k, (int)tm, (int)tn, (int)nt, (int)whole, s, (int)per, c.bm * c.bn, 0};
       }
     }
   }
+  if (microseconds) *microseconds = least;
   return least < 1e300;
+}
+
+// Two products that leave the card half empty each run side by side: all items of both on
+// the card at once, none whole rounds. Its time is that of the longest item alone or of a
+// CU's share of all the work.
+bool make_pair(Plan& p, Plan& q, const long long (&one)[3], const long long (&two)[3], int bf16,
+               double microseconds) {
+  const int kt = bf16 ? kTileK<__bf16> : kTileK<float>;
+  double least = microseconds;
+  const long long n1 = one[2] > 0 ? (one[2] + kt - 1) / kt : 1;
+  const long long n2 = two[2] > 0 ? (two[2] + kt - 1) / kt : 1;
+  for (int k = bf16 ? 0 : 1; k < 3; ++k) {
+    const Cost& c = (bf16 ? kBf16 : kF32)[k];
+    const long long m1 = (one[0] + c.bm - 1) / c.bm, c1 = (one[1] + c.bn - 1) / c.bn;
+    const long long m2 = 2 * ((two[0] + c.bm - 1) / c.bm), c2 = (two[1] + c.bn - 1) / c.bn;
+    const long long room = 256 * c.at_once;
+    if (m1 * c1 + m2 * c2 > room || m1 * c1 == 0 || m2 * c2 == 0) continue;
+    for (int s1 = 1; s1 <= 16 && (s1 == 1 || n1 / s1 >= 4); ++s1)
+      for (int s2 = 1; s2 <= 16 && (s2 == 1 || n2 / s2 >= 4); ++s2) {
+        const long long per1 = (n1 + s1 - 1) / s1, per2 = (n2 + s2 - 1) / s2;
+        if ((n1 + per1 - 1) / per1 != s1 || (n2 + per2 - 1) / per2 != s2) continue;
+        const long long w1 = m1 * c1 * s1, w2 = m2 * c2 * s2;
+        if (w1 + w2 > room) continue;
+        const long long longest = per1 > per2 ? per1 : per2;
+        const double all = c.share * (double)(w1 * per1 + w2 * per2) / 256;
+        double t = (longest * c.alone > all ? longest * c.alone : all) + c.each;
+        if (s1 > 1 || s2 > 1) t += kJoin;
+        if (s1 > 1) t += parts_time(w1, c);
+        if (s2 > 1) t += parts_time(w2, c);
+        if (t < least) {
+          least = t;
+          const int area = c.bm * c.bn;
+          p = Plan{k, (int)m1, (int)c1, (int)n1, 0, s1, (int)per1, area, 0};
+          q = Plan{k, (int)m2, (int)c2, (int)n2, 0, s2, (int)per2, area, 0};
+          q.parts_at = (long long)(parts_bytes(p) / sizeof(float));
+        }
+      }
+  }
+  return least < microseconds;
 }
 
 size_t parts_bytes(const Plan& p) {
   return p.splits > 1 ? (size_t)p.rest() * p.splits * p.area * sizeof(float) : 0;
 }
 
-namespace {
-
-// Up to three operands in one launch: rows of C elements to rows of Cp, zeros behind C.
-struct Pads {
-  const void* in[3];
-  void* out[3];
-  long long ld[3], end[3];    // end: of its groups of eight among all
-  int C, Cp;
-};
-template <typename T>
-__global__ __launch_bounds__(256) void ffn_pad_kernel(Pads p) {
-  const long long id = blockIdx.x * 256LL + threadIdx.x;
-  if (id >= p.end[2]) return;
-  const int k = id < p.end[0] ? 0 : id < p.end[1] ? 1 : 2;
-  const long long at = id - (k ? p.end[k - 1] : 0);
-  const unsigned per = p.Cp / 8;
-  const long long r = at / per;
-  const int c = (int)(at % per) * 8;
-  float v[8];
-  load_v<false, 8>((const T*)p.in[k] + r * p.ld[k] + c, p.C - c, v);
-  store_v<true, 8>((T*)p.out[k] + r * p.Cp + c, 8, v);
+size_t aligned_bytes(long long R, int C, int F, int bf16) {
+  const size_t row = (size_t)whole_eights(C) * (bf16 ? 2 : 4);
+  return round256(R * row) + (C % 8 ? 2 * round256(F * row) : 0);
 }
 
-template <typename T>
-int align_t(FfnArgs& a, char* room, hipStream_t s) {
+Pads align_operands(FfnArgs& a, char* room) {
+  const size_t es = a.bf16 ? 2 : 4;
   a.Cp = whole_eights(a.C);
   a.Fp = whole_eights(a.F);
-  const bool px = a.R > 0 && a.C > 0 &&
-                  (a.Cp != a.C || !on16(a.x) || a.xs * (long long)sizeof(T) % 16 != 0);
+  const bool px = a.R > 0 && a.C > 0 && (a.Cp != a.C || !on16(a.x) || a.xs * es % 16 != 0);
   const bool pw = a.Cp != a.C && a.F > 0;
-  if (!px && !pw) return 0;
   Pads p{};
   p.C = a.C;
   p.Cp = a.Cp;
@@ -325,7 +362,7 @@ int align_t(FfnArgs& a, char* room, hipStream_t s) {
     p.ld[k] = ld;
     end += rows * (a.Cp / 8);
     in = room;
-    room += round256((size_t)rows * a.Cp * sizeof(T));
+    room += round256((size_t)rows * a.Cp * es);
   };
   if (px) {
     take(0, a.x, a.xs, a.R);
@@ -336,23 +373,7 @@ int align_t(FfnArgs& a, char* room, hipStream_t s) {
   p.end[1] = end;
   if (pw) take(2, a.wu, a.C, a.F);
   p.end[2] = end;
-  const long long wgs = (end + 255) / 256;
-  if (!grid_ok(wgs, 256)) return -1;
-  const int tk = ktimer_before(s, "ffn_pad");
-  hipLaunchKernelGGL((ffn_pad_kernel<T>), dim3((unsigned)wgs), dim3(256), 0, s, p);
-  ktimer_after(s, tk);
-  return (int)hipGetLastError();
-}
-
-}  // namespace
-
-size_t aligned_bytes(long long R, int C, int F, int bf16) {
-  const size_t row = (size_t)whole_eights(C) * (bf16 ? 2 : 4);
-  return round256(R * row) + (C % 8 ? 2 * round256(F * row) : 0);
-}
-
-int align_operands(FfnArgs& a, char* room, hipStream_t s) {
-  return a.bf16 ? align_t<__bf16>(a, room, s) : align_t<float>(a, room, s);
+  return p;
 }
 
 }  // namespace ffn

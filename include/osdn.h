@@ -820,7 +820,8 @@ void osdn_kernel_timing(int enable);
  * ssm_bwd_parts, gated_norm, gated_norm_bwd, residual_norm, residual_norm_bwd,
  * column_sum (the operators around the recurrences), glr_part, glr, glr_decode,
  * glr_bwd_part, glr_bwd, qk_rotary, qk_rotary_bwd, ffn, ffn_join, ffn_rows, ffn_pad,
- * ffn_grad, ffn_dx, ffn_dx_join, ffn_dw, ffn_dw_join (the operators that complete a block).
+ * ffn_grad, ffn_dx, ffn_dx_join, ffn_dw, ffn_dw_join, ffn_dxdw, ffn_dxdw_join (the operators that
+ * complete a block).
  */
 int osdn_kernel_times(int max, const char** names, int* counts, float* mean_ms);
 
