@@ -37,16 +37,21 @@ constexpr int kTile = 2 * kWaves * K;
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 
 // Two channels of one token as they lie in memory. The base is the same in
-// all lanes and the byte offset 32 bits.
+// all lanes and the byte offset 32 bits. VEC: one access, of any alignment (global memory
+// takes them all: rows of 4096 bf16 channels 4097 apart 209 -> 140 us, their backward 370
+// -> 246). With an odd number of channels, where nothing is gained and the backward loses
+// (423 -> 510 us at 4095), by element.
+typedef unsigned __attribute__((aligned(2))) any_u32;
+typedef __attribute__((ext_vector_type(2), aligned(4))) float any_f32x2;
 template <typename T>
 struct Pair;
 template <>
 struct Pair<__bf16> {
   unsigned u;
-  template <bool ALN>
+  template <bool VEC>
   __device__ __forceinline__ void load(const char* base, unsigned o0, unsigned o1) {
-    if constexpr (ALN) {
-      u = *(const unsigned*)(base + o0);
+    if constexpr (VEC) {
+      u = *(const any_u32*)(base + o0);
     } else {
       u = (unsigned)*(const unsigned short*)(base + o0) |
           (unsigned)*(const unsigned short*)(base + o1) << 16;
@@ -59,11 +64,11 @@ struct Pair<__bf16> {
 template <>
 struct Pair<float> {
   float v[2];
-  template <bool ALN>
+  template <bool VEC>
   __device__ __forceinline__ void load(const char* base, unsigned o0, unsigned o1) {
-    if constexpr (ALN) {
-      const float2 t = *(const float2*)(base + o0);
-      v[0] = t.x; v[1] = t.y;
+    if constexpr (VEC) {
+      const any_f32x2 t = *(const any_f32x2*)(base + o0);
+      v[0] = t[0]; v[1] = t[1];
     } else {
       v[0] = *(const float*)(base + o0);
       v[1] = *(const float*)(base + o1);
@@ -783,12 +788,10 @@ int run_norm(const GlrArgs& a, hipStream_t s) {
 template <Call CALL, typename Tin>
 int run_t(const GlrArgs& a, hipStream_t s) {
   const size_t es = sizeof(Tin);
-  // every pair of channels starts on the size of a pair
-  const bool aln = a.C % 2 == 0 && a.xbs % 2 == 0 && a.xts % 2 == 0 && a.rbs % 2 == 0 &&
-                   a.rts % 2 == 0 && a.ibs % 2 == 0 && a.its % 2 == 0 && even(a.x, es) &&
-                   even(a.r, es) && even(a.i, es) && even(a.y, es) && even(a.dy, es) &&
-                   even(a.dx, es) && even(a.dr, es) && even(a.di, es) && even(a.h0, 4) &&
-                   even(a.hT, 4) && even(a.states, 4) && even(a.dh0, 4);
+  // every pair of channels exists and is stored where a pair may start (inputs are read at
+  // any alignment)
+  const bool aln = a.C % 2 == 0 && even(a.y, es) && even(a.dx, es) && even(a.dr, es) &&
+                   even(a.di, es) && even(a.hT, 4) && even(a.states, 4) && even(a.dh0, 4);
   if (aln) return a.i ? run_norm<CALL, Tin, true, true>(a, s) : run_norm<CALL, Tin, true, false>(a, s);
   return a.i ? run_norm<CALL, Tin, false, true>(a, s) : run_norm<CALL, Tin, false, false>(a, s);
 }
