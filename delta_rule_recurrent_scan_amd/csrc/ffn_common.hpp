@@ -3,18 +3,24 @@
 // along them (MN-major).
 //
 // A workgroup forms a BM x BN tile. Tiles of 128 bytes of k (64 bf16, 32 fp32) go
-// from global memory straight to LDS, 16 bytes a lane, into the one of two stages
-// that is not being read; each wave feeds its matrix instructions from the other.
+// from global memory straight to LDS, 16 bytes a lane, two tiles ahead of the one
+// that is used, through five buffers in turn; each wave fetches the operands of its next
+// matrix instructions while the last are worked off. A tile of k of 256 x 256 bf16 takes
+// 1.46 us (1470 TFLOP/s); what a product loses against that is its start, its results'
+// way to memory, and rounds of tiles that do not fill the card. Those are cut along k and
+// added by a second launch, in a fixed order, where a model of these costs says that it
+// pays (make_plan).
+//
 // LDS rows are swizzled in units of 16 bytes, so that the lanes that are served
 // together lie on different banks: unit u of K-major row r at u ^ (r & 7), of
-// MN-major row k at u ^ 2 f(k). MN-major bf16 is read by the LDS transpose load,
-// which gives a lane the run of k that a K-major row would.
+// MN-major row k at u ^ 2 f(k) (fp32: u ^ (k & 12)). MN-major bf16 is read by the LDS
+// transpose load, which gives a lane the run of k that a K-major row would.
 //
 // The last part of k goes through registers, with zeros behind the end of k. Rows
 // behind m and n repeat the last one; their products are not stored. All rows start on
 // 16 bytes and hold whole eights of elements: operands that do not are first copied so
 // (777 x 1021 x 2001 in bf16: with rows of any alignment through registers the products
-// took 40 to 97 us).
+// took 40 to 97 us, now 22 to 28).
 #pragma once
 
 #include "device_common.hpp"

@@ -3,10 +3,13 @@
 // activation and the product are taken from the accumulators in 32 bits and only
 // h (and, where a backward pass is to follow, g and u) are rounded and stored.
 //
-// Bound by the matrix units where there are many rows; by the weights' bytes for a
-// few (up to 64), which have a kernel of their own: 16 columns of both weights a
+// Bound by the matrix units where there are many rows: 8192 x 2048 x 5632 bf16 takes 360
+// us with g and u kept (1050 TFLOP/s) and 317 without (1190): a tile's results are 3 x 64
+// KB that its CU writes while it multiplies nothing. Bound by the weights' bytes for a few
+// rows (up to 64), which have a kernel of their own: 16 columns of both weights a
 // workgroup, its eight waves taking tiles of k in turn straight from memory into
-// registers, their sums joined in LDS.
+// registers, their sums joined in LDS (8 rows of the same weights: 13 us for 46 MB, of
+// which 4 are the launch).
 #include "ffn_common.hpp"
 
 namespace osdn {

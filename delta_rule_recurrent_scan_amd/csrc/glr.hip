@@ -8,12 +8,19 @@
 //
 // A workgroup walks the tokens of one sequence (or a segment of it) for 64
 // channels, a tile of 128 or 256 tokens at a time: a thread holds 8 or 16
-// tokens of 2 channels, two threads a wave's half each, eight waves a tile. Every thread
-// runs its own tokens from zero, the ends are joined over the waves through
-// LDS with one barrier a tile, and a second run over the registers from the
+// tokens of 2 channels, a wave two threads for each pair of channels, a tile eight
+// waves. Every thread runs its own tokens from zero, the ends are joined over the waves
+// through LDS with one barrier a tile, and a second run over the registers from the
 // joined state gives the results: every input is read once and every output
 // written once. Where the sequences and channels alone leave CUs idle the
 // tokens are cut into segments, whose sums a first launch forms.
+//
+// Bound by HBM, with the vector units close behind (some 45 instructions an element):
+// 4 x 4096 x 4096 bf16 with an input gate and the states 104 us for 554 MB (5.3 TB/s),
+// backward 220 us for 957 MB (4.4 TB/s; rows of 24 KB, 207 us with rows off that stride),
+// 1 x 9001 x 1536 fp32 in segments, the states alone, 57 us for 336 MB and the backward
+// from them 84 us for 498 MB (5.9 TB/s). Short calls are their launches: 13 us of host and 4 us of kernel for a
+// token of 128 x 4096 channels.
 //
 // Decays lie close to one and act over thousands of tokens. A product of
 // rounded decays would be off by their common rounding times the number of

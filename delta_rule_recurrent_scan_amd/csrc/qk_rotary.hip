@@ -9,7 +9,9 @@
 //   dx = r (f - n mean(n f))   (l2: sum; none: dx = f).
 //
 // Bound by HBM: every row is read and written once, 8 channels a lane, a head
-// being 4, 8 or 16 adjacent lanes. A workgroup takes a few tokens with all their
+// being 4, 8 or 16 adjacent lanes (16384 tokens of 32 heads of 128 bf16: 56 us for 269 MB,
+// 4.8 TB/s; backward of 20 heads with fp32 adjoints 66 us for 336 MB, 5.1 TB/s, and 5 us
+// of column sum). A workgroup takes a few tokens with all their
 // heads, so that an angle is worked out once for all heads: in turns and in 64
 // bits (a position of 2^31 keeps 29 bits of its turn), its cosine and sine in 32,
 // left in LDS. Weight gradients stay in registers while a workgroup walks its

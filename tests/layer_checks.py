@@ -7,10 +7,10 @@ values of the terms). Units of 2^-24 are counted along the path:
 
 * recurrence: a decay exp2(A log2(e) sigmoid(r)) is off by 2 units for the exp2 and
   6 times its logarithm for the argument, |la| exp(-|la|) <= 1/e of a whole memory:
-  under 3 together however long the memory is; each of the 8 tokens of a thread
-  rounds twice; every 16 tokens the carried state is rounded once more and its
-  factor's distance from one is off by 4 units of itself (again under 2 over a
-  memory). With the input factor (8), sigmoid(i) (4 and |i| <= 8 times its slope) and
+  under 3 together however long the memory is; each of the up to 16 tokens of a thread
+  rounds once; every two threads (16 tokens or more) the carried state is rounded once
+  more and its factor's distance from one is off by 4 units of itself (again under 2 over
+  a memory). With the input factor (8), sigmoid(i) (4 and |i| <= 8 times its slope) and
   the products: 48 + T / 16. The gradients pass through two such chains and three
   more factors: 112 + T / 8.
 * rotary: the sum of squares of a row is 8 additions a lane and 4 levels, its root 4
