@@ -12,7 +12,8 @@ import ctypes
 import torch
 
 from . import _DTYPE_CODE, load_library
-from .mixer import _begin, _call, _check, _ptr, _required, _rows
+from . import _check as _check_slow
+from .mixer import _begin, _call, _check, _ptr, _required
 from .mixer import _workspace as _any_workspace
 
 __all__ = ["glr_forward", "glr_decode", "glr_backward",
@@ -67,23 +68,36 @@ def _workspace(ws, need, dev):
     return ws.data_ptr(), ws.numel(), ws
 
 
+def _rows(t, name, shape, dt, dev):
+    """(pointer, batch stride, token stride) of token rows [B,T,C] with any strides over
+    tokens and batch entries."""
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dt
+            and t.device == dev):
+        if t is None:
+            raise ValueError("%s is required" % name)
+        _check_slow(t, name, shape, dt, dev)
+    bs, ts, cs = t.stride()
+    if cs != 1 and shape[2] > 1 and t.numel():
+        raise ValueError("%s must be contiguous along its channels" % name)
+    # strides of dimensions of one entry are never used and may be anything
+    return t.data_ptr(), bs if shape[0] > 1 else 0, ts if shape[1] > 1 else 0
+
+
 # ---------------------------------------------------------------------------
 # Gated linear recurrence
 # ---------------------------------------------------------------------------
 
 def _glr_checks(x, r, A, i):
     L, code, dev = _begin(x, "x")
-    if x.dim() != 3:
+    shape, dt = x.shape, x.dtype
+    if len(shape) != 3:
         raise ValueError("x must be [B, T, C]")
-    B, T, C = x.shape
-    rows = (_ptr(x),) + _rows(x, "x", B, T, C, x.dtype, dev)
-    rows += (_ptr(r),) + _rows(r, "r", B, T, C, x.dtype, dev)
-    rows += ((None, 0, 0) if i is None
-             else (_ptr(i),) + _rows(i, "i", B, T, C, x.dtype, dev))
     if A is None:
         raise ValueError("A is required")
-    _check(A, "A", (C,), torch.float32, dev)
-    return L, dev, (B, T, C), (B, T, C, code) + rows + (_ptr(A),)
+    _check(A, "A", shape[2:], torch.float32, dev)
+    return L, dev, shape, (
+        *shape, code, *_rows(x, "x", shape, dt, dev), *_rows(r, "r", shape, dt, dev),
+        *((None, 0, 0) if i is None else _rows(i, "i", shape, dt, dev)), A.data_ptr())
 
 
 def glr_forward_workspace_bytes(B, T, C):
@@ -136,11 +150,11 @@ def glr_decode(x, r, A, h, i=None, normalize=True, out=None, h_out=None):
         ho = h_out
         _check(ho, "h_out", (B, C), torch.float32, dev)
     if out is None:
-        y = torch.empty((B, T, C), dtype=x.dtype, device=dev)
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
     else:
         _check(y, "y", (B, T, C), x.dtype, dev)
-    _call(L.glr_decode, "glr_decode", dev, *args, _ptr(h), int(normalize), _ptr(y),
-          _ptr(ho))
+    _call(L.glr_decode, "glr_decode", dev, *args, h.data_ptr(), int(normalize),
+          y.data_ptr(), ho.data_ptr())
     return y
 
 
@@ -213,7 +227,7 @@ def _qk_checks(q, k, head_dim, inv_freq, q_weight, k_weight, positions, lengths,
         if D < 1 or C % D:
             raise ValueError("head_dim %d does not divide the %d channels" % (D, C))
         heads.append(C // D)
-        rows += (t.data_ptr(),) + _rows(t, name, B, T, C, dt, dev)
+        rows += _rows(t, name, (B, T, C), dt, dev)
     rot = 0
     if inv_freq is not None:
         if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
@@ -254,9 +268,8 @@ def qk_rotary_forward(q, k, head_dim, inv_freq=None, q_weight=None, k_weight=Non
         q, k, head_dim, inv_freq, q_weight, k_weight, positions, lengths, norm,
         interleaved, eps)
     if out is None:
-        yq, yk = (None if t is None else
-                  torch.empty((B, H, T, D), dtype=dt, device=dev)
-                  for t, H in ((q, Hq), (k, Hk)))
+        yq = None if q is None else q.new_empty((B, Hq, T, D))
+        yk = None if k is None else k.new_empty((B, Hk, T, D))
     else:
         yq, yk = out
         _check(yq, "out[0]", (B, Hq, T, D), dt, dev)
@@ -368,7 +381,7 @@ def gated_ffn_forward(x, w_gate, w_up, activation="silu", save=False, out=None,
     L, code, dev, (R, C, F), args = _ffn_checks(x, w_gate, w_up, activation)
     shape = tuple(x.shape[:-1]) + (F,)
     if out is None:
-        h = torch.empty(shape, dtype=x.dtype, device=dev)
+        h = x.new_empty(shape)
         gate, up = ((torch.empty_like(h), torch.empty_like(h)) if save
                     else (None, None))
     else:

@@ -240,3 +240,25 @@ def test_gradient_against_differences():
         scale = float((d[n].double() * v.double()).norm()) + 64 * UNIT * 100 / e
         print(n, num, want, scale, flush=True)
         assert abs(num - want) <= 2e-2 * scale
+
+
+def test_wrong_tensors_are_refused():
+    """What is missing, of another shape or type, or strided along its channels names
+    itself in a ValueError or TypeError before the library is called."""
+    x, A = torch.zeros(2, 3, 8, device=DEV), torch.zeros(8, device=DEV)
+    h = torch.zeros(2, 8, device=DEV)
+    for bad in (None, x[:1], x.double(), x.cpu(), x.transpose(0, 2).contiguous().transpose(0, 2),
+                1.0):
+        for call in (lambda: osdn.glr_forward(x, bad, A),
+                     lambda: osdn.glr_backward(x, bad, A, x),
+                     lambda: osdn.glr_decode(x, bad, A, h)):
+            with pytest.raises((ValueError, TypeError)):
+                call()
+    for bad in (None, A[:7], A.double(), torch.zeros(16, device=DEV)[::2]):
+        with pytest.raises((ValueError, TypeError)):
+            osdn.glr_forward(x, x, bad)
+    with pytest.raises(ValueError):
+        osdn.glr_forward(x[0], x[0], A)
+    for bad in (None, h[:1], h.double(), h.t().contiguous().t()):
+        with pytest.raises((ValueError, TypeError)):
+            osdn.glr_decode(x, x, A, bad)
