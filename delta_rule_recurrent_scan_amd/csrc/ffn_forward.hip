@@ -310,18 +310,32 @@ bool make_pair(Plan& p, Plan& q, const long long (&one)[3], const long long (&tw
   double least = microseconds;
   const long long n1 = one[2] > 0 ? (one[2] + kt - 1) / kt : 1;
   const long long n2 = two[2] > 0 ? (two[2] + kt - 1) / kt : 1;
+  // the parts that n tiles of k may be cut into, and their lengths
+  struct Cuts {
+    int n = 0, s[16];
+    long long per[16];
+    explicit Cuts(long long nt) {
+      for (int k = 1; k <= 16 && (k == 1 || nt >= 4 * k); ++k) {
+        const long long len = (nt + k - 1) / k;
+        if (len * (k - 1) >= nt) continue;         // (an empty part)
+        s[n] = k;
+        per[n++] = len;
+      }
+    }
+  };
+  const Cuts u(n1), v(n2);
   for (int k = bf16 ? 0 : 1; k < 3; ++k) {
     const Cost& c = (bf16 ? kBf16 : kF32)[k];
     const long long m1 = (one[0] + c.bm - 1) / c.bm, c1 = (one[1] + c.bn - 1) / c.bn;
     const long long m2 = 2 * ((two[0] + c.bm - 1) / c.bm), c2 = (two[1] + c.bn - 1) / c.bn;
     const long long room = 256 * c.at_once;
     if (m1 * c1 + m2 * c2 > room || m1 * c1 == 0 || m2 * c2 == 0) continue;
-    for (int s1 = 1; s1 <= 16 && (s1 == 1 || n1 / s1 >= 4); ++s1)
-      for (int s2 = 1; s2 <= 16 && (s2 == 1 || n2 / s2 >= 4); ++s2) {
-        const long long per1 = (n1 + s1 - 1) / s1, per2 = (n2 + s2 - 1) / s2;
-        if ((n1 + per1 - 1) / per1 != s1 || (n2 + per2 - 1) / per2 != s2) continue;
+    for (int i = 0; i < u.n; ++i)
+      for (int j = 0; j < v.n; ++j) {
+        const int s1 = u.s[i], s2 = v.s[j];
+        const long long per1 = u.per[i], per2 = v.per[j];
         const long long w1 = m1 * c1 * s1, w2 = m2 * c2 * s2;
-        if (w1 + w2 > room) continue;
+        if (w1 + w2 > room) break;                 // (more parts are more)
         const long long longest = per1 > per2 ? per1 : per2;
         const double all = c.share * (double)(w1 * per1 + w2 * per2) / 256;
         double t = (longest * c.alone > all ? longest * c.alone : all) + c.each;

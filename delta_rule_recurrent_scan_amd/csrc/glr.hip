@@ -19,8 +19,8 @@
 // 4 x 4096 x 4096 bf16 with an input gate and the states 104 us for 554 MB (5.3 TB/s),
 // backward 220 us for 957 MB (4.4 TB/s; rows of 24 KB, 207 us with rows off that stride),
 // 1 x 9001 x 1536 fp32 in segments, the states alone, 57 us for 336 MB and the backward
-// from them 84 us for 498 MB (5.9 TB/s). Short calls are their launches: 13 us of host and 4 us of kernel for a
-// token of 128 x 4096 channels.
+// from them 84 us for 498 MB (5.9 TB/s). Short calls are their launches: 11 us of host and
+// 4 us of kernel for a token of 128 x 4096 channels.
 //
 // Decays lie close to one and act over thousands of tokens. A product of
 // rounded decays would be off by their common rounding times the number of
