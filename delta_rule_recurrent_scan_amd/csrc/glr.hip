@@ -176,9 +176,12 @@ __device__ __forceinline__ float other_half(float x) {
 // of its wave and the waves before (FWD: 0 .. 7 in turn, else 7 .. 0). Returns
 // the state that enters this thread's tokens in `in` and carries the tile's.
 //
-// The carried state is updated as c + (H - (1 - exp2(L)) c): the factor's
-// distance from one keeps its digits, so that steps of long memory do not add up
-// the factors' roundings.
+// The carried state is updated as c + (H - (1 - exp2(L)) c) where exp2(L) is between a
+// half and one: the factor's distance from one keeps its digits, so that steps of long
+// memory do not add up the factors' roundings. Below (and above one, where A is positive)
+// it is exp2(L) c + H: from the distance a small factor would lose its digits, and H what
+// c outweighs. What is passed on is -|1 - exp2(L)|, told by its sign bit (zero's too), or
+// exp2(L).
 template <bool FWD>
 __device__ __forceinline__ void join(const float (&L)[2], const float (&H)[2], float (&carry)[2],
                                      float (&in)[2], float4* buf) {
@@ -187,11 +190,11 @@ __device__ __forceinline__ void join(const float (&L)[2], const float (&H)[2], f
   float p[2], po[2], Ho[2], Q[2], E[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const float l = 0.5f * (L[j] + other_half(L[j]));
+    const float l = 0.5f * (L[j] + other_half(L[j])), e = __builtin_amdgcn_exp2f(l);
     p[j] = __builtin_amdgcn_exp2f(L[j]);
     po[j] = other_half(p[j]);
     Ho[j] = other_half(H[j]);
-    Q[j] = one_minus_square(l, __builtin_amdgcn_exp2f(l));
+    Q[j] = l > -0.5f && l <= 0.f ? -fabsf(one_minus_square(l, e)) : e * e;
     E[j] = fmaf(p[j], Ho[j], H[j]);
   }
   if (!first) buf[w * 32 + (lane & 31)] = float4{Q[0], E[0], Q[1], E[1]};
@@ -205,8 +208,8 @@ __device__ __forceinline__ void join(const float (&L)[2], const float (&H)[2], f
       m0 = c0;
       m1 = c1;
     }
-    c0 += fmaf(-t.x, c0, t.y);
-    c1 += fmaf(-t.z, c1, t.w);
+    c0 = fmaf(t.x, c0, t.y) + (__float_as_int(t.x) < 0 ? c0 : 0.f);
+    c1 = fmaf(t.z, c1, t.w) + (__float_as_int(t.z) < 0 ? c1 : 0.f);
   }
   carry[0] = c0;
   carry[1] = c1;
