@@ -142,14 +142,19 @@ struct Rows {
   }
 };
 
-// 1 - 4^w for w <= 0 with e = 2^w: from -1/4 on, where the difference would lose
-// digits, w times the polynomial of degree 4 through the Chebyshev nodes of that range
-// (1.4e-8 off, 1.3e-7 with its roundings).
-__device__ __forceinline__ float one_minus_square(float w, float e) {
+// (1 - 4^w) / w for w in (-1/4, 0]: the polynomial of degree 4 through the Chebyshev
+// nodes of that range (1.4e-8 off, 1.3e-7 with its roundings).
+__device__ __forceinline__ float square_slope(float w) {
   float p = fmaf(-0.03698064014f, w, -0.15267968178f);
   p = fmaf(p, w, -0.44392627478f);
   p = fmaf(p, w, -0.96090275049f);
-  p = fmaf(p, w, -1.38629436493f);
+  return fmaf(p, w, -1.38629436493f);
+}
+
+// 1 - 4^w for w <= 0 with e = 2^w: from -1/4 on, where the difference would lose
+// digits, from the polynomial.
+__device__ __forceinline__ float one_minus_square(float w, float e) {
+  const float p = square_slope(w);     // (a branch around it costs more)
   return w > -0.25f ? w * p : fmaf(-e, e, 1.f);
 }
 
@@ -176,11 +181,11 @@ __device__ __forceinline__ float other_half(float x) {
 // of its wave and the waves before (FWD: 0 .. 7 in turn, else 7 .. 0). Returns
 // the state that enters this thread's tokens in `in` and carries the tile's.
 //
-// The carried state is updated as c + (H - (1 - exp2(L)) c) where exp2(L) is between a
-// half and one: the factor's distance from one keeps its digits, so that steps of long
+// The carried state is updated as c + (H - (1 - exp2(L)) c) where exp2(L) is between 0.7
+// and one: the factor's distance from one keeps its digits, so that steps of long
 // memory do not add up the factors' roundings. Below (and above one, where A is positive)
 // it is exp2(L) c + H: from the distance a small factor would lose its digits, and H what
-// c outweighs. What is passed on is -|1 - exp2(L)|, told by its sign bit (zero's too), or
+// c outweighs. What is passed on is exp2(L) - 1, told by its sign bit (zero's too), or
 // exp2(L).
 template <bool FWD>
 __device__ __forceinline__ void join(const float (&L)[2], const float (&H)[2], float (&carry)[2],
@@ -190,11 +195,14 @@ __device__ __forceinline__ void join(const float (&L)[2], const float (&H)[2], f
   float p[2], po[2], Ho[2], Q[2], E[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const float l = 0.5f * (L[j] + other_half(L[j])), e = __builtin_amdgcn_exp2f(l);
+    // (n: minus half the logarithm; as a number it is under 1/4 only if it is positive)
+    const float n = -0.5f * (L[j] + other_half(L[j]));
+    const bool near = __float_as_uint(n) < __float_as_uint(0.25f);
     p[j] = __builtin_amdgcn_exp2f(L[j]);
     po[j] = other_half(p[j]);
     Ho[j] = other_half(H[j]);
-    Q[j] = l > -0.5f && l <= 0.f ? -fabsf(one_minus_square(l, e)) : e * e;
+    const float q = n * square_slope(-n);
+    Q[j] = near ? q : p[j] * po[j];
     E[j] = fmaf(p[j], Ho[j], H[j]);
   }
   if (!first) buf[w * 32 + (lane & 31)] = float4{Q[0], E[0], Q[1], E[1]};
