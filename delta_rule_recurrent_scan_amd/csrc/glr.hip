@@ -50,28 +50,33 @@ constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 // (423 -> 510 us at 4095), by element.
 typedef unsigned __attribute__((aligned(2))) any_u32;
 typedef __attribute__((ext_vector_type(2), aligned(4))) float any_f32x2;
-template <typename T>
+template <typename T, bool VEC>
 struct Pair;
 template <>
-struct Pair<__bf16> {
+struct Pair<__bf16, true> {
   unsigned u;
-  template <bool VEC>
   __device__ __forceinline__ void load(const char* base, unsigned o0, unsigned o1) {
-    if constexpr (VEC) {
-      u = *(const any_u32*)(base + o0);
-    } else {
-      u = (unsigned)*(const unsigned short*)(base + o0) |
-          (unsigned)*(const unsigned short*)(base + o1) << 16;
-    }
+    u = *(const any_u32*)(base + o0);
   }
   __device__ __forceinline__ float get(int j) const { return j ? high_bf16(u) : low_bf16(u); }
   __device__ __forceinline__ void shut() { u = 0xff80ff80u; }   // -inf
   __device__ __forceinline__ void zero() { u = 0u; }
 };
+// (joined to one register each element would be waited for where it is loaded)
 template <>
-struct Pair<float> {
+struct Pair<__bf16, false> {
+  unsigned u[2];
+  __device__ __forceinline__ void load(const char* base, unsigned o0, unsigned o1) {
+    u[0] = *(const unsigned short*)(base + o0);
+    u[1] = *(const unsigned short*)(base + o1);
+  }
+  __device__ __forceinline__ float get(int j) const { return low_bf16(u[j]); }
+  __device__ __forceinline__ void shut() { u[0] = u[1] = 0xff80u; }
+  __device__ __forceinline__ void zero() { u[0] = u[1] = 0u; }
+};
+template <bool VEC>
+struct Pair<float, VEC> {
   float v[2];
-  template <bool VEC>
   __device__ __forceinline__ void load(const char* base, unsigned o0, unsigned o1) {
     if constexpr (VEC) {
       const any_f32x2 t = *(const any_f32x2*)(base + o0);
@@ -123,7 +128,7 @@ __device__ __forceinline__ Place place(int cb, int C) {
 // One input's rows of a tile.
 template <typename Tin, bool ALN, int K>
 struct Rows {
-  Pair<Tin> v[K];
+  Pair<Tin, ALN> v[K];
   // Token k of the thread's in the tile's rows at p with stride ts; tokens from n on read
   // token n - 1 (WHOLE: there are none).
   template <bool WHOLE>
@@ -134,10 +139,10 @@ struct Rows {
     const unsigned b0 = pl.c0 * (unsigned)sizeof(Tin), b1 = pl.c1 * (unsigned)sizeof(Tin);
     if constexpr (WHOLE) {
       const unsigned o = row * (unsigned)(pl.seg * K);
-      v[k].template load<ALN>(base + (size_t)row * k, o + b0, o + b1);
+      v[k].load(base + (size_t)row * k, o + b0, o + b1);
     } else {
       const unsigned o = row * (unsigned)min(pl.seg * K + k, n - 1 - tile);
-      v[k].template load<ALN>(base, o + b0, o + b1);
+      v[k].load(base, o + b0, o + b1);
     }
   }
 };
@@ -158,11 +163,26 @@ __device__ __forceinline__ float one_minus_square(float w, float e) {
   return w > -0.25f ? w * p : fmaf(-e, e, 1.f);
 }
 
-// Decay and input factor of one token and channel: A2 = A log2(e).
+// sigmoid(x) and 1 - sigmoid(x) = exp(-x) sigmoid(x): from the rounded sigmoid the
+// difference has no digits left at an open gate (off by 5e-4 at 10, 17 % at 15). Where
+// exp(-x) is infinite the product is NaN, which the minimum drops.
+__device__ __forceinline__ float sigmoid_and_rest(float x, float& rest) {
+  const float e = __builtin_amdgcn_exp2f(-kLog2e * x), s = __builtin_amdgcn_rcpf(1.f + e);
+  rest = fminf(e * s, 1.f);
+  return s;
+}
+
+// The smaller of sigmoid(x) and the rest with x's sign: both in one register, as the
+// larger is one less it.
+__device__ __forceinline__ float lesser(float s, float rest, float x) {
+  float v = copysignf(fminf(s, rest), x);
+  asm("" : "+v"(v));     // (else its size and its sign are kept apart)
+  return v;
+}
+
+// Decay and input factor of one token and channel: rho = sigmoid(r), A2 = A log2(e).
 template <bool NORM>
-__device__ __forceinline__ void factors(float r, float A2, float& rho, float& l2, float& a,
-                                        float& m) {
-  rho = sigmoid_f(r);
+__device__ __forceinline__ void factors(float rho, float A2, float& l2, float& a, float& m) {
   l2 = A2 * rho;
   a = __builtin_amdgcn_exp2f(l2);
   m = NORM ? __builtin_amdgcn_sqrtf(one_minus_square(l2, a)) : 1.f;
@@ -317,8 +337,8 @@ __global__ __launch_bounds__(kThreads) void glr_kernel(GlrArgs a, int ncb, int S
       for (int k = 0; k < K; ++k) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float rho, l2, m;
-          factors<NORM>(rr.v[k].get(j), A2[j], rho, l2, dec[k][j], m);
+          float l2, m;
+          factors<NORM>(sigmoid_f(rr.v[k].get(j)), A2[j], l2, dec[k][j], m);
           float u = rx.v[k].get(j);
           if constexpr (GATE) u *= sigmoid_f(ri.v[k].get(j));
           in[k][j] = m * u;
@@ -418,16 +438,16 @@ __global__ __launch_bounds__(256) void glr_decode_kernel(GlrArgs a) {
   const float A2[2] = {a.A[c] * kLog2e, a.A[c1] * kLog2e};
   float h[2] = {a.h0[(size_t)b * a.C + c], a.h0[(size_t)b * a.C + c1]};
   for (int t = 0; t < a.T; ++t) {
-    Pair<Tin> x, r, g;
+    Pair<Tin, ALN> x, r, g;
     const unsigned o = (unsigned)(c1 - c) * (unsigned)sizeof(Tin);
-    x.template load<ALN>((const char*)((const Tin*)a.x + b * a.xbs + t * a.xts + c), 0, o);
-    r.template load<ALN>((const char*)((const Tin*)a.r + b * a.rbs + t * a.rts + c), 0, o);
+    x.load((const char*)((const Tin*)a.x + b * a.xbs + t * a.xts + c), 0, o);
+    r.load((const char*)((const Tin*)a.r + b * a.rbs + t * a.rts + c), 0, o);
     if constexpr (GATE)
-      g.template load<ALN>((const char*)((const Tin*)a.i + b * a.ibs + t * a.its + c), 0, o);
+      g.load((const char*)((const Tin*)a.i + b * a.ibs + t * a.its + c), 0, o);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      float rho, l2, d, m, u = x.get(j);
-      factors<NORM>(r.get(j), A2[j], rho, l2, d, m);
+      float l2, d, m, u = x.get(j);
+      factors<NORM>(sigmoid_f(r.get(j)), A2[j], l2, d, m);
       if constexpr (GATE) u *= sigmoid_f(g.get(j));
       h[j] = fmaf(d, h[j], m * u);
     }
@@ -526,6 +546,10 @@ template <typename Tin, bool ALN, bool GATE, bool NORM>
 __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrArgs a, int ncb, int S,
                                                            float* parts) {
   constexpr int K = kBK, TILE = kTile<K>;
+  // fp32 rows and pairs by element take twice the registers of paired bf16 ones: rho and
+  // its slope are then kept in one (4 x 4096 x 4095 fp32 564 -> 551 us, as separate ones
+  // with what spills 572).
+  constexpr bool TIGHT = !ALN || sizeof(Tin) == 4;
   __shared__ float4 buf[2][kWaves * 32];
   __shared__ double red[2 * kWaves][kCols];
   const int cb = blockIdx.x % ncb, bq = blockIdx.x / ncb, q = bq % S, b = bq / S;
@@ -547,9 +571,11 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrArgs a, int ncb, i
   float s0 = 0.f, s1 = 0.f;
   auto fetch = [&](auto whole, int k, int tile) {
     rr.template load<whole()>(k, r, a.rts, tile, n, pl);
-    rd.template load<whole()>(k, dy, a.C, tile, n, pl);
     rx.template load<whole()>(k, x, a.xts, tile, n, pl);
     if constexpr (GATE) ri.template load<whole()>(k, gi, a.its, tile, n, pl);
+  };
+  auto fetch_dy = [&](auto whole, int k, int tile) {
+    rd.template load<whole()>(k, dy, a.C, tile, n, pl);
   };
   auto fetch_state = [&](int tile) {
     const int si = min((tile + pl.seg * K) / kGlrInterval, ns - 1);
@@ -561,7 +587,10 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrArgs a, int ncb, i
   if (t0 < t1) {
     fetch_state(last);
 #pragma unroll
-    for (int k = 0; k < K; ++k) fetch(std::false_type(), k, last);
+    for (int k = 0; k < K; ++k) {
+      fetch(std::false_type(), k, last);
+      fetch_dy(std::false_type(), k, last);
+    }
   }
   int par = 0;
   for (int tile = last; tile >= t0; tile -= TILE, par ^= 1) {
@@ -576,18 +605,32 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrArgs a, int ncb, i
           rd.v[k].zero();
         }
     }
-    float rho[K][2], dec[K][2], m[K][2], sg[K][2], u[K][2], d[K][2];
+    // What the results take from a token, with g the adjoint of its state: the factors
+    // of dx (sx), di (si), dr (slope) and dA (rho), and bw: the state before it less what
+    // reaches log a through m, by which dla = a g bw.
+    float rho[K][2], slope[K][2], dec[K][2], in[K][2], sx[K][2], si[K][2], bw[K][2], kept[K][2];
     float L[2] = {0.f, 0.f}, H[2] = {0.f, 0.f}, st[2] = {s0, s1};
     const int next = max(tile - TILE, t0);
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float l2;
-        factors<NORM>(rr.v[k].get(j), A2[j], rho[k][j], l2, dec[k][j], m[k][j]);
-        sg[k][j] = GATE ? sigmoid_f(ri.v[k].get(j)) : 1.f;
-        u[k][j] = rx.v[k].get(j) * sg[k][j];
-        d[k][j] = rd.v[k].get(j);
+        float l2, m, rest, u = rx.v[k].get(j);
+        rho[k][j] = sigmoid_and_rest(rr.v[k].get(j), rest);
+        slope[k][j] = rho[k][j] * rest;
+        if constexpr (TIGHT) kept[k][j] = lesser(rho[k][j], rest, rr.v[k].get(j));
+        L[j] += rho[k][j];
+        factors<NORM>(rho[k][j], A2[j], l2, dec[k][j], m);
+        sx[k][j] = m;
+        if constexpr (GATE) {
+          const float sg = sigmoid_and_rest(ri.v[k].get(j), rest);
+          u *= sg;
+          sx[k][j] *= sg;
+          si[k][j] = m * u * rest;
+        }
+        in[k][j] = m * u;
+        // (where a is one no gradient passes through m)
+        bw[k][j] = NORM && m > 0.f ? dec[k][j] * u * __builtin_amdgcn_rcpf(m) : 0.f;
       }
     // (token by token as in the forward the registers run out: 211 against 206 us)
     fetch_state(next);
@@ -603,26 +646,22 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrArgs a, int ncb, i
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        L[j] += rho[k][j];
-        F[j] = fmaf(dec[k][j], F[j], m[k][j] * u[k][j]);
-      }
+      for (int j = 0; j < 2; ++j) F[j] = fmaf(dec[k][j], F[j], in[k][j]);
     L[0] *= A2[0];
     L[1] *= A2[1];
 #pragma unroll
     for (int k = K - 1; k >= 0; --k)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) H[j] = dec[k][j] * (H[j] + d[k][j]);
+      for (int j = 0; j < 2; ++j) H[j] = dec[k][j] * (H[j] + rd.v[k].get(j));
     // the state before the second half's tokens is the first half's end
     const float f0 = other_half(F[0]), f1 = other_half(F[1]);
     float h[2] = {low ? st[0] : f0, low ? st[1] : f1};
-    float before[K][2];
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        before[k][j] = h[j];
-        h[j] = fmaf(dec[k][j], h[j], m[k][j] * u[k][j]);
+        bw[k][j] = h[j] - bw[k][j];
+        h[j] = fmaf(dec[k][j], h[j], in[k][j]);
       }
     float c[2], sA[2] = {0.f, 0.f};
     join<false>(L, H, carry, c, buf[par]);
@@ -637,20 +676,19 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrArgs a, int ncb, i
         float ox[2], orr[2], oi[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float g = d[k][j] + c[j];
+          const float g = rd.v[k].get(j) + c[j];
           c[j] = dec[k][j] * g;
-          const float du = g * m[k][j];
-          ox[j] = du * sg[k][j];
-          oi[j] = du * u[k][j] * (1.f - sg[k][j]);
-          float w = before[k][j];
-          // (where a is one no gradient passes through m)
-          if constexpr (NORM) {
-            const float v = dec[k][j] * u[k][j] * __builtin_amdgcn_rcpf(m[k][j]);
-            w -= m[k][j] > 0.f ? v : 0.f;
+          ox[j] = g * sx[k][j];
+          if constexpr (GATE) oi[j] = g * si[k][j];
+          const float dla = c[j] * bw[k][j];
+          float p = rho[k][j], s = slope[k][j];
+          if constexpr (TIGHT) {
+            const float lo = fabsf(kept[k][j]), hi = 1.f - lo;
+            p = __float_as_int(kept[k][j]) >= 0 ? hi : lo;
+            s = lo * hi;
           }
-          const float dla = c[j] * w * rho[k][j];    // of A
-          orr[j] = dla * (kLn2 * A2[j]) * (1.f - rho[k][j]);
-          sA[j] += dla;
+          orr[j] = dla * (kLn2 * A2[j]) * s;
+          sA[j] = fmaf(dla, p, sA[j]);
         }
         if (whole || t + k < n) {
           const int nc = whole ? 2 : pl.n;
@@ -664,6 +702,16 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrArgs a, int ncb, i
       tokens(true);
     } else {
       tokens(false);
+    }
+    // (behind the results: with the other rows dy's would take registers of their own
+    // while the tokens' factors are formed, 4 x 4096 x 4096 bf16 225 us for 238)
+    if (next + TILE <= n) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) fetch_dy(std::true_type(), k, next);
+      apart<true>();
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; ++k) fetch_dy(std::false_type(), k, next);
     }
     dA[0] += (double)sA[0];
     dA[1] += (double)sA[1];

@@ -67,19 +67,21 @@ def glr_backward_ref(x, r, A, dy, i=None, h0=None, dh_T=None, lengths=None,
         cm = np.abs(c)
         for t in range(n[b] - 1, -1, -1):
             rho, la, a, m = glr_factors(r[b, t], A, normalize)
+            # (1 - sigmoid(z) would lose its digits at an open gate)
+            shut = sigmoid(-r[b, t])
             gi = np.ones(C) if i is None else sigmoid(i[b, t])
             u = gi * x[b, t]
             now, nowm = c + dy[b, t], cm + np.abs(dy[b, t])
             g["x"][b, t], mag["x"][b, t] = now * m * gi, nowm * m * gi
             if i is not None:
-                g["i"][b, t] = now * m * u * (1 - gi)
-                mag["i"][b, t] = nowm * m * np.abs(u)
+                less = u * sigmoid(-i[b, t])
+                g["i"][b, t], mag["i"][b, t] = now * m * less, nowm * m * np.abs(less)
             w = np.zeros(C)
             if normalize:
                 np.divide(a * a * u, m, out=w, where=m > 0)
             dla = now * (a * before[b, t] - w)
             dlam = nowm * (a * big[b, t] + np.abs(w))
-            g["r"][b, t], mag["r"][b, t] = dla * la * (1 - rho), dlam * np.abs(la)
+            g["r"][b, t], mag["r"][b, t] = dla * la * shut, dlam * np.abs(la) * shut
             g["A"] += dla * rho
             mag["A"] += dlam * rho
             c, cm = a * now, a * nowm
