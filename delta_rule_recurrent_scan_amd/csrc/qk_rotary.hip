@@ -12,9 +12,10 @@
 // being 4, 8 or 16 adjacent lanes (16384 tokens of 32 heads of 128 bf16: 56 us for 269 MB,
 // 4.8 TB/s; backward of 20 heads with fp32 adjoints 66 us for 336 MB, 5.1 TB/s, and 5 us
 // of column sum). A workgroup takes a few tokens with all their
-// heads, so that an angle is worked out once for all heads: in turns and in 64
-// bits (a position of 2^31 keeps 29 bits of its turn), its cosine and sine in 32,
-// left in LDS. Weight gradients stay in registers while a workgroup walks its
+// heads, so that an angle is worked out once for all heads: in turns and in 64 bits,
+// with what the product and 1 / (2 pi) lose to them (2^31 at a frequency of one is 2^28
+// turns, of which 24 bits behind the point would be left), its cosine and sine in 32, left
+// in LDS. Weight gradients stay in registers while a workgroup walks its
 // tokens and leave as one partial row each, summed in a fixed order.
 #include "launch.hpp"
 #include "layer.hpp"
@@ -30,6 +31,15 @@ struct Turns {
   float2 cs[kThreads * 4];        // [token][pair] (cos, sin), 4 L pairs at most
 };
 
+// Turns of the angle p f, less whole ones.
+__device__ __forceinline__ double turns(double p, double f) {
+  constexpr double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;   // 1 / (2 pi)
+  const double w = p * f, t = w * hi;
+  const double rest = fma(w, lo, fma(p, f, -w) * hi);
+  const double turn = fma(w, hi, -rint(t)) + rest;
+  return turn - rint(turn);
+}
+
 // The cosines and sines of the tile's tokens; the caller's barrier follows.
 __device__ __forceinline__ void fill_turns(const QkArgs& a, Turns& s, long long tok, int nt) {
   const unsigned np = a.rot / 2;
@@ -37,8 +47,7 @@ __device__ __forceinline__ void fill_turns(const QkArgs& a, Turns& s, long long 
     const unsigned i = e / np, j = e % np;
     const long long at = tok + i;
     const double p = a.positions ? (double)a.positions[at] : (double)(at % a.T);
-    double turn = p * (double)a.inv_freq[j] * 0.15915494309189533577;
-    turn -= rint(turn);
+    const double turn = turns(p, (double)a.inv_freq[j]);
     float sn, cs;
     sincospif(2.f * (float)turn, &sn, &cs);
     s.cs[i * np + j] = float2{cs, sn};
