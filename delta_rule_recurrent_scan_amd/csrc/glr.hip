@@ -5,6 +5,7 @@
 //   dx = g m sigmoid(i),  di = g m x sigmoid'(i)
 //   dla = g (a h_{t-1} - (a^2 / m) sigmoid(i) x),  dr = dla la (1 - rho),
 //   dA = sum dla rho.
+// What g is multiplied by in each of them is formed as soon as a token's gates are there.
 //
 // A workgroup walks the tokens of one sequence (or a segment of it) for 64
 // channels, a tile of 128 or 256 tokens at a time: a thread holds 8 or 16
@@ -15,12 +16,13 @@
 // written once. Where the sequences and channels alone leave CUs idle the
 // tokens are cut into segments, whose sums a first launch forms.
 //
-// Bound by HBM, with the vector units close behind (some 45 instructions an element):
-// 4 x 4096 x 4096 bf16 with an input gate and the states 104 us for 554 MB (5.3 TB/s),
-// backward 220 us for 957 MB (4.4 TB/s; rows of 24 KB, 207 us with rows off that stride),
-// 1 x 9001 x 1536 fp32 in segments, the states alone, 57 us for 336 MB and the backward
-// from them 84 us for 498 MB (5.9 TB/s). Short calls are their launches: 11 us of host and
-// 4 us of kernel for a token of 128 x 4096 channels.
+// The forward is bound by HBM, with the vector units close behind (some 45 instructions an
+// element): 4 x 4096 x 4096 bf16 with an input gate and the states 105 us for 554 MB (5.3
+// TB/s). The backward in bf16 is bound by both (some 70 instructions an element, six or
+// seven of them of a quarter rate): 204 us for 957 MB (4.7 TB/s), where fp32 with its half
+// as many elements a byte reaches 5.9 TB/s: 1 x 9001 x 1536 in segments, the states alone,
+// 60 us for 336 MB and the backward from them 85 us for 497 MB. Short calls are their
+// launches: 11 us of host and 4 us of kernel for a token of 128 x 4096 channels.
 //
 // Decays lie close to one and act over thousands of tokens. A product of
 // rounded decays would be off by their common rounding times the number of
@@ -46,8 +48,8 @@ constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 // Two channels of one token as they lie in memory. The base is the same in
 // all lanes and the byte offset 32 bits. VEC: one access, of any alignment (global memory
 // takes them all: rows of 4096 bf16 channels 4097 apart 209 -> 140 us, their backward 370
-// -> 246). With an odd number of channels, where nothing is gained and the backward loses
-// (423 -> 510 us at 4095), by element.
+// -> 238). With an odd number of channels by element: a pair that begins on an odd element
+// gained nothing in the forward and lost in the backward.
 typedef unsigned __attribute__((aligned(2))) any_u32;
 typedef __attribute__((ext_vector_type(2), aligned(4))) float any_f32x2;
 template <typename T, bool VEC>
@@ -632,7 +634,7 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrArgs a, int ncb, i
         // (where a is one no gradient passes through m)
         bw[k][j] = NORM && m > 0.f ? dec[k][j] * u * __builtin_amdgcn_rcpf(m) : 0.f;
       }
-    // (token by token as in the forward the registers run out: 211 against 206 us)
+    // (token by token as in the forward the registers run out)
     fetch_state(next);
     if (next + TILE <= n) {
 #pragma unroll
@@ -746,12 +748,15 @@ int col_blocks(int C) { return (C + kCols - 1) / kCols; }
 // room for the tile ahead. Short sequences would leave waves of a tile empty.
 bool long_runs(int T, int bf16) { return bf16 && T >= 512; }
 
-// Segments of a sequence: one while the sequences and channels alone give three
-// quarters of the CUs a workgroup; otherwise as many as give each one, of 128 tokens at
-// least (1 x 8192 x 2048: 64 us with two a CU, 55 with one).
+// Segments of a sequence: one while the sequences and channels alone give more than half
+// the CUs a workgroup (2 x 8192 x 5120, 160 of them: 187 us, backward 348, and 275 and 402
+// in two segments, whose maps cost most of the inputs again); otherwise as many as give
+// each CU one (1 x 8192 x 2048: 64 us with two a CU, 55 with one), of 128 tokens at least.
+// They are dealt whole tiles, so that the last ones may get none: of the 5 of 1000 tokens
+// of 128 a tile 4 work, of the 16 of 2048 tokens of 256 a tile 8.
 int segments(int B, int T, int C) {
   const long long wgs = (long long)B * col_blocks(C);
-  if (wgs >= 192 || wgs == 0) return 1;
+  if (wgs == 0) return 1;
   long long S = 256 / wgs;
   if (S > T / 128) S = T / 128;
   return S < 2 ? 1 : (int)S;
