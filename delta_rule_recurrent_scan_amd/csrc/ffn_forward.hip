@@ -5,11 +5,11 @@
 //
 // Bound by the matrix units where there are many rows: 8192 x 2048 x 5632 bf16 takes 360
 // us with g and u kept (1050 TFLOP/s) and 317 without (1190): a tile's results are 3 x 64
-// KB that its CU writes while it multiplies nothing. Bound by the weights' bytes for a few
-// rows (up to 64), which have a kernel of their own: 16 columns of both weights a
-// workgroup, its eight waves taking tiles of k in turn straight from memory into
-// registers, their sums joined in LDS (8 rows of the same weights: 13 us for 46 MB, of
-// which 4 are the launch).
+// KB that its CU writes while it multiplies nothing. A few rows (up to 64) have a kernel
+// of their own, which streams the weights: 16 columns of both a workgroup, its eight waves
+// taking tiles of k in turn straight from memory into registers, their sums joined in LDS.
+// 8 rows of the same weights take 13 us for 46 MB, where a copy's rate would be 9: the 352
+// workgroups are alike, so that some of the 256 CUs stream two and some one.
 #include "ffn_common.hpp"
 
 namespace osdn {
@@ -197,6 +197,17 @@ __global__ __launch_bounds__(64 * kRowsWaves) void ffn_rows_kernel(FfnArgs a) {
 // Launches
 // ---------------------------------------------------------------------------
 
+// Rows up to which the weights are streamed. Microseconds of a call among others, with
+// weights from memory, by that kernel and by tiles:
+//                        16 rows        32 rows        64 rows
+//   bf16 1024 x 2816   5.6   10.4     6.4   10.7     8.8   10.8
+//        2048 x 5632   16.5  26.8     21.0  27.2     26.0  27.2
+//        4096 x 5632   29.4  24.4     37.3  25.3     47.4  26.2
+//   fp32 1024 x 2816   8.4   18.1     10.6  18.1     19.5  18.4
+//        2048 x 5632   28.3  38.1     36.5  38.7     66.8  38.8
+// So it is the faster one up to 32 rows of up to 8 KB, and up to 64 of up to 4 KB; longer
+// rows of more than 32 lose by it. (With eight fragments, 128 rows: 2048 x 5632 bf16 43 us
+// and tiles 19, the weights in the caches.)
 constexpr int kFewRows = 64;
 
 template <typename T, int NR>
@@ -303,7 +314,9 @@ bool make_plan(Plan& best, Kind kind, long long M, long long N, long long K, int
 
 // Two products that leave the card half empty each run side by side: all items of both on
 // the card at once, none whole rounds. Its time is that of the longest item alone or of a
-// CU's share of all the work.
+// CU's share of all the work, taken as even: items of two lengths dealt in turn are not
+// (333 x 509 x 1366 fp32: 192 of 22 tiles of k and 352 of 11, of which the busiest CU has
+// 44 and a CU on average 31.6; 44 at 0.64 are 28 of the launch's 30 us).
 bool make_pair(Plan& p, Plan& q, const long long (&one)[3], const long long (&two)[3], int bf16,
                double microseconds) {
   const int kt = bf16 ? kTileK<__bf16> : kTileK<float>;

@@ -111,7 +111,7 @@ def glr_forward(x, r, A, i=None, h0=None, lengths=None, normalize=True,
 
     x, r, i: [B,T,C] (one dtype, fp32 or bf16), contiguous along the channels
     (channel ranges of one wider projection are read in place; i None: no input
-    gate); A: [C] fp32, <= 0; h0: [B,C] fp32 (None: zeros); lengths: [B] int32 of
+    gate); A: [C] fp32, finite, <= 0; h0: [B,C] fp32 (None: zeros); lengths: [B] int32 of
     a padded batch. With a = exp(A sigmoid(r)), h <- a h + m sigmoid(i) x and
     y = h, where m = sqrt(1 - a^2), or 1 with ``normalize=False``. With ``save``,
     states [B, ceil(T / 16), C] fp32 are h before tokens 0, 16, 32, ... for

@@ -654,7 +654,8 @@ int residual_norm_backward(long long R, int C, int dtype, int res_dtype,
  *   x, r, i  [B,T,C] dtype: element (b,t,c) at x[b*x_batch_stride +
  *            t*x_token_stride + c] (strides >= 0), each a channel range of a wider
  *            projection or not; i NULL: no input gate (u_t = x_t)
- *   A        [C] fp32, <= 0 (required; with normalize a positive one gives NaN)
+ *   A        [C] fp32, finite, <= 0 (required; with normalize a positive one gives NaN,
+ *            without it a state that grows)
  *   h0       [B,C] fp32 (NULL: zeros)
  *   y        [B,T,C] dtype (NULL: not written);  h_T [B,C] fp32 (NULL: not written)
  *   states   [B,ceil(T/16),C] fp32: h before tokens 0, 16, 32, ..., for the backward
@@ -713,14 +714,15 @@ int glr_backward(int B, int T, int C, int dtype, const void* x,
  *   v = n * weight
  *   (y_a, y_b) = (v_a cos w - v_b sin w, v_b cos w + v_a sin w),  w = p inv_freq[j]
  * for j < rot / 2 and the channels (a, b) = (j, j + rot/2), or (2j, 2j + 1) with
- * `interleaved`; channels from rot on pass through (y = v). With eps = 0 a row of
- * zeros gives zeros, and zero gradients.
+ * `interleaved`; channels from rot on pass through (y = v). Squares are summed in 32
+ * bits; with eps = 0 a row whose sum is zero gives zeros, and zero gradients.
  *
  *   q        [B,T,Hq*D], k [B,T,Hk*D] dtype rows with strides as above (Hq or Hk 0:
  *            none)
  *   q_weight, k_weight  [D] fp32 (NULL: ones)
  *   inv_freq [rot/2] fp32 (required if rot > 0);  rot a multiple of 16, <= D
- *   positions [B,T] int32 (NULL: 0 .. T - 1). Angles are formed in 64 bits.
+ *   positions [B,T] int32 (NULL: 0 .. T - 1). Angles are formed in 64 bits, with what
+ *            their products lose to them: any position and frequency keeps its turn.
  *   q_out    [B,Hq,T,D], k_out [B,Hk,T,D] dtype
  * D in {32, 64, 128}. Outputs, adjoints and gradients of rows start on 16 bytes.
  */
@@ -766,7 +768,8 @@ int qk_rotary_backward(int B, int T, int Hq, int Hk, int D, int rot, int dtype,
  * OSDN_ERR_UNSUPPORTED). Where C is a multiple of 8 the weights start on 16 bytes
  * (OSDN_ERR_MISALIGNED). workspace: gated_ffn_forward_workspace_bytes(...) bytes,
  * 256-byte aligned: the parts of sums that are split where tiles are few, and room for
- * rows of x (and of weights whose C is not a multiple of 8) off 16 bytes.
+ * rows of x (and of weights whose C is not a multiple of 8) off 16 bytes. The room for x
+ * is counted wherever x may lie, also where it is then read in place.
  */
 enum { OSDN_ACT_SILU = 0, OSDN_ACT_GELU = 1, OSDN_ACT_GELU_TANH = 2 };
 size_t gated_ffn_forward_workspace_bytes(long long R, int C, int F, int dtype);
