@@ -18,7 +18,7 @@
 //
 // The forward is bound by HBM, with the vector units close behind (some 45 instructions an
 // element): 4 x 4096 x 4096 bf16 with an input gate and the states 105 us for 554 MB (5.3
-// TB/s). The backward in bf16 is bound by both (some 70 instructions an element, six or
+// TB/s). The backward in bf16 is bound by both (some 70 instructions an element,
 // seven of them of a quarter rate): 204 us for 957 MB (4.7 TB/s), where fp32 with its half
 // as many elements a byte reaches 5.9 TB/s: 1 x 9001 x 1536 in segments, the states alone,
 // 60 us for 336 MB and the backward from them 85 us for 497 MB. Short calls are their
